@@ -397,6 +397,124 @@ const char *dl_last_error(const dl_ctx *ctx);
 const char *dl_status_str(dl_status s);
 int32_t dl_abi_version(void);
 
+/* ------------------------------------------------------------------------ */
+/* Mixer operators: what a layer computes around its recurrence.             */
+/*                                                                            */
+/* Short causal convolution (dl_conv), selective state space scan (dl_ssm),   */
+/* gated norm of the heads' outputs (dl_gated_norm), residual sum and norm    */
+/* before the next block (dl_add_norm).  They need no context: the caller     */
+/* owns every buffer and names the stream (a cudaStream_t, NULL = legacy      */
+/* default stream).  Every call is asynchronous, allocates nothing, keeps     */
+/* nothing for the next call, and can be captured into a CUDA graph.  All     */
+/* arguments are checked on the host first; on a status other than DL_OK      */
+/* nothing has been enqueued (DL_ECUDA: a launch failed), and errbuf, if not  */
+/* NULL, holds a one-line reason.  Calls may come from several host threads.  */
+/*                                                                            */
+/* Activations are fp32, bf16 or fp16 (dl_dtype); sums, states, softmax-like  */
+/* factors and norms are fp32 and rounded once on output.  Strides are in     */
+/* elements and may be any value that keeps tensors apart; tensors need only  */
+/* their element's alignment (16-byte aligned tensors whose strides and       */
+/* widths are multiples of 16 bytes move as vectors).  Outputs must not       */
+/* overlap inputs unless a call says so.                                      */
+/* ------------------------------------------------------------------------ */
+typedef enum dl_dtype { DL_F32 = 0, DL_BF16 = 1, DL_F16 = 2 } dl_dtype;
+typedef enum dl_act { DL_ACT_NONE = 0, DL_ACT_SILU = 1, DL_ACT_SIGMOID = 2 } dl_act;
+typedef enum dl_norm_kind { DL_NORM_RMS = 0, DL_NORM_LAYER = 1 } dl_norm_kind;
+
+/* The rows (sequences) of a call and where their tokens are.  Row i has
+ * lengths[i] tokens (T of them if lengths is NULL; 0 is allowed) and, where a
+ * state pool is given, the state of slot slots[i].  packed = 0: token t of row
+ * i of a tensor is at t * stride_t + i * stride_n.  packed = 1: the rows'
+ * tokens follow one another, token t of row i at (lengths[0] + ... +
+ * lengths[i-1] + t) * stride_t (stride_n is not used).  A fresh row starts
+ * from an empty (zero) state and overwrites its slot's; others continue from
+ * it.  n <= 1024.  slots, lengths and fresh are host arrays, read before the
+ * call returns. */
+typedef struct dl_tokens {
+    const int32_t *slots;    /* [n]: distinct, in [0, num_slots); NULL without a state pool    */
+    const int32_t *lengths;  /* [n], 0 <= lengths[i] <= T, or NULL: T each (not when packed)   */
+    const uint8_t *fresh;    /* [n], nonzero: the row is fresh; NULL: fresh_all for every row   */
+    int64_t fresh_all;
+    int64_t n, T, packed, num_slots;
+} dl_tokens;
+
+typedef struct dl_view {     /* a per-token tensor on the device */
+    void *data;
+    int64_t stride_t, stride_n;
+} dl_view;
+
+/* Short causal convolution over each channel's last W tokens:
+ *   z[t][c] = bias[c] + sum_{j < W} weight[c][j] x[t - W + 1 + j][c],  y = act(z)
+ * x at t < 0 is the slot's carried input (its last W - 1 inputs, oldest first)
+ * or zero (fresh, or no state).  The first l2_channels channels are heads of
+ * head_dim, each divided by sqrt(sum of its y^2 + eps).  The outputs are
+ * n_parts consecutive channel ranges, each a tensor of its own.  state
+ * [num_slots][W - 1][C] (contiguous, dtype) is read and updated. */
+typedef struct dl_conv_args {
+    dl_tokens tokens;
+    int64_t dtype, weight_f32;          /* weight and bias are of dtype, or fp32              */
+    int64_t C, W, act, l2_channels, head_dim, n_parts;   /* W 2..4; head_dim 8, 16 .. 256      */
+    double eps;
+    dl_view x;                          /* C contiguous channels a token                      */
+    const void *weight, *bias;          /* [C][W]; [C] or NULL                                */
+    void *state;                        /* or NULL                                            */
+    dl_view y[4];
+    int64_t part_channels[4];           /* sum = C                                            */
+} dl_conv_args;
+dl_status dl_conv(const dl_conv_args *args, void *stream, char *errbuf, int32_t errlen);
+
+/* Selective state space scan (softplus = 0: d = raw + dt_bias):
+ *   d[t][h] = softplus(dt[t][h] + dt_bias[h])
+ *   S <- exp(d A[h]) S + (d x[t][h]) B[t][g]^T,   y[t][h] = S C[t][g] + D[h] x[t][h]
+ * with S [P][N] per row and head, g = h / (H / G).  state [num_slots][H][P][N]
+ * fp32 (contiguous) is read and updated; without it rows start at zero and
+ * the final states are dropped.  N <= 256.  dl_ssm_step is the same for one
+ * token a row (T = 1), reading and writing the states of n slots once. */
+typedef struct dl_ssm_args {
+    dl_tokens tokens;
+    int64_t dtype, dt_f32, softplus, H, G, P, N;
+    dl_view x, dt, B, C, y;             /* a token: [H][P], [H], [G][N], [G][N], [H][P], contiguous */
+    const float *A, *D, *dt_bias;       /* [H]; D and dt_bias may be NULL                     */
+    float *state;                       /* or NULL (dl_ssm only)                              */
+    void *workspace;                    /* device memory of dl_ssm_workspace bytes, 16-byte aligned */
+    int64_t workspace_bytes;
+} dl_ssm_args;
+dl_status dl_ssm(const dl_ssm_args *args, void *stream, char *errbuf, int32_t errlen);
+dl_status dl_ssm_step(const dl_ssm_args *args, void *stream, char *errbuf, int32_t errlen);
+/* Bytes of workspace that dl_ssm wants for these sizes (0 for most; data
+ * pointers are not looked at); -1 if the sizes are not valid. */
+int64_t dl_ssm_workspace(const dl_ssm_args *args);
+
+/* Norm and gate of every head of d values (d <= 16384), norm(x) = x / sqrt(mean
+ * x^2 + eps), or of x - mean x (DL_NORM_LAYER):
+ *   y = (norm(x) weight + bias) act(gate),  or gate_first:  y = norm(x act(gate)) weight + bias
+ * weight and bias are [d], or [H][d] when weight_heads.  Rows of H * d
+ * contiguous values, row strides in elements.  y may be x or gate itself
+ * (same address and stride). */
+typedef struct dl_gated_norm_args {
+    int64_t dtype, weight_f32, weight_heads, rows, H, d, kind, act, gate_first;
+    double eps;
+    const void *x, *gate, *weight, *bias;   /* gate, bias may be NULL */
+    void *y;
+    int64_t x_stride, gate_stride, y_stride;
+} dl_gated_norm_args;
+dl_status dl_gated_norm(const dl_gated_norm_args *args, void *stream, char *errbuf, int32_t errlen);
+
+/* Residual sum after a block and norm before the next, rows of D <= 16384:
+ *   x' = norm(x) post if post is given, else x
+ *   h = residual + alpha scale x'  (scale [D] or NULL: 1; residual NULL: 0),  y = norm(h) weight + bias
+ * The norm takes h in fp32, before it is rounded to its own type.  residual
+ * and h are of dtype, or fp32 when residual_f32.  h may be NULL, y may be x
+ * itself, and h residual (same address and stride). */
+typedef struct dl_add_norm_args {
+    int64_t dtype, residual_f32, weight_f32, rows, D, kind;
+    double eps, alpha;
+    const void *x, *residual, *weight, *bias, *scale, *post;
+    void *y, *h;
+    int64_t x_stride, residual_stride, y_stride, h_stride;
+} dl_add_norm_args;
+dl_status dl_add_norm(const dl_add_norm_args *args, void *stream, char *errbuf, int32_t errlen);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,309 @@
+// C entry points of the mixer operators: argument checks, tile planning and
+// launches.  Everything is checked before the first CUDA call; nothing is
+// allocated and nothing kept.  The launch arguments (up to 16 KiB of row plan)
+// are built in a thread's own storage.
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "../../include/deltalog.h"
+#include "mixer.h"
+
+namespace {
+
+using namespace dl::mx;
+
+struct ErrOut {
+  char* buf;
+  int32_t len;
+  dl_status operator()(dl_status s, const char* fmt, ...) const {
+    if (buf && len > 0) {
+      va_list ap;
+      va_start(ap, fmt);
+      vsnprintf(buf, (size_t)len, fmt, ap);
+      va_end(ap);
+    }
+    return s;
+  }
+};
+
+thread_local ConvArgs t_conv;
+thread_local SsmArgs t_ssm;
+
+constexpr int64_t MAX_DIM = (int64_t)1 << 30;   // sizes that the kernels hold in 32 bits
+
+int64_t elem(int64_t dtype) { return dtype == DL_F32 ? 4 : 2; }
+bool al(const void* p, int64_t b) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(b - 1)) == 0; }
+
+// Every launch: CUDA's sticky state is left clean for the caller's next call.
+dl_status done(const ErrOut& fail, cudaError_t e) {
+  if (e == cudaSuccess) return DL_OK;
+  (void)cudaGetLastError();
+  return fail(DL_ECUDA, "launch failed: %s", cudaGetErrorString(e));
+}
+
+// Distinct ids in [0, num_slots): an open-addressing table on the stack.
+dl_status check_slots(const ErrOut& fail, const int32_t* slots, int64_t n, int64_t num_slots) {
+  constexpr uint32_t SIZE = 4096;
+  int32_t seen[SIZE];
+  uint32_t mask = 15;
+  while (mask + 1 < 4 * (uint32_t)n) mask = 2 * mask + 1;
+  memset(seen, 0xff, (size_t)(mask + 1) * 4);
+  for (int64_t i = 0; i < n; ++i) {
+    const int32_t s = slots[i];
+    if (s < 0 || s >= num_slots)
+      return fail(DL_EINVAL, "slot %d of row %lld is not in [0, %lld)", s, (long long)i, (long long)num_slots);
+    uint32_t k = ((uint32_t)s * 2654435761u >> 12) & mask;
+    while (seen[k] != -1) {
+      if (seen[k] == s) return fail(DL_EINVAL, "slot %d appears twice", s);
+      k = (k + 1) & mask;
+    }
+    seen[k] = s;
+  }
+  return DL_OK;
+}
+
+// The rows' plan.  tt: tokens of a tile (every row has at least one tile, for
+// its state); returns the number of tiles, in per_row the tiles of every row
+// when all rows have the same number (else 0), and whether there is any token.
+dl_status plan_rows(const ErrOut& fail, const dl_tokens& k, bool state, int64_t tt, RowItem* items,
+                    int64_t& tiles, int32_t& per_row, bool& any) {
+  if (k.n < 0 || k.n > MX_ROWS) return fail(DL_EINVAL, "%lld rows: at most %d a call", (long long)k.n, MX_ROWS);
+  if (k.T < 0 || k.T > MAX_DIM) return fail(DL_EINVAL, "%lld tokens a row", (long long)k.T);
+  if (k.packed && !k.lengths && k.n > 0) return fail(DL_EINVAL, "packed tokens need lengths");
+  if (state) {
+    if (!k.slots && k.n > 0) return fail(DL_EINVAL, "a state pool needs slots");
+    if (k.num_slots < 1 || k.num_slots > 0x7fffffff) return fail(DL_EINVAL, "%lld slots", (long long)k.num_slots);
+    const dl_status s = check_slots(fail, k.slots, k.n, k.num_slots);
+    if (s != DL_OK) return s;
+  }
+  int64_t begin = 0;
+  tiles = 0;
+  any = false;
+  bool same = true;
+  for (int64_t i = 0; i < k.n; ++i) {
+    const int64_t len = k.lengths ? k.lengths[i] : k.T;
+    if (len < 0 || len > k.T) return fail(DL_EINVAL, "row %lld has %lld tokens, T is %lld", (long long)i, (long long)len, (long long)k.T);
+    const bool fresh = k.fresh ? k.fresh[i] != 0 : k.fresh_all != 0;
+    items[i] = RowItem{state ? k.slots[i] : 0, (int32_t)begin, (int32_t)len | (fresh || !state ? FRESH_BIT : 0),
+                       (int32_t)tiles};
+    const int64_t nt = len > tt ? (len + tt - 1) / tt : 1;
+    if (i == 0) per_row = (int32_t)nt;
+    same = same && nt == per_row;
+    any = any || len > 0;
+    tiles += nt;
+    if (k.packed) begin += len;
+    if (tiles > MAX_DIM || begin > MAX_DIM) return fail(DL_EINVAL, "too many tokens in one call");
+  }
+  if (!same) per_row = 0;
+  return DL_OK;
+}
+
+TokView view(const dl_view& v, bool packed) { return TokView{v.data, v.stride_t, packed ? 0 : v.stride_n}; }
+
+bool view_vec(const dl_view& v, int64_t dtype, bool packed) {
+  const int64_t per = 16 / elem(dtype);
+  return al(v.data, 16) && v.stride_t % per == 0 && (packed || v.stride_n % per == 0);
+}
+
+bool bad_type(int64_t t) { return t < DL_F32 || t > DL_F16; }
+
+}  // namespace
+
+extern "C" dl_status dl_conv(const dl_conv_args* p, void* stream, char* errbuf, int32_t errlen) {
+  const ErrOut fail{errbuf, errlen};
+  if (errbuf && errlen > 0) errbuf[0] = 0;
+  if (!p) return fail(DL_EINVAL, "NULL argument");
+  const dl_conv_args& q = *p;
+  const bool packed = q.tokens.packed != 0;
+  if (bad_type(q.dtype)) return fail(DL_EINVAL, "unknown dtype %lld", (long long)q.dtype);
+  if (q.C < 1 || q.C > MAX_DIM) return fail(DL_EINVAL, "%lld channels", (long long)q.C);
+  if (q.W < 2 || q.W > 4) return fail(DL_EUNSUPPORTED, "width %lld: 2 to 4 are supported", (long long)q.W);
+  if (q.act != DL_ACT_NONE && q.act != DL_ACT_SILU) return fail(DL_EINVAL, "activation %lld: none or silu", (long long)q.act);
+  if (q.n_parts < 1 || q.n_parts > CONV_PARTS) return fail(DL_EINVAL, "%lld output ranges: 1 to 4", (long long)q.n_parts);
+  if (q.l2_channels < 0 || q.l2_channels > q.C) return fail(DL_EINVAL, "%lld normalised channels of %lld", (long long)q.l2_channels, (long long)q.C);
+  if (q.l2_channels) {
+    const int64_t d = q.head_dim;
+    if (d < 8 || d > 256 || (d & (d - 1))) return fail(DL_EUNSUPPORTED, "head_dim %lld: a power of two from 8 to 256", (long long)d);
+    if (q.l2_channels % d) return fail(DL_EINVAL, "%lld normalised channels are not whole heads of %lld", (long long)q.l2_channels, (long long)d);
+    if (!(q.eps >= 0)) return fail(DL_EINVAL, "eps is negative");
+  }
+  ConvArgs& a = t_conv;
+  int64_t c = 0;
+  bool vec = q.C % 8 == 0;
+  for (int k = 0; k < CONV_PARTS; ++k) {
+    a.c0[k] = (int32_t)c;
+    a.y[k] = TokView{nullptr, 0, 0};
+    if (k >= q.n_parts) continue;
+    const int64_t ch = q.part_channels[k];
+    if (ch < 1 || c + ch > q.C) return fail(DL_EINVAL, "output ranges do not add up to %lld channels", (long long)q.C);
+    a.y[k] = view(q.y[k], packed);
+    vec = vec && ch % 8 == 0 && view_vec(q.y[k], q.dtype, packed);
+    c += ch;
+  }
+  if (c != q.C) return fail(DL_EINVAL, "output ranges do not add up to %lld channels", (long long)q.C);
+  a.c0[CONV_PARTS] = (int32_t)q.C;
+  for (int k = (int)q.n_parts; k < CONV_PARTS; ++k) a.c0[k] = (int32_t)q.C;
+  a.TT = 32;
+  int64_t tiles;
+  bool any;
+  const dl_status s = plan_rows(fail, q.tokens, q.state != nullptr, a.TT, a.items, tiles, a.per_row, any);
+  if (s != DL_OK) return s;
+  if (q.tokens.n == 0) return DL_OK;
+  const int64_t e = elem(q.dtype);
+  if ((!q.x.data && any) || !q.weight) return fail(DL_EINVAL, "NULL tensor pointer");
+  const int64_t we = q.weight_f32 ? 4 : e;
+  bool ok = al(q.x.data, e) && al(q.weight, we) && al(q.bias, we) && al(q.state, e);
+  for (int k = 0; k < q.n_parts; ++k) {
+    if (!q.y[k].data && any) return fail(DL_EINVAL, "NULL tensor pointer");
+    ok = ok && al(q.y[k].data, e);
+  }
+  if (!ok) return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
+  vec = vec && view_vec(q.x, q.dtype, packed) && al(q.state, 16);
+  a.x = view(q.x, packed);
+  a.w = q.weight;
+  a.b = q.bias;
+  a.state = q.state;
+  a.C = (int32_t)q.C;
+  a.W = (int32_t)q.W;
+  a.act = (int32_t)q.act;
+  a.l2c = (int32_t)q.l2_channels;
+  a.hd = (int32_t)q.head_dim;
+  a.w_f32 = q.weight_f32 ? 1 : 0;
+  a.rows = (int32_t)q.tokens.n;
+  a.tiles = (int32_t)tiles;
+  a.eps = (float)q.eps;
+  return done(fail, launch_conv((int)q.dtype, vec, a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+dl_status ssm_sizes(const ErrOut& fail, const dl_ssm_args& q) {
+  if (bad_type(q.dtype)) return fail(DL_EINVAL, "unknown dtype %lld", (long long)q.dtype);
+  if (q.H < 1 || q.H > 65536 || q.G < 1 || q.H % q.G)
+    return fail(DL_EINVAL, "%lld heads in %lld groups", (long long)q.H, (long long)q.G);
+  if (q.P < 1 || q.P > 65536 || q.N < 1) return fail(DL_EINVAL, "state of %lld x %lld", (long long)q.P, (long long)q.N);
+  if (q.N > 256) return fail(DL_EUNSUPPORTED, "N = %lld: at most 256 is supported", (long long)q.N);
+  return DL_OK;
+}
+
+dl_status ssm_args(const ErrOut& fail, const dl_ssm_args& q, SsmArgs& a) {
+  dl_status s = ssm_sizes(fail, q);
+  if (s != DL_OK) return s;
+  int64_t tiles;
+  int32_t per_row;
+  bool any;
+  const bool packed = q.tokens.packed != 0;
+  s = plan_rows(fail, q.tokens, q.state != nullptr, MAX_DIM, a.items, tiles, per_row, any);
+  if (s != DL_OK || q.tokens.n == 0) return s;
+  const int64_t e = elem(q.dtype);
+  for (const dl_view* v : {&q.x, &q.B, &q.C, &q.y}) {
+    if (!v->data && any) return fail(DL_EINVAL, "NULL tensor pointer");
+    if (!al(v->data, e)) return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
+  }
+  if ((!q.dt.data && any) || !q.A) return fail(DL_EINVAL, "NULL tensor pointer");
+  if (!al(q.dt.data, q.dt_f32 ? 4 : e) || !al(q.A, 4) || !al(q.D, 4) || !al(q.dt_bias, 4) || !al(q.state, 4))
+    return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
+  a.x = view(q.x, packed);
+  a.dt = view(q.dt, packed);
+  a.B = view(q.B, packed);
+  a.C = view(q.C, packed);
+  a.y = view(q.y, packed);
+  a.A = q.A;
+  a.D = q.D;
+  a.dt_bias = q.dt_bias;
+  a.state = q.state;
+  a.H = (int32_t)q.H;
+  a.G = (int32_t)q.G;
+  a.P = (int32_t)q.P;
+  a.N = (int32_t)q.N;
+  a.softplus = q.softplus ? 1 : 0;
+  a.dt_f32 = q.dt_f32 ? 1 : 0;
+  a.rows = (int32_t)q.tokens.n;
+  if ((int64_t)a.rows * q.H * q.P > (int64_t)1 << 31) return fail(DL_EINVAL, "too many state rows in one call");
+  return DL_OK;
+}
+
+}  // namespace
+
+extern "C" int64_t dl_ssm_workspace(const dl_ssm_args* p) {
+  const ErrOut quiet{nullptr, 0};
+  if (!p || ssm_sizes(quiet, *p) != DL_OK || p->tokens.n < 0 || p->tokens.n > MX_ROWS) return -1;
+  return 0;
+}
+
+extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, int32_t errlen) {
+  const ErrOut fail{errbuf, errlen};
+  if (errbuf && errlen > 0) errbuf[0] = 0;
+  if (!p) return fail(DL_EINVAL, "NULL argument");
+  SsmArgs& a = t_ssm;
+  const dl_status s = ssm_args(fail, *p, a);
+  if (s != DL_OK || p->tokens.n == 0) return s;
+  return done(fail, launch_ssm_scan((int)p->dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" dl_status dl_ssm_step(const dl_ssm_args* p, void* stream, char* errbuf, int32_t errlen) {
+  const ErrOut fail{errbuf, errlen};
+  if (errbuf && errlen > 0) errbuf[0] = 0;
+  if (!p) return fail(DL_EINVAL, "NULL argument");
+  if (!p->state) return fail(DL_EINVAL, "a step needs a state pool");
+  if (p->tokens.T != 1 || p->tokens.lengths) return fail(DL_EINVAL, "a step takes one token a row");
+  SsmArgs& a = t_ssm;
+  const dl_status s = ssm_args(fail, *p, a);
+  if (s != DL_OK || p->tokens.n == 0) return s;
+  return done(fail, launch_ssm_step((int)p->dtype, a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" dl_status dl_gated_norm(const dl_gated_norm_args* p, void* stream, char* errbuf, int32_t errlen) {
+  const ErrOut fail{errbuf, errlen};
+  if (errbuf && errlen > 0) errbuf[0] = 0;
+  if (!p) return fail(DL_EINVAL, "NULL argument");
+  const dl_gated_norm_args& q = *p;
+  if (bad_type(q.dtype)) return fail(DL_EINVAL, "unknown dtype %lld", (long long)q.dtype);
+  if (q.kind != DL_NORM_RMS && q.kind != DL_NORM_LAYER) return fail(DL_EINVAL, "unknown norm %lld", (long long)q.kind);
+  if (q.act < DL_ACT_NONE || q.act > DL_ACT_SIGMOID) return fail(DL_EINVAL, "unknown activation %lld", (long long)q.act);
+  if (q.rows < 0 || q.H < 1 || q.d < 1 || q.rows > MAX_DIM || q.H > MAX_DIM || q.rows * q.H > MAX_DIM)
+    return fail(DL_EINVAL, "%lld rows of %lld heads of %lld", (long long)q.rows, (long long)q.H, (long long)q.d);
+  if (q.d > 16384) return fail(DL_EUNSUPPORTED, "heads of %lld: at most 16384 is supported", (long long)q.d);
+  if (!(q.eps >= 0)) return fail(DL_EINVAL, "eps is negative");
+  if (q.rows == 0) return DL_OK;
+  if (!q.x || !q.y || !q.weight) return fail(DL_EINVAL, "NULL tensor pointer");
+  const int64_t e = elem(q.dtype), we = q.weight_f32 ? 4 : e, per = 16 / e;
+  if (!al(q.x, e) || !al(q.gate, e) || !al(q.y, e) || !al(q.weight, we) || !al(q.bias, we))
+    return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
+  const bool vec = q.d % 8 == 0 && al(q.x, 16) && al(q.gate, 16) && al(q.y, 16) && al(q.weight, 16) && al(q.bias, 16) &&
+                   q.x_stride % per == 0 && q.y_stride % per == 0 && (!q.gate || q.gate_stride % per == 0);
+  const GatedNormArgs a{q.x, q.gate, q.weight, q.bias, q.y, q.x_stride, q.gate_stride, q.y_stride, q.rows,
+                        (int32_t)q.H, (int32_t)q.d, (int32_t)q.kind, (int32_t)q.act, q.gate_first ? 1 : 0,
+                        q.weight_f32 ? 1 : 0, q.weight_heads ? 1 : 0, (float)q.eps};
+  return done(fail, launch_gated_norm((int)q.dtype, vec, a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" dl_status dl_add_norm(const dl_add_norm_args* p, void* stream, char* errbuf, int32_t errlen) {
+  const ErrOut fail{errbuf, errlen};
+  if (errbuf && errlen > 0) errbuf[0] = 0;
+  if (!p) return fail(DL_EINVAL, "NULL argument");
+  const dl_add_norm_args& q = *p;
+  if (bad_type(q.dtype)) return fail(DL_EINVAL, "unknown dtype %lld", (long long)q.dtype);
+  if (q.kind != DL_NORM_RMS && q.kind != DL_NORM_LAYER) return fail(DL_EINVAL, "unknown norm %lld", (long long)q.kind);
+  if (q.rows < 0 || q.rows > MAX_DIM || q.D < 1) return fail(DL_EINVAL, "%lld rows of %lld", (long long)q.rows, (long long)q.D);
+  if (q.D > 16384) return fail(DL_EUNSUPPORTED, "rows of %lld: at most 16384 is supported", (long long)q.D);
+  if (!(q.eps >= 0)) return fail(DL_EINVAL, "eps is negative");
+  if (q.rows == 0) return DL_OK;
+  if (!q.x || !q.y || !q.weight) return fail(DL_EINVAL, "NULL tensor pointer");
+  const bool r32 = q.residual_f32 || q.dtype == DL_F32;
+  const int64_t e = elem(q.dtype), re = r32 ? 4 : 2, we = q.weight_f32 ? 4 : e, per = 16 / e, rper = 16 / re;
+  if (!al(q.x, e) || !al(q.y, e) || !al(q.residual, re) || !al(q.h, re) || !al(q.weight, we) || !al(q.bias, we) ||
+      !al(q.scale, we) || !al(q.post, we))
+    return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
+  bool vec = q.D % 8 == 0 && q.x_stride % per == 0 && q.y_stride % per == 0 &&
+             (!q.residual || q.residual_stride % rper == 0) && (!q.h || q.h_stride % rper == 0);
+  for (const void* t : {q.x, q.residual, q.weight, q.bias, q.scale, q.post, (const void*)q.y, (const void*)q.h})
+    vec = vec && al(t, 16);
+  const AddNormArgs a{q.x, q.residual, q.weight, q.bias, q.scale, q.post, q.y, q.h, q.x_stride, q.residual_stride,
+                      q.y_stride, q.h_stride, q.rows, (int32_t)q.D, (int32_t)q.kind, q.weight_f32 ? 1 : 0,
+                      (float)q.eps, (float)q.alpha};
+  return done(fail, launch_add_norm((int)q.dtype, r32, vec, a, static_cast<cudaStream_t>(stream)));
+}

@@ -1,0 +1,141 @@
+// Element access shared by the mixer kernels: eight consecutive values of a
+// type, moved as 16-byte vectors when VEC (the host checked alignment) and one
+// by one otherwise, and held in 32 bits.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "mixer.h"
+
+namespace dl {
+namespace mx {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+template <class T> __device__ __forceinline__ T from_f(float x);
+template <> __device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+
+template <class T> __device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b);
+template <> __device__ __forceinline__ void unpack2<__nv_bfloat16>(uint32_t w, float& a, float& b) {
+  a = __uint_as_float(w << 16);
+  b = __uint_as_float(w & 0xffff0000u);
+}
+template <> __device__ __forceinline__ void unpack2<__half>(uint32_t w, float& a, float& b) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  a = f.x;
+  b = f.y;
+}
+template <class T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 p = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&p);
+}
+
+// Eight values of type T as they sit in memory.
+template <class T> struct Vec8 { uint32_t w[sizeof(T) == 4 ? 8 : 4]; };
+
+template <class T, bool VEC>
+__device__ __forceinline__ Vec8<T> load8(const T* p, int valid) {
+  Vec8<T> v;
+  constexpr int NW = sizeof(T) == 4 ? 8 : 4;
+  if (VEC) {
+    if (valid > 0) {
+#pragma unroll
+      for (int k = 0; k < NW / 4; ++k) {
+        const uint4 u = reinterpret_cast<const uint4*>(p)[k];
+        v.w[4 * k] = u.x;
+        v.w[4 * k + 1] = u.y;
+        v.w[4 * k + 2] = u.z;
+        v.w[4 * k + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NW; ++k) v.w[k] = 0u;
+    }
+  } else if (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v.w[k] = k < valid ? reinterpret_cast<const uint32_t*>(p)[k] : 0u;
+  } else {
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = 2 * k < valid ? q[2 * k] : 0u, hi = 2 * k + 1 < valid ? q[2 * k + 1] : 0u;
+      v.w[k] = lo | (hi << 16);
+    }
+  }
+  return v;
+}
+template <class T, bool VEC>
+__device__ __forceinline__ void store8(T* p, const Vec8<T>& v, int valid) {
+  constexpr int NW = sizeof(T) == 4 ? 8 : 4;
+  if (VEC) {
+    if (valid > 0) {
+#pragma unroll
+      for (int k = 0; k < NW / 4; ++k)
+        reinterpret_cast<uint4*>(p)[k] = make_uint4(v.w[4 * k], v.w[4 * k + 1], v.w[4 * k + 2], v.w[4 * k + 3]);
+    }
+  } else if (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < valid) reinterpret_cast<uint32_t*>(p)[k] = v.w[k];
+  } else {
+    uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < valid) q[k] = (uint16_t)(v.w[k >> 1] >> (16 * (k & 1)));
+  }
+}
+template <class T> __device__ __forceinline__ void unpack8(const Vec8<T>& v, float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v.w[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpack2<T>(v.w[k], f[2 * k], f[2 * k + 1]);
+  }
+}
+template <class T> __device__ __forceinline__ Vec8<T> pack8(const float (&f)[8]) {
+  Vec8<T> v;
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v.w[k] = __float_as_uint(f[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v.w[k] = pack2<T>(f[2 * k], f[2 * k + 1]);
+  }
+  return v;
+}
+// Eight weights that are fp32 or of the activations' type.
+template <class T, bool VEC>
+__device__ __forceinline__ void weights8(const void* base, int64_t i, int valid, int f32, float (&f)[8]) {
+  if (f32) {
+    unpack8<float>(load8<float, VEC>(static_cast<const float*>(base) + i, valid), f);
+  } else {
+    unpack8<T>(load8<T, VEC>(static_cast<const T*>(base) + i, valid), f);
+  }
+}
+
+// 1 / (1 + e^-z) and z / (1 + e^-z).  For a 16-bit type e^x and the quotient
+// are the fast forms, within about 2^-20 relative where the value is not tiny,
+// far below the type's own rounding; for fp32 they are the accurate ones.
+template <class T> __device__ __forceinline__ float sigmoid_f(float z) {
+  if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-z));
+  return __fdividef(1.f, 1.f + __expf(-z));
+}
+template <class T> __device__ __forceinline__ float act_f(float z, int act) {
+  return act == ACT_NONE ? z : act == ACT_SILU ? z * sigmoid_f<T>(z) : sigmoid_f<T>(z);
+}
+// log(1 + e^x) without overflow or loss for either sign.
+__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+}  // namespace mx
+}  // namespace dl
