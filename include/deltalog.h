@@ -485,6 +485,13 @@ dl_status dl_ssm_step(const dl_ssm_args *args, void *stream, char *errbuf, int32
  * pointers are not looked at); -1 if the sizes are not valid. */
 int64_t dl_ssm_workspace(const dl_ssm_args *args);
 
+/* Synchronise `stream`, then read and clear the mixer kernels' status word of
+ * the current device.  The tensor-core scan waits for its own products with a
+ * time limit; a wait that ran out since the last call is reported as
+ * DL_EDEVICE (*device_code, if not NULL, receives the code), and the outputs
+ * and states of the calls since then must not be trusted. */
+dl_status dl_mixer_sync(void *stream, int32_t *device_code, char *errbuf, int32_t errlen);
+
 /* Norm and gate of every head of d values (d <= 16384), norm(x) = x / sqrt(mean
  * x^2 + eps), or of x - mean x (DL_NORM_LAYER):
  *   y = (norm(x) weight + bias) act(gate),  or gate_first:  y = norm(x act(gate)) weight + bias

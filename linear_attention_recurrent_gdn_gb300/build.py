@@ -19,7 +19,7 @@ LIB = os.path.join(OUT_DIR, "libdeltalog.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["replay_prep.cu", "append_decode.cu", "append_fused_ne8.cu", "append_fused_ne16.cu",
               "append_fused_ne32.cu", "eager_step.cu", "slot_ops.cu", "prefill.cu", "prefill_tc.cu", "capi.cu",
-              "noalloc.cu", "mixer_capi.cu", "conv.cu", "ssm_scan.cu", "ssm_step.cu", "norms.cu"]
+              "noalloc.cu", "mixer_capi.cu", "conv.cu", "ssm_scan.cu", "ssm_tc.cu", "ssm_step.cu", "norms.cu"]
 CPP_SOURCES = ["slot_table.cpp"]
 
 

@@ -70,6 +70,20 @@ struct SsmArgs {
 cudaError_t launch_ssm_scan(int dtype, const SsmArgs& a, cudaStream_t s);
 cudaError_t launch_ssm_step(int dtype, const SsmArgs& a, cudaStream_t s);
 
+// How the tensor-core scan splits a call: nh heads of up to ph columns a CTA,
+// `units` CTAs a segment of seg_tokens tokens; split: a row may have several
+// segments, joined through a workspace.
+struct SsmPlan {
+  int32_t nh, ph, ptiles, units, seg_tokens;
+  bool split;
+};
+SsmPlan ssm_tc_plan(int H, int G, int P, int N, int rows, const int32_t* lens, int64_t T, int sms);
+// bf16, N <= 128.  ws: tiles * H * (P * N + 1) floats when split.
+cudaError_t launch_ssm_tc(bool vec, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row, float* ws,
+                          cudaStream_t s);
+// Wait for the stream, then read and clear the kernels' status word.
+cudaError_t read_mixer_status(cudaStream_t s, int32_t* code);
+
 struct GatedNormArgs {
   const void *x, *gate, *w, *b;
   void* y;

@@ -2,6 +2,7 @@
 // launches.  Everything is checked before the first CUDA call; nothing is
 // allocated and nothing kept.  The launch arguments (up to 16 KiB of row plan)
 // are built in a thread's own storage.
+#include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -9,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/deltalog.h"
+#include "dl_device.cuh"
 #include "mixer.h"
 
 namespace {
@@ -228,20 +230,94 @@ dl_status ssm_args(const ErrOut& fail, const dl_ssm_args& q, SsmArgs& a) {
 
 }  // namespace
 
+namespace {
+
+// Multiprocessors of the current device (a GB300's where there is none to ask).
+int num_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// The tensor cores take bf16 rows of at least TC_TOKENS tokens (the longest
+// row's): below that the chunk of 128 is mostly padding.
+constexpr int64_t TC_TOKENS = 32;
+
+bool on_tensor_cores(const dl_ssm_args& q) {
+  int64_t longest = q.tokens.lengths ? 0 : q.tokens.T;
+  if (q.tokens.lengths)
+    for (int64_t i = 0; i < q.tokens.n; ++i) longest = q.tokens.lengths[i] > longest ? q.tokens.lengths[i] : longest;
+  return q.dtype == DL_BF16 && q.N <= 128 && longest >= TC_TOKENS;
+}
+
+int64_t workspace_of(const dl_ssm_args& q, const SsmPlan& p, int64_t tiles) {
+  return p.split ? 4 * tiles * q.H * (q.P * q.N + 1) : 0;
+}
+
+}  // namespace
+
 extern "C" int64_t dl_ssm_workspace(const dl_ssm_args* p) {
   const ErrOut quiet{nullptr, 0};
   if (!p || ssm_sizes(quiet, *p) != DL_OK || p->tokens.n < 0 || p->tokens.n > MX_ROWS) return -1;
-  return 0;
+  if (p->tokens.n == 0 || !on_tensor_cores(*p)) return 0;
+  const SsmPlan k = ssm_tc_plan((int)p->H, (int)p->G, (int)p->P, (int)p->N, (int)p->tokens.n, p->tokens.lengths,
+                                p->tokens.T, num_sms());
+  int64_t tiles = 0;
+  for (int64_t i = 0; i < p->tokens.n; ++i) {
+    const int64_t len = p->tokens.lengths ? p->tokens.lengths[i] : p->tokens.T;
+    tiles += len > k.seg_tokens ? (len + k.seg_tokens - 1) / k.seg_tokens : 1;
+  }
+  return workspace_of(*p, k, tiles);
 }
 
 extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, int32_t errlen) {
   const ErrOut fail{errbuf, errlen};
   if (errbuf && errlen > 0) errbuf[0] = 0;
   if (!p) return fail(DL_EINVAL, "NULL argument");
+  const dl_ssm_args& q = *p;
   SsmArgs& a = t_ssm;
-  const dl_status s = ssm_args(fail, *p, a);
-  if (s != DL_OK || p->tokens.n == 0) return s;
-  return done(fail, launch_ssm_scan((int)p->dtype, a, static_cast<cudaStream_t>(stream)));
+  dl_status s = ssm_args(fail, q, a);
+  if (s != DL_OK || q.tokens.n == 0) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!on_tensor_cores(q)) return done(fail, launch_ssm_scan((int)q.dtype, a, st));
+  const SsmPlan k = ssm_tc_plan(a.H, a.G, a.P, a.N, a.rows, q.tokens.lengths, q.tokens.T, num_sms());
+  int64_t tiles;
+  int32_t per_row;
+  bool any;
+  s = plan_rows(fail, q.tokens, q.state != nullptr, k.seg_tokens, a.items, tiles, per_row, any);
+  if (s != DL_OK) return s;
+  const int64_t need = workspace_of(q, k, tiles);
+  if (need && (!q.workspace || q.workspace_bytes < need || !al(q.workspace, 16)))
+    return fail(DL_EINVAL, "the workspace needs %lld bytes, 16-byte aligned (dl_ssm_workspace)", (long long)need);
+  if (tiles * k.units > 0x7fffffff) return fail(DL_EINVAL, "too many tokens in one call");
+  const bool packed = q.tokens.packed != 0;
+  const bool vec = q.P % 8 == 0 && q.N % 8 == 0 && view_vec(q.x, DL_BF16, packed) && view_vec(q.B, DL_BF16, packed) &&
+                   view_vec(q.C, DL_BF16, packed) && view_vec(q.y, DL_BF16, packed);
+  return done(fail, launch_ssm_tc(vec, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
+}
+
+extern "C" dl_status dl_mixer_sync(void* stream, int32_t* device_code, char* errbuf, int32_t errlen) {
+  const ErrOut fail{errbuf, errlen};
+  if (errbuf && errlen > 0) errbuf[0] = 0;
+  int32_t code = 0;
+  const cudaError_t e = read_mixer_status(static_cast<cudaStream_t>(stream), &code);
+  if (device_code) *device_code = code;
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return fail(DL_ECUDA, "status read failed: %s", cudaGetErrorString(e));
+  }
+  return code ? fail(DL_EDEVICE, "kernel reported device status %d (%s)", code, dl::device_status_str(code)) : DL_OK;
 }
 
 extern "C" dl_status dl_ssm_step(const dl_ssm_args* p, void* stream, char* errbuf, int32_t errlen) {

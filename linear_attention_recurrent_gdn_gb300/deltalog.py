@@ -40,6 +40,7 @@ EXPORTS = [
     "dl_window_launch_ragged", "dl_prefill",
     "dl_step_noalloc", "dl_noalloc_sync",
     "dl_conv", "dl_ssm", "dl_ssm_step", "dl_ssm_workspace", "dl_gated_norm", "dl_add_norm",
+    "dl_mixer_sync",
 ]
 
 

@@ -50,6 +50,8 @@ def _signatures(lib):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int32]
         fn.restype = ctypes.c_int32
+    lib.dl_mixer_sync.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32), ctypes.c_char_p, ctypes.c_int32]
+    lib.dl_mixer_sync.restype = ctypes.c_int32
     lib.dl_ssm_workspace.argtypes = [ctypes.c_char_p]
     lib.dl_ssm_workspace.restype = ctypes.c_int64
     return lib
@@ -119,6 +121,14 @@ def _host(a, dtype, n, name):
     if a.shape != (n,):
         raise ValueError("%s: expected %d entries, got %s" % (name, n, a.shape))
     return a
+
+
+def sync(device=None):
+    """Wait for the current stream and report a kernel's error since the last call."""
+    err = ctypes.create_string_buffer(_ERR)
+    rc = _lib.dl_mixer_sync(torch.cuda.current_stream(device).cuda_stream, None, err, _ERR)
+    if rc:
+        raise _dl.DeltaLogError(rc, err.value.decode())
 
 
 class _Rows:
