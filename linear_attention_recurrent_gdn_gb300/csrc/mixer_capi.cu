@@ -271,7 +271,7 @@ extern "C" int64_t dl_ssm_workspace(const dl_ssm_args* p) {
   const ErrOut quiet{nullptr, 0};
   if (!p || ssm_sizes(quiet, *p) != DL_OK || p->tokens.n < 0 || p->tokens.n > MX_ROWS) return -1;
   if (p->tokens.n == 0 || !on_tensor_cores(*p)) return 0;
-  const SsmPlan k = ssm_tc_plan((int)p->H, (int)p->G, (int)p->P, (int)p->N, (int)p->tokens.n, p->tokens.lengths,
+  const SsmPlan k = ssm_tc_plan((int)p->H, (int)p->G, (int)p->P, (int)p->tokens.n, p->tokens.lengths,
                                 p->tokens.T, num_sms());
   int64_t tiles = 0;
   for (int64_t i = 0; i < p->tokens.n; ++i) {
@@ -291,7 +291,7 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   if (s != DL_OK || q.tokens.n == 0) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!on_tensor_cores(q)) return done(fail, launch_ssm_scan((int)q.dtype, a, st));
-  const SsmPlan k = ssm_tc_plan(a.H, a.G, a.P, a.N, a.rows, q.tokens.lengths, q.tokens.T, num_sms());
+  const SsmPlan k = ssm_tc_plan(a.H, a.G, a.P, a.rows, q.tokens.lengths, q.tokens.T, num_sms());
   int64_t tiles;
   int32_t per_row;
   bool any;
@@ -304,7 +304,9 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   const bool packed = q.tokens.packed != 0;
   const bool vec = q.P % 8 == 0 && q.N % 8 == 0 && view_vec(q.x, DL_BF16, packed) && view_vec(q.B, DL_BF16, packed) &&
                    view_vec(q.C, DL_BF16, packed) && view_vec(q.y, DL_BF16, packed);
-  return done(fail, launch_ssm_tc(vec, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
+  int64_t tokens = q.tokens.T;
+  if (packed) tokens = (int64_t)a.items[a.rows - 1].begin + row_len(a.items[a.rows - 1]);
+  return done(fail, launch_ssm_tc(vec, tokens, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
 }
 
 extern "C" dl_status dl_mixer_sync(void* stream, int32_t* device_code, char* errbuf, int32_t errlen) {

@@ -45,6 +45,17 @@ __device__ __forceinline__ uint64_t kmaj_desc(uint32_t base, int K, int kk) {
   return sdesc(base + (uint32_t)kk * 256u, 128u, (uint32_t)(K >> 3) * 128u);
 }
 
+// Descriptor of an operand in the 128-byte swizzle: rows of 128 bytes (64 values of one row
+// r), 16-byte piece c of row r at place c ^ (r & 7), eight rows to a 1024-byte aligned atom
+// (the layout a 128-byte-swizzled tensor copy writes).  K-major (rows are M or N, the 64
+// values K): sbo is the distance between 8-row groups, lbo is not used, and a K step of 16
+// values starts 32 bytes further.  MN-major (rows are K): sbo is the distance between groups of
+// 8 K rows, lbo between blocks of 64 M or N values, and a K step of 16 rows starts 2048 bytes
+// further.
+__device__ __forceinline__ uint64_t sdesc128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return sdesc(saddr, lbo, sbo) | (2ull << 61);
+}
+
 // Instruction descriptor of kind::f16: bf16 A and B, fp32 D, M x N; A and B
 // K-major unless a_mn / b_mn mark them MN-major (bits 15 and 16).
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool a_mn = false,
@@ -129,15 +140,12 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// Store 16 consecutive 32-bit columns of this thread's lane (warp-wide); complete for this
+// Store 8 consecutive 32-bit columns of this thread's lane (warp-wide); complete for this
 // thread after tmem_wait_st.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-      "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(taddr)
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
