@@ -24,8 +24,9 @@
 // product needs, so nothing is transposed; tensor copies bring them (and, but
 // for a row's ragged last chunk, take y away), the next chunk's as soon as a
 // buffer is free, across units too.  Warps 0-7 form W and y, warps 8-15 X's
-// terms and the state, two warps to a lane quarter in each, half of the
-// columns each.
+// terms; all of them hold the state, two to four warps to a lane quarter with
+// a part of the columns each.  With nearly all of the SM's memory used as
+// shared memory there is next to no L1 cache, so nothing may spill.
 //
 // Rows with few heads are split into segments: a first launch (STATE) runs
 // each segment from zero and leaves its end state and decay in the workspace,
@@ -58,9 +59,10 @@ struct Smem {
   static constexpr uint32_t F = X3 + XT;             // per head [2]: L, column factor
   static constexpr uint32_t FB = 2 * Q * 4;
   static constexpr uint32_t BLK = F + 2 * FB;        // per head and block of 32 tokens: L at its end [8],
-                                                     // e^{T} of its last token [8]; per head: T of all tokens [2]
-  static constexpr uint32_t BAR = BLK + 80;          // eight mbarriers, TMEM address
-  static constexpr uint32_t BYTES = BAR + 80;
+                                                     // e^{T} of its last token [8]; per head: T of all tokens [2],
+                                                     // of even and odd chunks
+  static constexpr uint32_t BAR = BLK + 80;          // ten mbarriers, TMEM address
+  static constexpr uint32_t BYTES = BAR + 96;
 };
 static_assert(Smem<128>::BYTES <= 232448, "shared memory");
 
@@ -95,39 +97,59 @@ struct TcArgs {
   CUtensorMap mx, mb, mc, my;   // x, B, C, y: [64 values][head or group][128 tokens][row] boxes
   SsmArgs a;
   float* ws;                    // segment states [tiles][H][P][N], then log2 decays [tiles][H]
-  int32_t seg_tokens, tiles, per_row, units, ptiles, total;
+  int32_t seg_tokens, tiles, per_row, units, ptiles, total, empty_rows;
 };
 
-// One unit of work: a segment of a row for one or two heads.
+// One unit of work: tokens [s0, s1) of a row (a segment) for the heads from h0
+// and, of each, the state rows from p0.
 struct Unit {
-  int row, tile, tile0, seg, nseg, h0, p0, g, s0, s1, nch;
-  RowItem it;
+  int tile, row, begin, h0, p0, s0, s1, chunks;
 };
-template <int NH, int PH, bool STATE>
+template <int NH, int PH>
 __device__ __forceinline__ Unit unit_at(const TcArgs& ta, int u) {
   const SsmArgs& a = ta.a;
   Unit w;
   w.tile = u / ta.units;
   const int k = u - w.tile * ta.units, hu = k / ta.ptiles;
   w.row = find_row(a.items, a.rows, w.tile, ta.per_row);
-  w.it = a.items[w.row];
-  const int len = row_len(w.it);
-  w.tile0 = ta.per_row ? w.row * ta.per_row : w.it.tile0;
-  w.seg = w.tile - w.tile0;
-  w.nseg = len > ta.seg_tokens ? (len + ta.seg_tokens - 1) / ta.seg_tokens : 1;
+  const RowItem it = a.items[w.row];
+  const int len = row_len(it), seg = w.tile - (ta.per_row ? w.row * ta.per_row : it.tile0);
+  w.begin = it.begin;
   w.h0 = hu * NH;
   w.p0 = (k - hu * ta.ptiles) * PH;
-  w.g = w.h0 / (a.H / a.G);
-  w.s0 = w.seg * ta.seg_tokens;
+  w.s0 = seg * ta.seg_tokens;
   w.s1 = min(len, w.s0 + ta.seg_tokens);
-  w.nch = STATE && w.seg == w.nseg - 1 ? 0 : (w.s1 - w.s0 + Q - 1) / Q;   // nothing follows the last segment
+  w.chunks = (w.s1 - w.s0 + Q - 1) / Q;
   return w;
 }
-// The first unit from u on that has tokens, or one past the last.
+// Segments of the unit's row before it and in all.
+__device__ __forceinline__ void segments(const TcArgs& ta, const Unit& w, int& seg, int& nseg) {
+  const RowItem it = ta.a.items[w.row];
+  const int len = row_len(it);
+  seg = w.tile - (ta.per_row ? w.row * ta.per_row : it.tile0);
+  nseg = len > ta.seg_tokens ? (len + ta.seg_tokens - 1) / ta.seg_tokens : 1;
+}
+// Whether a launch works on a unit: STATE leaves out last segments, which nothing follows.
+template <bool STATE>
+__device__ __forceinline__ bool skipped(const TcArgs& ta, const Unit& w) {
+  if (!STATE) return w.chunks == 0;
+  int seg, nseg;
+  segments(ta, w, seg, nseg);
+  return seg == nseg - 1;
+}
+// The first unit from u on (in steps of the grid) that has work; u moves there, or past the last.
 template <int NH, int PH, bool STATE>
-__device__ __forceinline__ int next_unit(const TcArgs& ta, int u, int step) {
-  while (u < ta.total && unit_at<NH, PH, STATE>(ta, u).nch == 0) u += step;
-  return u;
+__device__ __forceinline__ Unit next_unit(const TcArgs& ta, int& u) {
+  Unit w{};
+  for (; u < ta.total; u += gridDim.x) {
+    w = unit_at<NH, PH>(ta, u);
+    if (!skipped<STATE>(ta, w)) break;
+  }
+  return w;
+}
+// (Not inlined: the loops below have to stay in the instruction cache.)
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par) {
+  return mbar_wait(bar, par, &g_mixer_status, DEV_TIMEOUT_MMA);
 }
 
 // TMA: tensor copies (16-byte aligned tensors, widths and strides); else
@@ -135,35 +157,45 @@ __device__ __forceinline__ int next_unit(const TcArgs& ta, int u, int step) {
 template <int NH, int PH, bool STATE, bool TMA>
 __global__ void __launch_bounds__(TCT, 1)
 ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
-  constexpr int PC = NH * PH, HC = PC / 2;          // columns of a unit, and of one of two warps of a lane quarter
+  constexpr int PC = NH * PH;
+  constexpr int HC = PC / 2;      // columns of one of the two warps of a lane quarter in a group
+  constexpr int SC = PC / 4;      // state columns of one of the four warps of a lane quarter
   using L = Smem<PC>;
   extern __shared__ __align__(1024) unsigned char sm[];
   const SsmArgs& a = ta.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = warp & 3, hf = (warp >> 2) & 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = warp & 3, hf = (warp >> 2) & 1, cg = warp >> 2;
   const bool wgb = warp >= 8;
-  const int i = 32 * q4 + lane;                     // token row (warps 0-7), state column n (warps 8-15)
+  const int i = 32 * q4 + lane;                     // this thread's token row; its state column n
   const int nk = (a.N + 15) / 16;                   // K steps over the state columns
 
   const uint32_t sb = smem_u32(sm);
   float* F = reinterpret_cast<float*>(sm + L::F);
   float* blk = reinterpret_cast<float*>(sm + L::BLK);
   const uint32_t barG = sb + L::BAR, barC = barG + 8, barS = barG + 16, barY = barG + 24, fullB = barG + 32,
-                 fullC = barG + 40, fullX = barG + 48;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::BAR + 64);
+                 fullC = barG + 40, fullX = barG + 48, readyS = barG + 64, readyF = barG + 72;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::BAR + 80);
 
-  if (warp == 0) tc::tmem_alloc(sb + L::BAR + 64, 512);
+  if (warp == 0) tc::tmem_alloc(sb + L::BAR + 80, 512);
   if (tid == 0) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) mbar_init(barG + 8 * k, 1);
+    // products: one commit; loads: one thread's tensor copies, or the eight warps that copy; S: every warp;
+    // the decays: a warp a head
+    for (int k = 0; k < 4; ++k) mbar_init(barG + 8 * k, 1);
+    for (int k = 4; k < 8; ++k) mbar_init(barG + 8 * k, TMA ? 1 : 8);
+    mbar_init(readyS, TCT / 32);
+    mbar_init(readyF, NH);
     fence_mbar_init();
   }
 
-  auto tok = [&](const Unit& w, const TokView& v, int t) {
-    return (int64_t)(w.it.begin + t) * v.st + (int64_t)w.row * v.sn;
+  auto tok = [&](const Unit& w, const TokView& v, int t) { return (int64_t)(w.begin + t) * v.st + (int64_t)w.row * v.sn; };
+  auto arrive_warp = [&](uint32_t bar) {            // this warp's writes to shared memory are done
+    tc::fence_smem_to_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
   };
-  // Chunk c of unit w into the buffers.  TMA: one thread issues; else `n` threads copy.
-  auto copy_rows = [&](uint32_t dst, const uint16_t* src, int64_t st, int nt, int width, int cols, int t, int n) {
-    for (int e = t; e < Q * cols / 8; e += n) {
+  // Chunk c of unit w into the buffers.  TMA: one thread calls; else warps 8-15 copy.
+  auto copy_rows = [&](uint32_t dst, const uint16_t* src, int64_t st, int nt, int width, int cols) {
+#pragma unroll 1
+    for (int e = tid - 256; e < Q * cols / 8; e += 256) {
       const int r = e & (Q - 1), cv = e / Q;
       const uint16_t* p = src + (int64_t)r * st + cv * 8;
       uint32_t v[4];
@@ -176,7 +208,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       *reinterpret_cast<uint4*>(sm + dst + piece_off(r, cv)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   };
-  auto load_x = [&](const Unit& w, int c, uint32_t buf, int t, int n) {
+  auto load_x = [&](const Unit& w, int c, uint32_t buf) {
     const int t0 = w.s0 + c * Q;
     if (TMA) {
       const uint32_t bar = fullX + 8 * buf;
@@ -184,17 +216,18 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
 #pragma unroll
       for (int b = 0; b < PC / 64; ++b)
         tma_load(sb + L::X + buf * L::XT + b * BLK64, &ta.mx, w.p0 + (NH == 1 ? 64 * b : 0), w.h0 + (NH == 1 ? 0 : b),
-                 w.it.begin + t0, a.x.sn ? w.row : 0, bar);
+                 w.begin + t0, a.x.sn ? w.row : 0, bar);
     } else {
 #pragma unroll
       for (int hh = 0; hh < NH; ++hh)
         copy_rows(L::X + buf * L::XT + hh * BLK64,
                   static_cast<const uint16_t*>(a.x.p) + (int64_t)(w.h0 + hh) * a.P + w.p0 + tok(w, a.x, t0), a.x.st,
-                  min(Q, w.s1 - t0), min(PH, a.P - w.p0), PH, t, n);
+                  min(Q, w.s1 - t0), min(PH, a.P - w.p0), PH);
+      arrive_warp(fullX + 8 * buf);
     }
   };
-  auto load_bc = [&](const Unit& w, int c, bool isb, int t, int n) {
-    const int t0 = w.s0 + c * Q;
+  auto load_bc = [&](const Unit& w, int c, bool isb) {
+    const int t0 = w.s0 + c * Q, g = w.h0 / (a.H / a.G);
     const TokView& v = isb ? a.B : a.C;
     const uint32_t dst = isb ? L::B : L::C;
     if (TMA) {
@@ -202,202 +235,282 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       const int nb = a.N > 64 ? 2 : 1;
       mbar_arrive_expect_tx(bar, nb * BLK64);
       for (int b = 0; b < nb; ++b)
-        tma_load(sb + dst + b * BLK64, isb ? &ta.mb : &ta.mc, 64 * b, w.g, w.it.begin + t0, v.sn ? w.row : 0, bar);
+        tma_load(sb + dst + b * BLK64, isb ? &ta.mb : &ta.mc, 64 * b, g, w.begin + t0, v.sn ? w.row : 0, bar);
     } else {
-      copy_rows(dst, static_cast<const uint16_t*>(v.p) + (int64_t)w.g * a.N + tok(w, v, t0), v.st,
-                min(Q, w.s1 - t0), a.N, 128, t, n);
+      copy_rows(dst, static_cast<const uint16_t*>(v.p) + (int64_t)g * a.N + tok(w, v, t0), v.st, min(Q, w.s1 - t0), a.N,
+                128);
+      arrive_warp(isb ? fullB : fullC);
     }
   };
-  // raw dt of token t for head hh of the unit, zero past its segment
-  auto raw_dt = [&](const Unit& w, int t, int hh) {
-    if (t >= w.s1) return 0.f;
-    const int64_t o = tok(w, a.dt, t) + w.h0 + hh;
-    return a.dt_f32 ? static_cast<const float*>(a.dt.p)[o] : to_f(static_cast<const __nv_bfloat16*>(a.dt.p)[o]);
+  // dt of token t (past the segment: its last one) for head hh of the unit, as it sits in memory: the
+  // conversion waits for the load, so it is left to the use
+  auto raw_dt = [&](const Unit& w, int t, int hh) -> uint32_t {
+    const int64_t o = tok(w, a.dt, min(t, w.s1 - 1)) + w.h0 + hh;
+    return a.dt_f32 ? static_cast<const uint32_t*>(a.dt.p)[o] : static_cast<const uint16_t*>(a.dt.p)[o];
   };
-  auto step_of = [&](float raw, int h) {
-    const float d = raw + (a.dt_bias ? a.dt_bias[h] : 0.f);
+  auto dt_of = [&](uint32_t raw, float bias) {
+    const float d = __uint_as_float(a.dt_f32 ? raw : raw << 16) + bias;
     return a.softplus ? softplus_f(d) : d;
   };
+  auto bias_of = [&](int h) { return a.dt_bias ? a.dt_bias[h] : 0.f; };
 
-  int u = blockIdx.x, cur = next_unit<NH, PH, STATE>(ta, u, gridDim.x);
-  if (cur < ta.total) {
-    const Unit w = unit_at<NH, PH, STATE>(ta, cur);
-    if (!TMA) {
-      load_bc(w, 0, true, tid, TCT);
-      if (!STATE) load_bc(w, 0, false, tid, TCT);
-      load_x(w, 0, 0, tid, TCT);
-    }
-  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  if (TMA && tid == 0 && cur < ta.total) {
-    const Unit w = unit_at<NH, PH, STATE>(ta, cur);
-    load_bc(w, 0, true, 0, 1);
-    if (!STATE) load_bc(w, 0, false, 0, 1);
-    load_x(w, 0, 0, 0, 1);
-  }
   const uint32_t tm = *tslot;
   const uint32_t tl = tm + ((uint32_t)(32 * q4) << 16);
   bool ok = true;                 // a wait that ran out: no further waits, no results
   auto wait = [&](uint32_t bar, uint32_t par) {
-    ok = ok && mbar_wait(bar, par, &g_mixer_status, DEV_TIMEOUT_MMA);
+    if (ok && !mbar_try_wait(bar, par)) ok = wait_long(bar, par);
   };
-  uint32_t gc = 0;                // chunks done, over all units
   const int64_t per_tile = (int64_t)a.H * a.P * a.N;
 
-  // The two groups of warps run loops of their own; the barriers at a chunk's
-  // start (operands landed) and end (operands and accumulators free) join them.
-  auto chunk_begin = [&](int nt) {
-    if (TMA) {
-      wait(fullB, gc & 1);
-      if (!STATE) wait(fullC, gc & 1);
-      wait(fullX + 8 * (gc & 1), (gc >> 1) & 1);
-      if (nt < Q) {
-        // what lies behind the row's last token is not zero: clear it (C's rows give y rows that are not kept)
-        for (int e = tid; e < (Q - nt) * (16 + PC / 8); e += TCT) {
-          const int r = nt + e % (Q - nt), cv = e / (Q - nt);
-          const uint32_t off = cv < 16 ? L::B + piece_off(r, cv) : L::X + (gc & 1) * L::XT + piece_off(r, cv - 16);
-          *reinterpret_cast<uint4*>(sm + off) = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
+  // ---- the state: this thread holds S[column cg * SC + .][n = i] of the unit
+  float S[SC];
+  const int hcol = NH == 2 ? cg >> 1 : 0;           // head and first row p of its columns
+  const int pofs = NH == 2 ? (cg & 1) * SC : cg * SC;
+  auto elem0 = [&](const Unit& w) { return ((int64_t)(w.h0 + hcol) * a.P + w.p0 + pofs) * a.N + i; };
+  auto live_of = [&](const Unit& w) { return i < a.N ? a.P - w.p0 - pofs : 0; };
+  auto pool_of = [&](const Unit& w) { return a.state ? a.state + (int64_t)a.items[w.row].slot * per_tile : nullptr; };
+  auto load_state = [&](const Unit& w) {
+    int seg, nseg;
+    segments(ta, w, seg, nseg);
+    const bool fresh = row_fresh(a.items[w.row]);
+    const int64_t e0 = elem0(w);
+    const int live = live_of(w);
+    const float* from;
+    if (STATE || nseg == 1) from = seg == 0 && !fresh ? pool_of(w) : nullptr;
+    else if (seg == 0) from = fresh ? nullptr : ta.ws + (int64_t)w.tile * per_tile;
+    else from = ta.ws + (int64_t)(w.tile - seg + 1) * per_tile;
+#pragma unroll
+    for (int c = 0; c < SC; ++c) S[c] = from && c < live ? from[e0 + (int64_t)c * a.N] : 0.f;
+    if (STATE && seg == 0 && from) {
+      // the last segment's CTA overwrites the pool's entry in the full launch
+      float* to = ta.ws + (int64_t)w.tile * per_tile + e0;
+#pragma unroll
+      for (int c = 0; c < SC; ++c)
+        if (c < live) to[(int64_t)c * a.N] = S[c];
     }
-    tc::fence_smem_to_async();    // what threads wrote of B, C, X and S, for the tensor cores
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
+    if (!STATE)
+#pragma unroll 1
+      for (int k = 2; k <= seg; ++k) {
+        const float* add = ta.ws + (int64_t)(w.tile - seg + k) * per_tile + e0;
+        const float d = ex2(ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)(w.tile - seg + k - 1) * a.H + w.h0 + hcol]);
+#pragma unroll
+        for (int c = 0; c < SC; ++c) S[c] = fmaf(S[c], d, c < live ? add[(int64_t)c * a.N] : 0.f);
+      }
   };
-  auto chunk_end = [&]() {
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-    ++gc;
+  auto leave_state = [&](const Unit& w, float ltot) {
+    int seg, nseg;
+    segments(ta, w, seg, nseg);
+    const int64_t e0 = elem0(w);
+    const int live = live_of(w);
+    float* to = STATE ? ta.ws + (int64_t)(w.tile + 1) * per_tile : seg == nseg - 1 ? pool_of(w) : nullptr;
+    if (!ok) return;
+    if (to) {
+#pragma unroll
+      for (int c = 0; c < SC; ++c)
+        if (c < live) to[e0 + (int64_t)c * a.N] = S[c];
+    }
+    if (STATE && i == 0 && pofs == 0 && w.p0 == 0)
+      ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)w.tile * a.H + w.h0 + hcol] = ltot;
   };
-
-  if (wgb) {
-    const int bt = tid - 256;
-    const bool scans = warp - 8 < NH;               // warps 8, 9 scan head warp - 8, four tokens a lane
-    const int sh = warp - 8;
-    float raw[4];
-    auto load_dt = [&](const Unit& w, int c) {
-      if (scans) {
+  auto share_state = [&]() {      // S as a bf16 operand (rows n, columns contiguous), and its TMEM place is read
+    if (!STATE) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) raw[k] = raw_dt(w, w.s0 + c * Q + 4 * lane + k, sh);
-      }
-    };
-    // decays of chunk c, from raw
-    auto scan = [&](const Unit& w, int c) {
-      if (!scans) return;
-      const int nt = w.s1 - w.s0 - c * Q;
-      const float Ah = a.A[w.h0 + sh] * LOG2E;
-      float dt[4], l[4], suf[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        dt[k] = 4 * lane + k < nt ? step_of(raw[k], w.h0 + sh) : 0.f;
-        l[k] = dt[k] * Ah;
-      }
-      // tokens after j in its block of 32, summed from the end: no cancellation in the sums that matter
-      suf[3] = 0.f;
-      suf[2] = l[3];
-      suf[1] = suf[2] + l[2];
-      suf[0] = suf[1] + l[1];
-      float post = suf[0] + l[0];
-#pragma unroll
-      for (int k = 1; k < 4; ++k) l[k] += l[k - 1];
-      float pre = l[3];
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) {
-        const float d = __shfl_down_sync(0xffffffffu, post, o, 8);
-        if ((lane & 7) + o < 8) post += d;
-      }
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float v = __shfl_up_sync(0xffffffffu, pre, o);
-        if (lane >= o) pre += v;
-      }
-      const float before = pre - l[3];
-      const float nxt = __shfl_down_sync(0xffffffffu, post, 1, 8);
-      const float after = (lane & 7) < 7 ? nxt : 0.f;
-      float bs[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) bs[b] = __shfl_sync(0xffffffffu, post, 8 * b);
-      float* f = F + sh * 2 * Q;
-      *reinterpret_cast<float4*>(f + 4 * lane) = make_float4(before + l[0], before + l[1], before + l[2], pre);
-      *reinterpret_cast<float4*>(f + Q + 4 * lane) =
-          make_float4(ex2(after + suf[0]) * dt[0], ex2(after + suf[1]) * dt[1], ex2(after + suf[2]) * dt[2],
-                      ex2(after + suf[3]) * dt[3]);
-      if ((lane & 7) == 7) blk[sh * 4 + (lane >> 3)] = pre;
-      if (lane < 4)
-        blk[8 + sh * 4 + lane] = ex2(lane == 0 ? bs[3] + bs[2] + bs[1] : lane == 1 ? bs[3] + bs[2] : lane == 2 ? bs[3] : 0.f);
-      if (lane == 0) blk[16 + sh] = bs[3] + bs[2] + bs[1] + bs[0];
-    };
-    float S[HC];                                    // S[column hf * HC + .][n = i]
-    auto store_s = [&]() {                          // as a bf16 operand: rows n, columns contiguous
-#pragma unroll
-      for (int c8 = 0; c8 < HC / 8; ++c8) {
+      for (int c8 = 0; c8 < SC / 8; ++c8) {
         const float* s = S + 8 * c8;
-        *reinterpret_cast<uint4*>(sm + L::X3 + piece_off(i, hf * (HC / 8) + c8)) =
+        *reinterpret_cast<uint4*>(sm + L::X3 + piece_off(i, cg * (SC / 8) + c8)) =
             make_uint4(pack2<__nv_bfloat16>(s[0], s[1]), pack2<__nv_bfloat16>(s[2], s[3]),
                        pack2<__nv_bfloat16>(s[4], s[5]), pack2<__nv_bfloat16>(s[6], s[7]));
       }
-    };
-    if (cur < ta.total) {
-      const Unit w = unit_at<NH, PH, STATE>(ta, cur);
-      load_dt(w, 0);
-      scan(w, 0);
     }
-    for (; u < ta.total; u += gridDim.x) {
-      const Unit w = unit_at<NH, PH, STATE>(ta, u);
-      if (STATE && w.seg == w.nseg - 1) continue;
-      const int nxt = w.nch ? next_unit<NH, PH, STATE>(ta, u + gridDim.x, gridDim.x) : 0;
-      const Unit wn = w.nch && nxt < ta.total ? unit_at<NH, PH, STATE>(ta, nxt) : w;
-      // ---- the state at the segment's start
-      const float* wl = ta.ws + (int64_t)ta.tiles * per_tile;      // log2 decays of the segments
-      float* pool = a.state ? a.state + (int64_t)w.it.slot * per_tile : nullptr;
-      // columns [hf * HC, + HC): offset of the first one's element n = i, and how many there are
-      const int hcol = NH == 2 ? hf : 0, pcol = w.p0 + (NH == 2 ? 0 : hf * HC);
-      const int64_t e0 = ((int64_t)(w.h0 + hcol) * a.P + pcol) * a.N + i;
-      const int live = i < a.N ? a.P - pcol : 0;
-      {
-        const float* from;
-        if (STATE || w.nseg == 1) from = w.seg == 0 && pool && !row_fresh(w.it) ? pool : nullptr;
-        else if (w.seg == 0) from = row_fresh(w.it) ? nullptr : ta.ws + (int64_t)w.tile * per_tile;
-        else from = ta.ws + (int64_t)(w.tile0 + 1) * per_tile;
+    tc::fence_before_sync();
+    arrive_warp(readyS);
+  };
+  auto update_state = [&](float decl) {             // S' = e^{L_Q} S + dS
+    const float dec = ex2(decl);
 #pragma unroll
-        for (int c = 0; c < HC; ++c) S[c] = from && c < live ? from[e0 + (int64_t)c * a.N] : 0.f;
-        if (STATE && w.seg == 0 && from) {
-          // the last segment's CTA overwrites the pool's entry in the full launch
+    for (int b = 0; b < SC / 16; ++b) {
+      uint32_t r[16];
+      tc::tmem_ld16(tl + COL_DS + cg * SC + 16 * b, r);
+      tc::tmem_wait_ld16(r);
 #pragma unroll
-          for (int c = 0; c < HC; ++c)
-            if (c < live) ta.ws[(int64_t)w.tile * per_tile + e0 + (int64_t)c * a.N] = S[c];
-        }
-        if (!STATE)
-          for (int k = 2; k <= w.seg; ++k) {
-            const float* add = ta.ws + (int64_t)(w.tile0 + k) * per_tile + e0;
-            const float d = ex2(wl[(int64_t)(w.tile0 + k - 1) * a.H + w.h0 + hcol]);
+      for (int e = 0; e < 16; ++e) S[16 * b + e] = fmaf(S[16 * b + e], dec, __uint_as_float(r[e]));
+    }
+  };
+
+  // Rows without tokens: a fresh one's state is zero.
+  if (!STATE && ta.empty_rows)
+#pragma unroll 1
+    for (int e = blockIdx.x; e < ta.total; e += gridDim.x) {
+      const Unit v = unit_at<NH, PH>(ta, e);
+      float* to = pool_of(v);
+      if (v.chunks == 0 && to && row_fresh(a.items[v.row]))
+#pragma unroll 1
+        for (int c = 0; c < SC && c < live_of(v); ++c) to[elem0(v) + (int64_t)c * a.N] = 0.f;
+    }
+
+  int u = blockIdx.x;
+  Unit w = next_unit<NH, PH, STATE>(ta, u);
+  bool any = u < ta.total;
+  if (any && (TMA ? tid == 256 : wgb)) {
+    load_x(w, 0, 0);
+    load_bc(w, 0, true);
+    if (!STATE) load_bc(w, 0, false);
+  }
+  uint32_t gc = 0;                // chunks done, over all units
+
+  // The two groups of warps run loops of their own, joined by barriers in
+  // shared memory, so that one chunk's y is written while the next one's terms
+  // are formed.  Each barrier's phase is a chunk (gc counts them); none can run
+  // ahead by two: a chunk's products need the S that every warp shares after
+  // the chunk before, and W needs the decays, which are formed after the W
+  // before.
+  const int bt = tid - 256;
+  const bool scans = wgb && warp - 8 < NH;          // warps 8, 9 scan head warp - 8, four tokens a lane
+  const int sh = scans ? warp - 8 : 0;
+  // dt of the next chunk: the scanning warps' four tokens, the others' own token of every head
+  uint32_t raw[4];
+  float bias[NH], Ah = 0.f;
+  auto load_dt = [&](const Unit& v, int c) {
+    if (scans) {
 #pragma unroll
-            for (int c = 0; c < HC; ++c) S[c] = fmaf(S[c], d, c < live ? add[(int64_t)c * a.N] : 0.f);
-          }
+      for (int k = 0; k < 4; ++k) raw[k] = raw_dt(v, v.s0 + c * Q + 4 * lane + k, sh);
+      Ah = a.A[v.h0 + sh];
+      bias[0] = bias_of(v.h0 + sh);
+    } else if (!wgb && !STATE) {
+#pragma unroll
+      for (int hh = 0; hh < NH; ++hh) {
+        raw[hh] = raw_dt(v, v.s0 + c * Q + i, hh);
+        bias[hh] = bias_of(v.h0 + hh);
       }
-      if (!STATE && w.nch) store_s();
-      float ltot = 0.f;
-      for (int c = 0; c < w.nch; ++c) {
+    }
+  };
+  // decays of number k, a chunk of nt tokens, from raw
+  auto scan = [&](uint32_t k2, int nt) {
+    float dt[4], l[4], suf[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      dt[k] = 4 * lane + k < nt ? dt_of(raw[k], bias[0]) : 0.f;
+      l[k] = dt[k] * (Ah * LOG2E);
+    }
+    // tokens after j in its block of 32, summed from the end: no cancellation in the sums that matter
+    suf[3] = 0.f;
+    suf[2] = l[3];
+    suf[1] = suf[2] + l[2];
+    suf[0] = suf[1] + l[1];
+    float post = suf[0] + l[0];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) l[k] += l[k - 1];
+    float pre = l[3];
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) {
+      const float d = __shfl_down_sync(0xffffffffu, post, o, 8);
+      if ((lane & 7) + o < 8) post += d;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float v = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += v;
+    }
+    const float before = pre - l[3];
+    const float nxt = __shfl_down_sync(0xffffffffu, post, 1, 8);
+    const float after = (lane & 7) < 7 ? nxt : 0.f;
+    float bs[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) bs[b] = __shfl_sync(0xffffffffu, post, 8 * b);
+    float* f = F + sh * 2 * Q;
+    *reinterpret_cast<float4*>(f + 4 * lane) = make_float4(before + l[0], before + l[1], before + l[2], pre);
+    *reinterpret_cast<float4*>(f + Q + 4 * lane) =
+        make_float4(ex2(after + suf[0]) * dt[0], ex2(after + suf[1]) * dt[1], ex2(after + suf[2]) * dt[2],
+                    ex2(after + suf[3]) * dt[3]);
+    if ((lane & 7) == 7) blk[sh * 4 + (lane >> 3)] = pre;
+    if (lane < 4)
+      blk[8 + sh * 4 + lane] = ex2(lane == 0 ? bs[3] + bs[2] + bs[1] : lane == 1 ? bs[3] + bs[2] : lane == 2 ? bs[3] : 0.f);
+    if (lane == 0) blk[16 + 2 * (k2 & 1) + sh] = bs[3] + bs[2] + bs[1] + bs[0];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(readyF);
+  };
+  // G of the chunk that is number k, once its operands are there
+  auto issue_g = [&](uint32_t k) {
+    wait(fullB, k & 1);
+    wait(fullC, k & 1);
+    tc::fence_after_sync();
+    constexpr uint32_t idG = tc::idesc_bf16_f32(128, 128);
+#pragma unroll 1
+    for (int j = 0; j < nk; ++j) {
+      const uint32_t o = (uint32_t)(j >> 2) * BLK64 + (uint32_t)(j & 3) * 32u;
+      tc::mma_bf16(tm + COL_G, tc::sdesc128(sb + L::C + o, 16u, 1024u), tc::sdesc128(sb + L::B + o, 16u, 1024u), idG,
+                   j > 0);
+    }
+    tc::mma_commit(barG);
+  };
+  // its Y2, once S is there
+  auto issue_y2 = [&](uint32_t k) {
+    wait(readyS, k & 1);
+    tc::fence_after_sync();
+    constexpr uint32_t idY = tc::idesc_bf16_f32(128, PC, false, true);
+#pragma unroll 1
+    for (int j = 0; j < nk; ++j) {
+      const uint32_t o = (uint32_t)(j >> 2) * BLK64 + (uint32_t)(j & 3) * 32u;
+      tc::mma_bf16(tm + COL_Y2, tc::sdesc128(sb + L::C + o, 16u, 1024u),
+                   tc::sdesc128(sb + L::X3 + j * 2048u, BLK64, 1024u), idY, j > 0);
+    }
+    tc::mma_commit(barC);
+  };
+  // A ragged chunk (number k, nt tokens) brought by tensor copies: what lies behind its last token is
+  // cleared in B and X.  (C's rows there give rows of y that are not kept.)
+  auto clear_tail = [&](uint32_t k, int nt) {
+    if (!TMA || nt >= Q) return;
+    wait(fullB, k & 1);
+    wait(fullX + 8 * (k & 1), (k >> 1) & 1);
+#pragma unroll 1
+    for (int e = tid; e < (Q - nt) * (16 + PC / 8); e += 256) {
+      const int r = nt + e % (Q - nt), cv = e / (Q - nt);
+      const uint32_t off = cv < 16 ? L::B + piece_off(r, cv) : L::X + (k & 1) * L::XT + piece_off(r, cv - 16);
+      *reinterpret_cast<uint4*>(sm + off) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    tc::fence_smem_to_async();
+    bar_named(1);
+  };
+  if (any) {
+    load_dt(w, 0);
+    if (scans) scan(0, w.s1 - w.s0);
+  }
+  bool early = false;             // this chunk's G was issued in the chunk before
+#pragma unroll 1
+  while (any) {
+    int un = u + gridDim.x;
+    const Unit wn = next_unit<NH, PH, STATE>(ta, un);
+    const bool another = un < ta.total;
+    load_state(w);
+    share_state();
+    float ltot = 0.f;
+    if (wgb) {
+#pragma unroll 1
+      for (int c = 0; c < w.chunks; ++c, ++gc) {
         const uint32_t par = gc & 1u;
         const uint32_t xs = L::X + par * L::XT;
-        const bool last = c + 1 == w.nch, more = !last || nxt < ta.total;
-        const Unit& wf = last ? wn : w;             // the chunk after this one
+        const int nt = min(Q, w.s1 - w.s0 - c * Q);
+        const bool last = c + 1 == w.chunks, more = !last || another;
+        const Unit wf = last ? wn : w;              // the chunk after this one
         const int cf = last ? 0 : c + 1;
+        if (STATE && TMA && more && bt == 0) load_x(wf, cf, par ^ 1u);
         if (more) load_dt(wf, cf);
-        chunk_begin(min(Q, w.s1 - w.s0 - c * Q));
-        // ---- X's three terms, then S' = e^{L_Q} S + dS
-        const float decl = blk[16 + hcol];
+        wait(readyF, par);
+        wait(fullX + 8 * par, (gc >> 1) & 1);
+        // ---- X's three terms, then dS
+        const float decl = blk[16 + 2 * par + hcol];
         constexpr int PIECES = Q * PC / 8 / 256;
         uint32_t o3[PIECES][4];
 #pragma unroll
         for (int e = 0; e < PIECES; ++e) {
+          if (e % 4 == 0) asm volatile("" ::: "memory");   // four pieces in flight: registers
           const int idx = bt + e * 256, t = (idx >> 3) & (Q - 1), cv = (idx & 7) + 8 * (idx >> 10);
           const uint32_t off = piece_off(t, cv);
-          const uint4 xv = *reinterpret_cast<const uint4*>(sm + xs + off);
+          uint4 xv = *reinterpret_cast<const uint4*>(sm + xs + off);
+          if (t >= nt) xv = make_uint4(0u, 0u, 0u, 0u);     // a tensor copy brings what lies behind the row
           const int hh = NH == 2 ? cv >> 3 : 0;
           const float f = F[hh * 2 * Q + Q + t] * blk[8 + hh * 4 + (t >> 5)];
           const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
@@ -417,8 +530,14 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
           *reinterpret_cast<uint4*>(sm + L::X2 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
         }
         if (!STATE) {
-          wait(barC, par);        // Y2 has read S and C
-          if (more && TMA && bt == 0) load_bc(wf, cf, false, 0, 1);
+          wait(barC, par);        // Y2 has read S and C; B is there, its ragged end cleared
+          if (TMA && more && bt == 0) load_bc(wf, cf, false);
+        } else {
+          wait(fullB, par);
+          if (TMA && nt < Q)
+#pragma unroll 1
+            for (int e = bt; e < (Q - nt) * 16; e += 256)
+              *reinterpret_cast<uint4*>(sm + L::B + piece_off(nt + e % (Q - nt), e / (Q - nt))) = make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int e = 0; e < PIECES; ++e) {
@@ -429,242 +548,221 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         tc::fence_before_sync();
         bar_named(2);
         if (bt == 0) {
+          if (STATE) wait(readyS, par);             // every warp has read the dS before
           tc::fence_after_sync();
           constexpr uint32_t idS = tc::idesc_bf16_f32(128, PC, true, true);
 #pragma unroll 1
-          for (int term = 0; term < 3; ++term)
-#pragma unroll
-            for (int k = 0; k < Q / 16; ++k)
-              tc::mma_bf16(tm + COL_DS, tc::sdesc128(sb + L::B + k * 2048u, BLK64, 1024u),
-                           tc::sdesc128(sb + L::X1 + term * L::XT + k * 2048u, BLK64, 1024u), idS, term + k > 0);
+          for (int k = 0; k < 3 * Q / 16; ++k)
+            tc::mma_bf16(tm + COL_DS, tc::sdesc128(sb + L::B + (k & 7) * 2048u, BLK64, 1024u),
+                         tc::sdesc128(sb + L::X1 + (k >> 3) * L::XT + (k & 7) * 2048u, BLK64, 1024u), idS, k > 0);
           tc::mma_commit(barS);
         }
         wait(barS, par);
         tc::fence_after_sync();
-        if (more) {               // dS (and G before it) have read B
-          if (TMA) {
-            if (bt == 0) load_bc(wf, cf, true, 0, 1);
-          } else {
-            load_bc(wf, cf, true, bt, 256);
-            if (!STATE) load_bc(wf, cf, false, bt, 256);
-          }
-        }
-        const float dec = ex2(decl);
+        if (TMA && more && bt == 0) load_bc(wf, cf, true);   // dS (and G before it) have read B
         ltot += decl;
-#pragma unroll
-        for (int c32 = 0; c32 < HC / 32; ++c32) {
-          uint32_t r[32];
-          tc::tmem_ld32(tl + COL_DS + hf * HC + 32 * c32, r);
-          tc::tmem_wait_ld(r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) S[32 * c32 + e] = fmaf(S[32 * c32 + e], dec, __uint_as_float(r[e]));
+        update_state(decl);
+        if (!last) share_state();
+        if (!TMA && more) {
+          load_x(wf, cf, par ^ 1u);
+          load_bc(wf, cf, true);
+          if (!STATE) load_bc(wf, cf, false);
         }
-        if (!STATE && !last) store_s();
         if (more && scans) {
           if (!STATE) wait(barY, par);   // W has been formed: the decays' arrays are free
-          scan(wf, cf);
+          scan(gc + 1, wf.s1 - wf.s0 - cf * Q);
         }
-        chunk_end();
       }
-      if (ok) {
-        float* to = STATE ? ta.ws + (int64_t)(w.tile + 1) * per_tile : w.seg == w.nseg - 1 ? pool : nullptr;
-        if (to) {
-#pragma unroll
-          for (int c = 0; c < HC; ++c)
-            if (c < live) to[e0 + (int64_t)c * a.N] = S[c];
-        }
-        if (STATE && i == 0 && w.p0 == 0 && (NH == 2 || hf == 0))
-          ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)w.tile * a.H + w.h0 + hcol] = ltot;
-      }
-    }
-  } else {
-    float raw[NH];
-    auto load_dt = [&](const Unit& w, int c) {
-      if (!STATE) {
-#pragma unroll
-        for (int hh = 0; hh < NH; ++hh) raw[hh] = raw_dt(w, w.s0 + c * Q + i, hh);
-      }
-    };
-    if (cur < ta.total) load_dt(unit_at<NH, PH, STATE>(ta, cur), 0);
-    for (u = cur; u < ta.total;) {
-      const Unit w = unit_at<NH, PH, STATE>(ta, u);
-      const int nxt = next_unit<NH, PH, STATE>(ta, u + gridDim.x, gridDim.x);
-      const Unit wn = nxt < ta.total ? unit_at<NH, PH, STATE>(ta, nxt) : w;
-      for (int c = 0; c < w.nch; ++c) {
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < w.chunks; ++c, ++gc) {
         const uint32_t par = gc & 1u;
         const uint32_t xs = L::X + par * L::XT;
         const int t0 = w.s0 + c * Q, nt = min(Q, w.s1 - t0);
-        const bool last = c + 1 == w.nch, more = !last || nxt < ta.total;
-        const Unit& wf = last ? wn : w;
+        const bool last = c + 1 == w.chunks, more = !last || another;
+        const Unit wf = last ? wn : w;              // the chunk after this one
         const int cf = last ? 0 : c + 1;
+        if (STATE) {
+          wait(readyF, par);
+          const float decl = blk[16 + 2 * par + hcol];
+          wait(barS, par);
+          tc::fence_after_sync();
+          ltot += decl;
+          update_state(decl);
+          if (!last) share_state();
+          continue;
+        }
+        // ---- this chunk's G and Y2, and the next one's X
+        clear_tail(gc, nt);
+        if (tid == 0) {
+          if (!early) issue_g(gc);
+          issue_y2(gc);
+          if (TMA && more) {
+            bulk_wait_read();                       // y of the chunk before has left the buffer
+            load_x(wf, cf, par ^ 1u);
+          }
+        }
+        early = false;
         float own[NH];            // dt of token i
 #pragma unroll
-        for (int hh = 0; hh < NH; ++hh) own[hh] = !STATE && i < nt ? step_of(raw[hh], w.h0 + hh) : 0.f;
+        for (int hh = 0; hh < NH; ++hh) own[hh] = i < nt ? dt_of(raw[hh], bias[hh]) : 0.f;
         if (more) load_dt(wf, cf);
-        chunk_begin(nt);
-        if (!STATE && tid == 0) {
-          constexpr uint32_t idG = tc::idesc_bf16_f32(128, 128), idY = tc::idesc_bf16_f32(128, PC, false, true);
-          for (int k = 0; k < nk; ++k) {
-            const uint32_t o = (uint32_t)(k >> 2) * BLK64 + (uint32_t)(k & 3) * 32u;
-            tc::mma_bf16(tm + COL_G, tc::sdesc128(sb + L::C + o, 16u, 1024u), tc::sdesc128(sb + L::B + o, 16u, 1024u),
-                         idG, k > 0);
-          }
-          tc::mma_commit(barG);
-          for (int k = 0; k < nk; ++k) {
-            const uint32_t o = (uint32_t)(k >> 2) * BLK64 + (uint32_t)(k & 3) * 32u;
-            tc::mma_bf16(tm + COL_Y2, tc::sdesc128(sb + L::C + o, 16u, 1024u),
-                         tc::sdesc128(sb + L::X3 + k * 2048u, BLK64, 1024u), idY, k > 0);
-          }
-          tc::mma_commit(barC);
-        }
-        if (more) {
-          if (TMA) {
-            if (tid == 0) {
-              if (!STATE) bulk_wait_read();     // y of the chunk before has left the buffer
-              load_x(wf, cf, par ^ 1u, 0, 1);
-            }
-          } else {
-            load_x(wf, cf, par ^ 1u, tid, 256);
-          }
-        }
-        if (!STATE) {
-          // ---- W from G, in place of G: columns 32 b + 16 hf .. + 15 of every block b
-          wait(barG, par);
-          tc::fence_after_sync();
-          float G[64];
+        // ---- W from G, in place of G: columns 32 b + 16 hf .. + 15 of every block b.  The last head's W takes
+        // columns 64 .. 127, once both warps of the lanes have read blocks 2 and 3, another's 0 .. 63.
+        wait(readyF, par);
+        wait(fullX + 8 * par, (gc >> 1) & 1);
+        wait(barG, par);
+        tc::fence_after_sync();
+        const float decl = blk[16 + 2 * par + hcol];
+        float el[NH];
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (b <= q4) {
-              uint32_t r[16];
-              tc::tmem_ld16(tl + COL_G + 32 * b + 16 * hf, r);
-              tc::tmem_wait_ld16(r);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) G[16 * b + e] = __uint_as_float(r[e]);
-            }
-          tc::fence_before_sync();
-          bar_named(1);           // the other warp of these lanes has its values too
-          float li[NH];
+        for (int hh = 0; hh < NH; ++hh) el[hh] = F[hh * 2 * Q + i];
+        uint32_t v[NH][4][8];
+        auto form = [&](int b) {
+          const int j0 = 32 * b + 16 * hf;
+          uint32_t G[16];
+          if (b <= q4) {
+            tc::tmem_ld16(tl + COL_G + j0, G);
+            tc::tmem_wait_ld16(G);
+          }
 #pragma unroll
           for (int hh = 0; hh < NH; ++hh) {
             const float* f = F + hh * 2 * Q;
-            li[hh] = f[i];
+            const float li = el[hh];
+            if (b < q4) {
+              const float rf = ex2(li - blk[hh * 4 + b]);
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int j0 = 32 * b + 16 * hf;
-              uint32_t v[8];
-              if (b < q4) {
-                const float rf = ex2(li[hh] - blk[hh * 4 + b]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 cf4 = *reinterpret_cast<const float4*>(f + Q + j0 + 4 * e);
-                  const float* Gp = G + 16 * b + 4 * e;
-                  v[2 * e] = pack2<__nv_bfloat16>(Gp[0] * (rf * cf4.x), Gp[1] * (rf * cf4.y));
-                  v[2 * e + 1] = pack2<__nv_bfloat16>(Gp[2] * (rf * cf4.z), Gp[3] * (rf * cf4.w));
-                }
-              } else if (b == q4) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int j = j0 + 2 * e;
-                  const float2 lj = *reinterpret_cast<const float2*>(f + j);
-                  const float d0 = __shfl_sync(0xffffffffu, own[hh], 16 * hf + 2 * e),
-                              d1 = __shfl_sync(0xffffffffu, own[hh], 16 * hf + 2 * e + 1);
-                  v[e] = pack2<__nv_bfloat16>(j <= i ? G[16 * b + 2 * e] * (ex2(li[hh] - lj.x) * d0) : 0.f,
-                                              j + 1 <= i ? G[16 * b + 2 * e + 1] * (ex2(li[hh] - lj.y) * d1) : 0.f);
-                }
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = 0u;
+              for (int e = 0; e < 4; ++e) {
+                const float4 cf4 = *reinterpret_cast<const float4*>(f + Q + j0 + 4 * e);
+                v[hh][b][2 * e] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e]) * (rf * cf4.x),
+                                                       __uint_as_float(G[4 * e + 1]) * (rf * cf4.y));
+                v[hh][b][2 * e + 1] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e + 2]) * (rf * cf4.z),
+                                                           __uint_as_float(G[4 * e + 3]) * (rf * cf4.w));
               }
-              tc::tmem_st8(tl + COL_G + 64 * hh + 16 * b + 8 * hf, v);
+            } else if (b == q4) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int j = j0 + 2 * e;
+                const float2 lj = *reinterpret_cast<const float2*>(f + j);
+                const float d0 = __shfl_sync(0xffffffffu, own[hh], 16 * hf + 2 * e),
+                            d1 = __shfl_sync(0xffffffffu, own[hh], 16 * hf + 2 * e + 1);
+                v[hh][b][e] = pack2<__nv_bfloat16>(j <= i ? __uint_as_float(G[2 * e]) * (ex2(li - lj.x) * d0) : 0.f,
+                                                   j + 1 <= i ? __uint_as_float(G[2 * e + 1]) * (ex2(li - lj.y) * d1) : 0.f);
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[hh][b][e] = 0u;
             }
           }
-          tc::tmem_wait_st();
+        };
+        form(2);
+        form(3);
+        tc::fence_before_sync();
+        bar_named(1);
+        tc::tmem_st8(tl + COL_G + 64 + 16 * 2 + 8 * hf, v[NH - 1][2]);
+        tc::tmem_st8(tl + COL_G + 64 + 16 * 3 + 8 * hf, v[NH - 1][3]);
+        form(0);
+        tc::tmem_st8(tl + COL_G + 64 + 8 * hf, v[NH - 1][0]);
+        form(1);
+        tc::tmem_st8(tl + COL_G + 64 + 16 + 8 * hf, v[NH - 1][1]);
+        if (NH == 2) {
           tc::fence_before_sync();
           bar_named(1);
-          if (tid == 0) {
-            tc::fence_after_sync();
-            constexpr uint32_t id1 = tc::idesc_bf16_f32(128, PH, false, true);
 #pragma unroll
-            for (int hh = 0; hh < NH; ++hh)
-#pragma unroll
-              for (int k = 0; k < Q / 16; ++k)
-                tc::mma_bf16_ta(tm + COL_Y1 + hh * PH, tm + COL_G + 64 * hh + 8 * k,
-                                tc::sdesc128(sb + xs + hh * (PH / 64 * BLK64) + k * 2048u, BLK64, 1024u), id1, k > 0);
-            tc::mma_commit(barY);
-          }
-          // ---- y = Y1 + e^{L_i} Y2 + D x, over x in shared memory once its terms are formed
-          wait(barC, par);
-          wait(barY, par);
-          wait(barS, par);
+          for (int b = 0; b < 4; ++b) tc::tmem_st8(tl + COL_G + 16 * b + 8 * hf, v[0][b]);
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        bar_named(1);
+        if (tid == 0) {
           tc::fence_after_sync();
-          const int hh = NH == 2 ? hf : 0, pc0 = NH == 2 ? 0 : hf * HC;
-          const float el = ex2(NH == 2 ? li[hf ? NH - 1 : 0] : li[0]);
-          const float Dh = a.D ? a.D[w.h0 + hh] : 0.f;
-          const bool direct = !TMA || nt < Q;
-          uint16_t* yr = static_cast<uint16_t*>(const_cast<void*>(a.y.p)) + tok(w, a.y, t0 + i) +
-                         (int64_t)(w.h0 + hh) * a.P + w.p0 + pc0;
+          constexpr uint32_t id1 = tc::idesc_bf16_f32(128, PH, false, true);
+#pragma unroll 1
+          for (int k = 0; k < NH * Q / 16; ++k)
+            tc::mma_bf16_ta(tm + COL_Y1 + (k >> 3) * PH, tm + COL_G + (NH == 1 ? 64 : 64 * (k >> 3)) + 8 * (k & 7),
+                            tc::sdesc128(sb + xs + (k >> 3) * (PH / 64 * BLK64) + (k & 7) * 2048u, BLK64, 1024u), id1,
+                            (k & 7) > 0);
+          tc::mma_commit(barY);
+        }
+        wait(barC, par);
+        wait(barS, par);
+        tc::fence_after_sync();
+        update_state(decl);
+        if (!last) share_state();
+        wait(barY, par);
+        tc::fence_after_sync();
+        // the next chunk's G, now if its operands are there: W's place is free
+        if (tid == 0 && more && wf.s1 - wf.s0 - cf * Q >= Q && mbar_try_wait(fullB, par ^ 1u) &&
+            mbar_try_wait(fullC, par ^ 1u)) {
+          issue_g(gc + 1);
+          early = true;
+        }
+        // ---- y = Y1 + e^{L_i} Y2 + D x, over x in shared memory (its terms are formed)
+        const int hh = NH == 2 ? hf : 0;
+        const float ei = ex2(NH == 2 && hf ? el[NH - 1] : el[0]);
+        const float Dh = a.D ? a.D[w.h0 + hh] : 0.f;
+        const bool direct = !TMA || nt < Q;
+#pragma unroll 1
+        for (int c16 = 0; c16 < HC / 16; ++c16) {
+          uint32_t r1[16], r2[16];
+          tc::tmem_ld16(tl + COL_Y1 + hf * HC + 16 * c16, r1);
+          tc::tmem_ld16(tl + COL_Y2 + hf * HC + 16 * c16, r2);
+          tc::tmem_wait_ld16(r1);
+          tc::tmem_wait_ld16(r2);
 #pragma unroll
-          for (int c32 = 0; c32 < HC / 32; ++c32) {
-            uint32_t r1[32], r2[32];
-            tc::tmem_ld32(tl + COL_Y1 + hf * HC + 32 * c32, r1);
-            tc::tmem_ld32(tl + COL_Y2 + hf * HC + 32 * c32, r2);
-            tc::tmem_wait_ld(r1);
-            tc::tmem_wait_ld(r2);
+          for (int e8 = 0; e8 < 2; ++e8) {
+            uint4* xp = reinterpret_cast<uint4*>(sm + xs + piece_off(i, hf * (HC / 8) + 2 * c16 + e8));
+            const uint4 xv = *xp;
+            const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+            uint32_t o[4];
 #pragma unroll
-            for (int e8 = 0; e8 < 4; ++e8) {
-              uint4* xp = reinterpret_cast<uint4*>(sm + xs + piece_off(i, hf * (HC / 8) + 4 * c32 + e8));
-              const uint4 xv = *xp;
-              const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-              uint32_t o[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int e = 8 * e8 + 2 * k;
-                o[k] = pack2<__nv_bfloat16>(
-                    fmaf(Dh, __uint_as_float(xw[k] << 16), fmaf(el, __uint_as_float(r2[e]), __uint_as_float(r1[e]))),
-                    fmaf(Dh, __uint_as_float(xw[k] & 0xffff0000u),
-                         fmaf(el, __uint_as_float(r2[e + 1]), __uint_as_float(r1[e + 1]))));
-              }
-              if (!direct) {
-                *xp = make_uint4(o[0], o[1], o[2], o[3]);
-              } else if (i < nt && ok) {
-                uint16_t* p = yr + 32 * c32 + 8 * e8;
-                const int left = a.P - w.p0 - pc0 - (32 * c32 + 8 * e8);
-                if (TMA) {
-                  if (left > 0) *reinterpret_cast<uint4*>(p) = make_uint4(o[0], o[1], o[2], o[3]);
-                } else {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    if (k < left) p[k] = (uint16_t)(o[k >> 1] >> (16 * (k & 1)));
-                }
-              }
+            for (int k = 0; k < 4; ++k) {
+              const int e = 8 * e8 + 2 * k;
+              o[k] = pack2<__nv_bfloat16>(
+                  fmaf(Dh, __uint_as_float(xw[k] << 16), fmaf(ei, __uint_as_float(r2[e]), __uint_as_float(r1[e]))),
+                  fmaf(Dh, __uint_as_float(xw[k] & 0xffff0000u),
+                       fmaf(ei, __uint_as_float(r2[e + 1]), __uint_as_float(r1[e + 1]))));
             }
-          }
-          if (!direct) {
-            tc::fence_smem_to_async();
-            bar_named(1);
-            if (tid == 0 && ok) {
-#pragma unroll
-              for (int b = 0; b < PC / 64; ++b) {
-                const int p = w.p0 + (NH == 1 ? 64 * b : 0);
-                if (p < a.P)
-                  tma_store(&ta.my, p, w.h0 + (NH == 1 ? 0 : b), w.it.begin + t0, a.y.sn ? w.row : 0,
-                            sb + xs + b * BLK64);
-              }
-              bulk_commit();
-            }
+            *xp = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        chunk_end();
+        tc::fence_smem_to_async();
+        tc::fence_before_sync();
+        bar_named(1);             // y is in shared memory, and its accumulators are free
+        if (!direct) {
+          if (tid == 0 && ok) {
+#pragma unroll
+            for (int b = 0; b < PC / 64; ++b) {
+              const int p = w.p0 + (NH == 1 ? 64 * b : 0);
+              if (p < a.P)
+                tma_store(&ta.my, p, w.h0 + (NH == 1 ? 0 : b), w.begin + t0, a.y.sn ? w.row : 0, sb + xs + b * BLK64);
+            }
+            bulk_commit();
+          }
+        } else if (ok) {
+          // a ragged chunk's rows (or unaligned ones), value by value
+          uint16_t* yr = static_cast<uint16_t*>(const_cast<void*>(a.y.p)) + tok(w, a.y, t0) + (int64_t)w.h0 * a.P + w.p0;
+          const int pw = min(PH, a.P - w.p0);
+#pragma unroll 1
+          for (int e = tid; e < nt * PC; e += 256) {
+            const int t = e / PC, col = e % PC, p = col % PH;
+            if (p < pw)
+              yr[(int64_t)t * a.y.st + (int64_t)(col / PH) * a.P + p] =
+                  *reinterpret_cast<const uint16_t*>(sm + xs + piece_off(t, col >> 3) + 2 * (col & 7));
+          }
+          bar_named(1);           // read before the buffer is filled again
+        }
       }
-      u = nxt;
     }
-    if (TMA && !STATE && tid == 0) bulk_wait();
+    leave_state(w, ltot);
+    u = un;
+    w = wn;
+    any = another;
   }
+  if (TMA && !STATE && tid == 0) bulk_wait();
   if (!__syncthreads_and(ok)) {    // let what was issued land before the memory is given back
-    if (tid == 0 && gc > 0) {
-      mbar_drain(barS, (gc - 1) & 1u);
-      if (!STATE) mbar_drain(barY, (gc - 1) & 1u);
-    }
+    if (tid == 256 && gc > 0) mbar_drain(barS, (gc - 1) & 1u);
+    if (!STATE && tid == 0 && gc > 0) mbar_drain(barY, (gc - 1) & 1u);
     __syncthreads();
   }
   if (warp == 0) tc::tmem_dealloc(tm, 512);
@@ -767,6 +865,8 @@ cudaError_t launch_ssm_tc(bool vec, int64_t tokens, const SsmArgs& a, const SsmP
   t.units = p.units;
   t.ptiles = p.ptiles;
   t.total = tiles * p.units;
+  t.empty_rows = 0;
+  for (int i = 0; i < a.rows; ++i) t.empty_rows |= row_len(a.items[i]) == 0;
   const bool tma = vec && encode(&t.mx, a.x, a.P, a.H, tokens, a.rows) && encode(&t.mb, a.B, a.N, a.G, tokens, a.rows) &&
                    encode(&t.mc, a.C, a.N, a.G, tokens, a.rows) && encode(&t.my, a.y, a.P, a.H, tokens, a.rows);
   if (p.ph == 128) return tma ? both<1, 128, true>(t, p.split, p.sms, s) : both<1, 128, false>(t, p.split, p.sms, s);
