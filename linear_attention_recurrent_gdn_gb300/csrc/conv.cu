@@ -5,11 +5,14 @@
 // where x at a negative t is the slot's carried input (its last W - 1, oldest
 // first) or zero for a fresh row.
 //
-// A thread takes eight channels (one 16-byte vector of a 16-bit type) and
-// walks the tokens of its tile with the last W - 1 of them in registers, so a
-// value is read once a tile plus W - 1 of every TT tokens again.  Sums, the
-// activation and the norm are in 32 bits, rounded once.  About 2 W + 4
-// operations a value: HBM bound.
+// A thread takes eight channels and walks the tokens of its tile with the last
+// W - 1 of them in registers, the next few on their way from memory, so a value is read once a tile plus W - 1 of every TT tokens
+// again.  Aligned tensors: the eight channels are one 16-byte vector of a
+// 16-bit type.  Others: eight channels 32 apart, so that a warp's loads of one
+// value a lane are still contiguous.  Sums, the activation and the norm are in
+// 32 bits, rounded once; pairs of channels share a packed fp32 multiply-add,
+// and pairs of sigmoids a reciprocal.  About 2 W + 8 operations a value: HBM
+// bound.
 #include "mixer_device.cuh"
 
 namespace dl {
@@ -19,8 +22,287 @@ namespace {
 
 constexpr int CONV_THREADS = 128;
 
+// Eight values of a thread as they sit in memory: VEC: consecutive; else one
+// every 32 channels.
+template <class T, bool VEC>
+struct Eight {
+  static constexpr int NW = VEC && sizeof(T) == 2 ? 4 : 8;
+  uint32_t w[NW];
+
+  // p: the thread's first value; valid: how many of the channels from it on exist
+  __device__ __forceinline__ void load(const T* p, int valid) {
+    if constexpr (VEC) {
+      const Vec8<T> v = load8<T, true>(p, valid);
+#pragma unroll
+      for (int k = 0; k < NW; ++k) w[k] = v.w[k];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if constexpr (sizeof(T) == 4) w[k] = 32 * k < valid ? __float_as_uint(p[32 * k]) : 0u;
+        else w[k] = 32 * k < valid ? reinterpret_cast<const uint16_t*>(p)[32 * k] : 0u;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(T* p, int valid) const {
+    if constexpr (VEC) {
+      Vec8<T> v;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) v.w[k] = w[k];
+      store8<T, true>(p, v, valid);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (32 * k < valid) {
+          if constexpr (sizeof(T) == 4) p[32 * k] = __uint_as_float(w[k]);
+          else reinterpret_cast<uint16_t*>(p)[32 * k] = (uint16_t)w[k];
+        }
+    }
+  }
+  // the value pair 2 k, 2 k + 1 in 32 bits
+  __device__ __forceinline__ void pair(int k, float& a, float& b) const {
+    if constexpr (sizeof(T) == 4) {
+      a = __uint_as_float(w[2 * k]);
+      b = __uint_as_float(w[2 * k + 1]);
+    } else if constexpr (VEC) {
+      unpack2<T>(w[k], a, b);
+    } else {
+      unpack2<T>(w[2 * k] | (w[2 * k + 1] << 16), a, b);
+    }
+  }
+  __device__ __forceinline__ void set(int k, float a, float b) {
+    if constexpr (sizeof(T) == 4) {
+      w[2 * k] = __float_as_uint(a);
+      w[2 * k + 1] = __float_as_uint(b);
+    } else {
+      const uint32_t v = pack2<T>(a, b);
+      if constexpr (VEC) {
+        w[k] = v;
+      } else {
+        w[2 * k] = v & 0xffffu;
+        w[2 * k + 1] = v >> 16;
+      }
+    }
+  }
+};
+
+using f2 = unsigned long long;     // two fp32 values
+__device__ __forceinline__ f2 mk2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void un2(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float ex2_f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// silu of a pair: z / (1 + e^-z).  16-bit types: one reciprocal for both, 1 /
+// (p q); the exponentials are held at 2^62, so that the product is finite and
+// a NaN stays its own channel's, and z at -43 (a value of -9e-18 or less in
+// size either way).
+template <class T>
+__device__ __forceinline__ f2 silu2(f2 z) {
+  float a, b;
+  if constexpr (sizeof(T) == 4) {
+    un2(z, a, b);
+    return mk2(a * rcp_f(1.f + expf(-a)), b * rcp_f(1.f + expf(-b)));
+  } else {
+    un2(mul2(z, mk2(-1.4426950408889634f, -1.4426950408889634f)), a, b);
+    float p, q;
+    un2(add2(mk2(fminf(ex2_f(a), 0x1p62f), fminf(ex2_f(b), 0x1p62f)), mk2(1.f, 1.f)), p, q);
+    const float r = rcp_f(p * q);
+    un2(z, a, b);
+    return mul2(mk2(max_nan(a, -43.f), max_nan(b, -43.f)), mul2(mk2(q, p), mk2(r, r)));
+  }
+}
+
+// A thread's channels, weights and outputs.
 template <class T, int W, bool VEC>
-__global__ void __launch_bounds__(CONV_THREADS)
+struct Lane {
+  int c, valid;              // first channel, and how many from it on exist
+  bool normed;               // this warp has channels of normalised heads
+  f2 w[W][4], bias[4];
+
+  __device__ __forceinline__ int chan(int k) const { return VEC ? c + k : c + 32 * k; }
+
+  __device__ __forceinline__ void init(const ConvArgs& a) {
+    const int lane = threadIdx.x & 31, base = blockIdx.y * CONV_THREADS * 8 + (threadIdx.x >> 5) * 256;
+    c = VEC ? base + 8 * lane : base + lane;
+    valid = a.C - c;
+    normed = base < a.l2c;
+    float wf[W][8], bf[8];
+    if (VEC && valid > 0 && !a.w_f32 && sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0) {
+      // the W weights of eight channels are W vectors
+      float v[W * 8];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float t[8];
+        unpack8<T>(load8<T, true>(static_cast<const T*>(a.w) + (int64_t)c * W + 8 * j, 8), t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[8 * j + k] = t[k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < W; ++j) wf[j][k] = v[k * W + j];
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+          wf[j][k] = chan(k) >= a.C ? 0.f
+                     : a.w_f32      ? static_cast<const float*>(a.w)[(int64_t)chan(k) * W + j]
+                                    : to_f(static_cast<const T*>(a.w)[(int64_t)chan(k) * W + j]);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      bf[k] = !a.b || chan(k) >= a.C ? 0.f
+              : a.w_f32              ? static_cast<const float*>(a.b)[chan(k)]
+                                     : to_f(static_cast<const T*>(a.b)[chan(k)]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      bias[k] = mk2(bf[2 * k], bf[2 * k + 1]);
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[j][k] = mk2(wf[j][2 * k], wf[j][2 * k + 1]);
+    }
+  }
+
+  // One token: the window moves on by `cur`; returns y in `out`.  All lanes of the warp take part.
+  __device__ __forceinline__ void token(const ConvArgs& a, const Eight<T, VEC>& cur, f2 (&win)[W - 1][4],
+                                        Eight<T, VEC>& out) const {
+    f2 z[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float p, q;
+      cur.pair(k, p, q);
+      const f2 x = mk2(p, q);
+      f2 s = bias[k];
+#pragma unroll
+      for (int j = 0; j < W - 1; ++j) s = fma2(w[j][k], win[j][k], s);
+      s = fma2(w[W - 1][k], x, s);
+#pragma unroll
+      for (int j = 0; j + 2 < W; ++j) win[j][k] = win[j + 1][k];
+      win[W - 2][k] = x;
+      z[k] = a.act ? silu2<T>(s) : s;
+    }
+    if (normed) {
+      if constexpr (VEC) {
+        // a head is hd / 8 neighbouring lanes
+        f2 s2 = mul2(z[0], z[0]);
+#pragma unroll
+        for (int k = 1; k < 4; ++k) s2 = fma2(z[k], z[k], s2);
+        float ss, s1;
+        un2(s2, ss, s1);
+        ss += s1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1)
+          if (8 * o < a.hd) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = c < a.l2c ? rsqrtf(ss + a.eps) : 1.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], mk2(r, r));
+      } else {
+        // a head is hd lanes of one value, or hd / 32 values of every lane
+        float v[8], ss[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) un2(z[k], v[2 * k], v[2 * k + 1]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) ss[k] = v[k] * v[k];
+        const int g = a.hd >> 5;
+#pragma unroll
+        for (int s = 1; s < 8; s <<= 1)
+          if (g > s) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (!(k & s)) ss[k] = ss[k + s] = ss[k] + ss[k + s];
+          }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1)
+            if (o < a.hd) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
+          v[k] *= chan(k) < a.l2c ? rsqrtf(ss[k] + a.eps) : 1.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) z[k] = mk2(v[2 * k], v[2 * k + 1]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float p, q;
+      un2(z[k], p, q);
+      out.set(k, p, q);
+    }
+  }
+};
+
+// Where a thread's outputs of token t of a row go.
+template <class T, bool VEC>
+struct Out {
+  T* p;                      // token 0, or null: channels of several ranges
+  int64_t st;
+  __device__ __forceinline__ void init(const ConvArgs& a, int begin, int row, int c) {
+    int part = 0, end = 0;
+#pragma unroll
+    for (int k = 1; k < CONV_PARTS; ++k) {
+      part += c >= a.c0[k];
+      end += c + 224 >= a.c0[k];
+    }
+    st = a.y[part].st;
+    p = !VEC && part != end ? nullptr
+                            : static_cast<T*>(const_cast<void*>(a.y[part].p)) + (int64_t)begin * st +
+                                  (int64_t)row * a.y[part].sn + (c - a.c0[part]);
+  }
+  __device__ __forceinline__ void put(const ConvArgs& a, const Eight<T, VEC>& v, int begin, int row, int t, int c,
+                                      int valid) const {
+    if (VEC || p) {
+      v.store(p + (int64_t)t * st, valid);
+      return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int ch = c + 32 * k;
+      if (32 * k >= valid) continue;
+      int q = 0;
+#pragma unroll
+      for (int e = 1; e < CONV_PARTS; ++e) q += ch >= a.c0[e];
+      T* o = static_cast<T*>(const_cast<void*>(a.y[q].p)) + (int64_t)(begin + t) * a.y[q].st + (int64_t)row * a.y[q].sn +
+             (ch - a.c0[q]);
+      if constexpr (sizeof(T) == 4) *o = __uint_as_float(v.w[VEC ? 0 : k]);
+      else *reinterpret_cast<uint16_t*>(o) = (uint16_t)v.w[VEC ? 0 : k];
+    }
+  }
+};
+
+template <class T, int W, bool VEC>
+__global__ void __launch_bounds__(CONV_THREADS, 4)
 conv_kernel(const __grid_constant__ ConvArgs a) {
   const int tile = blockIdx.x;
   const int row = find_row(a.items, a.rows, tile, a.per_row);
@@ -28,126 +310,137 @@ conv_kernel(const __grid_constant__ ConvArgs a) {
   const int len = row_len(it);
   const int ti = tile - (a.per_row ? row * a.per_row : it.tile0);
   const int t0 = ti * a.TT, t1 = min(len, t0 + a.TT);
-  const int c = (blockIdx.y * CONV_THREADS + threadIdx.x) * 8;
-  const int valid = min(8, a.C - c);     // <= 0: only takes part in the shuffles
-  const T* x = static_cast<const T*>(a.x.p) + (int64_t)it.begin * a.x.st + (int64_t)row * a.x.sn + c;
-  const bool normed = c < a.l2c;
+  Lane<T, W, VEC> ln;
+  ln.init(a);
+  const T* x = static_cast<const T*>(a.x.p) + (int64_t)it.begin * a.x.st + (int64_t)row * a.x.sn + ln.c;
 
-  float w[W][8], bias[8];
+  constexpr int PF = VEC && sizeof(T) == 2 ? 4 : 2;   // tokens on their way: 16 registers
+  Eight<T, VEC> buf[PF];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-#pragma unroll
-    for (int j = 0; j < W; ++j)
-      w[j][k] = k >= valid ? 0.f
-                : a.w_f32  ? static_cast<const float*>(a.w)[(int64_t)(c + k) * W + j]
-                           : to_f(static_cast<const T*>(a.w)[(int64_t)(c + k) * W + j]);
-    bias[k] = k >= valid || !a.b ? 0.f
-              : a.w_f32          ? static_cast<const float*>(a.b)[c + k]
-                                 : to_f(static_cast<const T*>(a.b)[c + k]);
-  }
+  for (int e = 0; e < PF; ++e) buf[e].load(x + (int64_t)(t0 + e) * a.x.st, t0 + e < t1 ? ln.valid : 0);
 
   // the W - 1 inputs before t0
-  Vec8<T> hist[W - 1];
-  T* st = a.state ? static_cast<T*>(a.state) + (int64_t)it.slot * (W - 1) * a.C + c : nullptr;
+  Eight<T, VEC> hist[W - 1];
+  T* st = a.state ? static_cast<T*>(a.state) + (int64_t)it.slot * (W - 1) * a.C + ln.c : nullptr;
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) {
-    if (t0 > 0)
-      hist[j] = load8<T, VEC>(x + (int64_t)(t0 - (W - 1) + j) * a.x.st, valid);   // TT >= W - 1
-    else
-      hist[j] = load8<T, VEC>(st + (int64_t)j * a.C, st && !row_fresh(it) ? valid : 0);
+    if (t0 > 0) hist[j].load(x + (int64_t)(t0 - (W - 1) + j) * a.x.st, ln.valid);   // TT >= W - 1
+    else hist[j].load(st + (int64_t)j * a.C, st && !row_fresh(it) ? ln.valid : 0);
   }
-
   // Carried inputs after the call: the last W - 1 of (old ones, x).  Only the
   // row's first tile reads and writes them, so no other block can see them change.
   if (ti == 0 && st) {
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
       const int p = len - (W - 1) + j;
-      Vec8<T> v;
+      Eight<T, VEC> v;
       if (p >= 0) {
-        v = load8<T, VEC>(x + (int64_t)p * a.x.st, valid);
+        v.load(x + (int64_t)p * a.x.st, ln.valid);
       } else {
         v = hist[0];
 #pragma unroll
-        for (int i = 1; i < W - 1; ++i)
-          if (W - 1 + p == i) v = hist[i];
+        for (int e = 1; e < W - 1; ++e)
+          if (W - 1 + p == e) v = hist[e];
       }
-      store8<T, VEC>(st + (int64_t)j * a.C, v, valid);
+      v.store(st + (int64_t)j * a.C, ln.valid);
     }
   }
   if (t1 <= t0) return;
 
-  float win[W - 1][8];
+  f2 win[W - 1][4];
 #pragma unroll
-  for (int j = 0; j < W - 1; ++j) unpack8<T>(hist[j], win[j]);
-
-  int part = 0;
+  for (int j = 0; j < W - 1; ++j)
 #pragma unroll
-  for (int k = 1; k < CONV_PARTS; ++k) part += c >= a.c0[k];
-  T* y = static_cast<T*>(const_cast<void*>(a.y[part].p)) + (int64_t)it.begin * a.y[part].st +
-         (int64_t)row * a.y[part].sn + (c - a.c0[part]);
-  const int64_t yst = a.y[part].st;
-
-  for (int t = t0; t < t1; ++t) {
-    float cur[8], z[8];
-    unpack8<T>(load8<T, VEC>(x + (int64_t)t * a.x.st, valid), cur);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float s = bias[k];
-#pragma unroll
-      for (int j = 0; j < W - 1; ++j) s = fmaf(w[j][k], win[j][k], s);
-      s = fmaf(w[W - 1][k], cur[k], s);
-      z[k] = act_f<T>(s, a.act);
-#pragma unroll
-      for (int j = 0; j + 2 < W; ++j) win[j][k] = win[j + 1][k];
-      win[W - 2][k] = cur[k];
+    for (int k = 0; k < 4; ++k) {
+      float p, q;
+      hist[j].pair(k, p, q);
+      win[j][k] = mk2(p, q);
     }
-    if (a.l2c) {
-      float ss = 0.f;
+  Out<T, VEC> out;
+  out.init(a, it.begin, row, ln.c);
+
+  const T* ahead = x + (int64_t)(t0 + PF) * a.x.st;
+#pragma unroll 1
+  for (int t = t0; t < t1; t += PF) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss = fmaf(z[k], z[k], ss);
-      for (int o = 1; o < (a.hd >> 3); o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const float r = normed ? rsqrtf(ss + a.eps) : 1.f;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) z[k] *= r;
-    }
-    const Vec8<T> o = pack8<T>(z);
-    if (VEC) {
-      store8<T, true>(y + (int64_t)t * yst, o, valid);
-    } else {
-      // a vector may straddle two ranges
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < valid) {
-          int q = 0;
-#pragma unroll
-          for (int e = 1; e < CONV_PARTS; ++e) q += c + k >= a.c0[e];
-          static_cast<T*>(const_cast<void*>(a.y[q].p))[(int64_t)(it.begin + t) * a.y[q].st +
-                                                       (int64_t)row * a.y[q].sn + (c + k - a.c0[q])] =
-              from_f<T>(z[k]);
-        }
+    for (int e = 0; e < PF; ++e) {
+      Eight<T, VEC> y;
+      ln.token(a, buf[e], win, y);
+      buf[e].load(ahead, t + PF + e < t1 ? ln.valid : 0);
+      ahead += a.x.st;
+      if (t + e < t1) out.put(a, y, it.begin, row, t + e, ln.c, ln.valid);
     }
   }
 }
 
-template <class T, int W>
-cudaError_t go(bool vec, const ConvArgs& a, cudaStream_t s) {
+// One token of every row: a block takes TT rows, so that the weights are read
+// once for all of them.
+template <class T, int W, bool VEC>
+__global__ void __launch_bounds__(CONV_THREADS, 4)
+conv_step_kernel(const __grid_constant__ ConvArgs a) {
+  Lane<T, W, VEC> ln;
+  ln.init(a);
+  const int r1 = min(a.rows, (int)(blockIdx.x + 1) * a.TT);
+#pragma unroll 2
+  for (int row = blockIdx.x * a.TT; row < r1; ++row) {
+    const RowItem it = a.items[row];
+    Eight<T, VEC> cur, hist[W - 1], y;
+    T* st = a.state ? static_cast<T*>(a.state) + (int64_t)it.slot * (W - 1) * a.C + ln.c : nullptr;
+    cur.load(static_cast<const T*>(a.x.p) + (int64_t)row * a.x.sn + ln.c, ln.valid);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) hist[j].load(st + (int64_t)j * a.C, st && !row_fresh(it) ? ln.valid : 0);
+    if (st) {
+#pragma unroll
+      for (int j = 0; j + 1 < W - 1; ++j) hist[j + 1].store(st + (int64_t)j * a.C, ln.valid);
+      cur.store(st + (int64_t)(W - 2) * a.C, ln.valid);
+    }
+    f2 win[W - 1][4];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float p, q;
+        hist[j].pair(k, p, q);
+        win[j][k] = mk2(p, q);
+      }
+    ln.token(a, cur, win, y);
+    Out<T, VEC> out;
+    out.init(a, 0, row, ln.c);
+    out.put(a, y, 0, row, 0, ln.c, ln.valid);
+  }
+}
+
+template <class T, int W, bool VEC>
+cudaError_t go(bool step, const ConvArgs& a, cudaStream_t s) {
   const dim3 grid((unsigned)a.tiles, (unsigned)((a.C + 8 * CONV_THREADS - 1) / (8 * CONV_THREADS)));
-  if (vec) conv_kernel<T, W, true><<<grid, CONV_THREADS, 0, s>>>(a);
-  else conv_kernel<T, W, false><<<grid, CONV_THREADS, 0, s>>>(a);
+  if (step) conv_step_kernel<T, W, VEC><<<grid, CONV_THREADS, 0, s>>>(a);
+  else conv_kernel<T, W, VEC><<<grid, CONV_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
+template <class T, int W>
+cudaError_t go_v(bool step, bool vec, const ConvArgs& a, cudaStream_t s) {
+  return vec ? go<T, W, true>(step, a, s) : go<T, W, false>(step, a, s);
+}
 template <class T>
-cudaError_t go_w(bool vec, const ConvArgs& a, cudaStream_t s) {
-  return a.W == 2 ? go<T, 2>(vec, a, s) : a.W == 3 ? go<T, 3>(vec, a, s) : go<T, 4>(vec, a, s);
+cudaError_t go_w(bool step, bool vec, const ConvArgs& a, cudaStream_t s) {
+  return a.W == 2 ? go_v<T, 2>(step, vec, a, s) : a.W == 3 ? go_v<T, 3>(step, vec, a, s) : go_v<T, 4>(step, vec, a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_conv(int dtype, bool vec, const ConvArgs& a, cudaStream_t s) {
-  return dtype == T_F32    ? go_w<float>(vec, a, s)
-         : dtype == T_BF16 ? go_w<__nv_bfloat16>(vec, a, s)
-                           : go_w<__half>(vec, a, s);
+int conv_tile(int64_t tokens, int C, int sms) {
+  // As many tokens (rows, for a step) a tile as leave about eight blocks for every SM: longer tiles read fewer
+  // tokens twice and the weights less often.
+  const int64_t blocks_c = (C + 8 * CONV_THREADS - 1) / (8 * CONV_THREADS);
+  int tt = 64;
+  while (tt > 4 && (tokens + tt - 1) / tt * blocks_c < 8 * (int64_t)sms) tt >>= 1;
+  return tt;
+}
+
+cudaError_t launch_conv(int dtype, bool step, bool vec, const ConvArgs& a, cudaStream_t s) {
+  return dtype == T_F32    ? go_w<float>(step, vec, a, s)
+         : dtype == T_BF16 ? go_w<__nv_bfloat16>(step, vec, a, s)
+                           : go_w<__half>(step, vec, a, s);
 }
 
 }  // namespace mx

@@ -55,7 +55,10 @@ struct ConvArgs {
   float eps;
   RowItem items[MX_ROWS];
 };
-cudaError_t launch_conv(int dtype, bool vec, const ConvArgs& a, cudaStream_t s);
+// Tokens of a tile for this much work (a step: rows, one token each).
+int conv_tile(int64_t tokens, int C, int sms);
+// step: one token a row; tiles of TT rows.
+cudaError_t launch_conv(int dtype, bool step, bool vec, const ConvArgs& a, cudaStream_t s);
 
 struct SsmArgs {
   TokView x, dt, B, C, y;

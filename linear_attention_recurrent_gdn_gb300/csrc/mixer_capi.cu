@@ -110,6 +110,24 @@ bool view_vec(const dl_view& v, int64_t dtype, bool packed) {
   return al(v.data, 16) && v.stride_t % per == 0 && (packed || v.stride_n % per == 0);
 }
 
+// Multiprocessors of the current device (a GB300's where there is none to ask).
+int num_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  n = known[dev].load(std::memory_order_relaxed);
+  if (n) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 bool bad_type(int64_t t) { return t < DL_F32 || t > DL_F16; }
 
 }  // namespace
@@ -148,12 +166,19 @@ extern "C" dl_status dl_conv(const dl_conv_args* p, void* stream, char* errbuf, 
   if (c != q.C) return fail(DL_EINVAL, "output ranges do not add up to %lld channels", (long long)q.C);
   a.c0[CONV_PARTS] = (int32_t)q.C;
   for (int k = (int)q.n_parts; k < CONV_PARTS; ++k) a.c0[k] = (int32_t)q.C;
-  a.TT = 32;
+  const bool step = q.tokens.T == 1 && !q.tokens.lengths && !packed;
+  int64_t total = q.tokens.n > 0 ? q.tokens.n * q.tokens.T : 0;
+  if (q.tokens.lengths) {
+    total = 0;
+    for (int64_t i = 0; i < q.tokens.n && i < MX_ROWS; ++i) total += q.tokens.lengths[i];
+  }
+  a.TT = conv_tile(total, (int)q.C, num_sms());
   int64_t tiles;
   bool any;
   const dl_status s = plan_rows(fail, q.tokens, q.state != nullptr, a.TT, a.items, tiles, a.per_row, any);
   if (s != DL_OK) return s;
   if (q.tokens.n == 0) return DL_OK;
+  if (step) tiles = (q.tokens.n + a.TT - 1) / a.TT;
   const int64_t e = elem(q.dtype);
   if ((!q.x.data && any) || !q.weight) return fail(DL_EINVAL, "NULL tensor pointer");
   const int64_t we = q.weight_f32 ? 4 : e;
@@ -177,7 +202,7 @@ extern "C" dl_status dl_conv(const dl_conv_args* p, void* stream, char* errbuf, 
   a.rows = (int32_t)q.tokens.n;
   a.tiles = (int32_t)tiles;
   a.eps = (float)q.eps;
-  return done(fail, launch_conv((int)q.dtype, vec, a, static_cast<cudaStream_t>(stream)));
+  return done(fail, launch_conv((int)q.dtype, step, vec, a, static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
@@ -231,24 +256,6 @@ dl_status ssm_args(const ErrOut& fail, const dl_ssm_args& q, SsmArgs& a) {
 }  // namespace
 
 namespace {
-
-// Multiprocessors of the current device (a GB300's where there is none to ask).
-int num_sms() {
-  static std::atomic<int> known[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    (void)cudaGetLastError();
-    return 152;
-  }
-  n = known[dev].load(std::memory_order_relaxed);
-  if (n) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    return 152;
-  }
-  known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
 
 // The tensor cores take bf16 rows of at least TC_TOKENS tokens (the longest
 // row's): below that the chunk of 128 is mostly padding.

@@ -164,6 +164,24 @@ def test_conv_infinities_and_nan_stay_in_their_channel_and_window(mx):
     assert bad[5:9, 3:5].all() and int(bad.sum()) == 8
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_conv_activation_of_extreme_values(mx, dtype):
+    """Neighbouring channels do not touch each other, whatever their values."""
+    top = 6e4 if dtype == "fp16" else 1e30
+    row = torch.tensor([1.0, float("nan"), -2.0, float("inf"), 3.0, -top, 0.5, top, -1.0, -100.0, 30.0, -30.0,
+                        0.0, -44.0, -0.0, 88.0], dtype=DT[dtype])
+    x = row.repeat(1, 3, 1).cuda()          # one token of three rows: a zero weight times inf would be a NaN
+    w = torch.zeros(16, 2, device="cuda", dtype=DT[dtype])
+    w[:, 1] = 1
+    y = mx.conv(x, w)[0].cpu().double()
+    want = row.double() * torch.sigmoid(row.double())
+    assert torch.isnan(y[:, 1]).all() and (y[:, 3] == float("inf")).all()
+    ok = torch.isfinite(want) & torch.isfinite(row.double())
+    # below -43 the 16-bit forms give -9e-18
+    tol = half(DT[dtype]) * want.abs() + 64 * U * want.abs() + 1e-17 + tiny(DT[dtype])
+    assert ((y[:, ok] - want[ok]).abs() <= tol[ok]).all()
+
+
 # ---------------------------------------------------------------------- ssm --
 def check_ssm(mx, dtype, H, G, P, N, lengths, layout="token", fresh=False, pool=True, D=True, bias=True, softplus=True,
               dt32=False, seed=0, decay=(1.0, 16.0), step_scale=1.0, gap=0, mma=False):
