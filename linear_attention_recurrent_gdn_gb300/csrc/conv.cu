@@ -13,6 +13,9 @@
 // 32 bits, rounded once; pairs of channels share a packed fp32 multiply-add,
 // and pairs of sigmoids a reciprocal.  About 2 W + 8 operations a value: HBM
 // bound.
+#include <type_traits>
+
+#include "dl_device.cuh"
 #include "mixer_device.cuh"
 
 namespace dl {
@@ -195,7 +198,10 @@ struct Lane {
     }
   }
 
-  // One token: the window moves on by `cur`; returns y in `out`.  All lanes of the warp take part.
+  // One token: the window moves on by `cur`; returns y in `out`.  All lanes of the warp take part.  ACT, NORM:
+  // whether there is an activation, and normalised heads in this warp; without branches inside, the tokens of
+  // a group overlap.
+  template <bool ACT, bool NORM>
   __device__ __forceinline__ void token(const ConvArgs& a, const Eight<T, VEC>& cur, f2 (&win)[W - 1][4],
                                         Eight<T, VEC>& out) const {
     f2 z[4];
@@ -211,9 +217,9 @@ struct Lane {
 #pragma unroll
       for (int j = 0; j + 2 < W; ++j) win[j][k] = win[j + 1][k];
       win[W - 2][k] = x;
-      z[k] = a.act ? silu2<T>(s) : s;
+      z[k] = ACT ? silu2<T>(s) : s;
     }
-    if (normed) {
+    if constexpr (NORM) {
       if constexpr (VEC) {
         // a head is hd / 8 neighbouring lanes
         f2 s2 = mul2(z[0], z[0]);
@@ -223,8 +229,10 @@ struct Lane {
         un2(s2, ss, s1);
         ss += s1;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1)
-          if (8 * o < a.hd) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        for (int o = 1; o < 32; o <<= 1) {
+          const float v = __shfl_xor_sync(0xffffffffu, ss, o);
+          ss += 8 * o < a.hd ? v : 0.f;
+        }
         const float r = c < a.l2c ? rsqrtf(ss + a.eps) : 1.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) z[k] = mul2(z[k], mk2(r, r));
@@ -246,8 +254,10 @@ struct Lane {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1)
-            if (o < a.hd) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
+          for (int o = 1; o < 32; o <<= 1) {
+            const float u = __shfl_xor_sync(0xffffffffu, ss[k], o);
+            ss[k] += o < a.hd ? u : 0.f;
+          }
           v[k] *= chan(k) < a.l2c ? rsqrtf(ss[k] + a.eps) : 1.f;
         }
 #pragma unroll
@@ -314,10 +324,37 @@ conv_kernel(const __grid_constant__ ConvArgs a) {
   ln.init(a);
   const T* x = static_cast<const T*>(a.x.p) + (int64_t)it.begin * a.x.st + (int64_t)row * a.x.sn + ln.c;
 
-  constexpr int PF = VEC && sizeof(T) == 2 ? 4 : 2;   // tokens on their way: 16 registers
+  // Tokens come in groups of PF.  Aligned ones take the way through shared memory, two groups ahead, each
+  // thread its own 16-byte places (no barrier, and no registers held by loads on their way).
+  constexpr int PF = VEC && sizeof(T) == 2 ? 4 : 2, RING = 3;
+  constexpr int V16 = sizeof(T) == 4 ? 2 : 1;        // 16-byte pieces of eight values
+  __shared__ __align__(16) uint4 ring[VEC ? RING * PF * V16 : 1][CONV_THREADS];
+  const T* ahead = x + (int64_t)t0 * a.x.st;         // the next group to fetch, from token tf on
+  int tf = t0, slot = 0;
   Eight<T, VEC> buf[PF];
+  auto fetch = [&](int place) {
 #pragma unroll
-  for (int e = 0; e < PF; ++e) buf[e].load(x + (int64_t)(t0 + e) * a.x.st, t0 + e < t1 ? ln.valid : 0);
+    for (int e = 0; e < PF; ++e) {
+      if constexpr (VEC) {
+        if (tf + e < t1 && ln.valid > 0)
+#pragma unroll
+          for (int v = 0; v < V16; ++v)
+            cp_async16(smem_u32(&ring[(place * PF + e) * V16 + v][threadIdx.x]),
+                       reinterpret_cast<const uint4*>(ahead + (int64_t)e * a.x.st) + v);
+      } else {
+        buf[e].load(ahead + (int64_t)e * a.x.st, tf + e < t1 ? ln.valid : 0);
+      }
+    }
+    if constexpr (VEC) asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += (int64_t)PF * a.x.st;
+    tf += PF;
+  };
+  if constexpr (VEC) {
+    fetch(0);
+    fetch(1);
+  } else {
+    fetch(0);
+  }
 
   // the W - 1 inputs before t0
   Eight<T, VEC> hist[W - 1];
@@ -359,17 +396,42 @@ conv_kernel(const __grid_constant__ ConvArgs a) {
   Out<T, VEC> out;
   out.init(a, it.begin, row, ln.c);
 
-  const T* ahead = x + (int64_t)(t0 + PF) * a.x.st;
+  auto walk = [&](auto act, auto norm) {
 #pragma unroll 1
-  for (int t = t0; t < t1; t += PF) {
+    for (int t = t0; t < t1; t += PF) {
+      Eight<T, VEC> cur[PF], y[PF];
+      if constexpr (VEC) {
+        fetch(slot == 0 ? 2 : slot - 1);
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
 #pragma unroll
-    for (int e = 0; e < PF; ++e) {
-      Eight<T, VEC> y;
-      ln.token(a, buf[e], win, y);
-      buf[e].load(ahead, t + PF + e < t1 ? ln.valid : 0);
-      ahead += a.x.st;
-      if (t + e < t1) out.put(a, y, it.begin, row, t + e, ln.c, ln.valid);
+        for (int e = 0; e < PF; ++e)
+#pragma unroll
+          for (int v = 0; v < V16; ++v) {
+            const uint4 r = ring[(slot * PF + e) * V16 + v][threadIdx.x];
+            cur[e].w[4 * v] = r.x;
+            cur[e].w[4 * v + 1] = r.y;
+            cur[e].w[4 * v + 2] = r.z;
+            cur[e].w[4 * v + 3] = r.w;
+          }
+        slot = slot == 2 ? 0 : slot + 1;
+      } else {
+#pragma unroll
+        for (int e = 0; e < PF; ++e) cur[e] = buf[e];
+        fetch(0);
+      }
+#pragma unroll
+      for (int e = 0; e < PF; ++e) ln.template token<act.value, norm.value>(a, cur[e], win, y[e]);
+      // tokens past the last were whatever the places held; their window is not used again
+#pragma unroll
+      for (int e = 0; e < PF; ++e) out.put(a, y[e], it.begin, row, t + e, ln.c, t + e < t1 ? ln.valid : 0);
     }
+  };
+  if (a.act) {
+    if (ln.normed) walk(std::true_type{}, std::true_type{});
+    else walk(std::true_type{}, std::false_type{});
+  } else {
+    if (ln.normed) walk(std::false_type{}, std::true_type{});
+    else walk(std::false_type{}, std::false_type{});
   }
 }
 
@@ -403,7 +465,13 @@ conv_step_kernel(const __grid_constant__ ConvArgs a) {
         hist[j].pair(k, p, q);
         win[j][k] = mk2(p, q);
       }
-    ln.token(a, cur, win, y);
+    if (a.act) {
+      if (ln.normed) ln.template token<true, true>(a, cur, win, y);
+      else ln.template token<true, false>(a, cur, win, y);
+    } else {
+      if (ln.normed) ln.template token<false, true>(a, cur, win, y);
+      else ln.template token<false, false>(a, cur, win, y);
+    }
     Out<T, VEC> out;
     out.init(a, 0, row, ln.c);
     out.put(a, y, 0, row, 0, ln.c, ln.valid);
