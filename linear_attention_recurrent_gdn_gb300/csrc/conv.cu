@@ -162,13 +162,13 @@ struct Lane {
     valid = a.C - c;
     normed = base < a.l2c;
     float wf[W][8], bf[8];
-    if (VEC && valid > 0 && !a.w_f32 && sizeof(T) == 2 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0) {
-      // the W weights of eight channels are W vectors
+    if (VEC && valid > 0 && (reinterpret_cast<uintptr_t>(a.w) & 15) == 0) {
+      // the W weights of eight channels follow one another
       float v[W * 8];
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         float t[8];
-        unpack8<T>(load8<T, true>(static_cast<const T*>(a.w) + (int64_t)c * W + 8 * j, 8), t);
+        weights8<T, true>(a.w, (int64_t)c * W + 8 * j, 8, a.w_f32, t);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[8 * j + k] = t[k];
       }
@@ -312,7 +312,7 @@ struct Out {
 };
 
 template <class T, int W, bool VEC>
-__global__ void __launch_bounds__(CONV_THREADS, 4)
+__global__ void __launch_bounds__(CONV_THREADS, VEC ? 4 : 3)
 conv_kernel(const __grid_constant__ ConvArgs a) {
   const int tile = blockIdx.x;
   const int row = find_row(a.items, a.rows, tile, a.per_row);
@@ -326,7 +326,7 @@ conv_kernel(const __grid_constant__ ConvArgs a) {
 
   // Tokens come in groups of PF.  Aligned ones take the way through shared memory, two groups ahead, each
   // thread its own 16-byte places (no barrier, and no registers held by loads on their way).
-  constexpr int PF = VEC && sizeof(T) == 2 ? 4 : 2, RING = 3;
+  constexpr int PF = VEC ? 4 : 2, RING = 3;
   constexpr int V16 = sizeof(T) == 4 ? 2 : 1;        // 16-byte pieces of eight values
   __shared__ __align__(16) uint4 ring[VEC ? RING * PF * V16 : 1][CONV_THREADS];
   const T* ahead = x + (int64_t)t0 * a.x.st;         // the next group to fetch, from token tf on
@@ -438,7 +438,7 @@ conv_kernel(const __grid_constant__ ConvArgs a) {
 // One token of every row: a block takes TT rows, so that the weights are read
 // once for all of them.
 template <class T, int W, bool VEC>
-__global__ void __launch_bounds__(CONV_THREADS, 4)
+__global__ void __launch_bounds__(CONV_THREADS, 6)
 conv_step_kernel(const __grid_constant__ ConvArgs a) {
   Lane<T, W, VEC> ln;
   ln.init(a);
@@ -497,11 +497,11 @@ cudaError_t go_w(bool step, bool vec, const ConvArgs& a, cudaStream_t s) {
 }  // namespace
 
 int conv_tile(int64_t tokens, int C, int sms) {
-  // As many tokens (rows, for a step) a tile as leave about eight blocks for every SM: longer tiles read fewer
+  // As many tokens (rows, for a step) a tile as still give every SM its four blocks: longer tiles read fewer
   // tokens twice and the weights less often.
   const int64_t blocks_c = (C + 8 * CONV_THREADS - 1) / (8 * CONV_THREADS);
   int tt = 64;
-  while (tt > 4 && (tokens + tt - 1) / tt * blocks_c < 8 * (int64_t)sms) tt >>= 1;
+  while (tt > 4 && (tokens + tt - 1) / tt * blocks_c < 4 * (int64_t)sms) tt >>= 1;
   return tt;
 }
 
