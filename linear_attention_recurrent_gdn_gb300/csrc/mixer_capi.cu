@@ -268,6 +268,12 @@ bool on_tensor_cores(const dl_ssm_args& q) {
   return q.dtype == DL_BF16 && q.N <= 128 && longest >= TC_TOKENS;
 }
 
+SsmPlan plan_of(const dl_ssm_args& q) {
+  const int H = (int)q.H, P = (int)q.P, N = (int)q.N, n = (int)q.tokens.n;
+  return on_tensor_cores(q) ? ssm_tc_plan(H, (int)q.G, P, n, q.tokens.lengths, q.tokens.T, num_sms())
+                            : ssm_scan_plan(H, P, N, n, q.tokens.lengths, q.tokens.T, num_sms());
+}
+
 int64_t workspace_of(const dl_ssm_args& q, const SsmPlan& p, int64_t tiles) {
   return p.split ? 4 * tiles * q.H * (q.P * q.N + 1) : 0;
 }
@@ -277,9 +283,9 @@ int64_t workspace_of(const dl_ssm_args& q, const SsmPlan& p, int64_t tiles) {
 extern "C" int64_t dl_ssm_workspace(const dl_ssm_args* p) {
   const ErrOut quiet{nullptr, 0};
   if (!p || ssm_sizes(quiet, *p) != DL_OK || p->tokens.n < 0 || p->tokens.n > MX_ROWS) return -1;
-  if (p->tokens.n == 0 || !on_tensor_cores(*p)) return 0;
-  const SsmPlan k = ssm_tc_plan((int)p->H, (int)p->G, (int)p->P, (int)p->tokens.n, p->tokens.lengths,
-                                p->tokens.T, num_sms());
+  if (p->tokens.n == 0) return 0;
+  const SsmPlan k = plan_of(*p);
+  if (!k.split) return 0;
   int64_t tiles = 0;
   for (int64_t i = 0; i < p->tokens.n; ++i) {
     const int64_t len = p->tokens.lengths ? p->tokens.lengths[i] : p->tokens.T;
@@ -297,8 +303,7 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   dl_status s = ssm_args(fail, q, a);
   if (s != DL_OK || q.tokens.n == 0) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!on_tensor_cores(q)) return done(fail, launch_ssm_scan((int)q.dtype, a, st));
-  const SsmPlan k = ssm_tc_plan(a.H, a.G, a.P, a.rows, q.tokens.lengths, q.tokens.T, num_sms());
+  const SsmPlan k = plan_of(q);
   int64_t tiles;
   int32_t per_row;
   bool any;
@@ -308,6 +313,8 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   if (need && (!q.workspace || q.workspace_bytes < need || !al(q.workspace, 16)))
     return fail(DL_EINVAL, "the workspace needs %lld bytes, 16-byte aligned (dl_ssm_workspace)", (long long)need);
   if (tiles * k.units > 0x7fffffff) return fail(DL_EINVAL, "too many tokens in one call");
+  if (!on_tensor_cores(q))
+    return done(fail, launch_ssm_scan((int)q.dtype, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
   const bool packed = q.tokens.packed != 0;
   const bool vec = q.P % 8 == 0 && q.N % 8 == 0 && view_vec(q.x, DL_BF16, packed) && view_vec(q.B, DL_BF16, packed) &&
                    view_vec(q.C, DL_BF16, packed) && view_vec(q.y, DL_BF16, packed);

@@ -2,11 +2,17 @@
 //   dt = softplus(raw + bias_h),  S <- e^{dt A_h} S + (dt x) B^T,  y = S C + D_h x
 // with S [P, N] per (row, head) in fp32 and B, C shared by the heads of a group.
 //
-// One CTA per (row, head, tile of state rows).  A thread keeps PR state rows
-// times 16 state columns in registers for the whole row; NL threads share a
-// state row and add up their parts of y by shuffles.  Tokens come in chunks of
-// TC, staged in shared memory in 32 bits.  Three operations per state element
-// and token, so the FP32 cores bound it.  Every size and type runs here.
+// One CTA per (row, head, tile of state rows), and per segment of the row
+// where rows are few and long.  A thread keeps PR state rows times 16 state
+// columns in registers; NL threads share a state row and add up their parts of
+// y by shuffles.  Tokens come in chunks of TC, staged in shared memory in 32
+// bits.  Three operations per state element and token, two elements an
+// instruction (packed fp32), so the FP32 cores bound it.  Every size and type
+// runs here.
+//
+// Segments: a first launch (STATE) runs each but the last from zero (the first
+// from the row's state) and leaves its end state and decay in the workspace;
+// the full launch joins those before its segment.
 #include "mixer_device.cuh"
 
 namespace dl {
@@ -14,44 +20,90 @@ namespace mx {
 
 namespace {
 
-constexpr int SC_THREADS = 128, SC_PR = 2, SC_TC = 16;
+constexpr int SC_THREADS = 128, SC_TC = 16;
+constexpr float LOG2E = 1.4426950408889634f;
+
+// State rows of a thread: as many as leave a CTA 64 rows or so, so that a value
+// of B or C that was read from shared memory serves several.
+__host__ __device__ constexpr int rows_of(int nl) { return nl >= 8 ? 4 : nl == 4 ? 2 : 1; }
+
+struct ScanArgs {
+  SsmArgs a;
+  float* ws;                 // segment states [tiles][H][P][N], then log2 decays [tiles][H]
+  int32_t seg_tokens, tiles, per_row;
+};
 
 // Columns of the thread: 4 (ln + NL i) + e, i, e = 0..3, so that the NL threads
 // of a row read consecutive 16-byte vectors of a staged B or C.
-template <class T, int NL>
+template <class T, int NL, bool STATE>
 __global__ void __launch_bounds__(SC_THREADS)
-ssm_scan_kernel(const __grid_constant__ SsmArgs a) {
-  constexpr int NP = 16 * NL;                       // padded state columns
-  constexpr int PB = SC_THREADS / NL * SC_PR;       // state rows of the CTA
-  __shared__ __align__(16) float sB[SC_TC][NP], sC[SC_TC][NP];
-  __shared__ float sx[SC_TC][PB], sy[SC_TC][PB], sdt[SC_TC], sdec[SC_TC];
-  const int pt = (a.P + PB - 1) / PB;
-  const int tile = blockIdx.x % pt, rh = blockIdx.x / pt;
-  const int row = rh / a.H, h = rh - row * a.H, g = h / (a.H / a.G);
+ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
+  constexpr int PR = rows_of(NL), NP = 16 * NL, PB = SC_THREADS / NL * PR;
+  const SsmArgs& a = sa.a;
+  __shared__ __align__(16) float sB[SC_TC][NP], sC[STATE ? 1 : SC_TC][NP];
+  __shared__ float sx[SC_TC][PB], sy[STATE ? 1 : SC_TC][PB], sdt[SC_TC], sdec[SC_TC];
+  const int pt = (a.P + PB - 1) / PB, ph = pt * a.H;
+  const int tile = blockIdx.x / ph, rest = blockIdx.x - tile * ph, h = rest / pt, g = h / (a.H / a.G);
+  const int row = find_row(a.items, a.rows, tile, sa.per_row);
   const RowItem it = a.items[row];
-  const int len = row_len(it), p0 = tile * PB;
-  const int ln = threadIdx.x % NL, pl = threadIdx.x / NL * SC_PR;
+  const int len = row_len(it), p0 = (rest - h * pt) * PB;
+  const int seg = tile - (sa.per_row ? row * sa.per_row : it.tile0);
+  const int nseg = len > sa.seg_tokens ? (len + sa.seg_tokens - 1) / sa.seg_tokens : 1;
+  if (STATE && seg == nseg - 1) return;              // nothing follows the last segment
+  const int s0 = seg * sa.seg_tokens, s1 = min(len, s0 + sa.seg_tokens);
+  const int ln = threadIdx.x % NL, pl = threadIdx.x / NL * PR;
 
   auto at = [&](const TokView& v, int t) {
     return (int64_t)(it.begin + t) * v.st + (int64_t)row * v.sn;
   };
-  float* st = a.state ? a.state + ((int64_t)it.slot * a.H + h) * a.P * a.N : nullptr;
-  float S[SC_PR][16];
+  const int64_t per_tile = (int64_t)a.H * a.P * a.N, e0 = ((int64_t)h * a.P + p0 + pl) * a.N;
+  float* pool = a.state ? a.state + (int64_t)it.slot * per_tile : nullptr;
+  const float* wl = sa.ws + (int64_t)sa.tiles * per_tile;
+  auto col = [&](int i) { return 4 * (ln + NL * (i >> 2)) + (i & 3); };
+  auto on = [&](int r, int i) { return p0 + pl + r < a.P && col(i) < a.N; };
+  float S[PR][16];
+  {
+    const float* from;
+    if (STATE || nseg == 1) from = seg == 0 && pool && !row_fresh(it) ? pool : nullptr;
+    else if (seg == 0) from = row_fresh(it) ? nullptr : sa.ws + (int64_t)tile * per_tile;
+    else from = sa.ws + (int64_t)(tile - seg + 1) * per_tile;
 #pragma unroll
-  for (int r = 0; r < SC_PR; ++r)
+    for (int r = 0; r < PR; ++r)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int p = p0 + pl + r, n = 4 * (ln + NL * (i >> 2)) + (i & 3);
-      S[r][i] = st && !row_fresh(it) && p < a.P && n < a.N ? st[(int64_t)p * a.N + n] : 0.f;
+      for (int i = 0; i < 16; ++i) S[r][i] = from && on(r, i) ? from[e0 + (int64_t)r * a.N + col(i)] : 0.f;
+    if (STATE && seg == 0 && from) {
+      // the last segment's CTA overwrites the pool's entry in the full launch
+#pragma unroll
+      for (int r = 0; r < PR; ++r)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (on(r, i)) sa.ws[(int64_t)tile * per_tile + e0 + (int64_t)r * a.N + col(i)] = S[r][i];
     }
+    if (!STATE)
+#pragma unroll 1
+      for (int k = 2; k <= seg; ++k) {
+        const float* add = sa.ws + (int64_t)(tile - seg + k) * per_tile + e0;
+        const float d = exp2f(wl[(int64_t)(tile - seg + k - 1) * a.H + h]);
+#pragma unroll
+        for (int r = 0; r < PR; ++r)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) S[r][i] = fmaf(S[r][i], d, on(r, i) ? add[(int64_t)r * a.N + col(i)] : 0.f);
+      }
+  }
+  f2 S2[PR][8];
+#pragma unroll
+  for (int r = 0; r < PR; ++r)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) S2[r][i] = mk2(S[r][2 * i], S[r][2 * i + 1]);
   const float Ah = a.A[h], Dh = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+  float ltot = 0.f;
 
-  for (int t0 = 0; t0 < len; t0 += SC_TC) {
-    const int nt = min(SC_TC, len - t0);
+  for (int t0 = s0; t0 < s1; t0 += SC_TC) {
+    const int nt = min(SC_TC, s1 - t0);
     for (int i = threadIdx.x; i < nt * NP; i += SC_THREADS) {
       const int t = i / NP, n = i - t * NP;
       sB[t][n] = n < a.N ? to_f(static_cast<const T*>(a.B.p)[at(a.B, t0 + t) + (int64_t)g * a.N + n]) : 0.f;
-      sC[t][n] = n < a.N ? to_f(static_cast<const T*>(a.C.p)[at(a.C, t0 + t) + (int64_t)g * a.N + n]) : 0.f;
+      if (!STATE) sC[t][n] = n < a.N ? to_f(static_cast<const T*>(a.C.p)[at(a.C, t0 + t) + (int64_t)g * a.N + n]) : 0.f;
     }
     for (int i = threadIdx.x; i < nt * PB; i += SC_THREADS) {
       const int t = i / PB, p = p0 + i - t * PB;
@@ -67,71 +119,128 @@ ssm_scan_kernel(const __grid_constant__ SsmArgs a) {
     __syncthreads();
     for (int t = 0; t < nt; ++t) {
       const float dec = sdec[t], dt = sdt[t];
-      float xd[SC_PR], acc[SC_PR];
+      const f2 dec2 = mk2(dec, dec);
+      if (STATE) ltot = fmaf(dt, Ah, ltot);
+      f2 xd[PR], acc[PR];
 #pragma unroll
-      for (int r = 0; r < SC_PR; ++r) {
-        xd[r] = sx[t][pl + r] * dt;
-        acc[r] = 0.f;
+      for (int r = 0; r < PR; ++r) {
+        const float v = sx[t][pl + r] * dt;
+        xd[r] = mk2(v, v);
+        acc[r] = mk2(0.f, 0.f);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float4 b4 = *reinterpret_cast<const float4*>(&sB[t][4 * (ln + NL * q)]);
-        const float4 c4 = *reinterpret_cast<const float4*>(&sC[t][4 * (ln + NL * q)]);
-        const float bb[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
+        const f2 bb[2] = {mk2(b4.x, b4.y), mk2(b4.z, b4.w)};
+        f2 cc[2];
+        if (!STATE) {
+          const float4 c4 = *reinterpret_cast<const float4*>(&sC[t][4 * (ln + NL * q)]);
+          cc[0] = mk2(c4.x, c4.y);
+          cc[1] = mk2(c4.z, c4.w);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int r = 0; r < SC_PR; ++r) {
-            S[r][4 * q + e] = fmaf(S[r][4 * q + e], dec, xd[r] * bb[e]);
-            acc[r] = fmaf(S[r][4 * q + e], cc[e], acc[r]);
+          for (int r = 0; r < PR; ++r) {
+            S2[r][2 * q + e] = fma2(S2[r][2 * q + e], dec2, mul2(xd[r], bb[e]));
+            if (!STATE) acc[r] = fma2(S2[r][2 * q + e], cc[e], acc[r]);
           }
       }
+      if (!STATE)
 #pragma unroll
-      for (int r = 0; r < SC_PR; ++r) {
+        for (int r = 0; r < PR; ++r) {
+          float u, v;
+          un2(acc[r], u, v);
+          u += v;
 #pragma unroll
-        for (int o = 1; o < NL; o <<= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
-        if (ln == 0) sy[t][pl + r] = fmaf(Dh, sx[t][pl + r], acc[r]);
-      }
+          for (int o = 1; o < NL; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+          if (ln == 0) sy[t][pl + r] = fmaf(Dh, sx[t][pl + r], u);
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < nt * PB; i += SC_THREADS) {
-      const int t = i / PB, p = p0 + i - t * PB;
-      if (p < a.P)
-        static_cast<T*>(const_cast<void*>(a.y.p))[at(a.y, t0 + t) + (int64_t)h * a.P + p] = from_f<T>(sy[t][p - p0]);
-    }
+    if (!STATE)
+      for (int i = threadIdx.x; i < nt * PB; i += SC_THREADS) {
+        const int t = i / PB, p = p0 + i - t * PB;
+        if (p < a.P)
+          static_cast<T*>(const_cast<void*>(a.y.p))[at(a.y, t0 + t) + (int64_t)h * a.P + p] = from_f<T>(sy[t][p - p0]);
+      }
   }
-  if (!st) return;
+  float* to = STATE ? sa.ws + (int64_t)(tile + 1) * per_tile : seg == nseg - 1 ? pool : nullptr;
+  if (to) {
 #pragma unroll
-  for (int r = 0; r < SC_PR; ++r)
+    for (int r = 0; r < PR; ++r)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int p = p0 + pl + r, n = 4 * (ln + NL * (i >> 2)) + (i & 3);
-      if (p < a.P && n < a.N) st[(int64_t)p * a.N + n] = S[r][i];
-    }
+      for (int i = 0; i < 8; ++i) {
+        float u, v;
+        un2(S2[r][i], u, v);
+        if (on(r, 2 * i)) to[e0 + (int64_t)r * a.N + col(2 * i)] = u;
+        if (on(r, 2 * i + 1)) to[e0 + (int64_t)r * a.N + col(2 * i + 1)] = v;
+      }
+  }
+  if (STATE && p0 == 0 && threadIdx.x == 0)
+    sa.ws[(int64_t)sa.tiles * per_tile + (int64_t)tile * a.H + h] = ltot * LOG2E;
 }
 
+thread_local ScanArgs t_scan;
+
 template <class T, int NL>
-cudaError_t go(const SsmArgs& a, cudaStream_t s) {
-  constexpr int PB = SC_THREADS / NL * SC_PR;
-  const unsigned grid = (unsigned)((int64_t)a.rows * a.H * ((a.P + PB - 1) / PB));
-  ssm_scan_kernel<T, NL><<<grid, SC_THREADS, 0, s>>>(a);
+cudaError_t go(const ScanArgs& k, bool split, cudaStream_t s) {
+  constexpr int PB = SC_THREADS / NL * rows_of(NL);
+  const unsigned grid = (unsigned)((int64_t)k.tiles * k.a.H * ((k.a.P + PB - 1) / PB));
+  if (split) ssm_scan_kernel<T, NL, true><<<grid, SC_THREADS, 0, s>>>(k);
+  ssm_scan_kernel<T, NL, false><<<grid, SC_THREADS, 0, s>>>(k);
   return cudaGetLastError();
 }
+int lanes_of(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16; }
 template <class T>
-cudaError_t go_n(const SsmArgs& a, cudaStream_t s) {
-  return a.N <= 16    ? go<T, 1>(a, s)
-         : a.N <= 32  ? go<T, 2>(a, s)
-         : a.N <= 64  ? go<T, 4>(a, s)
-         : a.N <= 128 ? go<T, 8>(a, s)
-                      : go<T, 16>(a, s);
+cudaError_t go_n(const ScanArgs& k, bool split, cudaStream_t s) {
+  switch (lanes_of(k.a.N)) {
+    case 1: return go<T, 1>(k, split, s);
+    case 2: return go<T, 2>(k, split, s);
+    case 4: return go<T, 4>(k, split, s);
+    case 8: return go<T, 8>(k, split, s);
+    default: return go<T, 16>(k, split, s);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_ssm_scan(int dtype, const SsmArgs& a, cudaStream_t s) {
-  return dtype == T_F32    ? go_n<float>(a, s)
-         : dtype == T_BF16 ? go_n<__nv_bfloat16>(a, s)
-                           : go_n<__half>(a, s);
+SsmPlan ssm_scan_plan(int H, int P, int N, int rows, const int32_t* lens, int64_t T, int sms) {
+  SsmPlan p{};
+  const int nl = lanes_of(N), pb = SC_THREADS / nl * rows_of(nl);
+  p.units = H * ((P + pb - 1) / pb);
+  int64_t longest = 0;
+  for (int i = 0; i < rows; ++i) longest = (lens ? lens[i] : T) > longest ? (lens ? lens[i] : T) : longest;
+  p.seg_tokens = (int)(longest > 0 ? longest : 1);
+  // Segments for a call that would leave most SMs with less than one CTA: two
+  // launches instead of one, so at least four segments in the longest row, at
+  // most 16 (the last joins the states of all before it), of 32 tokens or more.
+  for (int64_t seg = (longest + 15) / 16 < 32 ? 32 : (longest + 15) / 16; 4 * seg <= longest; seg += (seg + 3) / 4) {
+    int64_t tiles = 0;
+    for (int i = 0; i < rows; ++i) {
+      const int64_t c = lens ? lens[i] : T;
+      tiles += c > seg ? (c + seg - 1) / seg : 1;
+    }
+    if (tiles * p.units <= 4 * (int64_t)sms) {
+      p.seg_tokens = (int)seg;
+      p.split = true;
+      break;
+    }
+  }
+  return p;
+}
+
+cudaError_t launch_ssm_scan(int dtype, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row, float* ws,
+                            cudaStream_t s) {
+  ScanArgs& k = t_scan;
+  k.a = a;
+  k.ws = ws;
+  k.seg_tokens = p.seg_tokens;
+  k.tiles = tiles;
+  k.per_row = per_row;
+  return dtype == T_F32    ? go_n<float>(k, p.split, s)
+         : dtype == T_BF16 ? go_n<__nv_bfloat16>(k, p.split, s)
+                           : go_n<__half>(k, p.split, s);
 }
 
 }  // namespace mx
