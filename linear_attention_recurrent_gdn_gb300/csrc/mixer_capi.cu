@@ -313,11 +313,11 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   if (need && (!q.workspace || q.workspace_bytes < need || !al(q.workspace, 16)))
     return fail(DL_EINVAL, "the workspace needs %lld bytes, 16-byte aligned (dl_ssm_workspace)", (long long)need);
   if (tiles * k.units > 0x7fffffff) return fail(DL_EINVAL, "too many tokens in one call");
-  if (!on_tensor_cores(q))
-    return done(fail, launch_ssm_scan((int)q.dtype, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
   const bool packed = q.tokens.packed != 0;
-  const bool vec = q.P % 8 == 0 && q.N % 8 == 0 && view_vec(q.x, DL_BF16, packed) && view_vec(q.B, DL_BF16, packed) &&
-                   view_vec(q.C, DL_BF16, packed) && view_vec(q.y, DL_BF16, packed);
+  const bool vec = q.P % 8 == 0 && q.N % 8 == 0 && view_vec(q.x, q.dtype, packed) && view_vec(q.B, q.dtype, packed) &&
+                   view_vec(q.C, q.dtype, packed) && view_vec(q.y, q.dtype, packed);
+  if (!on_tensor_cores(q))
+    return done(fail, launch_ssm_scan((int)q.dtype, vec, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
   int64_t tokens = q.tokens.T;
   if (packed) tokens = (int64_t)a.items[a.rows - 1].begin + row_len(a.items[a.rows - 1]);
   return done(fail, launch_ssm_tc(vec, tokens, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));

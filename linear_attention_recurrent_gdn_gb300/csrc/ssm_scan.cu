@@ -5,8 +5,8 @@
 // One CTA per (row, head, tile of state rows), and per segment of the row
 // where rows are few and long.  A thread keeps PR state rows times 16 state
 // columns in registers; NL threads share a state row and add up their parts of
-// y by shuffles.  Tokens come in chunks of TC, staged in shared memory in 32
-// bits.  Three operations per state element and token, two elements an
+// y by shuffles.  Tokens come in chunks of TC, fetched into registers a chunk
+// ahead (eight values a piece) and staged in shared memory in 32 bits.  Three operations per state element and token, two elements an
 // instruction (packed fp32), so the FP32 cores bound it.  Every size and type
 // runs here.
 //
@@ -25,7 +25,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 
 // State rows of a thread: as many as leave a CTA 64 rows or so, so that a value
 // of B or C that was read from shared memory serves several.
-__host__ __device__ constexpr int rows_of(int nl) { return nl >= 8 ? 4 : nl == 4 ? 2 : 1; }
+__host__ __device__ constexpr int rows_of(int nl) { return nl == 8 ? 4 : nl >= 4 ? 2 : 1; }
 
 struct ScanArgs {
   SsmArgs a;
@@ -35,13 +35,14 @@ struct ScanArgs {
 
 // Columns of the thread: 4 (ln + NL i) + e, i, e = 0..3, so that the NL threads
 // of a row read consecutive 16-byte vectors of a staged B or C.
-template <class T, int NL, bool STATE>
-__global__ void __launch_bounds__(SC_THREADS)
+template <class T, int NL, bool STATE, bool VEC>
+__global__ void __launch_bounds__(SC_THREADS, 4)
 ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
   constexpr int PR = rows_of(NL), NP = 16 * NL, PB = SC_THREADS / NL * PR;
   const SsmArgs& a = sa.a;
   __shared__ __align__(16) float sB[SC_TC][NP], sC[STATE ? 1 : SC_TC][NP];
-  __shared__ float sx[SC_TC][PB], sy[STATE ? 1 : SC_TC][PB], sdt[SC_TC], sdec[SC_TC];
+  __shared__ __align__(16) float sx[SC_TC][PB], sy[STATE ? 1 : SC_TC][PB];
+  __shared__ float sdt[SC_TC], sdec[SC_TC];
   const int pt = (a.P + PB - 1) / PB, ph = pt * a.H;
   const int tile = blockIdx.x / ph, rest = blockIdx.x - tile * ph, h = rest / pt, g = h / (a.H / a.G);
   const int row = find_row(a.items, a.rows, tile, sa.per_row);
@@ -98,24 +99,59 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
   const float Ah = a.A[h], Dh = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   float ltot = 0.f;
 
+  // The next chunk in registers: pieces of eight values of B, C and x, and dt.
+  constexpr int NB = SC_TC * NP / 8, NX = SC_TC * PB / 8;      // pieces of a chunk
+  constexpr int KB = (NB + SC_THREADS - 1) / SC_THREADS, KX = (NX + SC_THREADS - 1) / SC_THREADS;
+  Vec8<T> vb[KB], vc[STATE ? 1 : KB], vx[KX];
+  float vd = 0.f;
+  auto fetch = [&](int t0) {
+    const int nt = s1 - t0;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int i = threadIdx.x + k * SC_THREADS, t = i / (NP / 8), n = i % (NP / 8) * 8;
+      const int valid = i < NB && t < nt ? min(8, a.N - n) : 0;
+      vb[k] = load8<T, VEC>(static_cast<const T*>(a.B.p) + at(a.B, t0 + t) + (int64_t)g * a.N + n, valid);
+      if (!STATE) vc[k] = load8<T, VEC>(static_cast<const T*>(a.C.p) + at(a.C, t0 + t) + (int64_t)g * a.N + n, valid);
+    }
+#pragma unroll
+    for (int k = 0; k < KX; ++k) {
+      const int i = threadIdx.x + k * SC_THREADS, t = i / (PB / 8), p = p0 + i % (PB / 8) * 8;
+      vx[k] = load8<T, VEC>(static_cast<const T*>(a.x.p) + at(a.x, t0 + t) + (int64_t)h * a.P + p,
+                            i < NX && t < nt ? min(8, a.P - p) : 0);
+    }
+    if (threadIdx.x < SC_TC && (int)threadIdx.x < nt) {
+      const int64_t o = at(a.dt, t0 + threadIdx.x) + h;
+      vd = a.dt_f32 ? static_cast<const float*>(a.dt.p)[o] : to_f(static_cast<const T*>(a.dt.p)[o]);
+    }
+  };
+  auto put8 = [&](float* to, const Vec8<T>& v) {
+    float f[8];
+    unpack8<T>(v, f);
+    *reinterpret_cast<float4*>(to) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  };
+  if (s0 < s1) fetch(s0);
   for (int t0 = s0; t0 < s1; t0 += SC_TC) {
     const int nt = min(SC_TC, s1 - t0);
-    for (int i = threadIdx.x; i < nt * NP; i += SC_THREADS) {
-      const int t = i / NP, n = i - t * NP;
-      sB[t][n] = n < a.N ? to_f(static_cast<const T*>(a.B.p)[at(a.B, t0 + t) + (int64_t)g * a.N + n]) : 0.f;
-      if (!STATE) sC[t][n] = n < a.N ? to_f(static_cast<const T*>(a.C.p)[at(a.C, t0 + t) + (int64_t)g * a.N + n]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+      const int i = threadIdx.x + k * SC_THREADS;
+      if (i < NB) {
+        put8(&sB[0][0] + 8 * i, vb[k]);
+        if (!STATE) put8(&sC[0][0] + 8 * i, vc[k]);
+      }
     }
-    for (int i = threadIdx.x; i < nt * PB; i += SC_THREADS) {
-      const int t = i / PB, p = p0 + i - t * PB;
-      sx[t][p - p0] = p < a.P ? to_f(static_cast<const T*>(a.x.p)[at(a.x, t0 + t) + (int64_t)h * a.P + p]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < KX; ++k) {
+      const int i = threadIdx.x + k * SC_THREADS;
+      if (i < NX) put8(&sx[0][0] + 8 * i, vx[k]);
     }
-    if (threadIdx.x < nt) {
-      const int64_t o = at(a.dt, t0 + threadIdx.x) + h;
-      float d = (a.dt_f32 ? static_cast<const float*>(a.dt.p)[o] : to_f(static_cast<const T*>(a.dt.p)[o])) + bias;
-      d = a.softplus ? softplus_f(d) : d;
+    if (threadIdx.x < SC_TC) {
+      const float d = a.softplus ? softplus_f(vd + bias) : vd + bias;
       sdt[threadIdx.x] = d;
       sdec[threadIdx.x] = expf(d * Ah);
     }
+    if (t0 + SC_TC < s1) fetch(t0 + SC_TC);
     __syncthreads();
     for (int t = 0; t < nt; ++t) {
       const float dec = sdec[t], dt = sdt[t];
@@ -159,10 +195,15 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
     }
     __syncthreads();
     if (!STATE)
-      for (int i = threadIdx.x; i < nt * PB; i += SC_THREADS) {
-        const int t = i / PB, p = p0 + i - t * PB;
-        if (p < a.P)
-          static_cast<T*>(const_cast<void*>(a.y.p))[at(a.y, t0 + t) + (int64_t)h * a.P + p] = from_f<T>(sy[t][p - p0]);
+#pragma unroll
+      for (int k = 0; k < KX; ++k) {
+        const int i = threadIdx.x + k * SC_THREADS, t = i / (PB / 8), p = p0 + i % (PB / 8) * 8;
+        if (i >= NX || t >= nt) continue;
+        float f[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = (&sy[0][0])[8 * i + e];
+        store8<T, VEC>(static_cast<T*>(const_cast<void*>(a.y.p)) + at(a.y, t0 + t) + (int64_t)h * a.P + p, pack8<T>(f),
+                       min(8, a.P - p));
       }
   }
   float* to = STATE ? sa.ws + (int64_t)(tile + 1) * per_tile : seg == nseg - 1 ? pool : nullptr;
@@ -183,23 +224,27 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
 
 thread_local ScanArgs t_scan;
 
-template <class T, int NL>
-cudaError_t go(const ScanArgs& k, bool split, cudaStream_t s) {
+template <class T, int NL, bool VEC>
+cudaError_t go_vec(const ScanArgs& k, bool split, cudaStream_t s) {
   constexpr int PB = SC_THREADS / NL * rows_of(NL);
   const unsigned grid = (unsigned)((int64_t)k.tiles * k.a.H * ((k.a.P + PB - 1) / PB));
-  if (split) ssm_scan_kernel<T, NL, true><<<grid, SC_THREADS, 0, s>>>(k);
-  ssm_scan_kernel<T, NL, false><<<grid, SC_THREADS, 0, s>>>(k);
+  if (split) ssm_scan_kernel<T, NL, true, VEC><<<grid, SC_THREADS, 0, s>>>(k);
+  ssm_scan_kernel<T, NL, false, VEC><<<grid, SC_THREADS, 0, s>>>(k);
   return cudaGetLastError();
+}
+template <class T, int NL>
+cudaError_t go(const ScanArgs& k, bool vec, bool split, cudaStream_t s) {
+  return vec ? go_vec<T, NL, true>(k, split, s) : go_vec<T, NL, false>(k, split, s);
 }
 int lanes_of(int N) { return N <= 16 ? 1 : N <= 32 ? 2 : N <= 64 ? 4 : N <= 128 ? 8 : 16; }
 template <class T>
-cudaError_t go_n(const ScanArgs& k, bool split, cudaStream_t s) {
+cudaError_t go_n(const ScanArgs& k, bool vec, bool split, cudaStream_t s) {
   switch (lanes_of(k.a.N)) {
-    case 1: return go<T, 1>(k, split, s);
-    case 2: return go<T, 2>(k, split, s);
-    case 4: return go<T, 4>(k, split, s);
-    case 8: return go<T, 8>(k, split, s);
-    default: return go<T, 16>(k, split, s);
+    case 1: return go<T, 1>(k, vec, split, s);
+    case 2: return go<T, 2>(k, vec, split, s);
+    case 4: return go<T, 4>(k, vec, split, s);
+    case 8: return go<T, 8>(k, vec, split, s);
+    default: return go<T, 16>(k, vec, split, s);
   }
 }
 
@@ -230,7 +275,7 @@ SsmPlan ssm_scan_plan(int H, int P, int N, int rows, const int32_t* lens, int64_
   return p;
 }
 
-cudaError_t launch_ssm_scan(int dtype, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row, float* ws,
+cudaError_t launch_ssm_scan(int dtype, bool vec, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row, float* ws,
                             cudaStream_t s) {
   ScanArgs& k = t_scan;
   k.a = a;
@@ -238,9 +283,9 @@ cudaError_t launch_ssm_scan(int dtype, const SsmArgs& a, const SsmPlan& p, int t
   k.seg_tokens = p.seg_tokens;
   k.tiles = tiles;
   k.per_row = per_row;
-  return dtype == T_F32    ? go_n<float>(k, p.split, s)
-         : dtype == T_BF16 ? go_n<__nv_bfloat16>(k, p.split, s)
-                           : go_n<__half>(k, p.split, s);
+  return dtype == T_F32    ? go_n<float>(k, vec, p.split, s)
+         : dtype == T_BF16 ? go_n<__nv_bfloat16>(k, vec, p.split, s)
+                           : go_n<__half>(k, vec, p.split, s);
 }
 
 }  // namespace mx
