@@ -124,12 +124,17 @@ __device__ __forceinline__ void weights8(const void* base, int64_t i, int valid,
   }
 }
 
-// 1 / (1 + e^-z) and z / (1 + e^-z).  For a 16-bit type e^x and the quotient
-// are the fast forms, within about 2^-20 relative where the value is not tiny,
-// far below the type's own rounding; for fp32 they are the accurate ones.
+// 1 / x within one step of the last place.
+__device__ __forceinline__ float rcp_f(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 1 / (1 + e^-z) and z / (1 + e^-z).  For a 16-bit type e^x is the fast form,
+// within about 2^-20 relative where the value is not tiny, far below the
+// type's own rounding; for fp32 the accurate one.
 template <class T> __device__ __forceinline__ float sigmoid_f(float z) {
-  if constexpr (sizeof(T) == 4) return 1.f / (1.f + expf(-z));
-  return __fdividef(1.f, 1.f + __expf(-z));
+  return rcp_f(1.f + (sizeof(T) == 4 ? expf(-z) : __expf(-z)));
 }
 template <class T> __device__ __forceinline__ float act_f(float z, int act) {
   return act == ACT_NONE ? z : act == ACT_SILU ? z * sigmoid_f<T>(z) : sigmoid_f<T>(z);
