@@ -88,37 +88,6 @@ struct Eight {
   }
 };
 
-__device__ __forceinline__ float ex2_f(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// silu of a pair: z / (1 + e^-z).  16-bit types: one reciprocal for both, 1 /
-// (p q); the exponentials are held at 2^62, so that the product is finite and
-// a NaN stays its own channel's, and z at -43 (a value of -9e-18 or less in
-// size either way).
-template <class T>
-__device__ __forceinline__ f2 silu2(f2 z) {
-  float a, b;
-  if constexpr (sizeof(T) == 4) {
-    un2(z, a, b);
-    return mk2(a * rcp_f(1.f + expf(-a)), b * rcp_f(1.f + expf(-b)));
-  } else {
-    un2(mul2(z, mk2(-1.4426950408889634f, -1.4426950408889634f)), a, b);
-    float p, q;
-    un2(add2(mk2(fminf(ex2_f(a), 0x1p62f), fminf(ex2_f(b), 0x1p62f)), mk2(1.f, 1.f)), p, q);
-    const float r = rcp_f(p * q);
-    un2(z, a, b);
-    return mul2(mk2(max_nan(a, -43.f), max_nan(b, -43.f)), mul2(mk2(q, p), mk2(r, r)));
-  }
-}
-
 // A thread's channels, weights and outputs.
 template <class T, int W, bool VEC>
 struct Lane {
@@ -189,7 +158,7 @@ struct Lane {
 #pragma unroll
       for (int j = 0; j + 2 < W; ++j) win[j][k] = win[j + 1][k];
       win[W - 2][k] = x;
-      z[k] = ACT ? silu2<T>(s) : s;
+      z[k] = ACT ? act2<T, true>(s) : s;
     }
     if constexpr (NORM) {
       if constexpr (VEC) {

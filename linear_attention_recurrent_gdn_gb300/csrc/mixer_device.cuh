@@ -114,6 +114,13 @@ template <class T> __device__ __forceinline__ Vec8<T> pack8(const float (&f)[8])
   }
   return v;
 }
+// Eight values as four pairs.
+template <class T> __device__ __forceinline__ void pairs8(const Vec8<T>& v, unsigned long long (&f)[4]) {
+  float t[8];
+  unpack8<T>(v, t);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) asm("mov.b64 %0, {%1, %2};" : "=l"(f[k]) : "f"(t[2 * k]), "f"(t[2 * k + 1]));
+}
 // Eight weights that are fp32 or of the activations' type.
 template <class T, bool VEC>
 __device__ __forceinline__ void weights8(const void* base, int64_t i, int valid, int f32, float (&f)[8]) {
@@ -129,15 +136,6 @@ __device__ __forceinline__ float rcp_f(float x) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
-}
-// 1 / (1 + e^-z) and z / (1 + e^-z).  For a 16-bit type e^x is the fast form,
-// within about 2^-20 relative where the value is not tiny, far below the
-// type's own rounding; for fp32 the accurate one.
-template <class T> __device__ __forceinline__ float sigmoid_f(float z) {
-  return rcp_f(1.f + (sizeof(T) == 4 ? expf(-z) : __expf(-z)));
-}
-template <class T> __device__ __forceinline__ float act_f(float z, int act) {
-  return act == ACT_NONE ? z : act == ACT_SILU ? z * sigmoid_f<T>(z) : sigmoid_f<T>(z);
 }
 // Packed fp32 arithmetic: two values an instruction.
 using f2 = unsigned long long;     // two fp32 values
@@ -162,6 +160,42 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
   f2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+__device__ __forceinline__ float ex2_f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// silu (z / (1 + e^-z)) or sigmoid (1 / (1 + e^-z)) of a pair.  16-bit types:
+// the fast e^x, within about 2^-20 relative, far below the type's own
+// rounding, and one reciprocal for both, 1 / (p q); the exponentials are held
+// at 2^62, so that the product is finite and a NaN stays its own value's, and
+// silu's z at -43 (its value is -9e-18 or less in size either way).
+template <class T, bool SILU>
+__device__ __forceinline__ f2 act2(f2 z) {
+  float a, b;
+  if constexpr (sizeof(T) == 4) {
+    un2(z, a, b);
+    const float p = rcp_f(1.f + expf(-a)), q = rcp_f(1.f + expf(-b));
+    return SILU ? mk2(a * p, b * q) : mk2(p, q);
+  } else {
+    un2(mul2(z, mk2(-1.4426950408889634f, -1.4426950408889634f)), a, b);
+    float p, q;
+    un2(add2(mk2(fminf(ex2_f(a), 0x1p62f), fminf(ex2_f(b), 0x1p62f)), mk2(1.f, 1.f)), p, q);
+    const float r = rcp_f(p * q);
+    const f2 s = mul2(mk2(q, p), mk2(r, r));
+    un2(z, a, b);
+    if (SILU) return mul2(mk2(max_nan(a, -43.f), max_nan(b, -43.f)), s);
+    un2(s, p, q);
+    return mk2(a != a ? a : p, b != b ? b : q);    // a NaN stays one
+  }
 }
 
 // log(1 + e^x) without overflow or loss for either sign.

@@ -58,69 +58,17 @@ def _signatures(lib):
 
 
 _lib = _signatures(_dl.library())
+_raw_stream = torch._C._cuda_getCurrentRawStream     # the current stream's handle, without an object around it
+_F32 = torch.float32
 
 
-def _call(fn, args, device):
+def _call(fn, args, dev):
     err = getattr(_local, "err", None)
     if err is None:
         err = _local.err = ctypes.create_string_buffer(_ERR)
-    rc = fn(args, torch.cuda.current_stream(device).cuda_stream, err, _ERR)
+    rc = fn(args, _raw_stream(dev), err, _ERR)
     if rc:
         raise _dl.DeltaLogError(rc, err.value.decode())
-
-
-def _cuda(name, t, dtype, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.device != device:
-        raise ValueError("%s is on %s, x on %s" % (name, t.device, device))
-    if t.dtype != dtype:
-        raise ValueError("%s: expected %s, got %s" % (name, dtype, t.dtype))
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s requires a gradient: these operators have no backward" % name)
-
-
-def _x(t):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("x must be a CUDA tensor")
-    if t.dtype not in _DTYPE:
-        raise ValueError("x: %s is not supported" % t.dtype)
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("x requires a gradient: these operators have no backward")
-    return t.device
-
-
-def _dense(name, t, inner):
-    """The last `inner` dimensions are contiguous."""
-    want = 1
-    for size, stride in zip(t.shape[:-inner - 1:-1], t.stride()[:-inner - 1:-1]):
-        if size != 1 and stride != want:
-            raise ValueError("%s: the last %d dimension(s) must be contiguous" % (name, inner))
-        want *= size
-
-
-def _vector(name, t, shape, dtypes, device):
-    """A dense parameter; returns its address."""
-    if t is None:
-        return 0
-    _cuda(name, t, t.dtype if t.dtype in dtypes else dtypes[0], device)
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s: expected contiguous %s, got %s" % (name, shape, tuple(t.shape)))
-    return t.data_ptr()
-
-
-def _strides(t, lead):
-    """(data, stride between tokens, stride between rows)"""
-    if lead == 2:
-        return t.data_ptr(), t.stride(0), t.stride(1)
-    return t.data_ptr(), t.stride(0), 0
-
-
-def _host(a, dtype, n, name):
-    a = np.ascontiguousarray(a, dtype=dtype)
-    if a.shape != (n,):
-        raise ValueError("%s: expected %d entries, got %s" % (name, n, a.shape))
-    return a
 
 
 def sync(device=None):
@@ -131,91 +79,144 @@ def sync(device=None):
         raise _dl.DeltaLogError(rc, err.value.decode())
 
 
-class _Rows:
-    """The dl_tokens of a call: checks the lists against the tensors' layout."""
-    __slots__ = ("lead", "keep", "fields")
+# The checks below are written for few Python steps: in a decode loop they are
+# the cost of a call.
 
-    def __init__(self, lead_shape, step, slots, lengths, fresh, state, device, state_shape, state_dtype):
-        self.keep = []
-        packed = 0
-        if step:
-            n, T, self.lead = lead_shape[0], 1, 1
-        elif len(lead_shape) == 2:
-            (T, n), self.lead = lead_shape, 2
-        else:
-            if lengths is None:
-                raise ValueError("packed tokens need lengths")
-            packed, self.lead = 1, 1
-            lengths = np.ascontiguousarray(lengths, dtype=np.int32).reshape(-1)
-            n, T = lengths.size, int(lengths.max()) if lengths.size else 0
-            if int(lengths.sum(dtype=np.int64)) != lead_shape[0]:
-                raise ValueError("lengths add up to %d, x has %d tokens" % (int(lengths.sum(dtype=np.int64)), lead_shape[0]))
-        num_slots = 0
-        if state is not None:
-            _cuda("state", state, state_dtype, device)
-            if tuple(state.shape[1:]) != state_shape or not state.is_contiguous():
-                raise ValueError("state: expected contiguous [slots, %s], got %s"
-                                 % (", ".join(map(str, state_shape)), tuple(state.shape)))
-            if slots is None:
-                raise ValueError("a state pool needs slots")
-            num_slots = state.shape[0]
-            slots = _host(slots, np.int32, n, "slots")
-        elif slots is not None:
-            raise ValueError("slots need a state pool")
-        ptrs = [0, 0, 0]
-        if slots is not None:
-            ptrs[0] = slots.__array_interface__["data"][0]
+def _x(t):
+    """The first tensor of a call; returns its device's number."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("x must be a CUDA tensor")
+    if t.dtype not in _DTYPE:
+        raise ValueError("x: %s is not supported" % t.dtype)
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("x requires a gradient: these operators have no backward")
+    return t.get_device()
+
+
+def _cuda(name, t, dtype, dev):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError("%s: expected %s on device %d, got %s on %s" % (name, dtype, dev, t.dtype, t.device))
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires a gradient: these operators have no backward" % name)
+
+
+def _param(name, t, shape, dtype, dev):
+    """A contiguous parameter; returns its address (0 for None)."""
+    if t is None:
+        return 0
+    _cuda(name, t, dtype, dev)
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s: expected contiguous %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _dense(name, t, inner, stride):
+    """The last `inner` dimensions are contiguous (dimensions of one entry have no stride)."""
+    want = 1
+    shape = t.shape
+    for k in range(-1, -1 - inner, -1):
+        if stride[k] != want and shape[k] != 1:
+            raise ValueError("%s: the last %d dimension(s) must be contiguous" % (name, inner))
+        want *= shape[k]
+
+
+def _tokens(name, t, shape, dtype, dev, inner, lead):
+    """A per-token tensor: checks it and returns (data, stride between tokens, between rows)."""
+    _cuda(name, t, dtype, dev)
+    if t.shape != shape:
+        raise ValueError("%s: expected %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    stride = t.stride()
+    if not t.is_contiguous():
+        _dense(name, t, inner, stride)
+    if lead == 0:                          # one token a row
+        return t.data_ptr(), 0, stride[0]
+    if lead == 1:                          # packed
+        return t.data_ptr(), stride[0], 0
+    return t.data_ptr(), stride[0], stride[1]
+
+
+def _host(a, dtype, n, name):
+    """A host list as an array and its address."""
+    if type(a) is not np.ndarray or a.dtype != dtype or not a.flags.c_contiguous:
+        a = np.ascontiguousarray(a, dtype=dtype)
+    if a.shape != (n,):
+        raise ValueError("%s: expected %d entries, got %s" % (name, n, a.shape))
+    return a, a.__array_interface__["data"][0]
+
+
+def _rows(lead_shape, step, slots, lengths, fresh, state, dev, state_shape, state_dtype):
+    """The dl_tokens of a call, checked against the tensors' layout.  Returns
+    its fields, the state's address, the layout (0: one token a row, 1: packed,
+    2: token-major) and the arrays to keep until the call has read them."""
+    packed, plen, pfresh = 0, 0, 0
+    if step:
+        n, T, lead = lead_shape[0], 1, 0
+    elif len(lead_shape) == 2:
+        (T, n), lead = lead_shape, 2
         if lengths is not None:
-            lengths = _host(lengths, np.int32, n, "lengths")
-            ptrs[1] = lengths.__array_interface__["data"][0]
-        if fresh is True or fresh is False:
-            fresh_all = int(fresh)
-        else:
-            fresh_all = 0
-            fresh = _host(fresh, np.uint8, n, "fresh")
-            ptrs[2] = fresh.__array_interface__["data"][0]
-        self.keep = (slots, lengths, fresh)       # alive until the call has read them
-        self.fields = (ptrs[0], ptrs[1], ptrs[2], fresh_all, n, T, packed, num_slots)
-
-    def of(self, t, step):
-        """A tensor's (data, stride_t, stride_n)."""
-        if step:
-            return t.data_ptr(), 0, t.stride(0)
-        return _strides(t, self.lead)
+            lengths, plen = _host(lengths, np.int32, n, "lengths")
+    else:
+        if lengths is None:
+            raise ValueError("packed tokens need lengths")
+        packed, lead, n = 1, 1, len(lengths)
+        lengths, plen = _host(lengths, np.int32, n, "lengths")
+        T = int(lengths.max()) if n else 0
+        if int(lengths.sum(dtype=np.int64)) != lead_shape[0]:
+            raise ValueError("lengths add up to %d, x has %d tokens" % (lengths.sum(dtype=np.int64), lead_shape[0]))
+    if state is None:
+        if slots is not None:
+            raise ValueError("slots need a state pool")
+        pool = pslots = num_slots = 0
+    else:
+        num_slots = state.shape[0] if isinstance(state, torch.Tensor) and state.dim() else 0
+        pool = _param("state", state, (num_slots,) + state_shape, state_dtype, dev)
+        if slots is None:
+            raise ValueError("a state pool needs slots")
+        slots, pslots = _host(slots, np.int32, n, "slots")
+    if fresh is not True and fresh is not False:
+        fresh, pfresh = _host(fresh, np.uint8, n, "fresh")
+    return (pslots, plen, pfresh, fresh is True, n, T, packed, num_slots), pool, lead, (slots, lengths, fresh)
 
 
 def _conv(x, weight, bias, slots, state, lengths, fresh, activation, l2_channels, head_dim, eps, split, out, step):
-    dev = _x(x)
-    if x.dim() not in ((2,) if step else (2, 3)):
-        raise ValueError("x: expected %s, got %s" % ("[n, C]" if step else "[T, n, C] or [total, C]", tuple(x.shape)))
-    _dense("x", x, 1)
-    dt, lead = x.dtype, tuple(x.shape[:-1])
-    C, W = x.shape[-1], weight.shape[-1]
-    rows = _Rows(lead, step, slots, lengths, fresh, state, dev, (W - 1, C), dt)
-    wp = _vector("weight", weight, (C, W), (dt, torch.float32), dev)
-    bp = _vector("bias", bias, (C,), (weight.dtype,), dev)
+    dev, dt, shape = _x(x), x.dtype, x.shape
+    if len(shape) != 2 and (step or len(shape) != 3):
+        raise ValueError("x: expected %s, got %s" % ("[n, C]" if step else "[T, n, C] or [total, C]", tuple(shape)))
+    lead_shape, C = shape[:-1], shape[-1]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 2:
+        raise TypeError("weight must be a CUDA tensor [C, W]")
+    W, wt = weight.shape[1], _F32 if weight.dtype is _F32 else dt
+    wp = _param("weight", weight, (C, W), wt, dev)
+    bp = _param("bias", bias, (C,), wt, dev)
+    fields, pool, lead, keep = _rows(lead_shape, step, slots, lengths, fresh, state, dev, (W - 1, C), dt)
+    xv = _tokens("x", x, shape, dt, dev, 1, lead)
     parts = (C,) if split is None else tuple(split)
+    if not 1 <= len(parts) <= 4:
+        raise ValueError("split: 1 to 4 ranges")
+    views = []
     if out is None:
-        outs = [torch.empty(lead + (c,), dtype=dt, device=dev) for c in parts]
+        outs = []
+        for c in parts:
+            t = x.new_empty(lead_shape + (c,))
+            outs.append(t)
+            views += (t.data_ptr(), 0, c) if lead == 0 else (t.data_ptr(), c, 0) if lead == 1 else \
+                (t.data_ptr(), c * shape[1], c)
     else:
         outs = [out] if split is None else list(out)
         if len(outs) != len(parts):
             raise ValueError("out: expected %d tensors" % len(parts))
         for t, c in zip(outs, parts):
-            _cuda("out", t, dt, dev)
-            if tuple(t.shape) != lead + (c,):
-                raise ValueError("out: expected %s, got %s" % (lead + (c,), tuple(t.shape)))
-            _dense("out", t, 1)
-    if not 1 <= len(parts) <= 4:
-        raise ValueError("split: 1 to 4 ranges")
-    views, pad = [], 4 - len(parts)
-    for t in outs:
-        views += rows.of(t, step)
-    _call(_lib.dl_conv, _CONV.pack(*rows.fields, _DTYPE[dt], int(weight.dtype == torch.float32), C, W,
-                                   _ACT[activation], l2_channels, head_dim, len(parts), eps, *rows.of(x, step),
-                                   wp, bp, 0 if state is None else state.data_ptr(),
-                                   *views, *([0] * (3 * pad)), *parts, *([0] * pad)), dev)
+            views += _tokens("out", t, lead_shape + (c,), dt, dev, 1, lead)
+    pad = 4 - len(parts)
+    _call(_lib.dl_conv, _CONV.pack(*fields, _DTYPE[dt], wt is _F32, C, W, _ACT[activation], l2_channels, head_dim,
+                                   len(parts), eps, *xv, wp, bp, pool, *views, *_ZEROS[:3 * pad], *parts,
+                                   *_ZEROS[:pad]), dev)
     return outs[0] if split is None else tuple(outs)
+
+
+_ZEROS = (0,) * 12
 
 
 def conv(x, weight, bias=None, *, slots=None, state=None, lengths=None, fresh=False, activation="silu",
@@ -240,40 +241,31 @@ def conv_step(x, weight, bias=None, *, slots, state, activation="silu", l2_chann
 
 
 def _ssm(fn, x, dt, A, B, C, D, dt_bias, dt_softplus, slots, state, lengths, fresh, out, step):
-    dev = _x(x)
-    lead_dims = x.dim() - 2
-    if lead_dims not in ((1,) if step else (1, 2)):
+    dev, xt, shape = _x(x), x.dtype, x.shape
+    if len(shape) != 3 and (step or len(shape) != 4):
         raise ValueError("x: expected %s, got %s"
-                         % ("[n, H, P]" if step else "[T, n, H, P] or [total, H, P]", tuple(x.shape)))
-    lead, (H, P) = tuple(x.shape[:-2]), x.shape[-2:]
+                         % ("[n, H, P]" if step else "[T, n, H, P] or [total, H, P]", tuple(shape)))
+    if A is None or not isinstance(B, torch.Tensor) or B.dim() != len(shape) or not isinstance(dt, torch.Tensor):
+        raise TypeError("dt, A and B must be CUDA tensors, B with x's leading dimensions")
+    lead_shape, H, P = shape[:-2], shape[-2], shape[-1]
     G, N = B.shape[-2:]
-    for name, t, shape in (("dt", dt, (H,)), ("B", B, (G, N)), ("C", C, (G, N))):
-        _cuda(name, t, torch.float32 if name == "dt" and t.dtype == torch.float32 else x.dtype, dev)
-        if tuple(t.shape) != lead + shape:
-            raise ValueError("%s: expected %s, got %s" % (name, lead + shape, tuple(t.shape)))
-        _dense(name, t, len(shape))
-    _dense("x", x, 2)
-    rows = _Rows(lead, step, slots, lengths, fresh, state, dev, (H, P, N), torch.float32)
-    f32 = (torch.float32,)
+    fields, pool, lead, keep = _rows(lead_shape, step, slots, lengths, fresh, state, dev, (H, P, N), _F32)
+    maps, dtt = lead_shape + (G, N), _F32 if dt.dtype is _F32 else xt
     if out is None:
-        out = torch.empty(lead + (H, P), dtype=x.dtype, device=dev)
-    else:
-        _cuda("out", out, x.dtype, dev)
-        if out.shape != x.shape:
-            raise ValueError("out: expected %s, got %s" % (tuple(x.shape), tuple(out.shape)))
-        _dense("out", out, 2)
-    head = rows.fields + (_DTYPE[x.dtype], int(dt.dtype == torch.float32), int(dt_softplus), H, G, P, N,
-                          *rows.of(x, step), *rows.of(dt, step), *rows.of(B, step), *rows.of(C, step),
-                          *rows.of(out, step), _vector("A", A, (H,), f32, dev), _vector("D", D, (H,), f32, dev),
-                          _vector("dt_bias", dt_bias, (H,), f32, dev), 0 if state is None else state.data_ptr())
-    if A is None:
-        raise TypeError("A must be a CUDA tensor")
-    workspace, size = None, 0
+        out = x.new_empty(shape)
+    head = fields + (_DTYPE[xt], dtt is _F32, bool(dt_softplus), H, G, P, N) \
+        + _tokens("x", x, shape, xt, dev, 2, lead) + _tokens("dt", dt, lead_shape + (H,), dtt, dev, 1, lead) \
+        + _tokens("B", B, maps, xt, dev, 2, lead) + _tokens("C", C, maps, xt, dev, 2, lead) \
+        + _tokens("out", out, shape, xt, dev, 2, lead) \
+        + (_param("A", A, (H,), _F32, dev), _param("D", D, (H,), _F32, dev),
+           _param("dt_bias", dt_bias, (H,), _F32, dev), pool)
+    args = _SSM.pack(*head, 0, 0)
     if not step:
-        size = _lib.dl_ssm_workspace(_SSM.pack(*head, 0, 0))
+        size = _lib.dl_ssm_workspace(args)
         if size > 0:
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    _call(fn, _SSM.pack(*head, 0 if workspace is None else workspace.data_ptr(), max(size, 0)), dev)
+            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+            args = _SSM.pack(*head, workspace.data_ptr(), size)
+    _call(fn, args, dev)
     return out
 
 
@@ -293,12 +285,15 @@ def ssm_step(x, dt, A, B, C, D=None, *, dt_bias=None, dt_softplus=True, slots, s
     return _ssm(_lib.dl_ssm_step, x, dt, A, B, C, D, dt_bias, dt_softplus, slots, state, None, False, out, True)
 
 
-def _rows_of(name, t, shape, dtype, dev, inner):
+def _matrix(name, t, shape, dtype, dev, inner):
+    """A tensor of rows: checks it and returns its address and the stride between rows."""
     _cuda(name, t, dtype, dev)
-    if tuple(t.shape) != shape:
-        raise ValueError("%s: expected %s, got %s" % (name, shape, tuple(t.shape)))
-    _dense(name, t, inner)
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError("%s: expected %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    stride = t.stride()
+    if not t.is_contiguous():
+        _dense(name, t, inner, stride)
+    return t.data_ptr(), stride[0]
 
 
 def gated_norm(x, weight, gate=None, *, bias=None, kind="rms", activation="silu", gate_first=False, eps=1e-5,
@@ -308,22 +303,22 @@ def gated_norm(x, weight, gate=None, *, bias=None, kind="rms", activation="silu"
 
     weight and bias are [d] or [H, d], of x's type or fp32; the gate has x's
     shape and type.  ``out`` may be x or the gate."""
-    dev = _x(x)
-    if x.dim() != 3:
-        raise ValueError("x: expected [rows, H, d], got %s" % (tuple(x.shape),))
-    shape, dt = tuple(x.shape), x.dtype
-    _dense("x", x, 2)
-    wshape = shape[1:] if weight.dim() == 2 else shape[2:]
-    wp = _vector("weight", weight, wshape, (dt, torch.float32), dev)
-    bp = _vector("bias", bias, wshape, (weight.dtype,), dev)
-    gp = 0 if gate is None else _rows_of("gate", gate, shape, dt, dev, 2)
+    dev, dt, shape = _x(x), x.dtype, x.shape
+    if len(shape) != 3:
+        raise ValueError("x: expected [rows, H, d], got %s" % (tuple(shape),))
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a CUDA tensor")
+    heads, wt = weight.dim() == 2, _F32 if weight.dtype is _F32 else dt
+    wshape = shape[1:] if heads else shape[2:]
+    wp = _param("weight", weight, wshape, wt, dev)
+    bp = _param("bias", bias, wshape, wt, dev)
+    xp, xs = _matrix("x", x, shape, dt, dev, 2)
+    gp, gs = (0, 0) if gate is None else _matrix("gate", gate, shape, dt, dev, 2)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
-    op = _rows_of("out", out, shape, dt, dev, 2)
-    _call(_lib.dl_gated_norm, _GATED.pack(_DTYPE[dt], int(weight.dtype == torch.float32), int(weight.dim() == 2),
-                                          *shape, _KIND[kind], _ACT[activation], int(gate_first), eps, x.data_ptr(),
-                                          gp, wp, bp, op, x.stride(0), 0 if gate is None else gate.stride(0),
-                                          out.stride(0)), dev)
+        out = x.new_empty(shape)
+    op, os = _matrix("out", out, shape, dt, dev, 2)
+    _call(_lib.dl_gated_norm, _GATED.pack(_DTYPE[dt], wt is _F32, heads, *shape, _KIND[kind], _ACT[activation],
+                                          bool(gate_first), eps, xp, gp, wp, bp, op, xs, gs, os), dev)
     return out
 
 
@@ -336,26 +331,26 @@ def add_norm(x, residual, weight, *, bias=None, scale=None, alpha=1.0, post_weig
     is the stream h continues, in its type.  weight, bias, scale and
     post_weight are [D], all of x's type or all fp32.  ``out`` may be x,
     ``out_residual`` the residual."""
-    dev = _x(x)
-    if x.dim() != 2:
-        raise ValueError("x: expected [rows, D], got %s" % (tuple(x.shape),))
-    shape, dt = tuple(x.shape), x.dtype
-    _dense("x", x, 1)
-    wp = _vector("weight", weight, shape[1:], (dt, torch.float32), dev)
-    more = [_vector(name, t, shape[1:], (weight.dtype,), dev)
-            for name, t in (("bias", bias), ("scale", scale), ("post_weight", post_weight))]
-    rt = dt if residual is None and out_residual is None else (out_residual if residual is None else residual).dtype
-    if rt not in (dt, torch.float32):
-        raise ValueError("residual: expected %s or fp32, got %s" % (dt, rt))
-    rp = 0 if residual is None else _rows_of("residual", residual, shape, rt, dev, 1)
+    dev, dt, shape = _x(x), x.dtype, x.shape
+    if len(shape) != 2:
+        raise ValueError("x: expected [rows, D], got %s" % (tuple(shape),))
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError("weight must be a CUDA tensor")
+    wt, wshape = _F32 if weight.dtype is _F32 else dt, shape[1:]
+    wp = _param("weight", weight, wshape, wt, dev)
+    bp = _param("bias", bias, wshape, wt, dev)
+    sp = _param("scale", scale, wshape, wt, dev)
+    pp = _param("post_weight", post_weight, wshape, wt, dev)
+    stream = out_residual if residual is None else residual
+    rt = _F32 if isinstance(stream, torch.Tensor) and stream.dtype is _F32 else dt
+    xp, xs = _matrix("x", x, shape, dt, dev, 1)
+    rp, rs = (0, 0) if residual is None else _matrix("residual", residual, shape, rt, dev, 1)
     if out is None:
-        out = torch.empty(shape, dtype=dt, device=dev)
+        out = x.new_empty(shape)
     if out_residual is None:
-        out_residual = torch.empty(shape, dtype=rt, device=dev)
-    op = _rows_of("out", out, shape, dt, dev, 1)
-    hp = _rows_of("out_residual", out_residual, shape, rt, dev, 1)
-    _call(_lib.dl_add_norm, _ADD.pack(_DTYPE[dt], int(rt == torch.float32), int(weight.dtype == torch.float32),
-                                      *shape, _KIND[kind], eps, alpha, x.data_ptr(), rp, wp, *more, op, hp,
-                                      x.stride(0), 0 if residual is None else residual.stride(0), out.stride(0),
-                                      out_residual.stride(0)), dev)
+        out_residual = x.new_empty(shape, dtype=rt)
+    op, os = _matrix("out", out, shape, dt, dev, 1)
+    hp, hs = _matrix("out_residual", out_residual, shape, rt, dev, 1)
+    _call(_lib.dl_add_norm, _ADD.pack(_DTYPE[dt], rt is _F32, wt is _F32, *shape, _KIND[kind], eps, alpha, xp, rp, wp,
+                                      bp, sp, pp, op, hp, xs, rs, os, hs), dev)
     return out, out_residual

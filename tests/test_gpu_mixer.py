@@ -337,6 +337,24 @@ def test_gated_norm(mx, dtype, kind, rows, H, d):
              "y (%s)" % ((heads, bias, act, first),))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("act", ["silu", "sigmoid"])
+def test_gates_of_extreme_values(mx, dtype, act):
+    """Neighbouring values do not touch each other, whatever their gates."""
+    top = 6e4 if dtype == "fp16" else 1e30
+    gate = torch.tensor([1.0, float("nan"), -2.0, float("inf"), 3.0, -top, 0.5, top, -1.0, -100.0, 30.0, -30.0,
+                         0.0, -44.0, -0.0, 88.0], dtype=DT[dtype])
+    x = torch.ones(1, 1, 16, dtype=DT[dtype])
+    y = mx.gated_norm(x.cuda(), torch.ones(16, device="cuda", dtype=DT[dtype]), gate.view(1, 1, 16).cuda(),
+                      activation=act, eps=0.0)[0, 0].cpu().double()
+    g = gate.double()
+    want = torch.sigmoid(g) * (g if act == "silu" else 1.0)
+    assert torch.isnan(y[1]) and y[3] == (float("inf") if act == "silu" else 1.0)
+    ok = torch.isfinite(want)
+    tol = half(DT[dtype]) * want.abs() + 64 * U * want.abs() + 1e-17 + tiny(DT[dtype])
+    assert ((y[ok] - want[ok]).abs() <= tol[ok]).all()
+
+
 def test_gated_norm_strides_starts_and_in_place(mx):
     g = torch.Generator().manual_seed(0)
     for shift, dt in ((8, torch.bfloat16), (3, torch.bfloat16), (1, torch.float32)):
