@@ -254,7 +254,7 @@ struct Out {
 
 template <class T, int W, bool VEC>
 __global__ void __launch_bounds__(CONV_THREADS, VEC ? 4 : 3)
-conv_kernel(const __grid_constant__ ConvArgs a) {
+conv_kernel(const __grid_constant__ ConvPrompt a) {
   const int tile = blockIdx.x;
   const int row = find_row(a.items, a.rows, tile, a.per_row);
   const RowItem it = a.items[row];
@@ -380,18 +380,19 @@ conv_kernel(const __grid_constant__ ConvArgs a) {
 // once for all of them.
 template <class T, int W, bool VEC>
 __global__ void __launch_bounds__(CONV_THREADS, 6)
-conv_step_kernel(const __grid_constant__ ConvArgs a) {
+conv_step_kernel(const __grid_constant__ ConvStep a) {
   Lane<T, W, VEC> ln;
   ln.init(a);
   const int r1 = min(a.rows, (int)(blockIdx.x + 1) * a.TT);
 #pragma unroll 2
   for (int row = blockIdx.x * a.TT; row < r1; ++row) {
-    const RowItem it = a.items[row];
+    const int slot = a.slot[row];
+    const bool fresh = slot < 0;
     Eight<T, VEC> cur, hist[W - 1], y;
-    T* st = a.state ? static_cast<T*>(a.state) + (int64_t)it.slot * (W - 1) * a.C + ln.c : nullptr;
+    T* st = a.state ? static_cast<T*>(a.state) + (int64_t)(fresh ? ~slot : slot) * (W - 1) * a.C + ln.c : nullptr;
     cur.load(static_cast<const T*>(a.x.p) + (int64_t)row * a.x.sn + ln.c, ln.valid);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) hist[j].load(st + (int64_t)j * a.C, st && !row_fresh(it) ? ln.valid : 0);
+    for (int j = 0; j < W - 1; ++j) hist[j].load(st + (int64_t)j * a.C, st && !fresh ? ln.valid : 0);
     if (st) {
 #pragma unroll
       for (int j = 0; j + 1 < W - 1; ++j) hist[j + 1].store(st + (int64_t)j * a.C, ln.valid);
@@ -419,20 +420,26 @@ conv_step_kernel(const __grid_constant__ ConvArgs a) {
   }
 }
 
-template <class T, int W, bool VEC>
-cudaError_t go(bool step, const ConvArgs& a, cudaStream_t s) {
+template <class T, int W, bool VEC, class Args>
+cudaError_t go(const Args& a, cudaStream_t s) {
   const dim3 grid((unsigned)a.tiles, (unsigned)((a.C + 8 * CONV_THREADS - 1) / (8 * CONV_THREADS)));
-  if (step) conv_step_kernel<T, W, VEC><<<grid, CONV_THREADS, 0, s>>>(a);
+  if constexpr (std::is_same<Args, ConvStep>::value) conv_step_kernel<T, W, VEC><<<grid, CONV_THREADS, 0, s>>>(a);
   else conv_kernel<T, W, VEC><<<grid, CONV_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
-template <class T, int W>
-cudaError_t go_v(bool step, bool vec, const ConvArgs& a, cudaStream_t s) {
-  return vec ? go<T, W, true>(step, a, s) : go<T, W, false>(step, a, s);
+template <class T, int W, class Args>
+cudaError_t go_v(bool vec, const Args& a, cudaStream_t s) {
+  return vec ? go<T, W, true>(a, s) : go<T, W, false>(a, s);
 }
-template <class T>
-cudaError_t go_w(bool step, bool vec, const ConvArgs& a, cudaStream_t s) {
-  return a.W == 2 ? go_v<T, 2>(step, vec, a, s) : a.W == 3 ? go_v<T, 3>(step, vec, a, s) : go_v<T, 4>(step, vec, a, s);
+template <class T, class Args>
+cudaError_t go_w(bool vec, const Args& a, cudaStream_t s) {
+  return a.W == 2 ? go_v<T, 2>(vec, a, s) : a.W == 3 ? go_v<T, 3>(vec, a, s) : go_v<T, 4>(vec, a, s);
+}
+template <class Args>
+cudaError_t go_t(int dtype, bool vec, const Args& a, cudaStream_t s) {
+  return dtype == T_F32    ? go_w<float>(vec, a, s)
+         : dtype == T_BF16 ? go_w<__nv_bfloat16>(vec, a, s)
+                           : go_w<__half>(vec, a, s);
 }
 
 }  // namespace
@@ -446,11 +453,8 @@ int conv_tile(int64_t tokens, int C, int sms) {
   return tt;
 }
 
-cudaError_t launch_conv(int dtype, bool step, bool vec, const ConvArgs& a, cudaStream_t s) {
-  return dtype == T_F32    ? go_w<float>(step, vec, a, s)
-         : dtype == T_BF16 ? go_w<__nv_bfloat16>(step, vec, a, s)
-                           : go_w<__half>(step, vec, a, s);
-}
+cudaError_t launch_conv(int dtype, bool vec, const ConvPrompt& a, cudaStream_t s) { return go_t(dtype, vec, a, s); }
+cudaError_t launch_conv_step(int dtype, bool vec, const ConvStep& a, cudaStream_t s) { return go_t(dtype, vec, a, s); }
 
 }  // namespace mx
 }  // namespace dl

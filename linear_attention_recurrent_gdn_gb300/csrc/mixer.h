@@ -9,6 +9,10 @@ namespace dl {
 namespace mx {
 
 constexpr int MX_ROWS = 1024;          // rows of one call
+// Rows of one launch: their plan travels as a launch parameter, which costs
+// about 0.2 us of host time a KiB, so it is kept to 2 KiB.
+constexpr int MX_GROUP = 128;          // prompts
+constexpr int MX_STEP = 512;           // one token a row: only slots
 enum { T_F32 = 0, T_BF16 = 1, T_F16 = 2 };
 enum { ACT_NONE = 0, ACT_SILU = 1, ACT_SIGMOID = 2 };
 enum { NORM_RMS = 0, NORM_LAYER = 1 };
@@ -51,16 +55,22 @@ struct ConvArgs {
   TokView y[CONV_PARTS];    // outputs: consecutive channel ranges
   int32_t c0[CONV_PARTS + 1];   // first channel of each range; unused ranges start at C
   int32_t C, W, act, l2c, hd, w_f32;
-  int32_t rows, tiles, per_row, TT;   // TT: tokens of one tile
+  int32_t rows, tiles, per_row, TT;   // TT: tokens of one tile (step: rows)
   float eps;
-  RowItem items[MX_ROWS];
+};
+struct ConvPrompt : ConvArgs {
+  RowItem items[MX_GROUP];
+};
+struct ConvStep : ConvArgs {
+  int32_t slot[MX_STEP];    // ~slot for a fresh row
 };
 // Tokens of a tile for this much work (a step: rows, one token each).
 int conv_tile(int64_t tokens, int C, int sms);
-// step: one token a row; tiles of TT rows.
-cudaError_t launch_conv(int dtype, bool step, bool vec, const ConvArgs& a, cudaStream_t s);
+cudaError_t launch_conv(int dtype, bool vec, const ConvPrompt& a, cudaStream_t s);
+// One token a row, tiles of TT rows.
+cudaError_t launch_conv_step(int dtype, bool vec, const ConvStep& a, cudaStream_t s);
 
-struct SsmArgs {
+struct SsmBase {
   TokView x, dt, B, C, y;
   const float* A;           // [H]
   const float* D;           // [H] or null
@@ -68,9 +78,14 @@ struct SsmArgs {
   float* state;             // [num_slots, H, P, N] or null
   int32_t H, G, P, N, softplus, dt_f32;
   int32_t rows;
-  RowItem items[MX_ROWS];
 };
-cudaError_t launch_ssm_step(int dtype, const SsmArgs& a, cudaStream_t s);
+struct SsmArgs : SsmBase {
+  RowItem items[MX_GROUP];
+};
+struct SsmStep : SsmBase {
+  int32_t slot[MX_STEP];    // ~slot for a fresh row
+};
+cudaError_t launch_ssm_step(int dtype, const SsmStep& a, cudaStream_t s);
 
 // How a scan splits a call: `units` CTAs a segment of seg_tokens tokens (on the
 // tensor cores: nh heads of up to ph columns each); split: a row may have

@@ -1,7 +1,7 @@
 // C entry points of the mixer operators: argument checks, tile planning and
 // launches.  Everything is checked before the first CUDA call; nothing is
-// allocated and nothing kept.  The launch arguments (up to 16 KiB of row plan)
-// are built in a thread's own storage.
+// allocated and nothing kept.  A call's rows and the launch arguments are built
+// in a thread's own storage; calls of many rows take several launches.
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -31,8 +31,12 @@ struct ErrOut {
   }
 };
 
-thread_local ConvArgs t_conv;
+// Every row of a call, and the arguments of a launch.
+thread_local RowItem t_items[MX_ROWS];
+thread_local ConvPrompt t_conv;
+thread_local ConvStep t_conv_step;
 thread_local SsmArgs t_ssm;
+thread_local SsmStep t_ssm_step;
 
 constexpr int64_t MAX_DIM = (int64_t)1 << 30;   // sizes that the kernels hold in 32 bits
 
@@ -103,6 +107,21 @@ dl_status plan_rows(const ErrOut& fail, const dl_tokens& k, bool state, int64_t 
   return DL_OK;
 }
 
+// Rows [r0, r0 + n) of a call as a launch's own: tiles numbered from zero.
+void group_rows(const RowItem* all, int64_t r0, int64_t n, RowItem* items) {
+  for (int64_t i = 0; i < n; ++i) {
+    items[i] = all[r0 + i];
+    items[i].tile0 -= all[r0].tile0;
+  }
+}
+void group_slots(const RowItem* all, int64_t r0, int64_t n, int32_t* slot) {
+  for (int64_t i = 0; i < n; ++i) slot[i] = row_fresh(all[r0 + i]) ? ~all[r0 + i].slot : all[r0 + i].slot;
+}
+// A tensor as rows from r0 on see it.
+TokView from_row(const TokView& v, int64_t r0, int64_t elem) {
+  return TokView{static_cast<const char*>(v.p) + (v.p ? r0 * v.sn * elem : 0), v.st, v.sn};
+}
+
 TokView view(const dl_view& v, bool packed) { return TokView{v.data, v.stride_t, packed ? 0 : v.stride_n}; }
 
 bool view_vec(const dl_view& v, int64_t dtype, bool packed) {
@@ -150,7 +169,7 @@ extern "C" dl_status dl_conv(const dl_conv_args* p, void* stream, char* errbuf, 
     if (q.l2_channels % d) return fail(DL_EINVAL, "%lld normalised channels are not whole heads of %lld", (long long)q.l2_channels, (long long)d);
     if (!(q.eps >= 0)) return fail(DL_EINVAL, "eps is negative");
   }
-  ConvArgs& a = t_conv;
+  ConvArgs a{};
   int64_t c = 0;
   bool vec = q.C % 8 == 0;
   for (int k = 0; k < CONV_PARTS; ++k) {
@@ -175,10 +194,9 @@ extern "C" dl_status dl_conv(const dl_conv_args* p, void* stream, char* errbuf, 
   a.TT = conv_tile(total, (int)q.C, num_sms());
   int64_t tiles;
   bool any;
-  const dl_status s = plan_rows(fail, q.tokens, q.state != nullptr, a.TT, a.items, tiles, a.per_row, any);
+  const dl_status s = plan_rows(fail, q.tokens, q.state != nullptr, a.TT, t_items, tiles, a.per_row, any);
   if (s != DL_OK) return s;
   if (q.tokens.n == 0) return DL_OK;
-  if (step) tiles = (q.tokens.n + a.TT - 1) / a.TT;
   const int64_t e = elem(q.dtype);
   if ((!q.x.data && any) || !q.weight) return fail(DL_EINVAL, "NULL tensor pointer");
   const int64_t we = q.weight_f32 ? 4 : e;
@@ -199,10 +217,29 @@ extern "C" dl_status dl_conv(const dl_conv_args* p, void* stream, char* errbuf, 
   a.l2c = (int32_t)q.l2_channels;
   a.hd = (int32_t)q.head_dim;
   a.w_f32 = q.weight_f32 ? 1 : 0;
-  a.rows = (int32_t)q.tokens.n;
-  a.tiles = (int32_t)tiles;
   a.eps = (float)q.eps;
-  return done(fail, launch_conv((int)q.dtype, step, vec, a, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int64_t n = q.tokens.n, most = step ? MX_STEP : MX_GROUP;
+  for (int64_t r0 = 0; r0 < n; r0 += most) {
+    const int64_t m = n - r0 < most ? n - r0 : most;
+    ConvArgs& g = step ? static_cast<ConvArgs&>(t_conv_step) : t_conv;
+    g = a;
+    g.rows = (int32_t)m;
+    g.x = from_row(a.x, r0, e);
+    for (int k = 0; k < q.n_parts; ++k) g.y[k] = from_row(a.y[k], r0, e);
+    cudaError_t err;
+    if (step) {
+      g.tiles = (int32_t)((m + a.TT - 1) / a.TT);
+      group_slots(t_items, r0, m, t_conv_step.slot);
+      err = launch_conv_step((int)q.dtype, vec, t_conv_step, st);
+    } else {
+      g.tiles = (int32_t)((r0 + m < n ? t_items[r0 + m].tile0 : tiles) - t_items[r0].tile0);
+      group_rows(t_items, r0, m, t_conv.items);
+      err = launch_conv((int)q.dtype, vec, t_conv, st);
+    }
+    if (err != cudaSuccess) return done(fail, err);
+  }
+  return DL_OK;
 }
 
 namespace {
@@ -216,14 +253,14 @@ dl_status ssm_sizes(const ErrOut& fail, const dl_ssm_args& q) {
   return DL_OK;
 }
 
-dl_status ssm_args(const ErrOut& fail, const dl_ssm_args& q, SsmArgs& a) {
+dl_status ssm_args(const ErrOut& fail, const dl_ssm_args& q, SsmBase& a) {
   dl_status s = ssm_sizes(fail, q);
   if (s != DL_OK) return s;
   int64_t tiles;
   int32_t per_row;
   bool any;
   const bool packed = q.tokens.packed != 0;
-  s = plan_rows(fail, q.tokens, q.state != nullptr, MAX_DIM, a.items, tiles, per_row, any);
+  s = plan_rows(fail, q.tokens, q.state != nullptr, MAX_DIM, t_items, tiles, per_row, any);
   if (s != DL_OK || q.tokens.n == 0) return s;
   const int64_t e = elem(q.dtype);
   for (const dl_view* v : {&q.x, &q.B, &q.C, &q.y}) {
@@ -299,7 +336,7 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   if (errbuf && errlen > 0) errbuf[0] = 0;
   if (!p) return fail(DL_EINVAL, "NULL argument");
   const dl_ssm_args& q = *p;
-  SsmArgs& a = t_ssm;
+  SsmBase a{};
   dl_status s = ssm_args(fail, q, a);
   if (s != DL_OK || q.tokens.n == 0) return s;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -307,7 +344,7 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   int64_t tiles;
   int32_t per_row;
   bool any;
-  s = plan_rows(fail, q.tokens, q.state != nullptr, k.seg_tokens, a.items, tiles, per_row, any);
+  s = plan_rows(fail, q.tokens, q.state != nullptr, k.seg_tokens, t_items, tiles, per_row, any);
   if (s != DL_OK) return s;
   const int64_t need = workspace_of(q, k, tiles);
   if (need && (!q.workspace || q.workspace_bytes < need || !al(q.workspace, 16)))
@@ -316,11 +353,28 @@ extern "C" dl_status dl_ssm(const dl_ssm_args* p, void* stream, char* errbuf, in
   const bool packed = q.tokens.packed != 0;
   const bool vec = q.P % 8 == 0 && q.N % 8 == 0 && view_vec(q.x, q.dtype, packed) && view_vec(q.B, q.dtype, packed) &&
                    view_vec(q.C, q.dtype, packed) && view_vec(q.y, q.dtype, packed);
-  if (!on_tensor_cores(q))
-    return done(fail, launch_ssm_scan((int)q.dtype, vec, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
   int64_t tokens = q.tokens.T;
-  if (packed) tokens = (int64_t)a.items[a.rows - 1].begin + row_len(a.items[a.rows - 1]);
-  return done(fail, launch_ssm_tc(vec, tokens, a, k, (int)tiles, per_row, static_cast<float*>(q.workspace), st));
+  if (packed) tokens = (int64_t)t_items[q.tokens.n - 1].begin + row_len(t_items[q.tokens.n - 1]);
+  const bool tc = on_tensor_cores(q);
+  const int64_t n = q.tokens.n, e = elem(q.dtype);
+  float* ws = static_cast<float*>(q.workspace);
+  for (int64_t r0 = 0; r0 < n; r0 += MX_GROUP) {
+    const int64_t m = n - r0 < MX_GROUP ? n - r0 : MX_GROUP;
+    SsmArgs& g = t_ssm;
+    static_cast<SsmBase&>(g) = a;
+    g.rows = (int32_t)m;
+    g.x = from_row(a.x, r0, e);
+    g.B = from_row(a.B, r0, e);
+    g.C = from_row(a.C, r0, e);
+    g.y = from_row(a.y, r0, e);
+    g.dt = from_row(a.dt, r0, q.dt_f32 ? 4 : e);
+    group_rows(t_items, r0, m, g.items);
+    const int gt = (int)((r0 + m < n ? t_items[r0 + m].tile0 : tiles) - t_items[r0].tile0);
+    const cudaError_t err = tc ? launch_ssm_tc(vec, tokens, g, k, gt, per_row, ws, st)
+                               : launch_ssm_scan((int)q.dtype, vec, g, k, gt, per_row, ws, st);
+    if (err != cudaSuccess) return done(fail, err);
+  }
+  return DL_OK;
 }
 
 extern "C" dl_status dl_mixer_sync(void* stream, int32_t* device_code, char* errbuf, int32_t errlen) {
@@ -342,10 +396,25 @@ extern "C" dl_status dl_ssm_step(const dl_ssm_args* p, void* stream, char* errbu
   if (!p) return fail(DL_EINVAL, "NULL argument");
   if (!p->state) return fail(DL_EINVAL, "a step needs a state pool");
   if (p->tokens.T != 1 || p->tokens.lengths) return fail(DL_EINVAL, "a step takes one token a row");
-  SsmArgs& a = t_ssm;
+  SsmBase a{};
   const dl_status s = ssm_args(fail, *p, a);
   if (s != DL_OK || p->tokens.n == 0) return s;
-  return done(fail, launch_ssm_step((int)p->dtype, a, static_cast<cudaStream_t>(stream)));
+  const int64_t n = p->tokens.n, e = elem(p->dtype);
+  for (int64_t r0 = 0; r0 < n; r0 += MX_STEP) {
+    const int64_t m = n - r0 < MX_STEP ? n - r0 : MX_STEP;
+    SsmStep& g = t_ssm_step;
+    static_cast<SsmBase&>(g) = a;
+    g.rows = (int32_t)m;
+    g.x = from_row(a.x, r0, e);
+    g.B = from_row(a.B, r0, e);
+    g.C = from_row(a.C, r0, e);
+    g.y = from_row(a.y, r0, e);
+    g.dt = from_row(a.dt, r0, p->dt_f32 ? 4 : e);
+    group_slots(t_items, r0, m, g.slot);
+    const cudaError_t err = launch_ssm_step((int)p->dtype, g, static_cast<cudaStream_t>(stream));
+    if (err != cudaSuccess) return done(fail, err);
+  }
+  return DL_OK;
 }
 
 extern "C" dl_status dl_gated_norm(const dl_gated_norm_args* p, void* stream, char* errbuf, int32_t errlen) {

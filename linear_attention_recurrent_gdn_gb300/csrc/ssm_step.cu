@@ -35,17 +35,18 @@ __device__ __forceinline__ void st4(float* p, float4 v, int valid) {
 // load, ROWS loads a warp.
 template <class T, bool VEC, int IT, int ROWS>
 __global__ void __launch_bounds__(ST_THREADS)
-ssm_step_kernel(const __grid_constant__ SsmArgs a, int lpr, int tiles) {
+ssm_step_kernel(const __grid_constant__ SsmStep a, int lpr, int tiles) {
   const int lane = threadIdx.x & 31, per = 32 / lpr, ln = lane % lpr, sub = lane / lpr;
   const uint32_t w = blockIdx.x * (ST_THREADS / 32) + (threadIdx.x >> 5);
   const uint32_t rh = w / tiles;
   const int tile = (int)(w - rh * tiles);
   if (rh >= (uint32_t)(a.rows * a.H)) return;      // whole warps
   const int row = rh / a.H, h = rh - row * a.H, g = h / (a.H / a.G);
-  const RowItem it = a.items[row];
+  const bool fresh = a.slot[row] < 0;
+  const int slot = fresh ? ~a.slot[row] : a.slot[row];
   const int p0 = tile * ROWS * per + sub;
-  float* st = a.state + (((int64_t)it.slot * a.H + h) * a.P + p0) * a.N + 4 * ln;
-  auto off = [&](const TokView& v) { return (int64_t)it.begin * v.st + (int64_t)row * v.sn; };
+  float* st = a.state + (((int64_t)slot * a.H + h) * a.P + p0) * a.N + 4 * ln;
+  auto off = [&](const TokView& v) { return (int64_t)row * v.sn; };
 
   // every load before the first use
   float4 S[ROWS][IT];
@@ -54,7 +55,7 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int lpr, int tiles) {
 #pragma unroll
     for (int i = 0; i < IT; ++i)
       S[r][i] = ld4<VEC>(st + (int64_t)r * per * a.N + 4 * lpr * i,
-                         p0 + r * per < a.P && !row_fresh(it) ? a.N - 4 * (ln + lpr * i) : 0);
+                         p0 + r * per < a.P && !fresh ? a.N - 4 * (ln + lpr * i) : 0);
   const int64_t od = off(a.dt) + h;
   float dt = a.dt_f32 ? static_cast<const float*>(a.dt.p)[od] : to_f(static_cast<const T*>(a.dt.p)[od]);
   const float bias = a.dt_bias ? a.dt_bias[h] : 0.f, Ah = a.A[h], Dh = a.D ? a.D[h] : 0.f;
@@ -110,7 +111,7 @@ ssm_step_kernel(const __grid_constant__ SsmArgs a, int lpr, int tiles) {
 }
 
 template <class T, bool VEC, int ROWS>
-cudaError_t go_rows(const SsmArgs& a, int lpr, cudaStream_t s) {
+cudaError_t go_rows(const SsmStep& a, int lpr, cudaStream_t s) {
   const int rows = ROWS * (32 / lpr), tiles = (a.P + rows - 1) / rows;
   const int64_t warps = (int64_t)a.rows * a.H * tiles, wpb = ST_THREADS / 32;
   const unsigned grid = (unsigned)((warps + wpb - 1) / wpb);
@@ -119,7 +120,7 @@ cudaError_t go_rows(const SsmArgs& a, int lpr, cudaStream_t s) {
   return cudaGetLastError();
 }
 template <class T, bool VEC>
-cudaError_t go(const SsmArgs& a, cudaStream_t s) {
+cudaError_t go(const SsmStep& a, cudaStream_t s) {
   int lpr = 1;
   while (lpr < 32 && 4 * lpr < a.N) lpr <<= 1;
   // Eight rows a warp amortise its inputs; two where that leaves the GPU's SMs
@@ -130,7 +131,7 @@ cudaError_t go(const SsmArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_ssm_step(int dtype, const SsmArgs& a, cudaStream_t s) {
+cudaError_t launch_ssm_step(int dtype, const SsmStep& a, cudaStream_t s) {
   const bool vec = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.state) & 15) == 0;
   if (dtype == T_F32) return vec ? go<float, true>(a, s) : go<float, false>(a, s);
   if (dtype == T_BF16) return vec ? go<__nv_bfloat16, true>(a, s) : go<__nv_bfloat16, false>(a, s);

@@ -197,9 +197,9 @@ def _conv(x, weight, bias, slots, state, lengths, fresh, activation, l2_channels
         raise ValueError("split: 1 to 4 ranges")
     views = []
     if out is None:
-        outs = []
+        outs, place = [], x.device
         for c in parts:
-            t = x.new_empty(lead_shape + (c,))
+            t = torch.empty(lead_shape + (c,), dtype=dt, device=place)
             outs.append(t)
             views += (t.data_ptr(), 0, c) if lead == 0 else (t.data_ptr(), c, 0) if lead == 1 else \
                 (t.data_ptr(), c * shape[1], c)
@@ -252,7 +252,7 @@ def _ssm(fn, x, dt, A, B, C, D, dt_bias, dt_softplus, slots, state, lengths, fre
     fields, pool, lead, keep = _rows(lead_shape, step, slots, lengths, fresh, state, dev, (H, P, N), _F32)
     maps, dtt = lead_shape + (G, N), _F32 if dt.dtype is _F32 else xt
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
     head = fields + (_DTYPE[xt], dtt is _F32, bool(dt_softplus), H, G, P, N) \
         + _tokens("x", x, shape, xt, dev, 2, lead) + _tokens("dt", dt, lead_shape + (H,), dtt, dev, 1, lead) \
         + _tokens("B", B, maps, xt, dev, 2, lead) + _tokens("C", C, maps, xt, dev, 2, lead) \
@@ -315,7 +315,7 @@ def gated_norm(x, weight, gate=None, *, bias=None, kind="rms", activation="silu"
     xp, xs = _matrix("x", x, shape, dt, dev, 2)
     gp, gs = (0, 0) if gate is None else _matrix("gate", gate, shape, dt, dev, 2)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
     op, os = _matrix("out", out, shape, dt, dev, 2)
     _call(_lib.dl_gated_norm, _GATED.pack(_DTYPE[dt], wt is _F32, heads, *shape, _KIND[kind], _ACT[activation],
                                           bool(gate_first), eps, xp, gp, wp, bp, op, xs, gs, os), dev)
@@ -346,9 +346,9 @@ def add_norm(x, residual, weight, *, bias=None, scale=None, alpha=1.0, post_weig
     xp, xs = _matrix("x", x, shape, dt, dev, 1)
     rp, rs = (0, 0) if residual is None else _matrix("residual", residual, shape, rt, dev, 1)
     if out is None:
-        out = x.new_empty(shape)
+        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
     if out_residual is None:
-        out_residual = x.new_empty(shape, dtype=rt)
+        out_residual = torch.empty(shape, dtype=rt, device=x.device)
     op, os = _matrix("out", out, shape, dt, dev, 1)
     hp, hs = _matrix("out_residual", out_residual, shape, rt, dev, 1)
     _call(_lib.dl_add_norm, _ADD.pack(_DTYPE[dt], rt is _F32, wt is _F32, *shape, _KIND[kind], eps, alpha, xp, rp, wp,

@@ -264,6 +264,15 @@ def test_ssm_groups(mx, H, G):
     check_ssm(mx, "fp32", H, G, 24, 32, [30, 7], "packed", seed=H)
 
 
+def test_calls_of_several_launches(mx):
+    """More rows than one launch takes, in every layout."""
+    check_conv(mx, "bf16", 24, 4, [1] * 600, "step", seed=1)
+    check_conv(mx, "fp32", 24, 3, [(i * 7) % 11 for i in range(300)], "token", seed=2)
+    check_ssm(mx, "bf16", 2, 1, 8, 16, [1] * 530, "step", seed=3)
+    check_ssm(mx, "bf16", 2, 1, 8, 16, [33 + i % 9 for i in range(150)], "token", seed=4, mma=True)
+    check_ssm(mx, "fp32", 2, 2, 8, 16, [i % 5 for i in range(300)], "packed", seed=5)
+
+
 def test_ssm_options(mx):
     check_ssm(mx, "bf16", 4, 1, 64, 64, [50], D=False, bias=False, softplus=False, dt32=True, seed=1, mma=True)
     check_ssm(mx, "fp32", 4, 1, 64, 64, [50, 20], pool=False, seed=2)
