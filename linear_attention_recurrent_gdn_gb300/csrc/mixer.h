@@ -87,19 +87,18 @@ struct SsmStep : SsmBase {
 };
 cudaError_t launch_ssm_step(int dtype, const SsmStep& a, cudaStream_t s);
 
-// How a scan splits a call: `units` CTAs a segment of seg_tokens tokens (on the
-// tensor cores: nh heads of up to ph columns each); split: a row may have
-// several segments, joined through a workspace of tiles * H * (P * N + 1)
-// floats.
+// How a scan splits a call: `units` units of work a segment of seg_tokens
+// tokens (ptiles a head); split: a row may have several segments, joined
+// through a workspace of tiles * H * (P * N + 1) floats.
 struct SsmPlan {
-  int32_t nh, ph, ptiles, units, seg_tokens, sms;
+  int32_t ptiles, units, seg_tokens, sms;
   bool split;
 };
 SsmPlan ssm_scan_plan(int H, int P, int N, int rows, const int32_t* lens, int64_t T, int sms);
 // vec: x, B, C and y are 16-byte aligned, in their strides and widths too.
 cudaError_t launch_ssm_scan(int dtype, bool vec, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row, float* ws,
                             cudaStream_t s);
-SsmPlan ssm_tc_plan(int H, int G, int P, int rows, const int32_t* lens, int64_t T, int sms);
+SsmPlan ssm_tc_plan(int H, int P, int rows, const int32_t* lens, int64_t T, int sms);
 // bf16, N <= 128.  tokens: extent of the token axis (packed: all rows').
 cudaError_t launch_ssm_tc(bool vec, int64_t tokens, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row,
                           float* ws, cudaStream_t s);

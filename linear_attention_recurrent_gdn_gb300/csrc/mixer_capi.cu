@@ -307,7 +307,7 @@ bool on_tensor_cores(const dl_ssm_args& q) {
 
 SsmPlan plan_of(const dl_ssm_args& q) {
   const int H = (int)q.H, P = (int)q.P, N = (int)q.N, n = (int)q.tokens.n;
-  return on_tensor_cores(q) ? ssm_tc_plan(H, (int)q.G, P, n, q.tokens.lengths, q.tokens.T, num_sms())
+  return on_tensor_cores(q) ? ssm_tc_plan(H, P, n, q.tokens.lengths, q.tokens.T, num_sms())
                             : ssm_scan_plan(H, P, N, n, q.tokens.lengths, q.tokens.T, num_sms());
 }
 

@@ -4,29 +4,30 @@
 // dt_k A over tokens k <= i of the chunk and T_j the sum over tokens k > j,
 //   y_i = sum_{j <= i} (C_i . B_j) e^{L_i - L_j} dt_j x_j  +  e^{L_i} S C_i  +  D x_i
 //   S'  = e^{L_Q} S + sum_j (e^{T_j} dt_j x_j) B_j^T
-// Every factor is at most one for A < 0.  Per chunk, rows being tokens (or
-// state columns n for the last), tcgen05 MMAs with fp32 accumulators in TMEM:
-//   G  [128 x 128] = C B^T                     exact products of the inputs
-//   Y2 [128 x PC]  = C S^T                     S rounded to bf16
-//   Y1 [128 x PH]  = W X, per head             W_ij = G_ij e^{L_i - L_j} dt_j rounded to bf16, A in TMEM
-//   dS [128 x PC]  = B^T (X1 + X2 + X3)        e^{T_j} dt_j x_j as three bf16 terms (2^-25 of it is left)
+// Every factor is at most one for A < 0.  Per chunk and PC = 64 rows p of the
+// state, rows of a product being tokens (state columns n for the last), tcgen05
+// MMAs with fp32 accumulators in TMEM:
+//   G  [128 x 128] = C B^T               exact products of the inputs
+//   Y2 [128 x 64]  = C S^T               S rounded to bf16
+//   Y1 [128 x 64]  = W X                 W_ij = G_ij e^{L_i - L_j} dt_j rounded to bf16, A in TMEM
+//   dS [128 x 192] = B^T [X1 X2 X3]      e^{T_j} dt_j x_j as three bf16 terms (2^-25 of it is left)
 // W and the S of Y2 are rounded once, like the output itself (half a step of
 // bf16 each); the state keeps 32 bits: it lives in registers in fp32 and its
-// increments are formed from all 24 bits.  e^{L_i - L_j} outside the diagonal
-// 32 x 32 blocks is the product of a row and a column factor, both at most
-// one: e^{L_i - L_b} e^{L_b - L_j}, b the last token of j's block, so only the
-// diagonal blocks take an exponential a pair.
+// increments are formed from all 24 bits, the terms' sums side by side in one
+// product: fewer and wider MMAs.  e^{L_i - L_j} outside
+// the diagonal 32 x 32 blocks is the product of a row and a column factor, both
+// at most one: e^{L_i - L_b} e^{L_b - L_j}, b the last token of j's block, so
+// only the diagonal blocks take an exponential a pair.
 //
-// A persistent CTA of 512 threads takes units of PC = NH * PH columns: one
-// head of up to 128, or NH = 2 heads of up to 64 of one group, over a segment
-// of a row.  B and C of the group, X, its terms and S sit in shared memory as
-// rows of 64 values in the 128-byte swizzle, read K-major or MN-major as a
-// product needs, so nothing is transposed; tensor copies bring them (and, but
-// for a row's ragged last chunk, take y away), the next chunk's as soon as a
-// buffer is free, across units too.  Warps 0-7 form W and y, warps 8-15 X's
-// terms; all of them hold the state, two to four warps to a lane quarter with
-// a part of the columns each.  With nearly all of the SM's memory used as
-// shared memory there is next to no L1 cache, so nothing may spill.
+// A persistent CTA of 16 warps takes units: one head's 64 state rows over a
+// segment of a row.  B and C of the group, X, its terms and S sit in shared
+// memory as rows of 64 values in the 128-byte swizzle, read K-major or MN-major
+// as a product needs, so nothing is transposed; tensor copies bring B, C and X a
+// chunk ahead, across units too (and, but for a row's ragged last chunk, take y
+// away).  Warps 0-7 form W and y, warps 8-15 X's terms; all of them hold the
+// state, a quarter of the columns each.  With nearly all of the SM's memory
+// used as shared memory there is next to no L1 cache, so nothing may spill: 128
+// rows a unit, or two heads, measured slower for that.
 //
 // Rows with few heads are split into segments: a first launch (STATE) runs
 // each segment from zero and leaves its end state and decay in the workspace,
@@ -45,26 +46,23 @@ static __device__ int32_t g_mixer_status;
 
 namespace {
 
-constexpr int Q = 128, TCT = 512;
-constexpr uint32_t COL_G = 0, COL_Y1 = 128, COL_Y2 = 256, COL_DS = 384;
+constexpr int Q = 128, PC = 64, TCT = 512;
+constexpr int HC = PC / 2;        // columns of one of the two warps of a lane quarter in a group of warps
+constexpr int SC = PC / 4;        // state columns of one of the four warps of a lane quarter
+constexpr uint32_t COL_G = 0, COL_W = 128, COL_Y1 = 192, COL_Y2 = 256, COL_DS = 320;
 constexpr uint32_t BLK64 = Q * 128;                  // bytes of 128 rows of 64 values
 constexpr float LOG2E = 1.4426950408889634f;
 
-template <int PC>
-struct Smem {
+// Shared memory; B, C, X and the decays are doubled (even and odd chunks).
+struct Sm {
   static constexpr uint32_t TILE = 2 * BLK64;        // B or C: 128 tokens x 128 state columns
-  static constexpr uint32_t XT = PC / 64 * BLK64;    // X, one of its terms, or S (128 state columns x PC)
-  static constexpr uint32_t B = 0, C = TILE, X = 2 * TILE, X1 = X + 2 * XT, X2 = X1 + XT,
-                            X3 = X2 + XT;            // X doubled; S shares X3's place
-  static constexpr uint32_t F = X3 + XT;             // per head [2]: L, column factor
-  static constexpr uint32_t FB = 2 * Q * 4;
-  static constexpr uint32_t BLK = F + 2 * FB;        // per head and block of 32 tokens: L at its end [8],
-                                                     // e^{T} of its last token [8]; per head: T of all tokens [2],
-                                                     // of even and odd chunks
-  static constexpr uint32_t BAR = BLK + 80;          // ten mbarriers, TMEM address
-  static constexpr uint32_t BYTES = BAR + 96;
+  static constexpr uint32_t B = 0, C = 2 * TILE, X = 4 * TILE, X1 = X + 2 * BLK64, S = X1 + 3 * BLK64;
+  static constexpr uint32_t F = S + BLK64;           // L [128], column factors [128], L at the blocks' ends [4],
+  static constexpr uint32_t FB = (2 * Q + 12) * 4;   // e^{T} of the blocks' last tokens [4], log2 of the chunk's decay
+  static constexpr uint32_t BAR = F + 2 * FB;        // twelve mbarriers, TMEM address
+  static constexpr uint32_t BYTES = BAR + 112;
 };
-static_assert(Smem<128>::BYTES <= 232448, "shared memory");
+static_assert(Sm::BYTES <= 232448, "shared memory");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -92,6 +90,11 @@ __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_g
 __device__ __forceinline__ uint32_t piece_off(int r, int cv) {
   return (uint32_t)(cv >> 3) * BLK64 + (uint32_t)(r * 128 + (((cv & 7) ^ (r & 7)) << 4));
 }
+// Descriptors of K step k (16 values of K): rows are K (MN-major), or K runs along the rows (K-major).
+__device__ __forceinline__ uint64_t k_rows(uint32_t base, int k) { return tc::sdesc128(base + k * 2048u, BLK64, 1024u); }
+__device__ __forceinline__ uint64_t k_cols(uint32_t base, int k) {
+  return tc::sdesc128(base + (uint32_t)(k >> 2) * BLK64 + (uint32_t)(k & 3) * 32u, 16u, 1024u);
+}
 
 struct TcArgs {
   CUtensorMap mx, mb, mc, my;   // x, B, C, y: [64 values][head or group][128 tokens][row] boxes
@@ -100,23 +103,21 @@ struct TcArgs {
   int32_t seg_tokens, tiles, per_row, units, ptiles, total, empty_rows;
 };
 
-// One unit of work: tokens [s0, s1) of a row (a segment) for the heads from h0
-// and, of each, the state rows from p0.
+// One unit of work: tokens [s0, s1) of a row (a segment) for 64 state rows from p0 of head h.
 struct Unit {
-  int tile, row, begin, h0, p0, s0, s1, chunks;
+  int tile, row, begin, h, p0, s0, s1, chunks;
 };
-template <int NH, int PH>
 __device__ __forceinline__ Unit unit_at(const TcArgs& ta, int u) {
   const SsmArgs& a = ta.a;
   Unit w;
   w.tile = u / ta.units;
-  const int k = u - w.tile * ta.units, hu = k / ta.ptiles;
+  const int k = u - w.tile * ta.units;
   w.row = find_row(a.items, a.rows, w.tile, ta.per_row);
   const RowItem it = a.items[w.row];
   const int len = row_len(it), seg = w.tile - (ta.per_row ? w.row * ta.per_row : it.tile0);
   w.begin = it.begin;
-  w.h0 = hu * NH;
-  w.p0 = (k - hu * ta.ptiles) * PH;
+  w.h = k / ta.ptiles;
+  w.p0 = (k - w.h * ta.ptiles) * PC;
   w.s0 = seg * ta.seg_tokens;
   w.s1 = min(len, w.s0 + ta.seg_tokens);
   w.chunks = (w.s1 - w.s0 + Q - 1) / Q;
@@ -129,7 +130,7 @@ __device__ __forceinline__ void segments(const TcArgs& ta, const Unit& w, int& s
   seg = w.tile - (ta.per_row ? w.row * ta.per_row : it.tile0);
   nseg = len > ta.seg_tokens ? (len + ta.seg_tokens - 1) / ta.seg_tokens : 1;
 }
-// Whether a launch works on a unit: STATE leaves out last segments, which nothing follows.
+// Whether a launch leaves a unit out: STATE leaves out last segments, which nothing follows.
 template <bool STATE>
 __device__ __forceinline__ bool skipped(const TcArgs& ta, const Unit& w) {
   if (!STATE) return w.chunks == 0;
@@ -138,11 +139,11 @@ __device__ __forceinline__ bool skipped(const TcArgs& ta, const Unit& w) {
   return seg == nseg - 1;
 }
 // The first unit from u on (in steps of the grid) that has work; u moves there, or past the last.
-template <int NH, int PH, bool STATE>
+template <bool STATE>
 __device__ __forceinline__ Unit next_unit(const TcArgs& ta, int& u) {
   Unit w{};
   for (; u < ta.total; u += gridDim.x) {
-    w = unit_at<NH, PH>(ta, u);
+    w = unit_at(ta, u);
     if (!skipped<STATE>(ta, w)) break;
   }
   return w;
@@ -154,13 +155,9 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par) {
 
 // TMA: tensor copies (16-byte aligned tensors, widths and strides); else
 // threads copy value by value.
-template <int NH, int PH, bool STATE, bool TMA>
+template <bool STATE, bool TMA>
 __global__ void __launch_bounds__(TCT, 1)
 ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
-  constexpr int PC = NH * PH;
-  constexpr int HC = PC / 2;      // columns of one of the two warps of a lane quarter in a group
-  constexpr int SC = PC / 4;      // state columns of one of the four warps of a lane quarter
-  using L = Smem<PC>;
   extern __shared__ __align__(1024) unsigned char sm[];
   const SsmArgs& a = ta.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = warp & 3, hf = (warp >> 2) & 1, cg = warp >> 2;
@@ -169,20 +166,19 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
   const int nk = (a.N + 15) / 16;                   // K steps over the state columns
 
   const uint32_t sb = smem_u32(sm);
-  float* F = reinterpret_cast<float*>(sm + L::F);
-  float* blk = reinterpret_cast<float*>(sm + L::BLK);
-  const uint32_t barG = sb + L::BAR, barC = barG + 8, barS = barG + 16, barY = barG + 24, fullB = barG + 32,
-                 fullC = barG + 40, fullX = barG + 48, readyS = barG + 64, readyF = barG + 72;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + L::BAR + 80);
+  auto decays = [&](uint32_t k) { return reinterpret_cast<float*>(sm + Sm::F + (k & 1) * Sm::FB); };
+  const uint32_t barG = sb + Sm::BAR, barC = barG + 8, barS = barG + 16, barY = barG + 24, fullB = barG + 32,
+                 fullC = barG + 48, fullX = barG + 64, readyS = barG + 80, readyF = barG + 88;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sm::BAR + 96);
 
-  if (warp == 0) tc::tmem_alloc(sb + L::BAR + 80, 512);
+  if (warp == 0) tc::tmem_alloc(sb + Sm::BAR + 96, 512);
   if (tid == 0) {
     // products: one commit; loads: one thread's tensor copies, or the eight warps that copy; S: every warp;
-    // the decays: a warp a head
+    // the decays: one warp
     for (int k = 0; k < 4; ++k) mbar_init(barG + 8 * k, 1);
-    for (int k = 4; k < 8; ++k) mbar_init(barG + 8 * k, TMA ? 1 : 8);
+    for (int k = 4; k < 10; ++k) mbar_init(barG + 8 * k, TMA ? 1 : 8);
     mbar_init(readyS, TCT / 32);
-    mbar_init(readyF, NH);
+    mbar_init(readyF, 1);
     fence_mbar_init();
   }
 
@@ -192,7 +188,6 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
   };
-  // Chunk c of unit w into the buffers.  TMA: one thread calls; else warps 8-15 copy.
   auto copy_rows = [&](uint32_t dst, const uint16_t* src, int64_t st, int nt, int width, int cols) {
 #pragma unroll 1
     for (int e = tid - 256; e < Q * cols / 8; e += 256) {
@@ -208,51 +203,45 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       *reinterpret_cast<uint4*>(sm + dst + piece_off(r, cv)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   };
-  auto load_x = [&](const Unit& w, int c, uint32_t buf) {
-    const int t0 = w.s0 + c * Q;
+  // Chunk c of unit w, number k of all, into its buffers.  TMA: one thread calls; else warps 8-15 copy.
+  auto load = [&](const Unit& w, int c, uint32_t k) {
+    const uint32_t b = k & 1;
+    const int t0 = w.s0 + c * Q, g = w.h / (a.H / a.G);
+    const uint32_t xd = Sm::X + b * BLK64, bd = Sm::B + b * Sm::TILE, cd = Sm::C + b * Sm::TILE;
+    const uint32_t fx = fullX + 8 * b, fb = fullB + 8 * b, fc = fullC + 8 * b;
     if (TMA) {
-      const uint32_t bar = fullX + 8 * buf;
-      mbar_arrive_expect_tx(bar, L::XT);
-#pragma unroll
-      for (int b = 0; b < PC / 64; ++b)
-        tma_load(sb + L::X + buf * L::XT + b * BLK64, &ta.mx, w.p0 + (NH == 1 ? 64 * b : 0), w.h0 + (NH == 1 ? 0 : b),
-                 w.begin + t0, a.x.sn ? w.row : 0, bar);
-    } else {
-#pragma unroll
-      for (int hh = 0; hh < NH; ++hh)
-        copy_rows(L::X + buf * L::XT + hh * BLK64,
-                  static_cast<const uint16_t*>(a.x.p) + (int64_t)(w.h0 + hh) * a.P + w.p0 + tok(w, a.x, t0), a.x.st,
-                  min(Q, w.s1 - t0), min(PH, a.P - w.p0), PH);
-      arrive_warp(fullX + 8 * buf);
-    }
-  };
-  auto load_bc = [&](const Unit& w, int c, bool isb) {
-    const int t0 = w.s0 + c * Q, g = w.h0 / (a.H / a.G);
-    const TokView& v = isb ? a.B : a.C;
-    const uint32_t dst = isb ? L::B : L::C;
-    if (TMA) {
-      const uint32_t bar = isb ? fullB : fullC;
+      mbar_arrive_expect_tx(fx, BLK64);
+      tma_load(sb + xd, &ta.mx, w.p0, w.h, w.begin + t0, a.x.sn ? w.row : 0, fx);
       const int nb = a.N > 64 ? 2 : 1;
-      mbar_arrive_expect_tx(bar, nb * BLK64);
-      for (int b = 0; b < nb; ++b)
-        tma_load(sb + dst + b * BLK64, isb ? &ta.mb : &ta.mc, 64 * b, g, w.begin + t0, v.sn ? w.row : 0, bar);
+      mbar_arrive_expect_tx(fb, nb * BLK64);
+      for (int e = 0; e < nb; ++e) tma_load(sb + bd + e * BLK64, &ta.mb, 64 * e, g, w.begin + t0, a.B.sn ? w.row : 0, fb);
+      if (!STATE) {
+        mbar_arrive_expect_tx(fc, nb * BLK64);
+        for (int e = 0; e < nb; ++e) tma_load(sb + cd + e * BLK64, &ta.mc, 64 * e, g, w.begin + t0, a.C.sn ? w.row : 0, fc);
+      }
     } else {
-      copy_rows(dst, static_cast<const uint16_t*>(v.p) + (int64_t)g * a.N + tok(w, v, t0), v.st, min(Q, w.s1 - t0), a.N,
-                128);
-      arrive_warp(isb ? fullB : fullC);
+      const int nt = min(Q, w.s1 - t0);
+      const uint16_t* xp = static_cast<const uint16_t*>(a.x.p) + (int64_t)w.h * a.P + w.p0;
+      copy_rows(xd, xp + tok(w, a.x, t0), a.x.st, nt, min(PC, a.P - w.p0), PC);
+      arrive_warp(fx);
+      copy_rows(bd, static_cast<const uint16_t*>(a.B.p) + (int64_t)g * a.N + tok(w, a.B, t0), a.B.st, nt, a.N, 128);
+      arrive_warp(fb);
+      if (!STATE) {
+        copy_rows(cd, static_cast<const uint16_t*>(a.C.p) + (int64_t)g * a.N + tok(w, a.C, t0), a.C.st, nt, a.N, 128);
+        arrive_warp(fc);
+      }
     }
   };
-  // dt of token t (past the segment: its last one) for head hh of the unit, as it sits in memory: the
-  // conversion waits for the load, so it is left to the use
-  auto raw_dt = [&](const Unit& w, int t, int hh) -> uint32_t {
-    const int64_t o = tok(w, a.dt, min(t, w.s1 - 1)) + w.h0 + hh;
+  // dt of token t (past the segment: its last one), as it sits in memory: the conversion waits for the load,
+  // so it is left to the use
+  auto raw_dt = [&](const Unit& w, int t) -> uint32_t {
+    const int64_t o = tok(w, a.dt, min(t, w.s1 - 1)) + w.h;
     return a.dt_f32 ? static_cast<const uint32_t*>(a.dt.p)[o] : static_cast<const uint16_t*>(a.dt.p)[o];
   };
   auto dt_of = [&](uint32_t raw, float bias) {
     const float d = __uint_as_float(a.dt_f32 ? raw : raw << 16) + bias;
     return a.softplus ? softplus_f(d) : d;
   };
-  auto bias_of = [&](int h) { return a.dt_bias ? a.dt_bias[h] : 0.f; };
 
   tc::fence_before_sync();
   __syncthreads();
@@ -261,16 +250,15 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
   const uint32_t tl = tm + ((uint32_t)(32 * q4) << 16);
   bool ok = true;                 // a wait that ran out: no further waits, no results
   auto wait = [&](uint32_t bar, uint32_t par) {
-    if (ok && !mbar_try_wait(bar, par)) ok = wait_long(bar, par);
+    if (ok && !mbar_try_wait(bar, par & 1u)) ok = wait_long(bar, par & 1u);
   };
+  auto wait2 = [&](uint32_t bar, uint32_t k) { wait(bar + 8 * (k & 1), k >> 1); };   // one of a pair
   const int64_t per_tile = (int64_t)a.H * a.P * a.N;
 
   // ---- the state: this thread holds S[column cg * SC + .][n = i] of the unit
   float S[SC];
-  const int hcol = NH == 2 ? cg >> 1 : 0;           // head and first row p of its columns
-  const int pofs = NH == 2 ? (cg & 1) * SC : cg * SC;
-  auto elem0 = [&](const Unit& w) { return ((int64_t)(w.h0 + hcol) * a.P + w.p0 + pofs) * a.N + i; };
-  auto live_of = [&](const Unit& w) { return i < a.N ? a.P - w.p0 - pofs : 0; };
+  auto elem0 = [&](const Unit& w) { return ((int64_t)w.h * a.P + w.p0 + cg * SC) * a.N + i; };
+  auto live_of = [&](const Unit& w) { return i < a.N ? a.P - w.p0 - cg * SC : 0; };
   auto pool_of = [&](const Unit& w) { return a.state ? a.state + (int64_t)a.items[w.row].slot * per_tile : nullptr; };
   auto load_state = [&](const Unit& w) {
     int seg, nseg;
@@ -295,7 +283,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
 #pragma unroll 1
       for (int k = 2; k <= seg; ++k) {
         const float* add = ta.ws + (int64_t)(w.tile - seg + k) * per_tile + e0;
-        const float d = ex2(ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)(w.tile - seg + k - 1) * a.H + w.h0 + hcol]);
+        const float d = ex2(ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)(w.tile - seg + k - 1) * a.H + w.h]);
 #pragma unroll
         for (int c = 0; c < SC; ++c) S[c] = fmaf(S[c], d, c < live ? add[(int64_t)c * a.N] : 0.f);
       }
@@ -312,15 +300,15 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       for (int c = 0; c < SC; ++c)
         if (c < live) to[e0 + (int64_t)c * a.N] = S[c];
     }
-    if (STATE && i == 0 && pofs == 0 && w.p0 == 0)
-      ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)w.tile * a.H + w.h0 + hcol] = ltot;
+    if (STATE && tid == 0 && w.p0 == 0)
+      ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)w.tile * a.H + w.h] = ltot;
   };
   auto share_state = [&]() {      // S as a bf16 operand (rows n, columns contiguous), and its TMEM place is read
     if (!STATE) {
 #pragma unroll
       for (int c8 = 0; c8 < SC / 8; ++c8) {
         const float* s = S + 8 * c8;
-        *reinterpret_cast<uint4*>(sm + L::X3 + piece_off(i, cg * (SC / 8) + c8)) =
+        *reinterpret_cast<uint4*>(sm + Sm::S + piece_off(i, cg * (SC / 8) + c8)) =
             make_uint4(pack2<__nv_bfloat16>(s[0], s[1]), pack2<__nv_bfloat16>(s[2], s[3]),
                        pack2<__nv_bfloat16>(s[4], s[5]), pack2<__nv_bfloat16>(s[6], s[7]));
       }
@@ -328,23 +316,25 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     tc::fence_before_sync();
     arrive_warp(readyS);
   };
-  auto update_state = [&](float decl) {             // S' = e^{L_Q} S + dS
+  auto update_state = [&](float decl) {             // S' = e^{L_Q} S + dS, the small terms first
     const float dec = ex2(decl);
+    uint32_t r1[16], r2[16], r3[16];
+    tc::tmem_ld16(tl + COL_DS + cg * SC, r1);
+    tc::tmem_ld16(tl + COL_DS + PC + cg * SC, r2);
+    tc::tmem_ld16(tl + COL_DS + 2 * PC + cg * SC, r3);
+    tc::tmem_wait_ld16(r1);
+    tc::tmem_wait_ld16(r2);
+    tc::tmem_wait_ld16(r3);
 #pragma unroll
-    for (int b = 0; b < SC / 16; ++b) {
-      uint32_t r[16];
-      tc::tmem_ld16(tl + COL_DS + cg * SC + 16 * b, r);
-      tc::tmem_wait_ld16(r);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) S[16 * b + e] = fmaf(S[16 * b + e], dec, __uint_as_float(r[e]));
-    }
+    for (int e = 0; e < 16; ++e)
+      S[e] = fmaf(S[e], dec, (__uint_as_float(r3[e]) + __uint_as_float(r2[e])) + __uint_as_float(r1[e]));
   };
 
   // Rows without tokens: a fresh one's state is zero.
   if (!STATE && ta.empty_rows)
 #pragma unroll 1
     for (int e = blockIdx.x; e < ta.total; e += gridDim.x) {
-      const Unit v = unit_at<NH, PH>(ta, e);
+      const Unit v = unit_at(ta, e);
       float* to = pool_of(v);
       if (v.chunks == 0 && to && row_fresh(a.items[v.row]))
 #pragma unroll 1
@@ -352,47 +342,40 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     }
 
   int u = blockIdx.x;
-  Unit w = next_unit<NH, PH, STATE>(ta, u);
+  Unit w = next_unit<STATE>(ta, u);
   bool any = u < ta.total;
-  if (any && (TMA ? tid == 256 : wgb)) {
-    load_x(w, 0, 0);
-    load_bc(w, 0, true);
-    if (!STATE) load_bc(w, 0, false);
-  }
+  if (any && (TMA ? tid == 32 : wgb)) load(w, 0, 0);
   uint32_t gc = 0;                // chunks done, over all units
 
   // The two groups of warps run loops of their own, joined by barriers in
   // shared memory, so that one chunk's y is written while the next one's terms
-  // are formed.  Each barrier's phase is a chunk (gc counts them); none can run
-  // ahead by two: a chunk's products need the S that every warp shares after
-  // the chunk before, and W needs the decays, which are formed after the W
-  // before.
+  // are formed.  Each barrier's phase is a chunk (gc counts them; the pairs' a
+  // chunk of their parity).  A parity tells two phases apart, so nothing may
+  // complete two phases while somebody still waits for the first:
+  //   products  a chunk's dS, Y2 (and with it Y1 and the next G) need the S that
+  //             every warp shares, after its waits for the chunk before
+  //   decays    of chunk k + 1 are published after Y2 (STATE: dS) of chunk k,
+  //             which needs warps 0-7 to have seen those of chunk k
+  //   loads     of chunk k + 2 follow warps 0-7's (STATE: 8-15's) chunk k
   const int bt = tid - 256;
-  const bool scans = wgb && warp - 8 < NH;          // warps 8, 9 scan head warp - 8, four tokens a lane
-  const int sh = scans ? warp - 8 : 0;
-  // dt of the next chunk: the scanning warps' four tokens, the others' own token of every head
+  const bool scans = warp == 8;                     // four tokens a lane
+  // dt of the next chunk: the scanning warp's four tokens, the others' own token
   uint32_t raw[4];
-  float bias[NH], Ah = 0.f;
+  float bias = 0.f, Ah = 0.f;
   auto load_dt = [&](const Unit& v, int c) {
-    if (scans) {
+    if (wgb && !scans) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) raw[k] = raw_dt(v, v.s0 + c * Q + 4 * lane + k, sh);
-      Ah = a.A[v.h0 + sh];
-      bias[0] = bias_of(v.h0 + sh);
-    } else if (!wgb && !STATE) {
-#pragma unroll
-      for (int hh = 0; hh < NH; ++hh) {
-        raw[hh] = raw_dt(v, v.s0 + c * Q + i, hh);
-        bias[hh] = bias_of(v.h0 + hh);
-      }
-    }
+    for (int k = 0; k < 4; ++k)
+      if (scans || (k == 0 && !STATE)) raw[k] = raw_dt(v, v.s0 + c * Q + (scans ? 4 * lane + k : i));
+    Ah = a.A[v.h];
+    bias = a.dt_bias ? a.dt_bias[v.h] : 0.f;
   };
-  // decays of number k, a chunk of nt tokens, from raw
+  // decays of chunk number k with nt tokens, from raw
   auto scan = [&](uint32_t k2, int nt) {
     float dt[4], l[4], suf[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      dt[k] = 4 * lane + k < nt ? dt_of(raw[k], bias[0]) : 0.f;
+      dt[k] = 4 * lane + k < nt ? dt_of(raw[k], bias) : 0.f;
       l[k] = dt[k] * (Ah * LOG2E);
     }
     // tokens after j in its block of 32, summed from the end: no cancellation in the sums that matter
@@ -420,69 +403,63 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     float bs[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) bs[b] = __shfl_sync(0xffffffffu, post, 8 * b);
-    float* f = F + sh * 2 * Q;
+    float* f = decays(k2);
     *reinterpret_cast<float4*>(f + 4 * lane) = make_float4(before + l[0], before + l[1], before + l[2], pre);
     *reinterpret_cast<float4*>(f + Q + 4 * lane) =
         make_float4(ex2(after + suf[0]) * dt[0], ex2(after + suf[1]) * dt[1], ex2(after + suf[2]) * dt[2],
                     ex2(after + suf[3]) * dt[3]);
-    if ((lane & 7) == 7) blk[sh * 4 + (lane >> 3)] = pre;
+    if ((lane & 7) == 7) f[2 * Q + (lane >> 3)] = pre;
     if (lane < 4)
-      blk[8 + sh * 4 + lane] = ex2(lane == 0 ? bs[3] + bs[2] + bs[1] : lane == 1 ? bs[3] + bs[2] : lane == 2 ? bs[3] : 0.f);
-    if (lane == 0) blk[16 + 2 * (k2 & 1) + sh] = bs[3] + bs[2] + bs[1] + bs[0];
+      f[2 * Q + 4 + lane] = ex2(lane == 0 ? bs[3] + bs[2] + bs[1] : lane == 1 ? bs[3] + bs[2] : lane == 2 ? bs[3] : 0.f);
+    if (lane == 0) f[2 * Q + 8] = bs[3] + bs[2] + bs[1] + bs[0];
     __syncwarp();
     if (lane == 0) mbar_arrive(readyF);
   };
-  // G of the chunk that is number k, once its operands are there
+  // G and Y2 of chunk number k, once their operands are there.
   auto issue_g = [&](uint32_t k) {
-    wait(fullB, k & 1);
-    wait(fullC, k & 1);
+    wait2(fullB, k);
+    wait2(fullC, k);
     tc::fence_after_sync();
     constexpr uint32_t idG = tc::idesc_bf16_f32(128, 128);
+    const uint32_t bo = sb + Sm::B + (k & 1) * Sm::TILE, co = sb + Sm::C + (k & 1) * Sm::TILE;
 #pragma unroll 1
-    for (int j = 0; j < nk; ++j) {
-      const uint32_t o = (uint32_t)(j >> 2) * BLK64 + (uint32_t)(j & 3) * 32u;
-      tc::mma_bf16(tm + COL_G, tc::sdesc128(sb + L::C + o, 16u, 1024u), tc::sdesc128(sb + L::B + o, 16u, 1024u), idG,
-                   j > 0);
-    }
+    for (int j = 0; j < nk; ++j) tc::mma_bf16(tm + COL_G, k_cols(co, j), k_cols(bo, j), idG, j > 0);
     tc::mma_commit(barG);
   };
-  // its Y2, once S is there
   auto issue_y2 = [&](uint32_t k) {
-    wait(readyS, k & 1);
+    wait(readyS, k);
     tc::fence_after_sync();
     constexpr uint32_t idY = tc::idesc_bf16_f32(128, PC, false, true);
+    const uint32_t co = sb + Sm::C + (k & 1) * Sm::TILE;
 #pragma unroll 1
-    for (int j = 0; j < nk; ++j) {
-      const uint32_t o = (uint32_t)(j >> 2) * BLK64 + (uint32_t)(j & 3) * 32u;
-      tc::mma_bf16(tm + COL_Y2, tc::sdesc128(sb + L::C + o, 16u, 1024u),
-                   tc::sdesc128(sb + L::X3 + j * 2048u, BLK64, 1024u), idY, j > 0);
-    }
+    for (int j = 0; j < nk; ++j) tc::mma_bf16(tm + COL_Y2, k_cols(co, j), k_rows(sb + Sm::S, j), idY, j > 0);
     tc::mma_commit(barC);
   };
-  // A ragged chunk (number k, nt tokens) brought by tensor copies: what lies behind its last token is
-  // cleared in B and X.  (C's rows there give rows of y that are not kept.)
-  auto clear_tail = [&](uint32_t k, int nt) {
-    if (!TMA || nt >= Q) return;
-    wait(fullB, k & 1);
-    wait(fullX + 8 * (k & 1), (k >> 1) & 1);
+  // A ragged chunk (number k, nt tokens) brought by tensor copies: what lies behind its last token is cleared
+  // in B and X by the `n` threads from t on.  (C's rows there give rows of y that are not kept.)
+  auto clear_tail = [&](uint32_t k, int nt, int t) {
+    wait2(fullB, k);
+    if (!STATE) wait2(fullX, k);
 #pragma unroll 1
-    for (int e = tid; e < (Q - nt) * (16 + PC / 8); e += 256) {
+    for (int e = t; e < (Q - nt) * (STATE ? 16 : 24); e += 256) {
       const int r = nt + e % (Q - nt), cv = e / (Q - nt);
-      const uint32_t off = cv < 16 ? L::B + piece_off(r, cv) : L::X + (k & 1) * L::XT + piece_off(r, cv - 16);
+      const uint32_t off = cv < 16 ? Sm::B + (k & 1) * Sm::TILE + piece_off(r, cv)
+                                   : Sm::X + (k & 1) * BLK64 + piece_off(r, cv - 16);
       *reinterpret_cast<uint4*>(sm + off) = make_uint4(0u, 0u, 0u, 0u);
     }
     tc::fence_smem_to_async();
-    bar_named(1);
   };
   if (any) {
     load_dt(w, 0);
     if (scans) scan(0, w.s1 - w.s0);
+    wait(readyF, 0);
+    __syncthreads();
   }
   bool early = false;             // this chunk's G was issued in the chunk before
 #pragma unroll 1
   while (any) {
     int un = u + gridDim.x;
-    const Unit wn = next_unit<NH, PH, STATE>(ta, un);
+    const Unit wn = next_unit<STATE>(ta, un);
     const bool another = un < ta.total;
     load_state(w);
     share_state();
@@ -490,219 +467,170 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     if (wgb) {
 #pragma unroll 1
       for (int c = 0; c < w.chunks; ++c, ++gc) {
-        const uint32_t par = gc & 1u;
-        const uint32_t xs = L::X + par * L::XT;
         const int nt = min(Q, w.s1 - w.s0 - c * Q);
         const bool last = c + 1 == w.chunks, more = !last || another;
         const Unit wf = last ? wn : w;              // the chunk after this one
         const int cf = last ? 0 : c + 1;
-        if (STATE && TMA && more && bt == 0) load_x(wf, cf, par ^ 1u);
+        if (TMA && STATE && more && bt == 0) load(wf, cf, gc + 1);   // the chunk before is done with the buffers
         if (more) load_dt(wf, cf);
-        wait(readyF, par);
-        wait(fullX + 8 * par, (gc >> 1) & 1);
+        const float* f = decays(gc);
+        const uint32_t xs = Sm::X + (gc & 1) * BLK64;
+        wait(readyF, gc);
+        wait2(fullX, gc);
         // ---- X's three terms, then dS
-        const float decl = blk[16 + 2 * par + hcol];
-        constexpr int PIECES = Q * PC / 8 / 256;
-        uint32_t o3[PIECES][4];
+        const float decl = f[2 * Q + 8];
 #pragma unroll
-        for (int e = 0; e < PIECES; ++e) {
-          if (e % 4 == 0) asm volatile("" ::: "memory");   // four pieces in flight: registers
-          const int idx = bt + e * 256, t = (idx >> 3) & (Q - 1), cv = (idx & 7) + 8 * (idx >> 10);
+        for (int e = 0; e < Q * PC / 8 / 256; ++e) {
+          const int idx = bt + e * 256, t = idx >> 3, cv = idx & 7;
           const uint32_t off = piece_off(t, cv);
           uint4 xv = *reinterpret_cast<const uint4*>(sm + xs + off);
           if (t >= nt) xv = make_uint4(0u, 0u, 0u, 0u);     // a tensor copy brings what lies behind the row
-          const int hh = NH == 2 ? cv >> 3 : 0;
-          const float f = F[hh * 2 * Q + Q + t] * blk[8 + hh * 4 + (t >> 5)];
+          const float g = f[Q + t] * f[2 * Q + 4 + (t >> 5)];
           const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-          uint32_t o1[4], o2[4];
+          uint32_t o1[4], o2[4], o3[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float p = __uint_as_float(xw[k] << 16) * f, q = __uint_as_float(xw[k] & 0xffff0000u) * f;
+            float p = __uint_as_float(xw[k] << 16) * g, q = __uint_as_float(xw[k] & 0xffff0000u) * g;
             o1[k] = pack2<__nv_bfloat16>(p, q);
             p -= __uint_as_float(o1[k] << 16);
             q -= __uint_as_float(o1[k] & 0xffff0000u);
             o2[k] = pack2<__nv_bfloat16>(p, q);
             p -= __uint_as_float(o2[k] << 16);
             q -= __uint_as_float(o2[k] & 0xffff0000u);
-            o3[e][k] = pack2<__nv_bfloat16>(p, q);
+            o3[k] = pack2<__nv_bfloat16>(p, q);
           }
-          *reinterpret_cast<uint4*>(sm + L::X1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-          *reinterpret_cast<uint4*>(sm + L::X2 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+          *reinterpret_cast<uint4*>(sm + Sm::X1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+          *reinterpret_cast<uint4*>(sm + Sm::X1 + BLK64 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+          *reinterpret_cast<uint4*>(sm + Sm::X1 + 2 * BLK64 + off) = make_uint4(o3[0], o3[1], o3[2], o3[3]);
         }
-        if (!STATE) {
-          wait(barC, par);        // Y2 has read S and C; B is there, its ragged end cleared
-          if (TMA && more && bt == 0) load_bc(wf, cf, false);
-        } else {
-          wait(fullB, par);
-          if (TMA && nt < Q)
-#pragma unroll 1
-            for (int e = bt; e < (Q - nt) * 16; e += 256)
-              *reinterpret_cast<uint4*>(sm + L::B + piece_off(nt + e % (Q - nt), e / (Q - nt))) = make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int e = 0; e < PIECES; ++e) {
-          const int idx = bt + e * 256, t = (idx >> 3) & (Q - 1), cv = (idx & 7) + 8 * (idx >> 10);
-          *reinterpret_cast<uint4*>(sm + L::X3 + piece_off(t, cv)) = make_uint4(o3[e][0], o3[e][1], o3[e][2], o3[e][3]);
-        }
+        if (STATE && TMA && nt < Q) clear_tail(gc, nt, bt);
         tc::fence_smem_to_async();
-        tc::fence_before_sync();
         bar_named(2);
         if (bt == 0) {
-          if (STATE) wait(readyS, par);             // every warp has read the dS before
+          wait(readyS, gc);                         // every warp has read the dS before
+          if (STATE || nt == Q) wait2(fullB, gc);
+          else wait(barC, gc);                      // ragged: cleared before G and Y2
           tc::fence_after_sync();
-          constexpr uint32_t idS = tc::idesc_bf16_f32(128, PC, true, true);
+          constexpr uint32_t idS = tc::idesc_bf16_f32(128, 3 * PC, true, true);
+          const uint32_t bo = sb + Sm::B + (gc & 1) * Sm::TILE;
 #pragma unroll 1
-          for (int k = 0; k < 3 * Q / 16; ++k)
-            tc::mma_bf16(tm + COL_DS, tc::sdesc128(sb + L::B + (k & 7) * 2048u, BLK64, 1024u),
-                         tc::sdesc128(sb + L::X1 + (k >> 3) * L::XT + (k & 7) * 2048u, BLK64, 1024u), idS, k > 0);
+          for (int k = 0; k < Q / 16; ++k) tc::mma_bf16(tm + COL_DS, k_rows(bo, k), k_rows(sb + Sm::X1, k), idS, k > 0);
           tc::mma_commit(barS);
         }
-        wait(barS, par);
+        // Y2 done: S may be overwritten.  It was issued after warps 0-7 were done with the chunk before, whose
+        // decays and buffers are free
+        if (!STATE) wait(barC, gc);
+        else wait(barS, gc);
+        if (!TMA && more) load(wf, cf, gc + 1);
+        if (more && scans) scan(gc + 1, wf.s1 - wf.s0 - cf * Q);
+        wait(barS, gc);
         tc::fence_after_sync();
-        if (TMA && more && bt == 0) load_bc(wf, cf, true);   // dS (and G before it) have read B
         ltot += decl;
         update_state(decl);
         if (!last) share_state();
-        if (!TMA && more) {
-          load_x(wf, cf, par ^ 1u);
-          load_bc(wf, cf, true);
-          if (!STATE) load_bc(wf, cf, false);
-        }
-        if (more && scans) {
-          if (!STATE) wait(barY, par);   // W has been formed: the decays' arrays are free
-          scan(gc + 1, wf.s1 - wf.s0 - cf * Q);
-        }
       }
     } else {
 #pragma unroll 1
       for (int c = 0; c < w.chunks; ++c, ++gc) {
-        const uint32_t par = gc & 1u;
-        const uint32_t xs = L::X + par * L::XT;
         const int t0 = w.s0 + c * Q, nt = min(Q, w.s1 - t0);
         const bool last = c + 1 == w.chunks, more = !last || another;
         const Unit wf = last ? wn : w;              // the chunk after this one
         const int cf = last ? 0 : c + 1;
+        const float* f = decays(gc);
         if (STATE) {
-          wait(readyF, par);
-          const float decl = blk[16 + 2 * par + hcol];
-          wait(barS, par);
+          const float decl = f[2 * Q + 8];
+          wait(barS, gc);
           tc::fence_after_sync();
           ltot += decl;
           update_state(decl);
+          if (more) wait(readyF, gc + 1);
           if (!last) share_state();
           continue;
         }
-        // ---- this chunk's G and Y2, and the next one's X
-        clear_tail(gc, nt);
+        const uint32_t xs = Sm::X + (gc & 1) * BLK64;
+        // ---- this chunk's G and Y2, and the next one's operands
+        if (TMA && more && tid == 32) {
+          bulk_wait_read();                         // y of the chunk before has left its buffer
+          load(wf, cf, gc + 1);
+        }
+        if (TMA && nt < Q) {
+          clear_tail(gc, nt, tid);
+          bar_named(1);
+        }
         if (tid == 0) {
           if (!early) issue_g(gc);
           issue_y2(gc);
-          if (TMA && more) {
-            bulk_wait_read();                       // y of the chunk before has left the buffer
-            load_x(wf, cf, par ^ 1u);
-          }
         }
         early = false;
-        float own[NH];            // dt of token i
-#pragma unroll
-        for (int hh = 0; hh < NH; ++hh) own[hh] = i < nt ? dt_of(raw[hh], bias[hh]) : 0.f;
+        const float own = i < nt ? dt_of(raw[0], bias) : 0.f;     // dt of token i
         if (more) load_dt(wf, cf);
-        // ---- W from G, in place of G: columns 32 b + 16 hf .. + 15 of every block b.  The last head's W takes
-        // columns 64 .. 127, once both warps of the lanes have read blocks 2 and 3, another's 0 .. 63.
-        wait(readyF, par);
-        wait(fullX + 8 * par, (gc >> 1) & 1);
-        wait(barG, par);
+        // ---- W from G: columns 32 b + 16 hf .. + 15 of every block b
+        wait2(fullX, gc);
+        wait(barG, gc);
         tc::fence_after_sync();
-        const float decl = blk[16 + 2 * par + hcol];
-        float el[NH];
+        const float decl = f[2 * Q + 8], li = f[i];
 #pragma unroll
-        for (int hh = 0; hh < NH; ++hh) el[hh] = F[hh * 2 * Q + i];
-        uint32_t v[NH][4][8];
-        auto form = [&](int b) {
+        for (int b = 0; b < 4; ++b) {
           const int j0 = 32 * b + 16 * hf;
-          uint32_t G[16];
+          uint32_t v[8], G[16];
           if (b <= q4) {
             tc::tmem_ld16(tl + COL_G + j0, G);
             tc::tmem_wait_ld16(G);
           }
+          if (b < q4) {
+            const float rf = ex2(li - f[2 * Q + b]);
 #pragma unroll
-          for (int hh = 0; hh < NH; ++hh) {
-            const float* f = F + hh * 2 * Q;
-            const float li = el[hh];
-            if (b < q4) {
-              const float rf = ex2(li - blk[hh * 4 + b]);
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float4 cf4 = *reinterpret_cast<const float4*>(f + Q + j0 + 4 * e);
-                v[hh][b][2 * e] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e]) * (rf * cf4.x),
-                                                       __uint_as_float(G[4 * e + 1]) * (rf * cf4.y));
-                v[hh][b][2 * e + 1] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e + 2]) * (rf * cf4.z),
-                                                           __uint_as_float(G[4 * e + 3]) * (rf * cf4.w));
-              }
-            } else if (b == q4) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int j = j0 + 2 * e;
-                const float2 lj = *reinterpret_cast<const float2*>(f + j);
-                const float d0 = __shfl_sync(0xffffffffu, own[hh], 16 * hf + 2 * e),
-                            d1 = __shfl_sync(0xffffffffu, own[hh], 16 * hf + 2 * e + 1);
-                v[hh][b][e] = pack2<__nv_bfloat16>(j <= i ? __uint_as_float(G[2 * e]) * (ex2(li - lj.x) * d0) : 0.f,
-                                                   j + 1 <= i ? __uint_as_float(G[2 * e + 1]) * (ex2(li - lj.y) * d1) : 0.f);
-              }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[hh][b][e] = 0u;
+            for (int e = 0; e < 4; ++e) {
+              const float4 cf4 = *reinterpret_cast<const float4*>(f + Q + j0 + 4 * e);
+              v[2 * e] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e]) * (rf * cf4.x),
+                                              __uint_as_float(G[4 * e + 1]) * (rf * cf4.y));
+              v[2 * e + 1] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e + 2]) * (rf * cf4.z),
+                                                  __uint_as_float(G[4 * e + 3]) * (rf * cf4.w));
             }
-          }
-        };
-        form(2);
-        form(3);
-        tc::fence_before_sync();
-        bar_named(1);
-        tc::tmem_st8(tl + COL_G + 64 + 16 * 2 + 8 * hf, v[NH - 1][2]);
-        tc::tmem_st8(tl + COL_G + 64 + 16 * 3 + 8 * hf, v[NH - 1][3]);
-        form(0);
-        tc::tmem_st8(tl + COL_G + 64 + 8 * hf, v[NH - 1][0]);
-        form(1);
-        tc::tmem_st8(tl + COL_G + 64 + 16 + 8 * hf, v[NH - 1][1]);
-        if (NH == 2) {
-          tc::fence_before_sync();
-          bar_named(1);
+          } else if (b == q4) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b) tc::tmem_st8(tl + COL_G + 16 * b + 8 * hf, v[0][b]);
+            for (int e = 0; e < 8; ++e) {
+              const int j = j0 + 2 * e;
+              const float2 lj = *reinterpret_cast<const float2*>(f + j);
+              const float d0 = __shfl_sync(0xffffffffu, own, 16 * hf + 2 * e),
+                          d1 = __shfl_sync(0xffffffffu, own, 16 * hf + 2 * e + 1);
+              v[e] = pack2<__nv_bfloat16>(j <= i ? __uint_as_float(G[2 * e]) * (ex2(li - lj.x) * d0) : 0.f,
+                                          j + 1 <= i ? __uint_as_float(G[2 * e + 1]) * (ex2(li - lj.y) * d1) : 0.f);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 0u;
+          }
+          tc::tmem_st8(tl + COL_W + 16 * b + 8 * hf, v);
         }
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        bar_named(1);
+        bar_named(1);             // W is formed, G has been read
         if (tid == 0) {
           tc::fence_after_sync();
-          constexpr uint32_t id1 = tc::idesc_bf16_f32(128, PH, false, true);
+          constexpr uint32_t id1 = tc::idesc_bf16_f32(128, PC, false, true);
 #pragma unroll 1
-          for (int k = 0; k < NH * Q / 16; ++k)
-            tc::mma_bf16_ta(tm + COL_Y1 + (k >> 3) * PH, tm + COL_G + (NH == 1 ? 64 : 64 * (k >> 3)) + 8 * (k & 7),
-                            tc::sdesc128(sb + xs + (k >> 3) * (PH / 64 * BLK64) + (k & 7) * 2048u, BLK64, 1024u), id1,
-                            (k & 7) > 0);
+          for (int k = 0; k < Q / 16; ++k)
+            tc::mma_bf16_ta(tm + COL_Y1, tm + COL_W + 8 * k, k_rows(sb + xs, k), id1, k > 0);
           tc::mma_commit(barY);
+          // the next chunk's G, if its operands are there
+          if (more && wf.s1 - wf.s0 - cf * Q >= Q && mbar_try_wait(fullB + 8 * ((gc + 1) & 1), ((gc + 1) >> 1) & 1u) &&
+              mbar_try_wait(fullC + 8 * ((gc + 1) & 1), ((gc + 1) >> 1) & 1u)) {
+            issue_g(gc + 1);
+            early = true;
+          }
         }
-        wait(barC, par);
-        wait(barS, par);
+        wait(barC, gc);
+        wait(barS, gc);
         tc::fence_after_sync();
         update_state(decl);
         if (!last) share_state();
-        wait(barY, par);
+        wait(barY, gc);
         tc::fence_after_sync();
-        // the next chunk's G, now if its operands are there: W's place is free
-        if (tid == 0 && more && wf.s1 - wf.s0 - cf * Q >= Q && mbar_try_wait(fullB, par ^ 1u) &&
-            mbar_try_wait(fullC, par ^ 1u)) {
-          issue_g(gc + 1);
-          early = true;
-        }
         // ---- y = Y1 + e^{L_i} Y2 + D x, over x in shared memory (its terms are formed)
-        const int hh = NH == 2 ? hf : 0;
-        const float ei = ex2(NH == 2 && hf ? el[NH - 1] : el[0]);
-        const float Dh = a.D ? a.D[w.h0 + hh] : 0.f;
+        const float ei = ex2(li), Dh = a.D ? a.D[w.h] : 0.f;
         const bool direct = !TMA || nt < Q;
-#pragma unroll 1
+#pragma unroll
         for (int c16 = 0; c16 < HC / 16; ++c16) {
           uint32_t r1[16], r2[16];
           tc::tmem_ld16(tl + COL_Y1 + hf * HC + 16 * c16, r1);
@@ -726,30 +654,27 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
             *xp = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
+        if (more) wait(readyF, gc + 1);             // before the next Y2, after which the decays after those come
         tc::fence_smem_to_async();
         tc::fence_before_sync();
         bar_named(1);             // y is in shared memory, and its accumulators are free
         if (!direct) {
-          if (tid == 0 && ok) {
-#pragma unroll
-            for (int b = 0; b < PC / 64; ++b) {
-              const int p = w.p0 + (NH == 1 ? 64 * b : 0);
-              if (p < a.P)
-                tma_store(&ta.my, p, w.h0 + (NH == 1 ? 0 : b), w.begin + t0, a.y.sn ? w.row : 0, sb + xs + b * BLK64);
-            }
+          if (tid == 32 && ok) {
+            tma_store(&ta.my, w.p0, w.h, w.begin + t0, a.y.sn ? w.row : 0, sb + xs);
             bulk_commit();
           }
-        } else if (ok) {
+        } else {
           // a ragged chunk's rows (or unaligned ones), value by value
-          uint16_t* yr = static_cast<uint16_t*>(const_cast<void*>(a.y.p)) + tok(w, a.y, t0) + (int64_t)w.h0 * a.P + w.p0;
-          const int pw = min(PH, a.P - w.p0);
+          uint16_t* yr = static_cast<uint16_t*>(const_cast<void*>(a.y.p)) + tok(w, a.y, t0) + (int64_t)w.h * a.P + w.p0;
+          const int pw = min(PC, a.P - w.p0);
+          if (ok)
 #pragma unroll 1
-          for (int e = tid; e < nt * PC; e += 256) {
-            const int t = e / PC, col = e % PC, p = col % PH;
-            if (p < pw)
-              yr[(int64_t)t * a.y.st + (int64_t)(col / PH) * a.P + p] =
-                  *reinterpret_cast<const uint16_t*>(sm + xs + piece_off(t, col >> 3) + 2 * (col & 7));
-          }
+            for (int e = tid; e < nt * PC; e += 256) {
+              const int t = e / PC, p = e % PC;
+              if (p < pw)
+                yr[(int64_t)t * a.y.st + p] =
+                    *reinterpret_cast<const uint16_t*>(sm + xs + piece_off(t, p >> 3) + 2 * (p & 7));
+            }
           bar_named(1);           // read before the buffer is filled again
         }
       }
@@ -759,10 +684,12 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     w = wn;
     any = another;
   }
-  if (TMA && !STATE && tid == 0) bulk_wait();
+  if (TMA && !STATE && tid == 32) bulk_wait();
   if (!__syncthreads_and(ok)) {    // let what was issued land before the memory is given back
-    if (tid == 256 && gc > 0) mbar_drain(barS, (gc - 1) & 1u);
-    if (!STATE && tid == 0 && gc > 0) mbar_drain(barY, (gc - 1) & 1u);
+    if (tid == 0 && gc > 0) {
+      mbar_drain(barS, (gc - 1) & 1u);
+      if (!STATE) mbar_drain(barY, (gc - 1) & 1u);
+    }
     __syncthreads();
   }
   if (warp == 0) tc::tmem_dealloc(tm, 512);
@@ -770,28 +697,27 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
 
 thread_local TcArgs t_tc;
 
-template <int NH, int PH, bool STATE, bool TMA>
+template <bool STATE, bool TMA>
 cudaError_t go(const TcArgs& t, int sms, cudaStream_t s) {
-  constexpr int BYTES = (int)Smem<NH * PH>::BYTES;
   static thread_local int ready = -1;              // the device whose limit is raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (ready != dev) {
-    e = cudaFuncSetAttribute(ssm_tc_kernel<NH, PH, STATE, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    e = cudaFuncSetAttribute(ssm_tc_kernel<STATE, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sm::BYTES);
     if (e != cudaSuccess) return e;
     ready = dev;
   }
-  ssm_tc_kernel<NH, PH, STATE, TMA><<<(unsigned)(t.total < sms ? t.total : sms), TCT, BYTES, s>>>(t);
+  ssm_tc_kernel<STATE, TMA><<<(unsigned)(t.total < sms ? t.total : sms), TCT, Sm::BYTES, s>>>(t);
   return cudaGetLastError();
 }
-template <int NH, int PH, bool TMA>
+template <bool TMA>
 cudaError_t both(const TcArgs& t, bool split, int sms, cudaStream_t s) {
   if (split) {
-    const cudaError_t e = go<NH, PH, true, TMA>(t, sms, s);
+    const cudaError_t e = go<true, TMA>(t, sms, s);
     if (e != cudaSuccess) return e;
   }
-  return go<NH, PH, false, TMA>(t, sms, s);
+  return go<false, TMA>(t, sms, s);
 }
 
 using EncodeFn = decltype(&cuTensorMapEncodeTiled);
@@ -822,19 +748,16 @@ bool encode(CUtensorMap* m, const TokView& v, int width, int heads, int64_t toke
 
 }  // namespace
 
-SsmPlan ssm_tc_plan(int H, int G, int P, int rows, const int32_t* lens, int64_t T, int sms) {
+SsmPlan ssm_tc_plan(int H, int P, int rows, const int32_t* lens, int64_t T, int sms) {
   SsmPlan p{};
   p.sms = sms;
-  p.ph = P > 64 ? 128 : 64;
-  p.ptiles = (P + p.ph - 1) / p.ph;
+  p.ptiles = (P + PC - 1) / PC;
   int64_t longest = 0;
   for (int i = 0; i < rows; ++i) {
     const int64_t c = ((lens ? lens[i] : T) + Q - 1) / Q;
     longest = c > longest ? c : longest;
   }
-  const int64_t base = (int64_t)rows * H * p.ptiles;
-  p.nh = p.ph == 64 && (H / G) % 2 == 0 && base >= 2 * (int64_t)sms ? 2 : 1;
-  p.units = H / p.nh * p.ptiles;
+  p.units = H * p.ptiles;
   p.seg_tokens = Q * (int)(longest > 0 ? longest : 1);
   // Segments as short as still fill the GPU once: each runs two launches, so
   // at least three of them in the longest row are wanted, and at most 16,
@@ -869,9 +792,7 @@ cudaError_t launch_ssm_tc(bool vec, int64_t tokens, const SsmArgs& a, const SsmP
   for (int i = 0; i < a.rows; ++i) t.empty_rows |= row_len(a.items[i]) == 0;
   const bool tma = vec && encode(&t.mx, a.x, a.P, a.H, tokens, a.rows) && encode(&t.mb, a.B, a.N, a.G, tokens, a.rows) &&
                    encode(&t.mc, a.C, a.N, a.G, tokens, a.rows) && encode(&t.my, a.y, a.P, a.H, tokens, a.rows);
-  if (p.ph == 128) return tma ? both<1, 128, true>(t, p.split, p.sms, s) : both<1, 128, false>(t, p.split, p.sms, s);
-  if (p.nh == 2) return tma ? both<2, 64, true>(t, p.split, p.sms, s) : both<2, 64, false>(t, p.split, p.sms, s);
-  return tma ? both<1, 64, true>(t, p.split, p.sms, s) : both<1, 64, false>(t, p.split, p.sms, s);
+  return tma ? both<true>(t, p.split, p.sms, s) : both<false>(t, p.split, p.sms, s);
 }
 
 cudaError_t read_mixer_status(cudaStream_t s, int32_t* code) {
