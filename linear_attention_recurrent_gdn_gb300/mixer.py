@@ -48,7 +48,7 @@ _ADD = struct.Struct("=6q2d8q4q")
 def _signatures(lib):
     for name in ("dl_conv", "dl_ssm", "dl_ssm_step", "dl_gated_norm", "dl_add_norm"):
         fn = getattr(lib, name)
-        fn.argtypes = [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_char_p, ctypes.c_int32]
+        fn.argtypes = [ctypes.c_char_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32]
         fn.restype = ctypes.c_int32
     lib.dl_mixer_sync.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32), ctypes.c_char_p, ctypes.c_int32]
     lib.dl_mixer_sync.restype = ctypes.c_int32
@@ -63,10 +63,12 @@ _F32 = torch.float32
 
 
 def _call(fn, args, dev):
-    err = getattr(_local, "err", None)
-    if err is None:
-        err = _local.err = ctypes.create_string_buffer(_ERR)
-    rc = fn(args, _raw_stream(dev), err, _ERR)
+    try:
+        err, at = _local.err
+    except AttributeError:
+        err = ctypes.create_string_buffer(_ERR)
+        err, at = _local.err = err, ctypes.addressof(err)
+    rc = fn(args, _raw_stream(dev), at, _ERR)
     if rc:
         raise _dl.DeltaLogError(rc, err.value.decode())
 
@@ -80,7 +82,16 @@ def sync(device=None):
 
 
 # The checks below are written for few Python steps: in a decode loop they are
-# the cost of a call.
+# the cost of a call.  A CPU tensor's device number is -1.
+
+def _bad(name, t, dtype, dev):
+    """Says what is wrong with a tensor that failed a check."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires a gradient: these operators have no backward" % name)
+    raise ValueError("%s: expected %s on device %s, got %s on %s" % (name, dtype, dev, t.dtype, t.device))
+
 
 def _x(t):
     """The first tensor of a call; returns its device's number."""
@@ -93,22 +104,21 @@ def _x(t):
     return t.get_device()
 
 
-def _cuda(name, t, dtype, dev):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dtype is not dtype or t.get_device() != dev:
-        raise ValueError("%s: expected %s on device %d, got %s on %s" % (name, dtype, dev, t.dtype, t.device))
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s requires a gradient: these operators have no backward" % name)
+def _check(name, t, shape, dtype, dev):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or \
+            (t.requires_grad and torch.is_grad_enabled()):
+        _bad(name, t, dtype, dev)
+    if t.shape != shape:
+        raise ValueError("%s: expected %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
 def _param(name, t, shape, dtype, dev):
     """A contiguous parameter; returns its address (0 for None)."""
     if t is None:
         return 0
-    _cuda(name, t, dtype, dev)
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s: expected contiguous %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    _check(name, t, shape, dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
@@ -124,9 +134,7 @@ def _dense(name, t, inner, stride):
 
 def _tokens(name, t, shape, dtype, dev, inner, lead):
     """A per-token tensor: checks it and returns (data, stride between tokens, between rows)."""
-    _cuda(name, t, dtype, dev)
-    if t.shape != shape:
-        raise ValueError("%s: expected %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    _check(name, t, shape, dtype, dev)
     stride = t.stride()
     if not t.is_contiguous():
         _dense(name, t, inner, stride)
@@ -252,7 +260,7 @@ def _ssm(fn, x, dt, A, B, C, D, dt_bias, dt_softplus, slots, state, lengths, fre
     fields, pool, lead, keep = _rows(lead_shape, step, slots, lengths, fresh, state, dev, (H, P, N), _F32)
     maps, dtt = lead_shape + (G, N), _F32 if dt.dtype is _F32 else xt
     if out is None:
-        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     head = fields + (_DTYPE[xt], dtt is _F32, bool(dt_softplus), H, G, P, N) \
         + _tokens("x", x, shape, xt, dev, 2, lead) + _tokens("dt", dt, lead_shape + (H,), dtt, dev, 1, lead) \
         + _tokens("B", B, maps, xt, dev, 2, lead) + _tokens("C", C, maps, xt, dev, 2, lead) \
@@ -287,9 +295,7 @@ def ssm_step(x, dt, A, B, C, D=None, *, dt_bias=None, dt_softplus=True, slots, s
 
 def _matrix(name, t, shape, dtype, dev, inner):
     """A tensor of rows: checks it and returns its address and the stride between rows."""
-    _cuda(name, t, dtype, dev)
-    if t.shape != shape:
-        raise ValueError("%s: expected %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    _check(name, t, shape, dtype, dev)
     stride = t.stride()
     if not t.is_contiguous():
         _dense(name, t, inner, stride)
@@ -315,8 +321,10 @@ def gated_norm(x, weight, gate=None, *, bias=None, kind="rms", activation="silu"
     xp, xs = _matrix("x", x, shape, dt, dev, 2)
     gp, gs = (0, 0) if gate is None else _matrix("gate", gate, shape, dt, dev, 2)
     if out is None:
-        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
-    op, os = _matrix("out", out, shape, dt, dev, 2)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        op, os = out.data_ptr(), shape[1] * shape[2]
+    else:
+        op, os = _matrix("out", out, shape, dt, dev, 2)
     _call(_lib.dl_gated_norm, _GATED.pack(_DTYPE[dt], wt is _F32, heads, *shape, _KIND[kind], _ACT[activation],
                                           bool(gate_first), eps, xp, gp, wp, bp, op, xs, gs, os), dev)
     return out
@@ -346,11 +354,15 @@ def add_norm(x, residual, weight, *, bias=None, scale=None, alpha=1.0, post_weig
     xp, xs = _matrix("x", x, shape, dt, dev, 1)
     rp, rs = (0, 0) if residual is None else _matrix("residual", residual, shape, rt, dev, 1)
     if out is None:
-        out = torch.empty_like(x) if x.is_contiguous() else x.new_empty(shape)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        op, os = out.data_ptr(), shape[1]
+    else:
+        op, os = _matrix("out", out, shape, dt, dev, 1)
     if out_residual is None:
-        out_residual = torch.empty(shape, dtype=rt, device=x.device)
-    op, os = _matrix("out", out, shape, dt, dev, 1)
-    hp, hs = _matrix("out_residual", out_residual, shape, rt, dev, 1)
+        out_residual = torch.empty_like(x if rt is dt else residual, memory_format=torch.contiguous_format)
+        hp, hs = out_residual.data_ptr(), shape[1]
+    else:
+        hp, hs = _matrix("out_residual", out_residual, shape, rt, dev, 1)
     _call(_lib.dl_add_norm, _ADD.pack(_DTYPE[dt], rt is _F32, wt is _F32, *shape, _KIND[kind], eps, alpha, xp, rp, wp,
                                       bp, sp, pp, op, hp, xs, rs, os, hs), dev)
     return out, out_residual
