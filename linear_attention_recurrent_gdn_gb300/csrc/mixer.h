@@ -98,6 +98,8 @@ SsmPlan ssm_scan_plan(int H, int P, int N, int rows, const int32_t* lens, int64_
 // vec: x, B, C and y are 16-byte aligned, in their strides and widths too.
 cudaError_t launch_ssm_scan(int dtype, bool vec, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row, float* ws,
                             cudaStream_t s);
+// The states at the segments' starts from each segment's own end state and decay (in place).
+cudaError_t launch_ssm_join(const SsmArgs& a, int seg_tokens, int tiles, int per_row, float* ws, cudaStream_t s);
 SsmPlan ssm_tc_plan(int H, int P, int rows, const int32_t* lens, int64_t T, int sms);
 // bf16, N <= 128.  tokens: extent of the token axis (packed: all rows').
 cudaError_t launch_ssm_tc(bool vec, int64_t tokens, const SsmArgs& a, const SsmPlan& p, int tiles, int per_row,

@@ -11,8 +11,9 @@
 // runs here.
 //
 // Segments: a first launch (STATE) runs each but the last from zero (the first
-// from the row's state) and leaves its end state and decay in the workspace;
-// the full launch joins those before its segment.
+// from the row's state) and leaves its end state and decay in the workspace; a
+// second joins them to the states at the segments' starts; the full launch
+// goes on from those.
 #include "mixer_device.cuh"
 
 namespace dl {
@@ -59,15 +60,13 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
   };
   const int64_t per_tile = (int64_t)a.H * a.P * a.N, e0 = ((int64_t)h * a.P + p0 + pl) * a.N;
   float* pool = a.state ? a.state + (int64_t)it.slot * per_tile : nullptr;
-  const float* wl = sa.ws + (int64_t)sa.tiles * per_tile;
   auto col = [&](int i) { return 4 * (ln + NL * (i >> 2)) + (i & 3); };
   auto on = [&](int r, int i) { return p0 + pl + r < a.P && col(i) < a.N; };
   float S[PR][16];
   {
     const float* from;
     if (STATE || nseg == 1) from = seg == 0 && pool && !row_fresh(it) ? pool : nullptr;
-    else if (seg == 0) from = row_fresh(it) ? nullptr : sa.ws + (int64_t)tile * per_tile;
-    else from = sa.ws + (int64_t)(tile - seg + 1) * per_tile;
+    else from = seg == 0 && row_fresh(it) ? nullptr : sa.ws + (int64_t)tile * per_tile;
 #pragma unroll
     for (int r = 0; r < PR; ++r)
 #pragma unroll
@@ -80,16 +79,6 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
         for (int i = 0; i < 16; ++i)
           if (on(r, i)) sa.ws[(int64_t)tile * per_tile + e0 + (int64_t)r * a.N + col(i)] = S[r][i];
     }
-    if (!STATE)
-#pragma unroll 1
-      for (int k = 2; k <= seg; ++k) {
-        const float* add = sa.ws + (int64_t)(tile - seg + k) * per_tile + e0;
-        const float d = exp2f(wl[(int64_t)(tile - seg + k - 1) * a.H + h]);
-#pragma unroll
-        for (int r = 0; r < PR; ++r)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) S[r][i] = fmaf(S[r][i], d, on(r, i) ? add[(int64_t)r * a.N + col(i)] : 0.f);
-      }
   }
   f2 S2[PR][8];
 #pragma unroll
@@ -222,13 +211,51 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
     sa.ws[(int64_t)sa.tiles * per_tile + (int64_t)tile * a.H + h] = ltot * LOG2E;
 }
 
-thread_local ScanArgs t_scan;
+// Workspace entry tile0 + k of a row holds the state that segment k - 1 ended
+// with, having started from zero (segment 0: from the row's state).  Turns the
+// entries into the states that the segments start with:
+//   s_1 = e_1,  s_k = decay_{k-1} s_{k-1} + e_k
+// An element a thread; a few entries on their way at a time.
+__global__ void __launch_bounds__(256)
+ssm_join_kernel(const __grid_constant__ ScanArgs sa) {
+  const SsmArgs& a = sa.a;
+  const int row = blockIdx.y, len = row_len(a.items[row]);
+  const int tile0 = sa.per_row ? row * sa.per_row : a.items[row].tile0;
+  const int nseg = len > sa.seg_tokens ? (len + sa.seg_tokens - 1) / sa.seg_tokens : 1;
+  const int64_t per_tile = (int64_t)a.H * a.P * a.N, e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= per_tile || nseg < 3) return;
+  const float* dl = sa.ws + (int64_t)sa.tiles * per_tile + (int64_t)tile0 * a.H + e / (a.P * a.N);
+  float* at = sa.ws + (int64_t)(tile0 + 1) * per_tile + e;
+  float s = *at;
+  constexpr int U = 5;
+  for (int k = 2; k < nseg; k += U) {
+    float v[U], d[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const bool on = k + i < nseg;
+      v[i] = on ? at[(int64_t)(k + i - 1) * per_tile] : 0.f;
+      d[i] = on ? dl[(int64_t)(k + i - 1) * a.H] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+      if (k + i < nseg) {
+        s = fmaf(s, exp2f(d[i]), v[i]);
+        at[(int64_t)(k + i - 1) * per_tile] = s;
+      }
+  }
+}
+
+thread_local ScanArgs t_scan, t_join;
 
 template <class T, int NL, bool VEC>
 cudaError_t go_vec(const ScanArgs& k, bool split, cudaStream_t s) {
   constexpr int PB = SC_THREADS / NL * rows_of(NL);
   const unsigned grid = (unsigned)((int64_t)k.tiles * k.a.H * ((k.a.P + PB - 1) / PB));
-  if (split) ssm_scan_kernel<T, NL, true, VEC><<<grid, SC_THREADS, 0, s>>>(k);
+  if (split) {
+    ssm_scan_kernel<T, NL, true, VEC><<<grid, SC_THREADS, 0, s>>>(k);
+    const cudaError_t e = launch_ssm_join(k.a, k.seg_tokens, k.tiles, k.per_row, k.ws, s);
+    if (e != cudaSuccess) return e;
+  }
   ssm_scan_kernel<T, NL, false, VEC><<<grid, SC_THREADS, 0, s>>>(k);
   return cudaGetLastError();
 }
@@ -250,6 +277,18 @@ cudaError_t go_n(const ScanArgs& k, bool vec, bool split, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t launch_ssm_join(const SsmArgs& a, int seg_tokens, int tiles, int per_row, float* ws, cudaStream_t s) {
+  ScanArgs& k = t_join;
+  k.a = a;
+  k.ws = ws;
+  k.seg_tokens = seg_tokens;
+  k.tiles = tiles;
+  k.per_row = per_row;
+  const int64_t n = (int64_t)a.H * a.P * a.N;
+  ssm_join_kernel<<<dim3((unsigned)((n + 255) / 256), (unsigned)a.rows), 256, 0, s>>>(k);
+  return cudaGetLastError();
+}
+
 SsmPlan ssm_scan_plan(int H, int P, int N, int rows, const int32_t* lens, int64_t T, int sms) {
   SsmPlan p{};
   const int nl = lanes_of(N), pb = SC_THREADS / nl * rows_of(nl);
@@ -258,8 +297,8 @@ SsmPlan ssm_scan_plan(int H, int P, int N, int rows, const int32_t* lens, int64_
   for (int i = 0; i < rows; ++i) longest = (lens ? lens[i] : T) > longest ? (lens ? lens[i] : T) : longest;
   p.seg_tokens = (int)(longest > 0 ? longest : 1);
   // Segments for a call that would leave most SMs with less than one CTA: two
-  // launches instead of one, so at least four segments in the longest row, at
-  // most 16 (the last joins the states of all before it), of 32 tokens or more.
+  // more launches, so at least four segments in the longest row, at most 16, of
+  // 32 tokens or more.
   for (int64_t seg = (longest + 15) / 16 < 32 ? 32 : (longest + 15) / 16; 4 * seg <= longest; seg += (seg + 3) / 4) {
     int64_t tiles = 0;
     for (int i = 0; i < rows; ++i) {

@@ -10,28 +10,29 @@
 //   G  [128 x 128] = C B^T               exact products of the inputs
 //   Y2 [128 x 64]  = C S^T               S rounded to bf16
 //   Y1 [128 x 64]  = W X                 W_ij = G_ij e^{L_i - L_j} dt_j rounded to bf16, A in TMEM
-//   dS [128 x 192] = B^T [X1 X2 X3]      e^{T_j} dt_j x_j as three bf16 terms (2^-25 of it is left)
+//   dS [128 x 64]  = B^T (X3 + X2 + X1)  e^{T_j} dt_j x_j as three bf16 terms (2^-25 of it is left)
 // W and the S of Y2 are rounded once, like the output itself (half a step of
 // bf16 each); the state keeps 32 bits: it lives in registers in fp32 and its
-// increments are formed from all 24 bits, the terms' sums side by side in one
-// product: fewer and wider MMAs.  e^{L_i - L_j} outside
-// the diagonal 32 x 32 blocks is the product of a row and a column factor, both
-// at most one: e^{L_i - L_b} e^{L_b - L_j}, b the last token of j's block, so
-// only the diagonal blocks take an exponential a pair.
+// increments are formed from all 24 bits.  e^{L_i - L_j} outside the diagonal
+// 32 x 32 blocks is the product of a row and a column factor, both at most
+// one: e^{L_i - L_b} e^{L_b - L_j}, b the last token of j's block, so only the
+// diagonal blocks take an exponential a pair.
 //
-// A persistent CTA of 16 warps takes units: one head's 64 state rows over a
+// A persistent CTA of eight warps takes units: one head's 64 state rows over a
 // segment of a row.  B and C of the group, X, its terms and S sit in shared
 // memory as rows of 64 values in the 128-byte swizzle, read K-major or MN-major
-// as a product needs, so nothing is transposed; tensor copies bring B, C and X a
-// chunk ahead, across units too (and, but for a row's ragged last chunk, take y
-// away).  Warps 0-7 form W and y, warps 8-15 X's terms; all of them hold the
-// state, a quarter of the columns each.  With nearly all of the SM's memory
-// used as shared memory there is next to no L1 cache, so nothing may spill: 128
-// rows a unit, or two heads, measured slower for that.
+// as a product needs, so nothing is transposed; tensor copies bring B, C and X
+// (and, but for a row's ragged last chunk, take y away).  A chunk's phases
+// depend on one another, so the latency of each counts; two CTAs on an SM fill
+// each other's waits.  For that a CTA keeps to half of the shared memory and of
+// TMEM: the terms take the places of C and S once Y2 has read them, W and dS
+// those of G.  With nearly all of the SM's memory used as shared memory there
+// is next to no L1 cache, so nothing may spill.
 //
 // Rows with few heads are split into segments: a first launch (STATE) runs
-// each segment from zero and leaves its end state and decay in the workspace,
-// and the full launch joins those before its segment.
+// each segment from zero and leaves its end state and decay in the workspace, a
+// second joins them to the states at the segments' starts, and the full launch
+// goes on from those.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -46,30 +47,29 @@ static __device__ int32_t g_mixer_status;
 
 namespace {
 
-constexpr int Q = 128, PC = 64, TCT = 512;
-constexpr int HC = PC / 2;        // columns of one of the two warps of a lane quarter in a group of warps
-constexpr int SC = PC / 4;        // state columns of one of the four warps of a lane quarter
-constexpr uint32_t COL_G = 0, COL_W = 128, COL_Y1 = 192, COL_Y2 = 256, COL_DS = 320;
+constexpr int Q = 128, PC = 64, TCT = 256;
+constexpr int HC = PC / 2;        // columns of one of the two warps of a lane quarter
+constexpr uint32_t COL_G = 0, COL_DS = 0, COL_W = 64, COL_Y1 = 128, COL_Y2 = 192, COLS = 256;
 constexpr uint32_t BLK64 = Q * 128;                  // bytes of 128 rows of 64 values
 constexpr float LOG2E = 1.4426950408889634f;
 
-// Shared memory; B, C, X and the decays are doubled (even and odd chunks).
 struct Sm {
   static constexpr uint32_t TILE = 2 * BLK64;        // B or C: 128 tokens x 128 state columns
-  static constexpr uint32_t B = 0, C = 2 * TILE, X = 4 * TILE, X1 = X + 2 * BLK64, S = X1 + 3 * BLK64;
+  static constexpr uint32_t B = 0, C = TILE, X = 2 * TILE, S = X + BLK64;
+  static constexpr uint32_t X1 = C, X2 = C + BLK64, X3 = S;
   static constexpr uint32_t F = S + BLK64;           // L [128], column factors [128], L at the blocks' ends [4],
   static constexpr uint32_t FB = (2 * Q + 12) * 4;   // e^{T} of the blocks' last tokens [4], log2 of the chunk's decay
-  static constexpr uint32_t BAR = F + 2 * FB;        // twelve mbarriers, TMEM address
-  static constexpr uint32_t BYTES = BAR + 112;
+  static constexpr uint32_t BAR = F + FB;            // seven mbarriers, TMEM address
+  static constexpr uint32_t BYTES = BAR + 64;
 };
-static_assert(Sm::BYTES <= 232448, "shared memory");
+static_assert(2 * (Sm::BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void bar_named(int id) { asm volatile("bar.sync %0, 256;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void bar_pair(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3,
                                          uint32_t bar) {
   asm volatile(
@@ -156,41 +156,31 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par) {
 // TMA: tensor copies (16-byte aligned tensors, widths and strides); else
 // threads copy value by value.
 template <bool STATE, bool TMA>
-__global__ void __launch_bounds__(TCT, 1)
+__global__ void __launch_bounds__(TCT, 2)
 ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
   extern __shared__ __align__(1024) unsigned char sm[];
   const SsmArgs& a = ta.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = warp & 3, hf = (warp >> 2) & 1, cg = warp >> 2;
-  const bool wgb = warp >= 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, q4 = warp & 3, hf = warp >> 2;
   const int i = 32 * q4 + lane;                     // this thread's token row; its state column n
   const int nk = (a.N + 15) / 16;                   // K steps over the state columns
+  const bool scans = warp == 7;                     // this warp forms the decays, four tokens a lane
 
   const uint32_t sb = smem_u32(sm);
-  auto decays = [&](uint32_t k) { return reinterpret_cast<float*>(sm + Sm::F + (k & 1) * Sm::FB); };
+  float* f = reinterpret_cast<float*>(sm + Sm::F);
   const uint32_t barG = sb + Sm::BAR, barC = barG + 8, barS = barG + 16, barY = barG + 24, fullB = barG + 32,
-                 fullC = barG + 48, fullX = barG + 64, readyS = barG + 80, readyF = barG + 88;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sm::BAR + 96);
+                 fullC = barG + 40, fullX = barG + 48;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sm::BAR + 56);
 
-  if (warp == 0) tc::tmem_alloc(sb + Sm::BAR + 96, 512);
+  if (warp == 0) tc::tmem_alloc(sb + Sm::BAR + 56, COLS);
   if (tid == 0) {
-    // products: one commit; loads: one thread's tensor copies, or the eight warps that copy; S: every warp;
-    // the decays: one warp
-    for (int k = 0; k < 4; ++k) mbar_init(barG + 8 * k, 1);
-    for (int k = 4; k < 10; ++k) mbar_init(barG + 8 * k, TMA ? 1 : 8);
-    mbar_init(readyS, TCT / 32);
-    mbar_init(readyF, 1);
+    for (int k = 0; k < 7; ++k) mbar_init(barG + 8 * k, 1);
     fence_mbar_init();
   }
 
   auto tok = [&](const Unit& w, const TokView& v, int t) { return (int64_t)(w.begin + t) * v.st + (int64_t)w.row * v.sn; };
-  auto arrive_warp = [&](uint32_t bar) {            // this warp's writes to shared memory are done
-    tc::fence_smem_to_async();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-  };
   auto copy_rows = [&](uint32_t dst, const uint16_t* src, int64_t st, int nt, int width, int cols) {
 #pragma unroll 1
-    for (int e = tid - 256; e < Q * cols / 8; e += 256) {
+    for (int e = tid; e < Q * cols / 8; e += TCT) {
       const int r = e & (Q - 1), cv = e / Q;
       const uint16_t* p = src + (int64_t)r * st + cv * 8;
       uint32_t v[4];
@@ -203,33 +193,34 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       *reinterpret_cast<uint4*>(sm + dst + piece_off(r, cv)) = make_uint4(v[0], v[1], v[2], v[3]);
     }
   };
-  // Chunk c of unit w, number k of all, into its buffers.  TMA: one thread calls; else warps 8-15 copy.
-  auto load = [&](const Unit& w, int c, uint32_t k) {
-    const uint32_t b = k & 1;
+  // Chunk c of unit w into its places.  TMA: one thread calls; else all copy.
+  auto load_bc = [&](const Unit& w, int c) {
     const int t0 = w.s0 + c * Q, g = w.h / (a.H / a.G);
-    const uint32_t xd = Sm::X + b * BLK64, bd = Sm::B + b * Sm::TILE, cd = Sm::C + b * Sm::TILE;
-    const uint32_t fx = fullX + 8 * b, fb = fullB + 8 * b, fc = fullC + 8 * b;
     if (TMA) {
-      mbar_arrive_expect_tx(fx, BLK64);
-      tma_load(sb + xd, &ta.mx, w.p0, w.h, w.begin + t0, a.x.sn ? w.row : 0, fx);
       const int nb = a.N > 64 ? 2 : 1;
-      mbar_arrive_expect_tx(fb, nb * BLK64);
-      for (int e = 0; e < nb; ++e) tma_load(sb + bd + e * BLK64, &ta.mb, 64 * e, g, w.begin + t0, a.B.sn ? w.row : 0, fb);
+      mbar_arrive_expect_tx(fullB, nb * BLK64);
+      for (int e = 0; e < nb; ++e)
+        tma_load(sb + Sm::B + e * BLK64, &ta.mb, 64 * e, g, w.begin + t0, a.B.sn ? w.row : 0, fullB);
       if (!STATE) {
-        mbar_arrive_expect_tx(fc, nb * BLK64);
-        for (int e = 0; e < nb; ++e) tma_load(sb + cd + e * BLK64, &ta.mc, 64 * e, g, w.begin + t0, a.C.sn ? w.row : 0, fc);
+        mbar_arrive_expect_tx(fullC, nb * BLK64);
+        for (int e = 0; e < nb; ++e)
+          tma_load(sb + Sm::C + e * BLK64, &ta.mc, 64 * e, g, w.begin + t0, a.C.sn ? w.row : 0, fullC);
       }
     } else {
       const int nt = min(Q, w.s1 - t0);
-      const uint16_t* xp = static_cast<const uint16_t*>(a.x.p) + (int64_t)w.h * a.P + w.p0;
-      copy_rows(xd, xp + tok(w, a.x, t0), a.x.st, nt, min(PC, a.P - w.p0), PC);
-      arrive_warp(fx);
-      copy_rows(bd, static_cast<const uint16_t*>(a.B.p) + (int64_t)g * a.N + tok(w, a.B, t0), a.B.st, nt, a.N, 128);
-      arrive_warp(fb);
-      if (!STATE) {
-        copy_rows(cd, static_cast<const uint16_t*>(a.C.p) + (int64_t)g * a.N + tok(w, a.C, t0), a.C.st, nt, a.N, 128);
-        arrive_warp(fc);
-      }
+      copy_rows(Sm::B, static_cast<const uint16_t*>(a.B.p) + (int64_t)g * a.N + tok(w, a.B, t0), a.B.st, nt, a.N, 128);
+      if (!STATE)
+        copy_rows(Sm::C, static_cast<const uint16_t*>(a.C.p) + (int64_t)g * a.N + tok(w, a.C, t0), a.C.st, nt, a.N, 128);
+    }
+  };
+  auto load_x = [&](const Unit& w, int c) {
+    const int t0 = w.s0 + c * Q;
+    if (TMA) {
+      mbar_arrive_expect_tx(fullX, BLK64);
+      tma_load(sb + Sm::X, &ta.mx, w.p0, w.h, w.begin + t0, a.x.sn ? w.row : 0, fullX);
+    } else {
+      copy_rows(Sm::X, static_cast<const uint16_t*>(a.x.p) + (int64_t)w.h * a.P + w.p0 + tok(w, a.x, t0), a.x.st,
+                min(Q, w.s1 - t0), min(PC, a.P - w.p0), PC);
     }
   };
   // dt of token t (past the segment: its last one), as it sits in memory: the conversion waits for the load,
@@ -249,16 +240,15 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
   const uint32_t tm = *tslot;
   const uint32_t tl = tm + ((uint32_t)(32 * q4) << 16);
   bool ok = true;                 // a wait that ran out: no further waits, no results
-  auto wait = [&](uint32_t bar, uint32_t par) {
-    if (ok && !mbar_try_wait(bar, par & 1u)) ok = wait_long(bar, par & 1u);
+  auto wait = [&](uint32_t bar, uint32_t k) {       // for phase number k
+    if (ok && !mbar_try_wait(bar, k & 1u)) ok = wait_long(bar, k & 1u);
   };
-  auto wait2 = [&](uint32_t bar, uint32_t k) { wait(bar + 8 * (k & 1), k >> 1); };   // one of a pair
   const int64_t per_tile = (int64_t)a.H * a.P * a.N;
 
-  // ---- the state: this thread holds S[column cg * SC + .][n = i] of the unit
-  float S[SC];
-  auto elem0 = [&](const Unit& w) { return ((int64_t)w.h * a.P + w.p0 + cg * SC) * a.N + i; };
-  auto live_of = [&](const Unit& w) { return i < a.N ? a.P - w.p0 - cg * SC : 0; };
+  // ---- the state: this thread holds S[column hf * HC + .][n = i] of the unit
+  float S[HC];
+  auto elem0 = [&](const Unit& w) { return ((int64_t)w.h * a.P + w.p0 + hf * HC) * a.N + i; };
+  auto live_of = [&](const Unit& w) { return i < a.N ? a.P - w.p0 - hf * HC : 0; };
   auto pool_of = [&](const Unit& w) { return a.state ? a.state + (int64_t)a.items[w.row].slot * per_tile : nullptr; };
   auto load_state = [&](const Unit& w) {
     int seg, nseg;
@@ -268,25 +258,16 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     const int live = live_of(w);
     const float* from;
     if (STATE || nseg == 1) from = seg == 0 && !fresh ? pool_of(w) : nullptr;
-    else if (seg == 0) from = fresh ? nullptr : ta.ws + (int64_t)w.tile * per_tile;
-    else from = ta.ws + (int64_t)(w.tile - seg + 1) * per_tile;
+    else from = seg == 0 && fresh ? nullptr : ta.ws + (int64_t)w.tile * per_tile;
 #pragma unroll
-    for (int c = 0; c < SC; ++c) S[c] = from && c < live ? from[e0 + (int64_t)c * a.N] : 0.f;
+    for (int c = 0; c < HC; ++c) S[c] = from && c < live ? from[e0 + (int64_t)c * a.N] : 0.f;
     if (STATE && seg == 0 && from) {
       // the last segment's CTA overwrites the pool's entry in the full launch
       float* to = ta.ws + (int64_t)w.tile * per_tile + e0;
 #pragma unroll
-      for (int c = 0; c < SC; ++c)
+      for (int c = 0; c < HC; ++c)
         if (c < live) to[(int64_t)c * a.N] = S[c];
     }
-    if (!STATE)
-#pragma unroll 1
-      for (int k = 2; k <= seg; ++k) {
-        const float* add = ta.ws + (int64_t)(w.tile - seg + k) * per_tile + e0;
-        const float d = ex2(ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)(w.tile - seg + k - 1) * a.H + w.h]);
-#pragma unroll
-        for (int c = 0; c < SC; ++c) S[c] = fmaf(S[c], d, c < live ? add[(int64_t)c * a.N] : 0.f);
-      }
   };
   auto leave_state = [&](const Unit& w, float ltot) {
     int seg, nseg;
@@ -297,37 +278,21 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     if (!ok) return;
     if (to) {
 #pragma unroll
-      for (int c = 0; c < SC; ++c)
+      for (int c = 0; c < HC; ++c)
         if (c < live) to[e0 + (int64_t)c * a.N] = S[c];
     }
     if (STATE && tid == 0 && w.p0 == 0)
       ta.ws[(int64_t)ta.tiles * per_tile + (int64_t)w.tile * a.H + w.h] = ltot;
   };
-  auto share_state = [&]() {      // S as a bf16 operand (rows n, columns contiguous), and its TMEM place is read
-    if (!STATE) {
+  auto share_state = [&]() {      // S as a bf16 operand: rows n, columns contiguous
+    if (STATE) return;
 #pragma unroll
-      for (int c8 = 0; c8 < SC / 8; ++c8) {
-        const float* s = S + 8 * c8;
-        *reinterpret_cast<uint4*>(sm + Sm::S + piece_off(i, cg * (SC / 8) + c8)) =
-            make_uint4(pack2<__nv_bfloat16>(s[0], s[1]), pack2<__nv_bfloat16>(s[2], s[3]),
-                       pack2<__nv_bfloat16>(s[4], s[5]), pack2<__nv_bfloat16>(s[6], s[7]));
-      }
+    for (int c8 = 0; c8 < HC / 8; ++c8) {
+      const float* s = S + 8 * c8;
+      *reinterpret_cast<uint4*>(sm + Sm::S + piece_off(i, hf * (HC / 8) + c8)) =
+          make_uint4(pack2<__nv_bfloat16>(s[0], s[1]), pack2<__nv_bfloat16>(s[2], s[3]),
+                     pack2<__nv_bfloat16>(s[4], s[5]), pack2<__nv_bfloat16>(s[6], s[7]));
     }
-    tc::fence_before_sync();
-    arrive_warp(readyS);
-  };
-  auto update_state = [&](float decl) {             // S' = e^{L_Q} S + dS, the small terms first
-    const float dec = ex2(decl);
-    uint32_t r1[16], r2[16], r3[16];
-    tc::tmem_ld16(tl + COL_DS + cg * SC, r1);
-    tc::tmem_ld16(tl + COL_DS + PC + cg * SC, r2);
-    tc::tmem_ld16(tl + COL_DS + 2 * PC + cg * SC, r3);
-    tc::tmem_wait_ld16(r1);
-    tc::tmem_wait_ld16(r2);
-    tc::tmem_wait_ld16(r3);
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      S[e] = fmaf(S[e], dec, (__uint_as_float(r3[e]) + __uint_as_float(r2[e])) + __uint_as_float(r1[e]));
   };
 
   // Rows without tokens: a fresh one's state is zero.
@@ -338,40 +303,23 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       float* to = pool_of(v);
       if (v.chunks == 0 && to && row_fresh(a.items[v.row]))
 #pragma unroll 1
-        for (int c = 0; c < SC && c < live_of(v); ++c) to[elem0(v) + (int64_t)c * a.N] = 0.f;
+        for (int c = 0; c < HC && c < live_of(v); ++c) to[elem0(v) + (int64_t)c * a.N] = 0.f;
     }
 
-  int u = blockIdx.x;
-  Unit w = next_unit<STATE>(ta, u);
-  bool any = u < ta.total;
-  if (any && (TMA ? tid == 32 : wgb)) load(w, 0, 0);
-  uint32_t gc = 0;                // chunks done, over all units
-
-  // The two groups of warps run loops of their own, joined by barriers in
-  // shared memory, so that one chunk's y is written while the next one's terms
-  // are formed.  Each barrier's phase is a chunk (gc counts them; the pairs' a
-  // chunk of their parity).  A parity tells two phases apart, so nothing may
-  // complete two phases while somebody still waits for the first:
-  //   products  a chunk's dS, Y2 (and with it Y1 and the next G) need the S that
-  //             every warp shares, after its waits for the chunk before
-  //   decays    of chunk k + 1 are published after Y2 (STATE: dS) of chunk k,
-  //             which needs warps 0-7 to have seen those of chunk k
-  //   loads     of chunk k + 2 follow warps 0-7's (STATE: 8-15's) chunk k
-  const int bt = tid - 256;
-  const bool scans = warp == 8;                     // four tokens a lane
-  // dt of the next chunk: the scanning warp's four tokens, the others' own token
-  uint32_t raw[4];
+  // dt of the next chunk: the scanning warp's four tokens, everybody's own token
+  uint32_t raw[4], rawi = 0;
   float bias = 0.f, Ah = 0.f;
   auto load_dt = [&](const Unit& v, int c) {
-    if (wgb && !scans) return;
+    if (scans) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (scans || (k == 0 && !STATE)) raw[k] = raw_dt(v, v.s0 + c * Q + (scans ? 4 * lane + k : i));
+      for (int k = 0; k < 4; ++k) raw[k] = raw_dt(v, v.s0 + c * Q + 4 * lane + k);
+    }
+    if (!STATE) rawi = raw_dt(v, v.s0 + c * Q + i);
     Ah = a.A[v.h];
     bias = a.dt_bias ? a.dt_bias[v.h] : 0.f;
   };
-  // decays of chunk number k with nt tokens, from raw
-  auto scan = [&](uint32_t k2, int nt) {
+  // decays of a chunk of nt tokens, from raw
+  auto scan = [&](int nt) {
     float dt[4], l[4], suf[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -403,7 +351,6 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     float bs[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) bs[b] = __shfl_sync(0xffffffffu, post, 8 * b);
-    float* f = decays(k2);
     *reinterpret_cast<float4*>(f + 4 * lane) = make_float4(before + l[0], before + l[1], before + l[2], pre);
     *reinterpret_cast<float4*>(f + Q + 4 * lane) =
         make_float4(ex2(after + suf[0]) * dt[0], ex2(after + suf[1]) * dt[1], ex2(after + suf[2]) * dt[2],
@@ -412,50 +359,21 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     if (lane < 4)
       f[2 * Q + 4 + lane] = ex2(lane == 0 ? bs[3] + bs[2] + bs[1] : lane == 1 ? bs[3] + bs[2] : lane == 2 ? bs[3] : 0.f);
     if (lane == 0) f[2 * Q + 8] = bs[3] + bs[2] + bs[1] + bs[0];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(readyF);
   };
-  // G and Y2 of chunk number k, once their operands are there.
-  auto issue_g = [&](uint32_t k) {
-    wait2(fullB, k);
-    wait2(fullC, k);
-    tc::fence_after_sync();
-    constexpr uint32_t idG = tc::idesc_bf16_f32(128, 128);
-    const uint32_t bo = sb + Sm::B + (k & 1) * Sm::TILE, co = sb + Sm::C + (k & 1) * Sm::TILE;
-#pragma unroll 1
-    for (int j = 0; j < nk; ++j) tc::mma_bf16(tm + COL_G, k_cols(co, j), k_cols(bo, j), idG, j > 0);
-    tc::mma_commit(barG);
-  };
-  auto issue_y2 = [&](uint32_t k) {
-    wait(readyS, k);
-    tc::fence_after_sync();
-    constexpr uint32_t idY = tc::idesc_bf16_f32(128, PC, false, true);
-    const uint32_t co = sb + Sm::C + (k & 1) * Sm::TILE;
-#pragma unroll 1
-    for (int j = 0; j < nk; ++j) tc::mma_bf16(tm + COL_Y2, k_cols(co, j), k_rows(sb + Sm::S, j), idY, j > 0);
-    tc::mma_commit(barC);
-  };
-  // A ragged chunk (number k, nt tokens) brought by tensor copies: what lies behind its last token is cleared
-  // in B and X by the `n` threads from t on.  (C's rows there give rows of y that are not kept.)
-  auto clear_tail = [&](uint32_t k, int nt, int t) {
-    wait2(fullB, k);
-    if (!STATE) wait2(fullX, k);
-#pragma unroll 1
-    for (int e = t; e < (Q - nt) * (STATE ? 16 : 24); e += 256) {
-      const int r = nt + e % (Q - nt), cv = e / (Q - nt);
-      const uint32_t off = cv < 16 ? Sm::B + (k & 1) * Sm::TILE + piece_off(r, cv)
-                                   : Sm::X + (k & 1) * BLK64 + piece_off(r, cv - 16);
-      *reinterpret_cast<uint4*>(sm + off) = make_uint4(0u, 0u, 0u, 0u);
-    }
-    tc::fence_smem_to_async();
-  };
+
+  int u = blockIdx.x;
+  Unit w = next_unit<STATE>(ta, u);
+  bool any = u < ta.total;
   if (any) {
+    if (!TMA || tid == 32) {
+      load_x(w, 0);
+      load_bc(w, 0);
+    }
     load_dt(w, 0);
-    if (scans) scan(0, w.s1 - w.s0);
-    wait(readyF, 0);
-    __syncthreads();
+    if (scans) scan(w.s1 - w.s0);
   }
-  bool early = false;             // this chunk's G was issued in the chunk before
+  uint32_t gc = 0;                // chunks done, over all units: every barrier's phase
+
 #pragma unroll 1
   while (any) {
     int un = u + gridDim.x;
@@ -463,116 +381,57 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     const bool another = un < ta.total;
     load_state(w);
     share_state();
+    tc::fence_smem_to_async();
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
     float ltot = 0.f;
-    if (wgb) {
 #pragma unroll 1
-      for (int c = 0; c < w.chunks; ++c, ++gc) {
-        const int nt = min(Q, w.s1 - w.s0 - c * Q);
-        const bool last = c + 1 == w.chunks, more = !last || another;
-        const Unit wf = last ? wn : w;              // the chunk after this one
-        const int cf = last ? 0 : c + 1;
-        if (TMA && STATE && more && bt == 0) load(wf, cf, gc + 1);   // the chunk before is done with the buffers
-        if (more) load_dt(wf, cf);
-        const float* f = decays(gc);
-        const uint32_t xs = Sm::X + (gc & 1) * BLK64;
-        wait(readyF, gc);
-        wait2(fullX, gc);
-        // ---- X's three terms, then dS
-        const float decl = f[2 * Q + 8];
-#pragma unroll
-        for (int e = 0; e < Q * PC / 8 / 256; ++e) {
-          const int idx = bt + e * 256, t = idx >> 3, cv = idx & 7;
-          const uint32_t off = piece_off(t, cv);
-          uint4 xv = *reinterpret_cast<const uint4*>(sm + xs + off);
-          if (t >= nt) xv = make_uint4(0u, 0u, 0u, 0u);     // a tensor copy brings what lies behind the row
-          const float g = f[Q + t] * f[2 * Q + 4 + (t >> 5)];
-          const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
-          uint32_t o1[4], o2[4], o3[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float p = __uint_as_float(xw[k] << 16) * g, q = __uint_as_float(xw[k] & 0xffff0000u) * g;
-            o1[k] = pack2<__nv_bfloat16>(p, q);
-            p -= __uint_as_float(o1[k] << 16);
-            q -= __uint_as_float(o1[k] & 0xffff0000u);
-            o2[k] = pack2<__nv_bfloat16>(p, q);
-            p -= __uint_as_float(o2[k] << 16);
-            q -= __uint_as_float(o2[k] & 0xffff0000u);
-            o3[k] = pack2<__nv_bfloat16>(p, q);
-          }
-          *reinterpret_cast<uint4*>(sm + Sm::X1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-          *reinterpret_cast<uint4*>(sm + Sm::X1 + BLK64 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-          *reinterpret_cast<uint4*>(sm + Sm::X1 + 2 * BLK64 + off) = make_uint4(o3[0], o3[1], o3[2], o3[3]);
+    for (int c = 0; c < w.chunks; ++c, ++gc) {
+      const int t0 = w.s0 + c * Q, nt = min(Q, w.s1 - t0);
+      const bool last = c + 1 == w.chunks, more = !last || another;
+      const Unit wf = last ? wn : w;                // the chunk after this one
+      const int cf = last ? 0 : c + 1;
+      const float decl = f[2 * Q + 8], li = f[i];
+      if (TMA && nt < Q) {
+        // a ragged chunk: what lies behind its last token is cleared in B and X (C's rows there give rows of y
+        // that are not kept)
+        wait(fullB, gc);
+        wait(fullX, gc);
+#pragma unroll 1
+        for (int e = tid; e < (Q - nt) * 24; e += TCT) {
+          const int r = nt + e % (Q - nt), cv = e / (Q - nt);
+          const uint32_t off = cv < 16 ? Sm::B + piece_off(r, cv) : Sm::X + piece_off(r, cv - 16);
+          *reinterpret_cast<uint4*>(sm + off) = make_uint4(0u, 0u, 0u, 0u);
         }
-        if (STATE && TMA && nt < Q) clear_tail(gc, nt, bt);
         tc::fence_smem_to_async();
-        bar_named(2);
-        if (bt == 0) {
-          wait(readyS, gc);                         // every warp has read the dS before
-          if (STATE || nt == Q) wait2(fullB, gc);
-          else wait(barC, gc);                      // ragged: cleared before G and Y2
-          tc::fence_after_sync();
-          constexpr uint32_t idS = tc::idesc_bf16_f32(128, 3 * PC, true, true);
-          const uint32_t bo = sb + Sm::B + (gc & 1) * Sm::TILE;
-#pragma unroll 1
-          for (int k = 0; k < Q / 16; ++k) tc::mma_bf16(tm + COL_DS, k_rows(bo, k), k_rows(sb + Sm::X1, k), idS, k > 0);
-          tc::mma_commit(barS);
-        }
-        // Y2 done: S may be overwritten.  It was issued after warps 0-7 were done with the chunk before, whose
-        // decays and buffers are free
-        if (!STATE) wait(barC, gc);
-        else wait(barS, gc);
-        if (!TMA && more) load(wf, cf, gc + 1);
-        if (more && scans) scan(gc + 1, wf.s1 - wf.s0 - cf * Q);
-        wait(barS, gc);
-        tc::fence_after_sync();
-        ltot += decl;
-        update_state(decl);
-        if (!last) share_state();
+        __syncthreads();
       }
-    } else {
-#pragma unroll 1
-      for (int c = 0; c < w.chunks; ++c, ++gc) {
-        const int t0 = w.s0 + c * Q, nt = min(Q, w.s1 - t0);
-        const bool last = c + 1 == w.chunks, more = !last || another;
-        const Unit wf = last ? wn : w;              // the chunk after this one
-        const int cf = last ? 0 : c + 1;
-        const float* f = decays(gc);
-        if (STATE) {
-          const float decl = f[2 * Q + 8];
-          wait(barS, gc);
-          tc::fence_after_sync();
-          ltot += decl;
-          update_state(decl);
-          if (more) wait(readyF, gc + 1);
-          if (!last) share_state();
-          continue;
-        }
-        const uint32_t xs = Sm::X + (gc & 1) * BLK64;
-        // ---- this chunk's G and Y2, and the next one's operands
-        if (TMA && more && tid == 32) {
-          bulk_wait_read();                         // y of the chunk before has left its buffer
-          load(wf, cf, gc + 1);
-        }
-        if (TMA && nt < Q) {
-          clear_tail(gc, nt, tid);
-          bar_named(1);
-        }
+      if (!STATE) {
         if (tid == 0) {
-          if (!early) issue_g(gc);
-          issue_y2(gc);
+          if (TMA) {
+            wait(fullB, gc);
+            wait(fullC, gc);
+          }
+          tc::fence_after_sync();
+          constexpr uint32_t idG = tc::idesc_bf16_f32(128, 128), idY = tc::idesc_bf16_f32(128, PC, false, true);
+#pragma unroll 1
+          for (int k = 0; k < nk; ++k) tc::mma_bf16(tm + COL_G, k_cols(sb + Sm::C, k), k_cols(sb + Sm::B, k), idG, k > 0);
+          tc::mma_commit(barG);
+#pragma unroll 1
+          for (int k = 0; k < nk; ++k) tc::mma_bf16(tm + COL_Y2, k_cols(sb + Sm::C, k), k_rows(sb + Sm::S, k), idY, k > 0);
+          tc::mma_commit(barC);
         }
-        early = false;
-        const float own = i < nt ? dt_of(raw[0], bias) : 0.f;     // dt of token i
+        const float own = i < nt ? dt_of(rawi, bias) : 0.f;       // dt of token i
         if (more) load_dt(wf, cf);
-        // ---- W from G: columns 32 b + 16 hf .. + 15 of every block b
-        wait2(fullX, gc);
+        // ---- W from G: columns 32 b + 16 hf .. + 15 of every block b, in place of blocks 2 and 3 of G once both
+        // warps of the lanes have read them
+        if (TMA) wait(fullX, gc);
         wait(barG, gc);
         tc::fence_after_sync();
-        const float decl = f[2 * Q + 8], li = f[i];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
+        auto form = [&](int b, uint32_t (&v)[8]) {
           const int j0 = 32 * b + 16 * hf;
-          uint32_t v[8], G[16];
+          uint32_t G[16];
           if (b <= q4) {
             tc::tmem_ld16(tl + COL_G + j0, G);
             tc::tmem_wait_ld16(G);
@@ -601,35 +460,79 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0u;
           }
-          tc::tmem_st8(tl + COL_W + 16 * b + 8 * hf, v);
-        }
+        };
+        uint32_t v2[8], v3[8];
+        form(2, v2);
+        form(3, v3);
+        tc::fence_before_sync();
+        bar_pair(1 + q4);
+        tc::tmem_st8(tl + COL_W + 32 + 8 * hf, v2);
+        tc::tmem_st8(tl + COL_W + 48 + 8 * hf, v3);
+        form(0, v2);
+        tc::tmem_st8(tl + COL_W + 8 * hf, v2);
+        form(1, v3);
+        tc::tmem_st8(tl + COL_W + 16 + 8 * hf, v3);
         tc::tmem_wait_st();
         tc::fence_before_sync();
-        bar_named(1);             // W is formed, G has been read
+        __syncthreads();
         if (tid == 0) {
           tc::fence_after_sync();
           constexpr uint32_t id1 = tc::idesc_bf16_f32(128, PC, false, true);
 #pragma unroll 1
           for (int k = 0; k < Q / 16; ++k)
-            tc::mma_bf16_ta(tm + COL_Y1, tm + COL_W + 8 * k, k_rows(sb + xs, k), id1, k > 0);
+            tc::mma_bf16_ta(tm + COL_Y1, tm + COL_W + 8 * k, k_rows(sb + Sm::X, k), id1, k > 0);
           tc::mma_commit(barY);
-          // the next chunk's G, if its operands are there
-          if (more && wf.s1 - wf.s0 - cf * Q >= Q && mbar_try_wait(fullB + 8 * ((gc + 1) & 1), ((gc + 1) >> 1) & 1u) &&
-              mbar_try_wait(fullC + 8 * ((gc + 1) & 1), ((gc + 1) >> 1) & 1u)) {
-            issue_g(gc + 1);
-            early = true;
-          }
         }
-        wait(barC, gc);
-        wait(barS, gc);
+        wait(barC, gc);           // G and Y2 have read C and S: the terms take their places
+      } else {
+        if (more) load_dt(wf, cf);
+        if (TMA) {
+          wait(fullX, gc);
+          wait(fullB, gc);
+        }
+      }
+      // ---- X's three terms, then dS
+#pragma unroll
+      for (int e = 0; e < Q * PC / 8 / TCT; ++e) {
+        const int idx = tid + e * TCT, t = idx >> 3, cv = idx & 7;
+        const uint32_t off = piece_off(t, cv);
+        const uint4 xv = *reinterpret_cast<const uint4*>(sm + Sm::X + off);
+        const float g = f[Q + t] * f[2 * Q + 4 + (t >> 5)];
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+        uint32_t o1[4], o2[4], o3[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float p = __uint_as_float(xw[k] << 16) * g, q = __uint_as_float(xw[k] & 0xffff0000u) * g;
+          o1[k] = pack2<__nv_bfloat16>(p, q);
+          p -= __uint_as_float(o1[k] << 16);
+          q -= __uint_as_float(o1[k] & 0xffff0000u);
+          o2[k] = pack2<__nv_bfloat16>(p, q);
+          p -= __uint_as_float(o2[k] << 16);
+          q -= __uint_as_float(o2[k] & 0xffff0000u);
+          o3[k] = pack2<__nv_bfloat16>(p, q);
+        }
+        *reinterpret_cast<uint4*>(sm + Sm::X1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+        *reinterpret_cast<uint4*>(sm + Sm::X2 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+        *reinterpret_cast<uint4*>(sm + Sm::X3 + off) = make_uint4(o3[0], o3[1], o3[2], o3[3]);
+      }
+      tc::fence_smem_to_async();
+      __syncthreads();            // the decays are free too
+      if (tid == 0) {
         tc::fence_after_sync();
-        update_state(decl);
-        if (!last) share_state();
+        constexpr uint32_t idS = tc::idesc_bf16_f32(128, PC, true, true);
+#pragma unroll 1
+        for (int k = 0; k < 3 * Q / 16; ++k) {      // the small terms first
+          const uint32_t xo = k < 8 ? Sm::X3 : k < 16 ? Sm::X2 : Sm::X1;
+          tc::mma_bf16(tm + COL_DS, k_rows(sb + Sm::B, k & 7), k_rows(sb + xo, k & 7), idS, k > 0);
+        }
+        tc::mma_commit(barS);
+      }
+      if (more && scans) scan(wf.s1 - wf.s0 - cf * Q);
+      if (!STATE) {
+        // ---- y = Y1 + e^{L_i} Y2 + D x, over x in shared memory
+        const float ei = ex2(li), Dh = a.D ? a.D[w.h] : 0.f;
         wait(barY, gc);
         tc::fence_after_sync();
-        // ---- y = Y1 + e^{L_i} Y2 + D x, over x in shared memory (its terms are formed)
-        const float ei = ex2(li), Dh = a.D ? a.D[w.h] : 0.f;
-        const bool direct = !TMA || nt < Q;
 #pragma unroll
         for (int c16 = 0; c16 < HC / 16; ++c16) {
           uint32_t r1[16], r2[16];
@@ -639,7 +542,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
           tc::tmem_wait_ld16(r2);
 #pragma unroll
           for (int e8 = 0; e8 < 2; ++e8) {
-            uint4* xp = reinterpret_cast<uint4*>(sm + xs + piece_off(i, hf * (HC / 8) + 2 * c16 + e8));
+            uint4* xp = reinterpret_cast<uint4*>(sm + Sm::X + piece_off(i, hf * (HC / 8) + 2 * c16 + e8));
             const uint4 xv = *xp;
             const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
             uint32_t o[4];
@@ -654,28 +557,56 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
             *xp = make_uint4(o[0], o[1], o[2], o[3]);
           }
         }
-        if (more) wait(readyF, gc + 1);             // before the next Y2, after which the decays after those come
-        tc::fence_smem_to_async();
-        tc::fence_before_sync();
-        bar_named(1);             // y is in shared memory, and its accumulators are free
-        if (!direct) {
-          if (tid == 32 && ok) {
-            tma_store(&ta.my, w.p0, w.h, w.begin + t0, a.y.sn ? w.row : 0, sb + xs);
-            bulk_commit();
-          }
-        } else {
-          // a ragged chunk's rows (or unaligned ones), value by value
-          uint16_t* yr = static_cast<uint16_t*>(const_cast<void*>(a.y.p)) + tok(w, a.y, t0) + (int64_t)w.h * a.P + w.p0;
-          const int pw = min(PC, a.P - w.p0);
-          if (ok)
+      }
+      // ---- S' = e^{L_Q} S + dS
+      wait(barS, gc);
+      tc::fence_after_sync();
+      if (TMA && more && tid == 32) load_bc(wf, cf);
+      ltot += decl;
+      {
+        const float dec = ex2(decl);
+#pragma unroll
+        for (int c16 = 0; c16 < HC / 16; ++c16) {
+          uint32_t r[16];
+          tc::tmem_ld16(tl + COL_DS + hf * HC + 16 * c16, r);
+          tc::tmem_wait_ld16(r);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) S[16 * c16 + e] = fmaf(S[16 * c16 + e], dec, __uint_as_float(r[e]));
+        }
+      }
+      if (!last) share_state();
+      tc::fence_smem_to_async();
+      tc::fence_before_sync();
+      __syncthreads();            // y and S are in shared memory, TMEM and the next decays are read and written
+      tc::fence_after_sync();
+      if (!STATE && TMA && nt == Q) {
+        if (tid == 32 && ok) {
+          tma_store(&ta.my, w.p0, w.h, w.begin + t0, a.y.sn ? w.row : 0, sb + Sm::X);
+          bulk_commit();
+          bulk_wait_read();
+        }
+      } else if (!STATE) {
+        // a ragged chunk's rows (or unaligned ones), value by value
+        uint16_t* yr = static_cast<uint16_t*>(const_cast<void*>(a.y.p)) + tok(w, a.y, t0) + (int64_t)w.h * a.P + w.p0;
+        const int pw = min(PC, a.P - w.p0);
+        if (ok)
 #pragma unroll 1
-            for (int e = tid; e < nt * PC; e += 256) {
-              const int t = e / PC, p = e % PC;
-              if (p < pw)
-                yr[(int64_t)t * a.y.st + p] =
-                    *reinterpret_cast<const uint16_t*>(sm + xs + piece_off(t, p >> 3) + 2 * (p & 7));
-            }
-          bar_named(1);           // read before the buffer is filled again
+          for (int e = tid; e < nt * PC; e += TCT) {
+            const int t = e / PC, p = e % PC;
+            if (p < pw)
+              yr[(int64_t)t * a.y.st + p] =
+                  *reinterpret_cast<const uint16_t*>(sm + Sm::X + piece_off(t, p >> 3) + 2 * (p & 7));
+          }
+        __syncthreads();          // read before the place is filled again
+      }
+      if (more) {
+        if (TMA) {
+          if (tid == 32) load_x(wf, cf);
+        } else {
+          load_x(wf, cf);
+          load_bc(wf, cf);
+          tc::fence_smem_to_async();
+          __syncthreads();
         }
       }
     }
@@ -692,7 +623,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     }
     __syncthreads();
   }
-  if (warp == 0) tc::tmem_dealloc(tm, 512);
+  if (warp == 0) tc::tmem_dealloc(tm, COLS);
 }
 
 thread_local TcArgs t_tc;
@@ -708,18 +639,19 @@ cudaError_t go(const TcArgs& t, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready = dev;
   }
-  ssm_tc_kernel<STATE, TMA><<<(unsigned)(t.total < sms ? t.total : sms), TCT, Sm::BYTES, s>>>(t);
+  ssm_tc_kernel<STATE, TMA><<<(unsigned)(t.total < 2 * sms ? t.total : 2 * sms), TCT, Sm::BYTES, s>>>(t);
   return cudaGetLastError();
 }
 template <bool TMA>
 cudaError_t both(const TcArgs& t, bool split, int sms, cudaStream_t s) {
   if (split) {
-    const cudaError_t e = go<true, TMA>(t, sms, s);
+    cudaError_t e = go<true, TMA>(t, sms, s);
+    if (e != cudaSuccess) return e;
+    e = launch_ssm_join(t.a, t.seg_tokens, t.tiles, t.per_row, t.ws, s);
     if (e != cudaSuccess) return e;
   }
   return go<false, TMA>(t, sms, s);
 }
-
 using EncodeFn = decltype(&cuTensorMapEncodeTiled);
 EncodeFn encode_fn() {
   static const EncodeFn fn = [] {
@@ -768,7 +700,7 @@ SsmPlan ssm_tc_plan(int H, int P, int rows, const int32_t* lens, int64_t T, int 
       const int64_t c = ((lens ? lens[i] : T) + Q - 1) / Q;
       tiles += c > seg ? (c + seg - 1) / seg : 1;
     }
-    if (tiles * p.units <= sms) {
+    if (tiles * p.units <= 2 * (int64_t)sms) {
       p.seg_tokens = (int)(Q * seg);
       p.split = true;
       break;
