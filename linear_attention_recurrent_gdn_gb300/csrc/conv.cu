@@ -12,7 +12,14 @@
 // value a lane are still contiguous.  Sums, the activation and the norm are in
 // 32 bits, rounded once; pairs of channels share a packed fp32 multiply-add,
 // and pairs of sigmoids a reciprocal.  About 2 W + 8 operations a value: HBM
-// bound.
+// bound, with the instructions not far behind.
+//
+// Measured on a GB300 (copy: 6.7 TB/s): prompts of 16 x 512 tokens of 12288
+// bf16 channels with the L2 norm of two thirds of them 74 us, 5.5 TB/s (with
+// tokens fetched into registers instead of shared memory 110 us: 16 warps an SM
+// hold too few loads); one token of 256 x 12288 10 us, 5.0 TB/s; of 1 x 768 2.1
+// us, the launch; 3100 packed tokens of 5123 fp16 channels 33 us, 2.0 TB/s,
+// bound by loads and stores of two bytes a lane.
 #include <type_traits>
 
 #include "dl_device.cuh"
@@ -446,7 +453,8 @@ cudaError_t go_t(int dtype, bool vec, const Args& a, cudaStream_t s) {
 
 int conv_tile(int64_t tokens, int C, int sms) {
   // As many tokens (rows, for a step) a tile as still give every SM its four blocks: longer tiles read fewer
-  // tokens twice and the weights less often.
+  // tokens twice and the weights less often (16 x 512 x 12288: 74 us at 64 tokens, 86 at 16), shorter ones fill
+  // the GPU (a step of 256 x 12288: 10 us at 4 rows, 60 at 64).
   const int64_t blocks_c = (C + 8 * CONV_THREADS - 1) / (8 * CONV_THREADS);
   int tt = 64;
   while (tt > 4 && (tokens + tt - 1) / tt * blocks_c < 4 * (int64_t)sms) tt >>= 1;

@@ -27,7 +27,15 @@
 // each other's waits.  For that a CTA keeps to half of the shared memory and of
 // TMEM: the terms take the places of C and S once Y2 has read them, W and dS
 // those of G.  With nearly all of the SM's memory used as shared memory there
-// is next to no L1 cache, so nothing may spill.
+// is next to no L1 cache, so nothing may spill (300 bytes a thread cost 15%).
+//
+// Measured on a GB300: 16 x 512 tokens of 32 heads of 128 x 128 106 us (1.7
+// TB/s of the 6.7 of a copy; the FP32 cores took 1.1 ms), of 64 x 128 59 us; one
+// row of 2048 tokens of 16 heads of 64 x 128 24 us in three launches.  A chunk's
+// products are some 2500 cycles of the tensor cores and its operands 3700 of
+// shared memory, of about 5000; the schedulers issue 40% of the time.  One CTA
+// of 16 warps with everything doubled and the warps specialised took 138 us, 128
+// state rows a unit 127 us (spilling), two heads a unit 87 us for 59.
 //
 // Rows with few heads are split into segments: a first launch (STATE) runs
 // each segment from zero and leaves its end state and decay in the workspace, a
@@ -90,11 +98,13 @@ __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_g
 __device__ __forceinline__ uint32_t piece_off(int r, int cv) {
   return (uint32_t)(cv >> 3) * BLK64 + (uint32_t)(r * 128 + (((cv & 7) ^ (r & 7)) << 4));
 }
-// Descriptors of K step k (16 values of K): rows are K (MN-major), or K runs along the rows (K-major).
-__device__ __forceinline__ uint64_t k_rows(uint32_t base, int k) { return tc::sdesc128(base + k * 2048u, BLK64, 1024u); }
-__device__ __forceinline__ uint64_t k_cols(uint32_t base, int k) {
-  return tc::sdesc128(base + (uint32_t)(k >> 2) * BLK64 + (uint32_t)(k & 3) * 32u, 16u, 1024u);
-}
+// Descriptors of an operand whose rows are K (MN-major), or along whose rows K runs (K-major), and what K step k
+// (16 values of K) adds to them, in 16 bytes.  With the steps as constants an MMA costs its thread a few
+// instructions; formed one by one, the 48 of a chunk took 6% of the time.
+__device__ __forceinline__ uint64_t by_rows(uint32_t base) { return tc::sdesc128(base, BLK64, 1024u); }
+__device__ __forceinline__ uint64_t by_cols(uint32_t base) { return tc::sdesc128(base, 16u, 1024u); }
+__device__ constexpr uint32_t row_step(int k) { return k * (2048u >> 4); }
+__device__ constexpr uint32_t col_step(int k) { return (k >> 2) * (BLK64 >> 4) + (k & 3) * 2u; }
 
 struct TcArgs {
   CUtensorMap mx, mb, mc, my;   // x, B, C, y: [64 values][head or group][128 tokens][row] boxes
@@ -415,11 +425,14 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
           }
           tc::fence_after_sync();
           constexpr uint32_t idG = tc::idesc_bf16_f32(128, 128), idY = tc::idesc_bf16_f32(128, PC, false, true);
-#pragma unroll 1
-          for (int k = 0; k < nk; ++k) tc::mma_bf16(tm + COL_G, k_cols(sb + Sm::C, k), k_cols(sb + Sm::B, k), idG, k > 0);
+          const uint64_t dc = by_cols(sb + Sm::C), db = by_cols(sb + Sm::B), ds = by_rows(sb + Sm::S);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < nk) tc::mma_bf16(tm + COL_G, dc + col_step(k), db + col_step(k), idG, k > 0);
           tc::mma_commit(barG);
-#pragma unroll 1
-          for (int k = 0; k < nk; ++k) tc::mma_bf16(tm + COL_Y2, k_cols(sb + Sm::C, k), k_rows(sb + Sm::S, k), idY, k > 0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (k < nk) tc::mma_bf16(tm + COL_Y2, dc + col_step(k), ds + row_step(k), idY, k > 0);
           tc::mma_commit(barC);
         }
         const float own = i < nt ? dt_of(rawi, bias) : 0.f;       // dt of token i
@@ -478,9 +491,9 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         if (tid == 0) {
           tc::fence_after_sync();
           constexpr uint32_t id1 = tc::idesc_bf16_f32(128, PC, false, true);
-#pragma unroll 1
-          for (int k = 0; k < Q / 16; ++k)
-            tc::mma_bf16_ta(tm + COL_Y1, tm + COL_W + 8 * k, k_rows(sb + Sm::X, k), id1, k > 0);
+          const uint64_t dx = by_rows(sb + Sm::X);
+#pragma unroll
+          for (int k = 0; k < Q / 16; ++k) tc::mma_bf16_ta(tm + COL_Y1, tm + COL_W + 8 * k, dx + row_step(k), id1, k > 0);
           tc::mma_commit(barY);
         }
         wait(barC, gc);           // G and Y2 have read C and S: the terms take their places
@@ -520,11 +533,10 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       if (tid == 0) {
         tc::fence_after_sync();
         constexpr uint32_t idS = tc::idesc_bf16_f32(128, PC, true, true);
-#pragma unroll 1
-        for (int k = 0; k < 3 * Q / 16; ++k) {      // the small terms first
-          const uint32_t xo = k < 8 ? Sm::X3 : k < 16 ? Sm::X2 : Sm::X1;
-          tc::mma_bf16(tm + COL_DS, k_rows(sb + Sm::B, k & 7), k_rows(sb + xo, k & 7), idS, k > 0);
-        }
+        const uint64_t db = by_rows(sb + Sm::B), dx[3] = {by_rows(sb + Sm::X3), by_rows(sb + Sm::X2), by_rows(sb + Sm::X1)};
+#pragma unroll
+        for (int k = 0; k < 3 * Q / 16; ++k)        // the small terms first
+          tc::mma_bf16(tm + COL_DS, db + row_step(k & 7), dx[k >> 3] + row_step(k & 7), idS, k > 0);
         tc::mma_commit(barS);
       }
       if (more && scans) scan(wf.s1 - wf.s0 - cf * Q);
@@ -691,9 +703,10 @@ SsmPlan ssm_tc_plan(int H, int P, int rows, const int32_t* lens, int64_t T, int 
   }
   p.units = H * p.ptiles;
   p.seg_tokens = Q * (int)(longest > 0 ? longest : 1);
-  // Segments as short as still fill the GPU once: each runs two launches, so
-  // at least three of them in the longest row are wanted, and at most 16,
-  // since the last of a row joins the states of all before it.
+  // Segments as short as still fill the GPU once (two CTAs an SM): they take
+  // three launches and half the work again, so at least three of them in the
+  // longest row are wanted, and at most 16.  One row of 2048 tokens of 16 heads
+  // of 64 x 128: 24 us, 70 whole.
   for (int64_t seg = (longest + 15) / 16; seg > 0 && 3 * seg <= longest; ++seg) {
     int64_t tiles = 0;
     for (int i = 0; i < rows; ++i) {
