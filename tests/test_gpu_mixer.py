@@ -502,3 +502,45 @@ def test_binding_refusals(mx):
         mx.gated_norm(h, torch.ones(63, device="cuda"))
     with pytest.raises(ValueError):
         mx.add_norm(h[:, 0], h[:, 0].half(), torch.ones(64, device="cuda"))
+
+
+# ------------------------------------------------------ large offsets --------
+def test_offsets_past_32_bits(mx):
+    """The last slots, rows and tokens of tensors of more than 2^31 values, against the same ones alone."""
+    g = torch.Generator(device="cuda").manual_seed(0)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    H, P, N = 16, 128, 128
+    pool = torch.empty(8200, H, P, N, device="cuda")
+    one = torch.randn(1, H, P, N, generator=g, device="cuda")
+    pool[8199:] = one
+    x, B, C, dt, A = rn(1, H, P), rn(1, 1, N), rn(1, 1, N), rn(1, H), -torch.rand(H, device="cuda")
+    y = mx.ssm_step(x, dt, A, B, C, slots=[8199], state=pool)
+    z = mx.ssm_step(x, dt, A, B, C, slots=[0], state=one)
+    assert torch.equal(y, z) and torch.equal(pool[8199:], one)
+    del pool
+    T, K = 270000, 100
+    x = torch.zeros(T, 8192, device="cuda", dtype=torch.bfloat16)
+    x[-K:] = rn(K, 8192)
+    w = rn(8192, 4)
+    y = mx.conv(x, w, lengths=[T - K, K])
+    assert torch.equal(y[-K:], mx.conv(x[-K:].clone(), w, lengths=[K]))
+    del y
+    h = x.view(T, 128, 64)
+    B, C, dt, A = rn(T, 1, 64), rn(T, 1, 64), rn(T, 128), -torch.rand(128, device="cuda")
+    y = mx.ssm(h, dt, A, B, C, lengths=[T - K, K])
+    z = mx.ssm(h[-K:].clone(), dt[-K:].clone(), A, B[-K:].clone(), C[-K:].clone(), lengths=[K])
+    assert torch.equal(y[-K:], z)
+    del y
+    w = rn(64)
+    v = mx.gated_norm(h, w, h)
+    assert torch.equal(v[-K:], mx.gated_norm(h[-K:].clone(), w, h[-K:].clone()))
+    del v
+    w = rn(8192)
+    v, r = mx.add_norm(x, x, w)
+    v1, r1 = mx.add_norm(x[-K:].clone(), x[-K:].clone(), w)
+    assert torch.equal(v[-K:], v1) and torch.equal(r[-K:], r1)
+
+
+def test_status_word_is_clean(mx):
+    """No wait of the tensor-core scan ran out in the tests before."""
+    mx.sync()
