@@ -10,15 +10,15 @@
 // the variance from the centred values.  About ten operations a value: HBM
 // bound, so what counts is bytes on their way.  A row of up to 256 values takes
 // a part of a warp (gt threads, a power of two), four rows a thread where there
-// are many; one of up to 1024 a warp with up to four pieces a thread; a wider
+// are many (of the same head, so that its weights are loaded once); one of up to 1024 a warp with up to four pieces a thread; a wider
 // one a block of a quarter of its pieces' threads.
 //
 // Measured on a GB300 (copy: 6.7 TB/s): residual sum and norm of 8192 x 4096
 // bf16 42 us, 6.4 TB/s, with an fp32 stream and both norms 67 us, 6.0 TB/s;
-// gated RMS norm of 8192 x 32 heads of 128 40 us, 5.0 TB/s; layer norm with bias
-// and gate of 8192 x 40 heads of 64 29 us, 4.3 TB/s (short rows: a warp's sums,
-// weights and gates are some 250 instructions for 32 x 8 values, and the
-// schedulers issue two thirds of the time); one token 2.4 us, the launch.
+// gated RMS norm of 8192 x 32 heads of 128 35 us, 5.8 TB/s; layer norm with bias
+// and gate of 8192 x 40 heads of 64 24 us, 5.2 TB/s (short rows: a warp's sums,
+// weights and gates are some 200 instructions for 32 x 8 values, and the
+// schedulers issue 63% of the time); one token 2.4 us, the launch.
 #include "mixer_device.cuh"
 
 namespace dl {
@@ -126,42 +126,32 @@ __device__ __forceinline__ Vec8<T> pack_pairs(const f2 (&v)[4]) {
 
 constexpr int NT = 128;                  // threads of a block of small rows
 
-// U rows a group of gt threads (neighbouring groups' rows in between), VPT
-// pieces a thread; FULL: the group's threads have eight values in every piece.
+// The same head of U following rows a group of gt threads (one load of its
+// weights), VPT pieces a thread; FULL: the group's threads have eight values in
+// every piece.
 template <class T, bool VEC, bool FULL, int U, int VPT, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 512 : NT)
 gated_norm_kernel(const __grid_constant__ GatedNormArgs a, int gt) {
   __shared__ float sm[32];
   const int per = BLOCK ? 1 : NT / gt, G = BLOCK ? blockDim.x : gt;
   const int lane = BLOCK ? threadIdx.x : threadIdx.x & (gt - 1);
-  const uint32_t u0 = blockIdx.x * (uint32_t)(per * U) + (BLOCK ? 0 : threadIdx.x / gt);
-  const uint32_t units = (uint32_t)(a.rows * a.H);
-  const int dr = per / a.H, dh = per - dr * a.H;    // from a unit to the next one of the group
+  const uint32_t u0 = blockIdx.x * (uint32_t)per + (BLOCK ? 0 : threadIdx.x / gt);
+  const int row0 = (int)(u0 / (uint32_t)a.H) * U, h = (int)(u0 % (uint32_t)a.H);
   int valid[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) valid[i] = FULL ? 8 : min(8, a.d - 8 * (lane + G * i));
 
   Vec8<T> xv[U][VPT], gv[U][VPT];
-  int64_t yo[U];
-  int h[U];
-  int row = (int)(u0 / (uint32_t)a.H), hh = (int)(u0 - (uint32_t)row * (uint32_t)a.H);
+  const int64_t in = (int64_t)h * a.d + 8 * lane;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const bool on = u0 + u * per < units;           // idle groups still take part in the shuffles
-    const int64_t in = (int64_t)hh * a.d + 8 * lane;
-    h[u] = hh;
-    yo[u] = on ? (int64_t)row * a.ys + in : -1;
+    const bool on = row0 + u < a.rows;              // idle groups still take part in the shuffles
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      xv[u][i] = load8<T, VEC>(static_cast<const T*>(a.x) + (int64_t)row * a.xs + in + 8 * G * i, on ? valid[i] : 0);
+      xv[u][i] = load8<T, VEC>(static_cast<const T*>(a.x) + (int64_t)(row0 + u) * a.xs + in + 8 * G * i, on ? valid[i] : 0);
       if (a.gate)
-        gv[u][i] = load8<T, VEC>(static_cast<const T*>(a.gate) + (int64_t)row * a.gs + in + 8 * G * i, on ? valid[i] : 0);
-    }
-    row += dr;
-    hh += dh;
-    if (hh >= a.H) {
-      hh -= a.H;
-      ++row;
+        gv[u][i] =
+            load8<T, VEC>(static_cast<const T*>(a.gate) + (int64_t)(row0 + u) * a.gs + in + 8 * G * i, on ? valid[i] : 0);
     }
   }
   f2 v[U][VPT][4];
@@ -185,22 +175,23 @@ gated_norm_kernel(const __grid_constant__ GatedNormArgs a, int gt) {
   }
   norm_regs<BLOCK, FULL, U, VPT>(v, valid, a.d, a.kind, a.eps, gt, sm);
 #pragma unroll
-  for (int u = 0; u < U; ++u)
+  for (int i = 0; i < VPT; ++i) {
+    const int64_t wo = (a.w_heads ? (int64_t)h * a.d : 0) + 8 * (lane + G * i);
+    f2 w[4], b[4];
+    wpairs<T, VEC>(a.w, wo, valid[i], a.w_f32, w);
+    if (a.b) {
+      wpairs<T, VEC>(a.b, wo, valid[i], a.w_f32, b);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int64_t wo = (a.w_heads ? (int64_t)(yo[u] < 0 ? 0 : h[u]) * a.d : 0) + 8 * (lane + G * i);
-      f2 w[4];
-      wpairs<T, VEC>(a.w, wo, valid[i], a.w_f32, w);
-      if (a.b) {
-        f2 b[4];
-        wpairs<T, VEC>(a.b, wo, valid[i], a.w_f32, b);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[u][i][k] = fma2(v[u][i][k], w[k], b[k]);
-      } else {
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[u][i][k] = mul2(v[u][i][k], w[k]);
-      }
     }
+  }
   if (a.gate && !a.gate_first) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -216,7 +207,8 @@ gated_norm_kernel(const __grid_constant__ GatedNormArgs a, int gt) {
   for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-      store8<T, VEC>(static_cast<T*>(a.y) + yo[u] + 8 * G * i, pack_pairs<T>(v[u][i]), yo[u] < 0 ? 0 : valid[i]);
+      store8<T, VEC>(static_cast<T*>(a.y) + (int64_t)(row0 + u) * a.ys + in + 8 * G * i, pack_pairs<T>(v[u][i]),
+                     row0 + u < a.rows ? valid[i] : 0);
 }
 
 template <class T, class R, bool VEC, bool FULL, int U, int VPT, bool BLOCK>
@@ -299,14 +291,15 @@ add_norm_kernel(const __grid_constant__ AddNormArgs a, int gt) {
   }
 }
 
-// How `units` rows of n values run.  Mode 0: a part of a warp and four rows a
-// thread (8192 x 40 heads of 64: 29 us, 32 with one row); 1: the same with one
-// row where four leave the SMs with less than four times their threads (256 x 32
-// heads of 128: 3.1 us, 3.6 with four); 2, 3: a warp with two or four pieces a
+// How rows of `heads` times n values run.  Mode 0: a part of a warp and four rows
+// a thread (8192 x 40 heads of 64: 24 us, 31 with one row); 1: the same with one
+// row where there are fewer, or where four leave the SMs with less than four times
+// their threads (256 x 32 heads of 128: 2.7 us, 2.9 with four); 2, 3: a warp with two or four pieces a
 // thread; 4, 5: a block with one piece a thread for a few rows (one of 4096: 2.4
 // us, 3.2 with four pieces) or four (8192 rows: 67 us, 85 with one).
 struct Shape { int mode, gt, threads; bool full; unsigned grid; };
-Shape shape_of(int n, int64_t units) {
+Shape shape_of(int n, int64_t rows, int64_t heads) {
+  const int64_t units = rows * heads;
   const int vecs = (n + 7) / 8;
   const bool few = units < 2 * 152;
   if (vecs > 128 || (vecs > 32 && few)) {
@@ -315,9 +308,9 @@ Shape shape_of(int n, int64_t units) {
   }
   int gt = 1;
   while (gt < vecs && gt < 32) gt <<= 1;
-  const int mode = vecs > 64 ? 3 : vecs > 32 ? 2 : units * gt >= 4 * 152 * 2048 ? 0 : 1;
-  const int64_t per = (int64_t)NT / gt * (mode == 0 ? 4 : 1);
-  return {mode, gt, NT, n == 8 * gt * (mode == 3 ? 4 : mode == 2 ? 2 : 1), (unsigned)((units + per - 1) / per)};
+  const int mode = vecs > 64 ? 3 : vecs > 32 ? 2 : rows >= 4 && units * gt >= 4 * 152 * 2048 ? 0 : 1;
+  const int64_t groups = (mode == 0 ? (rows + 3) / 4 : rows) * heads, per = NT / gt;
+  return {mode, gt, NT, n == 8 * gt * (mode == 3 ? 4 : mode == 2 ? 2 : 1), (unsigned)((groups + per - 1) / per)};
 }
 
 template <class T, bool VEC, bool FULL>
@@ -334,7 +327,7 @@ cudaError_t go_gated(const Shape& k, const GatedNormArgs& a, cudaStream_t s) {
 }
 template <class T>
 cudaError_t go_gated_v(bool vec, const GatedNormArgs& a, cudaStream_t s) {
-  const Shape k = shape_of(a.d, a.rows * a.H);
+  const Shape k = shape_of(a.d, a.rows, a.H);
   return !vec ? go_gated<T, false, false>(k, a, s) : k.full ? go_gated<T, true, true>(k, a, s) : go_gated<T, true, false>(k, a, s);
 }
 template <class T, class R, bool VEC, bool FULL>
@@ -351,7 +344,7 @@ cudaError_t go_add(const Shape& k, const AddNormArgs& a, cudaStream_t s) {
 }
 template <class T, class R>
 cudaError_t go_add_v(bool vec, const AddNormArgs& a, cudaStream_t s) {
-  const Shape k = shape_of(a.D, a.rows);
+  const Shape k = shape_of(a.D, a.rows, 1);
   return !vec     ? go_add<T, R, false, false>(k, a, s)
          : k.full ? go_add<T, R, true, true>(k, a, s)
                   : go_add<T, R, true, false>(k, a, s);
