@@ -17,7 +17,7 @@
 // Measured on a GB300 (copy: 6.7 TB/s): prompts of 16 x 512 tokens of 12288
 // bf16 channels with the L2 norm of two thirds of them 74 us, 5.5 TB/s (with
 // tokens fetched into registers instead of shared memory 110 us: 16 warps an SM
-// hold too few loads); one token of 256 x 12288 10 us, 5.0 TB/s; of 1 x 768 2.1
+// hold too few loads), fp32 of 4 x 512 x 12288 46 us, 4.4 TB/s; one token of 256 x 12288 10 us, 5.0 TB/s; of 1 x 768 2.1
 // us, the launch; 3100 packed tokens of 5123 fp16 channels 33 us, 2.0 TB/s,
 // bound by loads and stores of two bytes a lane.
 #include <type_traits>
@@ -273,22 +273,31 @@ conv_kernel(const __grid_constant__ ConvPrompt a) {
   const T* x = static_cast<const T*>(a.x.p) + (int64_t)it.begin * a.x.st + (int64_t)row * a.x.sn + ln.c;
 
   // Tokens come in groups of PF.  Aligned ones take the way through shared memory, two groups ahead, each
-  // thread its own 16-byte places (no barrier, and no registers held by loads on their way).
-  constexpr int PF = VEC ? 4 : 2, RING = 3;
+  // thread its own 16-byte places (no barrier, and no registers held by loads on their way).  Eight fp32 values
+  // are two such pieces: two neighbouring lanes move the pieces of the one, then of the other, so that every
+  // access takes whole 32-byte sectors (4 x 512 x 12288: 46 us, 65 with two pieces of its own a lane), and groups are two
+  // tokens (89 us with four: registers spill), three groups ahead (five: 47 us).
   constexpr int V16 = sizeof(T) == 4 ? 2 : 1;        // 16-byte pieces of eight values
+  constexpr int PF = VEC && V16 == 1 ? 4 : 2, RING = V16 == 1 ? 3 : 4;
   __shared__ __align__(16) uint4 ring[VEC ? RING * PF * V16 : 1][CONV_THREADS];
   const T* ahead = x + (int64_t)t0 * a.x.st;         // the next group to fetch, from token tf on
   int tf = t0, slot = 0;
+  const int odd = threadIdx.x & 1;
   Eight<T, VEC> buf[PF];
   auto fetch = [&](int place) {
 #pragma unroll
     for (int e = 0; e < PF; ++e) {
       if constexpr (VEC) {
-        if (tf + e < t1 && ln.valid > 0)
+        if constexpr (V16 == 1) {
+          if (tf + e < t1 && ln.valid > 0)
+            cp_async16(smem_u32(&ring[place * PF + e][threadIdx.x]), ahead + (int64_t)e * a.x.st);
+        } else {
 #pragma unroll
           for (int v = 0; v < V16; ++v)
-            cp_async16(smem_u32(&ring[(place * PF + e) * V16 + v][threadIdx.x]),
-                       reinterpret_cast<const uint4*>(ahead + (int64_t)e * a.x.st) + v);
+            if (tf + e < t1 && ln.valid > 8 * (v - odd))
+              cp_async16(smem_u32(&ring[(place * PF + e) * V16 + v][threadIdx.x]),
+                         ahead + (int64_t)e * a.x.st + 8 * (v - odd) + 4 * odd);
+        }
       } else {
         buf[e].load(ahead + (int64_t)e * a.x.st, tf + e < t1 ? ln.valid : 0);
       }
@@ -298,8 +307,8 @@ conv_kernel(const __grid_constant__ ConvPrompt a) {
     tf += PF;
   };
   if constexpr (VEC) {
-    fetch(0);
-    fetch(1);
+#pragma unroll
+    for (int g = 0; g + 1 < RING; ++g) fetch(g);
   } else {
     fetch(0);
   }
@@ -343,25 +352,33 @@ conv_kernel(const __grid_constant__ ConvPrompt a) {
     }
   Out<T, VEC> out;
   out.init(a, it.begin, row, ln.c);
+  Out<T, VEC> first, second;                           // of this pair of lanes
+  if constexpr (VEC && V16 == 2) {
+    first.init(a, it.begin, row, ln.c - 8 * odd);
+    second.init(a, it.begin, row, ln.c + 8 - 8 * odd);
+  }
 
   auto walk = [&](auto act, auto norm) {
 #pragma unroll 1
     for (int t = t0; t < t1; t += PF) {
       Eight<T, VEC> cur[PF], y[PF];
       if constexpr (VEC) {
-        fetch(slot == 0 ? 2 : slot - 1);
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        if constexpr (V16 == 2) __syncwarp();          // the neighbour has read what is overwritten
+        fetch(slot == 0 ? RING - 1 : slot - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(RING - 1) : "memory");
+        if constexpr (V16 == 2) __syncwarp();          // the neighbour's pieces
 #pragma unroll
         for (int e = 0; e < PF; ++e)
 #pragma unroll
           for (int v = 0; v < V16; ++v) {
-            const uint4 r = ring[(slot * PF + e) * V16 + v][threadIdx.x];
+            const uint4 r = V16 == 1 ? ring[slot * PF + e][threadIdx.x]
+                                     : ring[(slot * PF + e) * V16 + odd][(threadIdx.x & ~1) + v];
             cur[e].w[4 * v] = r.x;
             cur[e].w[4 * v + 1] = r.y;
             cur[e].w[4 * v + 2] = r.z;
             cur[e].w[4 * v + 3] = r.w;
           }
-        slot = slot == 2 ? 0 : slot + 1;
+        slot = slot == RING - 1 ? 0 : slot + 1;
       } else {
 #pragma unroll
         for (int e = 0; e < PF; ++e) cur[e] = buf[e];
@@ -371,7 +388,26 @@ conv_kernel(const __grid_constant__ ConvPrompt a) {
       for (int e = 0; e < PF; ++e) ln.template token<act.value, norm.value>(a, cur[e], win, y[e]);
       // tokens past the last were whatever the places held; their window is not used again
 #pragma unroll
-      for (int e = 0; e < PF; ++e) out.put(a, y[e], it.begin, row, t + e, ln.c, t + e < t1 ? ln.valid : 0);
+      for (int e = 0; e < PF; ++e) {
+        if constexpr (VEC && V16 == 2) {
+          uint32_t other[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) other[k] = __shfl_xor_sync(0xffffffffu, odd ? y[e].w[k] : y[e].w[4 + k], 1);
+          if (t + e < t1) {
+            // the even lane's values, then the odd lane's; half `odd` of each
+            if (ln.valid > -8 * odd)
+              *reinterpret_cast<uint4*>(first.p + (int64_t)(t + e) * first.st + 4 * odd) =
+                  odd ? make_uint4(other[0], other[1], other[2], other[3])
+                      : make_uint4(y[e].w[0], y[e].w[1], y[e].w[2], y[e].w[3]);
+            if (ln.valid > 8 - 8 * odd)
+              *reinterpret_cast<uint4*>(second.p + (int64_t)(t + e) * second.st + 4 * odd) =
+                  odd ? make_uint4(y[e].w[4], y[e].w[5], y[e].w[6], y[e].w[7])
+                      : make_uint4(other[0], other[1], other[2], other[3]);
+          }
+        } else {
+          out.put(a, y[e], it.begin, row, t + e, ln.c, t + e < t1 ? ln.valid : 0);
+        }
+      }
     }
   };
   if (a.act) {
