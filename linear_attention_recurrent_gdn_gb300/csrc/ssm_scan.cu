@@ -5,16 +5,18 @@
 // One CTA per (row, head, tile of state rows), and per segment of the row
 // where rows are few and long.  A thread keeps PR state rows times 16 state
 // columns in registers; NL threads share a state row and add up their parts of
-// y by shuffles.  Tokens come in chunks of TC, fetched into registers a chunk
-// ahead (eight values a piece) and staged in shared memory in 32 bits.  Three operations per state element and token, two elements an
-// instruction (packed fp32), so the FP32 cores bound it: 16 x 512 tokens of 32
-// heads of 64 x 128 take 374 us in fp16 on a GB300, 174 of them at the cores'
-// full rate.  Every size and type runs here.
+// y.  Tokens come in chunks of TC, fetched a chunk ahead (eight values a piece)
+// and staged in shared memory in 32 bits.  Three operations per state element
+// and token, two elements an instruction (packed fp32), so the FP32 cores bound
+// it: 16 x 512 tokens of 32 heads of 64 x 128 take 360 us in fp16 on a GB300, 174
+// of them at the cores' full rate; 4 x 512 in fp32 163.  Every size and type runs
+// here.
 //
 // Segments: a first launch (STATE) runs each but the last from zero (the first
 // from the row's state) and leaves its end state and decay in the workspace; a
 // second joins them to the states at the segments' starts; the full launch
 // goes on from those.
+#include "dl_device.cuh"
 #include "mixer_device.cuh"
 
 namespace dl {
@@ -22,12 +24,13 @@ namespace mx {
 
 namespace {
 
-constexpr int SC_THREADS = 128, SC_TC = 16;
+constexpr int SC_THREADS = 128;
 constexpr float LOG2E = 1.4426950408889634f;
 
 // State rows of a thread: as many as leave a CTA 64 rows or so, so that a value
 // of B or C that was read from shared memory serves several (16 x 512 tokens of
-// 32 heads of 64 x 128: 374 us with four, 399 with two, 722 with one).
+// 32 heads of 64 x 128: 374 us with four, 399 with two, 722 with one, before the
+// steps below).
 __host__ __device__ constexpr int rows_of(int nl) { return nl == 8 ? 4 : nl >= 4 ? 2 : 1; }
 
 struct ScanArgs {
@@ -41,11 +44,19 @@ struct ScanArgs {
 template <class T, int NL, bool STATE, bool VEC>
 __global__ void __launch_bounds__(SC_THREADS, 4)
 ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
+  // Chunks of eight tokens leave eight threads a row the shared memory for their
+  // parts of y; UN tokens overlap.
+  constexpr int TC = NL == 8 ? 8 : 16, UN = NL <= 2 ? 4 : NL == 8 ? 2 : 1;
   constexpr int PR = rows_of(NL), NP = 16 * NL, PB = SC_THREADS / NL * PR;
   const SsmArgs& a = sa.a;
-  __shared__ __align__(16) float sB[SC_TC][NP], sC[STATE ? 1 : SC_TC][NP];
-  __shared__ __align__(16) float sx[SC_TC][PB], sy[STATE ? 1 : SC_TC][PB];
-  __shared__ float sdt[SC_TC], sdec[SC_TC];
+  __shared__ __align__(16) float sB[TC][NP], sC[STATE ? 1 : TC][NP];
+  // The NL parts of a value of y: with four or eight threads a row they wait in
+  // shared memory for the chunk's end (16-byte pieces in an order that spares
+  // both sides bank conflicts), else shuffles add them at once (4 x 512 tokens of 32 heads in fp32: 64 x 64
+  // 74 us, 95 with shuffles; 64 x 128 163 us, 202).
+  constexpr bool PARTS = NL == 4 || NL == 8;
+  __shared__ __align__(16) float sx[TC][PB], sy[STATE ? 1 : TC][PARTS ? PR * SC_THREADS : PB];
+  __shared__ float sdt[TC], sdec[TC];
   const int pt = (a.P + PB - 1) / PB, ph = pt * a.H;
   const int tile = blockIdx.x / ph, rest = blockIdx.x - tile * ph, h = rest / pt, g = h / (a.H / a.G);
   const int row = find_row(a.items, a.rows, tile, sa.per_row);
@@ -56,6 +67,8 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
   if (STATE && seg == nseg - 1) return;              // nothing follows the last segment
   const int s0 = seg * sa.seg_tokens, s1 = min(len, s0 + sa.seg_tokens);
   const int ln = threadIdx.x % NL, pl = threadIdx.x / NL * PR;
+  auto place = [](int i) { return ((i >> 2) ^ (i >> 5)) << 2 | (i & 3); };   // of thread i's part
+  const int mine = place(threadIdx.x);
 
   auto at = [&](const TokView& v, int t) {
     return (int64_t)(it.begin + t) * v.st + (int64_t)row * v.sn;
@@ -90,27 +103,60 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
   const float Ah = a.A[h], Dh = a.D ? a.D[h] : 0.f, bias = a.dt_bias ? a.dt_bias[h] : 0.f;
   float ltot = 0.f;
 
-  // The next chunk in registers: pieces of eight values of B, C and x, and dt.
-  constexpr int NB = SC_TC * NP / 8, NX = SC_TC * PB / 8;      // pieces of a chunk
+  // The next chunk's pieces of eight values of B, C and x on their way: in registers, or where the state takes
+  // most of those (eight threads a row), aligned ones to a place of the thread's own in shared memory (64 x 128
+  // in fp32 163 us, 173 in registers; with four threads a row 99 us for 74).
+  constexpr int NB = TC * NP / 8, NX = TC * PB / 8;      // pieces of a chunk
   constexpr int KB = (NB + SC_THREADS - 1) / SC_THREADS, KX = (NX + SC_THREADS - 1) / SC_THREADS;
+  constexpr int KC = STATE ? 0 : KB, V16 = sizeof(T) / 2;
+  constexpr bool RAW = VEC && NL == 8;
+  __shared__ __align__(16) uint4 raw[RAW ? (KB + KC + KX) * V16 : 1][SC_THREADS];
   Vec8<T> vb[KB], vc[STATE ? 1 : KB], vx[KX];
   float vd = 0.f;
+  auto bring = [&](Vec8<T>& v, int k, const T* p, int valid) {
+    if constexpr (RAW) {
+      if (valid > 0)
+#pragma unroll
+        for (int e = 0; e < V16; ++e)
+          cp_async16(smem_u32(&raw[k * V16 + e][threadIdx.x]), reinterpret_cast<const uint4*>(p) + e);
+    } else {
+      v = load8<T, VEC>(p, valid);
+    }
+  };
+  auto take = [&](const Vec8<T>& v, int k, bool valid) {
+    if constexpr (RAW) {
+      Vec8<T> r;
+#pragma unroll
+      for (int e = 0; e < V16; ++e) {
+        const uint4 q = valid ? raw[k * V16 + e][threadIdx.x] : make_uint4(0, 0, 0, 0);
+        r.w[4 * e] = q.x;
+        r.w[4 * e + 1] = q.y;
+        r.w[4 * e + 2] = q.z;
+        r.w[4 * e + 3] = q.w;
+      }
+      return r;
+    } else {
+      return v;
+    }
+  };
   auto fetch = [&](int t0) {
     const int nt = s1 - t0;
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
       const int i = threadIdx.x + k * SC_THREADS, t = i / (NP / 8), n = i % (NP / 8) * 8;
       const int valid = i < NB && t < nt ? min(8, a.N - n) : 0;
-      vb[k] = load8<T, VEC>(static_cast<const T*>(a.B.p) + at(a.B, t0 + t) + (int64_t)g * a.N + n, valid);
-      if (!STATE) vc[k] = load8<T, VEC>(static_cast<const T*>(a.C.p) + at(a.C, t0 + t) + (int64_t)g * a.N + n, valid);
+      bring(vb[k], k, static_cast<const T*>(a.B.p) + at(a.B, t0 + t) + (int64_t)g * a.N + n, valid);
+      if constexpr (!STATE)
+        bring(vc[k], KB + k, static_cast<const T*>(a.C.p) + at(a.C, t0 + t) + (int64_t)g * a.N + n, valid);
     }
 #pragma unroll
     for (int k = 0; k < KX; ++k) {
       const int i = threadIdx.x + k * SC_THREADS, t = i / (PB / 8), p = p0 + i % (PB / 8) * 8;
-      vx[k] = load8<T, VEC>(static_cast<const T*>(a.x.p) + at(a.x, t0 + t) + (int64_t)h * a.P + p,
-                            i < NX && t < nt ? min(8, a.P - p) : 0);
+      bring(vx[k], KB + KC + k, static_cast<const T*>(a.x.p) + at(a.x, t0 + t) + (int64_t)h * a.P + p,
+            i < NX && t < nt ? min(8, a.P - p) : 0);
     }
-    if (threadIdx.x < SC_TC && (int)threadIdx.x < nt) {
+    if constexpr (RAW) asm volatile("cp.async.commit_group;" ::: "memory");
+    if (threadIdx.x < TC && (int)threadIdx.x < nt) {
       const int64_t o = at(a.dt, t0 + threadIdx.x) + h;
       vd = a.dt_f32 ? static_cast<const float*>(a.dt.p)[o] : to_f(static_cast<const T*>(a.dt.p)[o]);
     }
@@ -122,28 +168,32 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
     *reinterpret_cast<float4*>(to + 4) = make_float4(f[4], f[5], f[6], f[7]);
   };
   if (s0 < s1) fetch(s0);
-  for (int t0 = s0; t0 < s1; t0 += SC_TC) {
-    const int nt = min(SC_TC, s1 - t0);
+  for (int t0 = s0; t0 < s1; t0 += TC) {
+    const int nt = min(TC, s1 - t0);
+    if constexpr (RAW) asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
       const int i = threadIdx.x + k * SC_THREADS;
+      const bool valid = i / (NP / 8) < nt && i % (NP / 8) * 8 < a.N;
       if (i < NB) {
-        put8(&sB[0][0] + 8 * i, vb[k]);
-        if (!STATE) put8(&sC[0][0] + 8 * i, vc[k]);
+        put8(&sB[0][0] + 8 * i, take(vb[k], k, valid));
+        if constexpr (!STATE) put8(&sC[0][0] + 8 * i, take(vc[k], KB + k, valid));
       }
     }
 #pragma unroll
     for (int k = 0; k < KX; ++k) {
       const int i = threadIdx.x + k * SC_THREADS;
-      if (i < NX) put8(&sx[0][0] + 8 * i, vx[k]);
+      const bool valid = i / (PB / 8) < nt && p0 + i % (PB / 8) * 8 < a.P;
+      if (i < NX) put8(&sx[0][0] + 8 * i, take(vx[k], KB + KC + k, valid));
     }
-    if (threadIdx.x < SC_TC) {
+    if (threadIdx.x < TC) {
       const float d = a.softplus ? softplus_f(vd + bias) : vd + bias;
       sdt[threadIdx.x] = d;
       sdec[threadIdx.x] = expf(d * Ah);
     }
-    if (t0 + SC_TC < s1) fetch(t0 + SC_TC);
+    if (t0 + TC < s1) fetch(t0 + TC);
     __syncthreads();
+#pragma unroll UN
     for (int t = 0; t < nt; ++t) {
       const float dec = sdec[t], dt = sdt[t];
       const f2 dec2 = mk2(dec, dec);
@@ -179,9 +229,13 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
           float u, v;
           un2(acc[r], u, v);
           u += v;
+          if constexpr (PARTS) {
+            sy[t][r * SC_THREADS + mine] = ln == 0 ? fmaf(Dh, sx[t][pl + r], u) : u;
+          } else {
 #pragma unroll
-          for (int o = 1; o < NL; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-          if (ln == 0) sy[t][pl + r] = fmaf(Dh, sx[t][pl + r], u);
+            for (int o = 1; o < NL; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
+            if (ln == 0) sy[t][pl + r] = fmaf(Dh, sx[t][pl + r], u);
+          }
         }
     }
     __syncthreads();
@@ -192,7 +246,19 @@ ssm_scan_kernel(const __grid_constant__ ScanArgs sa) {
         if (i >= NX || t >= nt) continue;
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = (&sy[0][0])[8 * i + e];
+        for (int e = 0; e < 8; ++e) {
+          if constexpr (PARTS) {
+            const int q = i % (PB / 8) * 8 + e;
+            f[e] = 0.f;
+#pragma unroll
+            for (int n = 0; n < NL; n += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(&sy[t][q % PR * SC_THREADS + place(q / PR * NL + n)]);
+              f[e] += (v.x + v.y) + (v.z + v.w);
+            }
+          } else {
+            f[e] = (&sy[0][0])[8 * i + e];
+          }
+        }
         store8<T, VEC>(static_cast<T*>(const_cast<void*>(a.y.p)) + at(a.y, t0 + t) + (int64_t)h * a.P + p, pack8<T>(f),
                        min(8, a.P - p));
       }
@@ -301,7 +367,7 @@ SsmPlan ssm_scan_plan(int H, int P, int N, int rows, const int32_t* lens, int64_
   // Segments for a call that would leave most SMs with less than one CTA: two
   // more launches and half the work again, so at least four segments in the
   // longest row, at most 16, of 32 tokens or more.  One row of 4096 tokens of 8
-  // heads of 64 x 128: 132 us, 844 whole; 11 rows of up to 203 tokens of 6 heads
+  // heads of 64 x 128: 132 us, 844 whole (125 since chunks have eight tokens); 11 rows of up to 203 tokens of 6 heads
   // of 40 x 72: 33 us, 41 whole.
   for (int64_t seg = (longest + 15) / 16 < 32 ? 32 : (longest + 15) / 16; 4 * seg <= longest; seg += (seg + 3) / 4) {
     int64_t tiles = 0;
