@@ -31,10 +31,9 @@
 //
 // Measured on a GB300: 16 x 512 tokens of 32 heads of 128 x 128 106 us (1.7
 // TB/s of the 6.7 of a copy; a first kernel on the FP32 cores 1.1 ms), of 64 x
-// 128 59 us; one
-// row of 2048 tokens of 16 heads of 64 x 128 24 us in three launches.  A chunk's
+// 128 59 us; one row of 2048 tokens of 16 heads of 64 x 128 24 us in three launches.  A chunk's
 // products are some 2500 cycles of the tensor cores and its operands 3700 of
-// shared memory, of about 5000; the schedulers issue 40% of the time.  One CTA
+// shared memory, of about 5000; the schedulers issue 43% of the time.  One CTA
 // of 16 warps with everything doubled and the warps specialised took 138 us, 128
 // state rows a unit 127 us (spilling), two heads a unit 87 us for 59.
 //
