@@ -404,7 +404,8 @@ int32_t dl_abi_version(void);
 /* gated norm of the heads' outputs (dl_gated_norm), residual sum and norm    */
 /* before the next block (dl_add_norm).  They need no context: the caller     */
 /* owns every buffer and names the stream (a cudaStream_t, NULL = legacy      */
-/* default stream).  Every call is asynchronous, allocates nothing, keeps     */
+/* default stream); the buffers and the stream belong to the calling thread's */
+/* current device.  Every call is asynchronous, allocates nothing, keeps      */
 /* nothing for the next call, and can be captured into a CUDA graph.  All     */
 /* arguments are checked on the host first; on a status other than DL_OK      */
 /* nothing has been enqueued (DL_ECUDA: a launch failed), and errbuf, if not  */

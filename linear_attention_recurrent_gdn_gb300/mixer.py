@@ -8,9 +8,10 @@
 
 Marshalling of the dl_conv, dl_ssm, dl_ssm_step, dl_gated_norm and dl_add_norm
 calls (include/deltalog.h says what each computes); every step runs in the
-library's kernels, on torch's current stream.  Calls are asynchronous and can
-be captured into a CUDA graph; outputs and workspaces come from torch's
-allocator.  Inference only: a tensor that asks for a gradient is refused.
+library's kernels, on the current stream of the tensors' device.  Calls are
+asynchronous and can be captured into a CUDA graph; outputs and workspaces come
+from torch's allocator.  Inference only: a tensor that asks for a gradient is
+refused.
 
 Tokens of ``n`` rows (sequences) are laid out
   token-major  [T, n, ...]: with ``lengths``, row i has its first lengths[i]
@@ -59,7 +60,16 @@ def _signatures(lib):
 
 _lib = _signatures(_dl.library())
 _raw_stream = torch._C._cuda_getCurrentRawStream     # the current stream's handle, without an object around it
+_device = torch._C._cuda_getDevice                   # the current device's number
 _F32 = torch.float32
+
+
+def _on(dev, fn, *args):
+    """fn(*args) with ``dev`` as the current device: the library's calls launch on that one, whatever their stream."""
+    if dev == _device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _call(fn, args, dev):
@@ -68,15 +78,16 @@ def _call(fn, args, dev):
     except AttributeError:
         err = ctypes.create_string_buffer(_ERR)
         err, at = _local.err = err, ctypes.addressof(err)
-    rc = fn(args, _raw_stream(dev), at, _ERR)
+    rc = _on(dev, fn, args, _raw_stream(dev), at, _ERR)
     if rc:
         raise _dl.DeltaLogError(rc, err.value.decode())
 
 
 def sync(device=None):
-    """Wait for the current stream and report a kernel's error since the last call."""
+    """Wait for the device's current stream and report an error of its kernels since the last call."""
+    stream = torch.cuda.current_stream(device)
     err = ctypes.create_string_buffer(_ERR)
-    rc = _lib.dl_mixer_sync(torch.cuda.current_stream(device).cuda_stream, None, err, _ERR)
+    rc = _on(stream.device_index, _lib.dl_mixer_sync, stream.cuda_stream, None, err, _ERR)
     if rc:
         raise _dl.DeltaLogError(rc, err.value.decode())
 
@@ -269,7 +280,7 @@ def _ssm(fn, x, dt, A, B, C, D, dt_bias, dt_softplus, slots, state, lengths, fre
            _param("dt_bias", dt_bias, (H,), _F32, dev), pool)
     args = _SSM.pack(*head, 0, 0)
     if not step:
-        size = _lib.dl_ssm_workspace(args)
+        size = _on(dev, _lib.dl_ssm_workspace, args)
         if size > 0:
             workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
             args = _SSM.pack(*head, workspace.data_ptr(), size)

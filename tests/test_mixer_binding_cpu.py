@@ -1,0 +1,65 @@
+"""What the mixer binding does on the host before a call reaches the library (no GPU needed)."""
+import types
+
+import pytest
+import torch
+
+from linear_attention_recurrent_gdn_gb300 import build
+
+
+@pytest.fixture(scope="module")
+def mx():
+    build.build()
+    from linear_attention_recurrent_gdn_gb300 import mixer
+    return mixer
+
+
+# ------------------------------------------------------------------ devices --
+class Devices:
+    """Two devices on the host: which one is current, and what the library saw as it was called."""
+
+    def __init__(self, mx, monkeypatch):
+        self.current, self.seen, outer = 0, [], self
+
+        class Guard:
+            def __init__(self, dev):
+                self.dev = dev
+
+            def __enter__(self):
+                self.before, outer.current = outer.current, self.dev
+
+            def __exit__(self, *exc):
+                outer.current = self.before
+
+        monkeypatch.setattr(mx, "_device", lambda: self.current, raising=False)
+        monkeypatch.setattr(mx, "_raw_stream", lambda dev: 1000 + dev)
+        monkeypatch.setattr(torch.cuda, "device", Guard)
+        monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: types.SimpleNamespace(
+            device_index=self.current if device is None else device,
+            cuda_stream=1000 + (self.current if device is None else device)))
+
+    def library(self, result):
+        def call(*args):
+            self.seen.append((self.current,) + args)
+            return result
+        return call
+
+
+def test_calls_run_with_their_tensors_device_current(mx, monkeypatch):
+    """A launch goes to the current device whatever its stream; stream 0 is every device's default stream."""
+    devs = Devices(mx, monkeypatch)
+    mx._call(devs.library(0), b"args", 0)
+    mx._call(devs.library(0), b"args", 1)
+    assert [s[:3] for s in devs.seen] == [(0, b"args", 1000), (1, b"args", 1001)]
+    assert devs.current == 0
+    with pytest.raises(mx._dl.DeltaLogError):
+        mx._call(devs.library(1), b"args", 1)
+    assert devs.current == 0
+
+
+def test_sync_reads_the_status_of_the_named_device(mx, monkeypatch):
+    devs = Devices(mx, monkeypatch)
+    monkeypatch.setattr(mx, "_lib", types.SimpleNamespace(dl_mixer_sync=devs.library(0)))
+    mx.sync()
+    mx.sync(1)
+    assert [s[:2] for s in devs.seen] == [(0, 1000), (1, 1001)] and devs.current == 0
