@@ -157,9 +157,14 @@ def _tokens(name, t, shape, dtype, dev, inner, lead):
 
 
 def _host(a, dtype, n, name):
-    """A host list as an array and its address."""
+    """A host list as an array and its address.  Whole numbers only, and none that `dtype` cannot hold."""
     if type(a) is not np.ndarray or a.dtype != dtype or not a.flags.c_contiguous:
-        a = np.ascontiguousarray(a, dtype=dtype)
+        given = np.asarray(a)
+        if given.dtype.kind not in "iub" and given.size:
+            raise ValueError("%s: whole numbers wanted, got %s" % (name, given.dtype))
+        a = np.ascontiguousarray(given, dtype=dtype)
+        if (a != given).any():
+            raise ValueError("%s: a number does not fit into %s" % (name, a.dtype))
     if a.shape != (n,):
         raise ValueError("%s: expected %d entries, got %s" % (name, n, a.shape))
     return a, a.__array_interface__["data"][0]

@@ -1,6 +1,7 @@
 """What the mixer binding does on the host before a call reaches the library (no GPU needed)."""
 import types
 
+import numpy as np
 import pytest
 import torch
 
@@ -63,3 +64,34 @@ def test_sync_reads_the_status_of_the_named_device(mx, monkeypatch):
     mx.sync()
     mx.sync(1)
     assert [s[:2] for s in devs.seen] == [(0, 1000), (1, 1001)] and devs.current == 0
+
+
+# --------------------------------------------------------------- host lists --
+@pytest.mark.parametrize("given,dtype", [
+    ([0.7, 1.0], np.int32), (np.array([0.0, 1.0]), np.int32), ([1, None], np.int32), (["0", "1"], np.int32),
+    (np.array([1, 2 ** 32 + 1]), np.int32), ([2 ** 32 + 1, 0], np.int32), ([-2 ** 31 - 1, 0], np.int32),
+    (np.array([3, 2 ** 31], dtype=np.uint32), np.int32), ([0, 2 ** 70], np.int32),
+    ([0, 256], np.uint8), ([-1, 0], np.uint8), (np.array([0.5, 1.0]), np.uint8),
+    ([0, 1, 2], np.int32), ([[0, 1]], np.int32), (5, np.int32),
+])
+def test_host_lists_that_are_refused(mx, given, dtype):
+    """Slots, lengths and flags are whole numbers of their type; none is cut or wrapped to one."""
+    with pytest.raises((ValueError, TypeError)):
+        mx._host(given, dtype, 2, "list")
+
+
+@pytest.mark.parametrize("given,dtype,want", [
+    ([3, 2 ** 31 - 1], np.int32, [3, 2 ** 31 - 1]), (np.array([-1, 7]), np.int32, [-1, 7]),
+    (np.array([1, 9, 2, 9], dtype=np.int32)[::2], np.int32, [1, 2]), (torch.tensor([4, 5]), np.int32, [4, 5]),
+    (np.array([True, False]), np.uint8, [1, 0]), ([True, False], np.uint8, [1, 0]), ([1, 0], np.uint8, [1, 0]),
+    (range(2), np.int32, [0, 1]),
+])
+def test_host_lists_that_are_taken(mx, given, dtype, want):
+    a, at = mx._host(given, dtype, 2, "list")
+    assert a.dtype == dtype and a.tolist() == want and at == a.ctypes.data and a.flags.c_contiguous
+
+
+def test_empty_and_ready_lists(mx):
+    assert mx._host([], np.int32, 0, "list")[0].shape == (0,)
+    ready = np.array([1, 2], np.int32)
+    assert mx._host(ready, np.int32, 2, "list")[0] is ready
