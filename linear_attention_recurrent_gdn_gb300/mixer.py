@@ -10,8 +10,8 @@ Marshalling of the dl_conv, dl_ssm, dl_ssm_step, dl_gated_norm and dl_add_norm
 calls (include/deltalog.h says what each computes); every step runs in the
 library's kernels, on the current stream of the tensors' device.  Calls are
 asynchronous and can be captured into a CUDA graph; outputs and workspaces come
-from torch's allocator.  Inference only: a tensor that asks for a gradient is
-refused.
+from torch's allocator.  Inference only: a tensor that asks for a gradient, or
+carries a forward-mode tangent, is refused.
 
 Tokens of ``n`` rows (sequences) are laid out
   token-major  [T, n, ...]: with ``lengths``, row i has its first lengths[i]
@@ -30,6 +30,7 @@ import threading
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad as _fwd
 
 from . import deltalog as _dl
 
@@ -95,12 +96,18 @@ def sync(device=None):
 # The checks below are written for few Python steps: in a decode loop they are
 # the cost of a call.  A CPU tensor's device number is -1.
 
+def _differentiated(t):
+    """Whether the tensor asks for a gradient or, inside a forward-mode level, carries a tangent."""
+    return t.requires_grad and torch.is_grad_enabled() or \
+        _fwd._current_level >= 0 and _fwd.unpack_dual(t).tangent is not None
+
+
 def _bad(name, t, dtype, dev):
     """Says what is wrong with a tensor that failed a check."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s requires a gradient: these operators have no backward" % name)
+    if _differentiated(t):
+        raise ValueError("%s is being differentiated: these operators have no derivatives" % name)
     raise ValueError("%s: expected %s on device %s, got %s on %s" % (name, dtype, dev, t.dtype, t.device))
 
 
@@ -110,14 +117,13 @@ def _x(t):
         raise TypeError("x must be a CUDA tensor")
     if t.dtype not in _DTYPE:
         raise ValueError("x: %s is not supported" % t.dtype)
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("x requires a gradient: these operators have no backward")
+    if _differentiated(t):
+        _bad("x", t, t.dtype, t.get_device())
     return t.get_device()
 
 
 def _check(name, t, shape, dtype, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or \
-            (t.requires_grad and torch.is_grad_enabled()):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or _differentiated(t):
         _bad(name, t, dtype, dev)
     if t.shape != shape:
         raise ValueError("%s: expected %s, got %s" % (name, tuple(shape), tuple(t.shape)))

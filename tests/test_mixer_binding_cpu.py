@@ -95,3 +95,30 @@ def test_empty_and_ready_lists(mx):
     assert mx._host([], np.int32, 0, "list")[0].shape == (0,)
     ready = np.array([1, 2], np.int32)
     assert mx._host(ready, np.int32, 2, "list")[0] is ready
+
+
+# ------------------------------------------------------------- derivatives --
+def test_tensors_that_are_differentiated_are_refused(mx):
+    """Backward or forward: a result without its derivative would be taken for a constant."""
+    fwd = torch.autograd.forward_ad
+    t = torch.ones(3)
+    check = lambda v: mx._check("weight", v, (3,), torch.float32, -1)  # noqa: E731  (a CPU tensor's device)
+    check(t)
+    with pytest.raises((ValueError, TypeError)):
+        check(torch.ones(3, requires_grad=True))
+    with torch.no_grad():
+        check(torch.ones(3, requires_grad=True))
+    with fwd.dual_level():
+        check(t)
+        with torch.inference_mode():
+            check(torch.ones(3))
+        with pytest.raises((ValueError, TypeError)):
+            check(fwd.make_dual(t, torch.ones(3)))
+    check(t)
+    seen = []
+
+    def f(v):
+        seen.append(mx._differentiated(v))
+        return v * 2
+    torch.func.jvp(f, (t,), (torch.ones(3),))
+    assert seen == [True]
