@@ -149,6 +149,14 @@ def _dense(name, t, inner, stride):
         want *= shape[k]
 
 
+def _one_of(names, name, what):
+    """The number of an activation or a norm."""
+    try:
+        return names[name]
+    except (KeyError, TypeError):
+        raise ValueError("%s: expected one of %s, got %r" % (what, ", ".join(map(repr, names)), name)) from None
+
+
 def _tokens(name, t, shape, dtype, dev, inner, lead):
     """A per-token tensor: checks it and returns (data, stride between tokens, between rows)."""
     _check(name, t, shape, dtype, dev)
@@ -240,7 +248,8 @@ def _conv(x, weight, bias, slots, state, lengths, fresh, activation, l2_channels
         for t, c in zip(outs, parts):
             views += _tokens("out", t, lead_shape + (c,), dt, dev, 1, lead)
     pad = 4 - len(parts)
-    _call(_lib.dl_conv, _CONV.pack(*fields, _DTYPE[dt], wt is _F32, C, W, _ACT[activation], l2_channels, head_dim,
+    act = _one_of(_ACT, activation, "activation")
+    _call(_lib.dl_conv, _CONV.pack(*fields, _DTYPE[dt], wt is _F32, C, W, act, l2_channels, head_dim,
                                    len(parts), eps, *xv, wp, bp, pool, *views, *_ZEROS[:3 * pad], *parts,
                                    *_ZEROS[:pad]), dev)
     return outs[0] if split is None else tuple(outs)
@@ -347,8 +356,9 @@ def gated_norm(x, weight, gate=None, *, bias=None, kind="rms", activation="silu"
         op, os = out.data_ptr(), shape[1] * shape[2]
     else:
         op, os = _matrix("out", out, shape, dt, dev, 2)
-    _call(_lib.dl_gated_norm, _GATED.pack(_DTYPE[dt], wt is _F32, heads, *shape, _KIND[kind], _ACT[activation],
-                                          bool(gate_first), eps, xp, gp, wp, bp, op, xs, gs, os), dev)
+    act, kind = _one_of(_ACT, activation, "activation"), _one_of(_KIND, kind, "kind")
+    _call(_lib.dl_gated_norm, _GATED.pack(_DTYPE[dt], wt is _F32, heads, *shape, kind, act, bool(gate_first), eps,
+                                          xp, gp, wp, bp, op, xs, gs, os), dev)
     return out
 
 
@@ -385,6 +395,6 @@ def add_norm(x, residual, weight, *, bias=None, scale=None, alpha=1.0, post_weig
         hp, hs = out_residual.data_ptr(), shape[1]
     else:
         hp, hs = _matrix("out_residual", out_residual, shape, rt, dev, 1)
-    _call(_lib.dl_add_norm, _ADD.pack(_DTYPE[dt], rt is _F32, wt is _F32, *shape, _KIND[kind], eps, alpha, xp, rp, wp,
-                                      bp, sp, pp, op, hp, xs, rs, os, hs), dev)
+    _call(_lib.dl_add_norm, _ADD.pack(_DTYPE[dt], rt is _F32, wt is _F32, *shape, _one_of(_KIND, kind, "kind"), eps,
+                                      alpha, xp, rp, wp, bp, sp, pp, op, hp, xs, rs, os, hs), dev)
     return out, out_residual

@@ -24,3 +24,12 @@ def test_forward_mode_tensors_are_refused(mx):
                 call()
         y, _ = mx.add_norm(x, None, w)
     assert torch.equal(y, mx.add_norm(x, None, w)[0])
+
+
+def test_unknown_activations_and_norms_are_refused(mx):
+    x, w = torch.ones(2, 4, 64, device="cuda"), torch.ones(64, device="cuda")
+    for call in (lambda: mx.conv(x, torch.ones(64, 4, device="cuda"), activation="relu"),
+                 lambda: mx.gated_norm(x, w, x, activation="gelu"), lambda: mx.gated_norm(x, w, kind="batch"),
+                 lambda: mx.add_norm(x[0], None, w, kind=0)):
+        with pytest.raises(ValueError, match="expected one of"):
+            call()

@@ -122,3 +122,11 @@ def test_tensors_that_are_differentiated_are_refused(mx):
         return v * 2
     torch.func.jvp(f, (t,), (torch.ones(3),))
     assert seen == [True]
+
+
+# -------------------------------------------------------------------- names --
+def test_unknown_activations_and_norms(mx):
+    assert [mx._one_of(mx._ACT, a, "activation") for a in (None, "none", "silu", "sigmoid")] == [0, 0, 1, 2]
+    for names, name in ((mx._ACT, "relu"), (mx._ACT, 1), (mx._KIND, None), (mx._KIND, ["rms"])):
+        with pytest.raises(ValueError, match="expected one of"):
+            mx._one_of(names, name, "name")
