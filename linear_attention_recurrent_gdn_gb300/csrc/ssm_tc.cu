@@ -1,22 +1,25 @@
 // Selective state space scan of bf16 prompts on the 5th-generation tensor cores.
 //
 // A chunk is Q = 128 tokens.  With S the state at its start, L_i the sum of
-// dt_k A over tokens k <= i of the chunk and T_j the sum over tokens k > j,
-//   y_i = sum_{j <= i} (C_i . B_j) e^{L_i - L_j} dt_j x_j  +  e^{L_i} S C_i  +  D x_i
+// dt_k A over tokens k <= i of the chunk, L_ij over j < k <= i and T_j over k > j,
+//   y_i = sum_{j <= i} (C_i . B_j) e^{L_ij} dt_j x_j  +  e^{L_i} S C_i  +  D x_i
 //   S'  = e^{L_Q} S + sum_j (e^{T_j} dt_j x_j) B_j^T
 // Every factor is at most one for A < 0.  Per chunk and PC = 64 rows p of the
 // state, rows of a product being tokens (state columns n for the last), tcgen05
 // MMAs with fp32 accumulators in TMEM:
 //   G  [128 x 128] = C B^T               exact products of the inputs
 //   Y2 [128 x 64]  = C S^T               S rounded to bf16
-//   Y1 [128 x 64]  = W X                 W_ij = G_ij e^{L_i - L_j} dt_j rounded to bf16, A in TMEM
+//   Y1 [128 x 64]  = W X                 W_ij = G_ij e^{L_ij} dt_j rounded to bf16, A in TMEM
 //   dS [128 x 64]  = B^T (X3 + X2 + X1)  e^{T_j} dt_j x_j as three bf16 terms (2^-25 of it is left)
 // W and the S of Y2 are rounded once, like the output itself (half a step of
 // bf16 each); the state keeps 32 bits: it lives in registers in fp32 and its
-// increments are formed from all 24 bits.  e^{L_i - L_j} outside the diagonal
-// 32 x 32 blocks is the product of a row and a column factor, both at most
-// one: e^{L_i - L_b} e^{L_b - L_j}, b the last token of j's block, so only the
-// diagonal blocks take an exponential a pair.
+// increments are formed from all 24 bits.  e^{L_ij} outside the diagonal 32 x 32
+// blocks is the product of a row and a column factor, both at most one, with b
+// the last token of j's block: e^{L_ib} e^{L_bj}, so only the diagonal blocks
+// take an exponential a pair.  Their exponents are summed token by token from i
+// downwards: as differences of sums from the chunk's start they would be off by
+// a rounding of the whole chunk's decay (one token of dt A = -1.6e5 left
+// weights after it 17% off).
 //
 // A persistent CTA of eight warps takes units: one head's 64 state rows over a
 // segment of a row.  B and C of the group, X, its terms and S sit in shared
@@ -65,11 +68,15 @@ struct Sm {
   static constexpr uint32_t TILE = 2 * BLK64;        // B or C: 128 tokens x 128 state columns
   static constexpr uint32_t B = 0, C = TILE, X = 2 * TILE, S = X + BLK64;
   static constexpr uint32_t X1 = C, X2 = C + BLK64, X3 = S;
-  static constexpr uint32_t F = S + BLK64;           // L [128], column factors [128], L at the blocks' ends [4],
-  static constexpr uint32_t FB = (2 * Q + 12) * 4;   // e^{T} of the blocks' last tokens [4], log2 of the chunk's decay
+  static constexpr uint32_t F = S + BLK64;           // the chunk's decays, see F_* below
+  static constexpr uint32_t FB = (4 * Q + 16) * 4;
   static constexpr uint32_t BAR = F + FB;            // seven mbarriers, TMEM address
   static constexpr uint32_t BYTES = BAR + 64;
 };
+// dt, log2 of the tokens' decays, their sums from every 16th token on, the pair weights' column factors (128 of each);
+// sums over the blocks of 32 and over their first halves, e^{T} of the blocks' last tokens (4 of each); the whole sum.
+constexpr int F_DT = 0, F_L = Q, F_H = 2 * Q, F_COL = 3 * Q, F_BLK = 4 * Q, F_HALF = F_BLK + 4, F_ET = F_BLK + 8,
+              F_SUM = F_BLK + 12;
 static_assert(2 * (Sm::BYTES + 1024) <= 228 * 1024, "two CTAs an SM");
 
 __device__ __forceinline__ float ex2(float x) {
@@ -316,19 +323,19 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         for (int c = 0; c < HC && c < live_of(v); ++c) to[elem0(v) + (int64_t)c * a.N] = 0.f;
     }
 
-  // dt of the next chunk: the scanning warp's four tokens, everybody's own token
-  uint32_t raw[4], rawi = 0;
+  // dt of the next chunk: the scanning warp's four tokens
+  uint32_t raw[4];
   float bias = 0.f, Ah = 0.f;
   auto load_dt = [&](const Unit& v, int c) {
-    if (scans) {
+    if (!scans) return;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) raw[k] = raw_dt(v, v.s0 + c * Q + 4 * lane + k);
-    }
-    if (!STATE) rawi = raw_dt(v, v.s0 + c * Q + i);
+    for (int k = 0; k < 4; ++k) raw[k] = raw_dt(v, v.s0 + c * Q + 4 * lane + k);
     Ah = a.A[v.h];
     bias = a.dt_bias ? a.dt_bias[v.h] : 0.f;
   };
-  // decays of a chunk of nt tokens, from raw
+  // Decays of a chunk of nt tokens, from raw.  Every exponent that is used is a sum of the logs it spans and never a
+  // difference of longer sums: of one sign for A < 0, such a sum is off by a few steps of its own size, however
+  // strong the decays around it are, and one that overflows is -inf (a factor of zero).
   auto scan = [&](int nt) {
     float dt[4], l[4], suf[4];
 #pragma unroll
@@ -336,7 +343,9 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       dt[k] = 4 * lane + k < nt ? dt_of(raw[k], bias) : 0.f;
       l[k] = dt[k] * (Ah * LOG2E);
     }
-    // tokens after j in its block of 32, summed from the end: no cancellation in the sums that matter
+    *reinterpret_cast<float4*>(f + F_DT + 4 * lane) = make_float4(dt[0], dt[1], dt[2], dt[3]);
+    *reinterpret_cast<float4*>(f + F_L + 4 * lane) = make_float4(l[0], l[1], l[2], l[3]);
+    // over the tokens after one in its block of 32
     suf[3] = 0.f;
     suf[2] = l[3];
     suf[1] = suf[2] + l[2];
@@ -350,25 +359,27 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       const float d = __shfl_down_sync(0xffffffffu, post, o, 8);
       if ((lane & 7) + o < 8) post += d;
     }
+    // up to a token from the first of its 16
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const float v = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += v;
+    for (int o = 1; o < 4; o <<= 1) {
+      const float v = __shfl_up_sync(0xffffffffu, pre, o, 4);
+      if ((lane & 3) >= o) pre += v;
     }
-    const float before = pre - l[3];
-    const float nxt = __shfl_down_sync(0xffffffffu, post, 1, 8);
-    const float after = (lane & 7) < 7 ? nxt : 0.f;
+    const float prv = __shfl_up_sync(0xffffffffu, pre, 1, 4), nxt = __shfl_down_sync(0xffffffffu, post, 1, 8);
+    const float before = (lane & 3) > 0 ? prv : 0.f, after = (lane & 7) < 7 ? nxt : 0.f;
     float bs[4];
 #pragma unroll
     for (int b = 0; b < 4; ++b) bs[b] = __shfl_sync(0xffffffffu, post, 8 * b);
-    *reinterpret_cast<float4*>(f + 4 * lane) = make_float4(before + l[0], before + l[1], before + l[2], pre);
-    *reinterpret_cast<float4*>(f + Q + 4 * lane) =
+    *reinterpret_cast<float4*>(f + F_H + 4 * lane) = make_float4(before + l[0], before + l[1], before + l[2], pre);
+    *reinterpret_cast<float4*>(f + F_COL + 4 * lane) =
         make_float4(ex2(after + suf[0]) * dt[0], ex2(after + suf[1]) * dt[1], ex2(after + suf[2]) * dt[2],
                     ex2(after + suf[3]) * dt[3]);
-    if ((lane & 7) == 7) f[2 * Q + (lane >> 3)] = pre;
-    if (lane < 4)
-      f[2 * Q + 4 + lane] = ex2(lane == 0 ? bs[3] + bs[2] + bs[1] : lane == 1 ? bs[3] + bs[2] : lane == 2 ? bs[3] : 0.f);
-    if (lane == 0) f[2 * Q + 8] = bs[3] + bs[2] + bs[1] + bs[0];
+    if ((lane & 7) == 3) f[F_HALF + (lane >> 3)] = pre;
+    if (lane < 4) {
+      f[F_BLK + lane] = lane == 0 ? bs[0] : lane == 1 ? bs[1] : lane == 2 ? bs[2] : bs[3];
+      f[F_ET + lane] = ex2(lane == 0 ? bs[3] + bs[2] + bs[1] : lane == 1 ? bs[3] + bs[2] : lane == 2 ? bs[3] : 0.f);
+    }
+    if (lane == 0) f[F_SUM] = bs[3] + bs[2] + bs[1] + bs[0];
   };
 
   int u = blockIdx.x;
@@ -402,7 +413,11 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       const bool last = c + 1 == w.chunks, more = !last || another;
       const Unit wf = last ? wn : w;                // the chunk after this one
       const int cf = last ? 0 : c + 1;
-      const float decl = f[2 * Q + 8], li = f[i];
+      const float decl = f[F_SUM];
+      // the sums up to token i from the first of its 16, of its block, of the chunk
+      const float4 blk = *reinterpret_cast<const float4*>(f + F_BLK);
+      const float hi = f[F_H + i], ri = lane >= 16 ? hi + f[F_HALF + q4] : hi;
+      const float li = q4 == 0 ? ri : q4 == 1 ? ri + blk.x : q4 == 2 ? ri + (blk.x + blk.y) : ri + (blk.x + blk.y + blk.z);
       if (TMA && nt < Q) {
         // a ragged chunk: what lies behind its last token is cleared in B and X (C's rows there give rows of y
         // that are not kept)
@@ -435,7 +450,6 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
             if (k < nk) tc::mma_bf16(tm + COL_Y2, dc + col_step(k), ds + row_step(k), idY, k > 0);
           tc::mma_commit(barC);
         }
-        const float own = i < nt ? dt_of(rawi, bias) : 0.f;       // dt of token i
         if (more) load_dt(wf, cf);
         // ---- W from G: columns 32 b + 16 hf .. + 15 of every block b, in place of blocks 2 and 3 of G once both
         // warps of the lanes have read them
@@ -450,24 +464,35 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
             tc::tmem_wait_ld16(G);
           }
           if (b < q4) {
-            const float rf = ex2(li - f[2 * Q + b]);
+            // from the end of block b to token i
+            const float rf = ex2(b == 0 ? (q4 == 1 ? ri : q4 == 2 ? ri + blk.y : ri + (blk.y + blk.z))
+                                        : b == 1 && q4 == 3 ? ri + blk.z : ri);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float4 cf4 = *reinterpret_cast<const float4*>(f + Q + j0 + 4 * e);
+              const float4 cf4 = *reinterpret_cast<const float4*>(f + F_COL + j0 + 4 * e);
               v[2 * e] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e]) * (rf * cf4.x),
                                               __uint_as_float(G[4 * e + 1]) * (rf * cf4.y));
               v[2 * e + 1] = pack2<__nv_bfloat16>(__uint_as_float(G[4 * e + 2]) * (rf * cf4.z),
                                                   __uint_as_float(G[4 * e + 3]) * (rf * cf4.w));
             }
           } else if (b == q4) {
+            // from the last column down, a token's log at a time
+            float sum = hf == 0 && lane >= 16 ? hi : 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int j = j0 + 2 * e;
-              const float2 lj = *reinterpret_cast<const float2*>(f + j);
-              const float d0 = __shfl_sync(0xffffffffu, own, 16 * hf + 2 * e),
-                          d1 = __shfl_sync(0xffffffffu, own, 16 * hf + 2 * e + 1);
-              v[e] = pack2<__nv_bfloat16>(j <= i ? __uint_as_float(G[2 * e]) * (ex2(li - lj.x) * d0) : 0.f,
-                                          j + 1 <= i ? __uint_as_float(G[2 * e + 1]) * (ex2(li - lj.y) * d1) : 0.f);
+            for (int e4 = 3; e4 >= 0; --e4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(f + F_L + j0 + 4 * e4);
+              const float4 d4 = *reinterpret_cast<const float4*>(f + F_DT + j0 + 4 * e4);
+              const float l[4] = {l4.x, l4.y, l4.z, l4.w}, d[4] = {d4.x, d4.y, d4.z, d4.w};
+              float w[4];
+#pragma unroll
+              for (int k = 3; k >= 0; --k) {
+                const int e = 4 * e4 + k;             // column j0 + e
+                const bool in = 16 * hf + e <= lane;
+                w[k] = in ? __uint_as_float(G[e]) * (ex2(sum) * d[k]) : 0.f;
+                if (in) sum += l[k];
+              }
+              v[2 * e4] = pack2<__nv_bfloat16>(w[0], w[1]);
+              v[2 * e4 + 1] = pack2<__nv_bfloat16>(w[2], w[3]);
             }
           } else {
 #pragma unroll
@@ -510,7 +535,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         const int idx = tid + e * TCT, t = idx >> 3, cv = idx & 7;
         const uint32_t off = piece_off(t, cv);
         const uint4 xv = *reinterpret_cast<const uint4*>(sm + Sm::X + off);
-        const float g = f[Q + t] * f[2 * Q + 4 + (t >> 5)];
+        const float g = f[F_COL + t] * f[F_ET + (t >> 5)];
         const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
         uint32_t o1[4], o2[4], o3[4];
 #pragma unroll
