@@ -44,6 +44,8 @@
 // each segment from zero and leaves its end state and decay in the workspace, a
 // second joins them to the states at the segments' starts, and the full launch
 // goes on from those.
+#include <cstdlib>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 
@@ -70,8 +72,10 @@ struct Sm {
   static constexpr uint32_t X1 = C, X2 = C + BLK64, X3 = S;
   static constexpr uint32_t F = S + BLK64;           // the chunk's decays, see F_* below
   static constexpr uint32_t FB = (4 * Q + 16) * 4;
-  static constexpr uint32_t BAR = F + FB;            // seven mbarriers, TMEM address
-  static constexpr uint32_t BYTES = BAR + 64;
+  static constexpr uint32_t BAR = F + FB;            // eight mbarriers
+  static constexpr uint32_t TSLOT = BAR + 64;        // TMEM address
+  static constexpr uint32_t NEXT = TSLOT + 16;       // the unit after the current one, in turns
+  static constexpr uint32_t BYTES = NEXT + 2 * 48;
 };
 // dt, log2 of the tokens' decays, their sums from every 16th token on, the pair weights' column factors (128 of each);
 // sums over the blocks of 32 and over their first halves, e^{T} of the blocks' last tokens (4 of each); the whole sum.
@@ -118,12 +122,17 @@ struct TcArgs {
   SsmArgs a;
   float* ws;                    // segment states [tiles][H][P][N], then log2 decays [tiles][H]
   int32_t seg_tokens, tiles, per_row, units, ptiles, total, empty_rows;
+  // Test only (0 in normal use): a thread of CTA 0 also waits, for wait_ns / 2, on a barrier that nothing arrives on.
+  int32_t test_stall;
+  unsigned long long wait_ns;   // how long a wait spins before it gives up (WAIT_LIMIT_NS but in tests)
 };
 
 // One unit of work: tokens [s0, s1) of a row (a segment) for 64 state rows from p0 of head h.
 struct Unit {
   int tile, row, begin, h, p0, s0, s1, chunks;
+  int u;                        // its number; from TcArgs::total on: none
 };
+static_assert(sizeof(Unit) <= 48, "its place in shared memory");
 __device__ __forceinline__ Unit unit_at(const TcArgs& ta, int u) {
   const SsmArgs& a = ta.a;
   Unit w;
@@ -155,20 +164,22 @@ __device__ __forceinline__ bool skipped(const TcArgs& ta, const Unit& w) {
   segments(ta, w, seg, nseg);
   return seg == nseg - 1;
 }
-// The first unit from u on (in steps of the grid) that has work; u moves there, or past the last.
+// The first unit from u on (in steps of the grid) that has work.
 template <bool STATE>
-__device__ __forceinline__ Unit next_unit(const TcArgs& ta, int& u) {
+__device__ __forceinline__ Unit next_unit(const TcArgs& ta, int u) {
   Unit w{};
   for (; u < ta.total; u += gridDim.x) {
     w = unit_at(ta, u);
     if (!skipped<STATE>(ta, w)) break;
   }
+  w.u = u;
   return w;
 }
 // (Not inlined: the loops below have to stay in the instruction cache.)
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par) {
-  return mbar_wait(bar, par, &g_mixer_status, DEV_TIMEOUT_MMA);
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par, int32_t code, unsigned long long ns) {
+  return mbar_wait(bar, par, &g_mixer_status, code, ns);
 }
+__device__ __noinline__ void drain_long(uint32_t bar, uint32_t par) { mbar_drain(bar, par); }
 
 // TMA: tensor copies (16-byte aligned tensors, widths and strides); else
 // threads copy value by value.
@@ -185,12 +196,12 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
   const uint32_t sb = smem_u32(sm);
   float* f = reinterpret_cast<float*>(sm + Sm::F);
   const uint32_t barG = sb + Sm::BAR, barC = barG + 8, barS = barG + 16, barY = barG + 24, fullB = barG + 32,
-                 fullC = barG + 40, fullX = barG + 48;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sm::BAR + 56);
+                 fullC = barG + 40, fullX = barG + 48, never = barG + 56;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(sm + Sm::TSLOT);
 
-  if (warp == 0) tc::tmem_alloc(sb + Sm::BAR + 56, COLS);
+  if (warp == 0) tc::tmem_alloc(sb + Sm::TSLOT, COLS);
   if (tid == 0) {
-    for (int k = 0; k < 7; ++k) mbar_init(barG + 8 * k, 1);
+    for (int k = 0; k < 8; ++k) mbar_init(barG + 8 * k, 1);
     fence_mbar_init();
   }
 
@@ -256,9 +267,29 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
   tc::fence_after_sync();
   const uint32_t tm = *tslot;
   const uint32_t tl = tm + ((uint32_t)(32 * q4) << 16);
-  bool ok = true;                 // a wait that ran out: no further waits, no results
+  // A wait that ran out: this thread waits no more, and at the chunk's end the CTA leaves: no results, and nothing is
+  // started over what may still be on its way.
+  bool ok = true;
   auto wait = [&](uint32_t bar, uint32_t k) {       // for phase number k
-    if (ok && !mbar_try_wait(bar, k & 1u)) ok = wait_long(bar, k & 1u);
+    if (ok && !mbar_try_wait(bar, k & 1u)) ok = wait_long(bar, k & 1u, DEV_TIMEOUT_MMA, ta.wait_ns);
+  };
+  // After a wait that ran out in chunk number k: let its products and copies land before the memory is given back.
+  // ahead: B and C of the next chunk are on their way as well.
+  auto drain = [&](uint32_t k, bool ahead) {
+    if (tid == 0) {
+      if (!STATE) {
+        drain_long(barG, k & 1u);
+        drain_long(barC, k & 1u);
+        drain_long(barY, k & 1u);
+      }
+      drain_long(barS, k & 1u);
+    }
+    if (TMA && tid == 32) {
+      drain_long(fullX, k & 1u);
+      if (ahead) ++k;
+      drain_long(fullB, k & 1u);
+      if (!STATE) drain_long(fullC, k & 1u);
+    }
   };
   const int64_t per_tile = (int64_t)a.H * a.P * a.N;
 
@@ -292,7 +323,6 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     const int64_t e0 = elem0(w);
     const int live = live_of(w);
     float* to = STATE ? ta.ws + (int64_t)(w.tile + 1) * per_tile : seg == nseg - 1 ? pool_of(w) : nullptr;
-    if (!ok) return;
     if (to) {
 #pragma unroll
       for (int c = 0; c < HC; ++c)
@@ -327,7 +357,6 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
   uint32_t raw[4];
   float bias = 0.f, Ah = 0.f;
   auto load_dt = [&](const Unit& v, int c) {
-    if (!scans) return;
 #pragma unroll
     for (int k = 0; k < 4; ++k) raw[k] = raw_dt(v, v.s0 + c * Q + 4 * lane + k);
     Ah = a.A[v.h];
@@ -382,37 +411,43 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
     if (lane == 0) f[F_SUM] = bs[3] + bs[2] + bs[1] + bs[0];
   };
 
-  int u = blockIdx.x;
-  Unit w = next_unit<STATE>(ta, u);
-  bool any = u < ta.total;
-  if (any) {
+  Unit w = next_unit<STATE>(ta, blockIdx.x);
+  if (w.u < ta.total) {
     if (!TMA || tid == 32) {
       load_x(w, 0);
       load_bc(w, 0);
     }
-    load_dt(w, 0);
-    if (scans) scan(w.s1 - w.s0);
+    if (scans) {
+      load_dt(w, 0);
+      scan(w.s1 - w.s0);
+    }
   }
+  if (ta.test_stall && blockIdx.x == 0 && tid == 64) ok = wait_long(never, 0, DEV_TEST_STALL, ta.wait_ns / 2);
   uint32_t gc = 0;                // chunks done, over all units: every barrier's phase
 
+  uint32_t place = Sm::NEXT;      // of the next unit; one thread looks it up, and few of them want it, so that it costs
+                                  // no registers
 #pragma unroll 1
-  while (any) {
-    int un = u + gridDim.x;
-    const Unit wn = next_unit<STATE>(ta, un);
-    const bool another = un < ta.total;
+  while (w.u < ta.total) {
+    if (tid == 64) *reinterpret_cast<Unit*>(sm + place) = next_unit<STATE>(ta, w.u + gridDim.x);
     load_state(w);
     share_state();
     tc::fence_smem_to_async();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
+    const volatile Unit* wn = reinterpret_cast<const volatile Unit*>(sm + place);
+    const bool another = wn->u < ta.total;
     float ltot = 0.f;
 #pragma unroll 1
     for (int c = 0; c < w.chunks; ++c, ++gc) {
       const int t0 = w.s0 + c * Q, nt = min(Q, w.s1 - t0);
       const bool last = c + 1 == w.chunks, more = !last || another;
-      const Unit wf = last ? wn : w;                // the chunk after this one
-      const int cf = last ? 0 : c + 1;
+      const int cf = last ? 0 : c + 1;              // the chunk after this one, of this unit or the next
+      auto after = [&]() -> Unit {
+        if (!last) return w;
+        return Unit{wn->tile, wn->row, wn->begin, wn->h, wn->p0, wn->s0, wn->s1, wn->chunks, wn->u};
+      };
       const float decl = f[F_SUM];
       // the sums up to token i from the first of its 16, of its block, of the chunk
       const float4 blk = *reinterpret_cast<const float4*>(f + F_BLK);
@@ -450,7 +485,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
             if (k < nk) tc::mma_bf16(tm + COL_Y2, dc + col_step(k), ds + row_step(k), idY, k > 0);
           tc::mma_commit(barC);
         }
-        if (more) load_dt(wf, cf);
+        if (more && scans) load_dt(after(), cf);
         // ---- W from G: columns 32 b + 16 hf .. + 15 of every block b, in place of blocks 2 and 3 of G once both
         // warps of the lanes have read them
         if (TMA) wait(fullX, gc);
@@ -523,7 +558,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         }
         wait(barC, gc);           // G and Y2 have read C and S: the terms take their places
       } else {
-        if (more) load_dt(wf, cf);
+        if (more && scans) load_dt(after(), cf);
         if (TMA) {
           wait(fullX, gc);
           wait(fullB, gc);
@@ -564,7 +599,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
           tc::mma_bf16(tm + COL_DS, db + row_step(k & 7), dx[k >> 3] + row_step(k & 7), idS, k > 0);
         tc::mma_commit(barS);
       }
-      if (more && scans) scan(wf.s1 - wf.s0 - cf * Q);
+      if (more && scans) scan(last ? wn->s1 - wn->s0 : w.s1 - w.s0 - cf * Q);
       if (!STATE) {
         // ---- y = Y1 + e^{L_i} Y2 + D x, over x in shared memory
         const float ei = ex2(li), Dh = a.D ? a.D[w.h] : 0.f;
@@ -598,7 +633,11 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       // ---- S' = e^{L_Q} S + dS
       wait(barS, gc);
       tc::fence_after_sync();
-      if (TMA && more && tid == 32) load_bc(wf, cf);
+      if (TMA && more && tid == 32) {
+        wait(fullB, gc);          // landed long ago, unless a wait ran out
+        if (!STATE) wait(fullC, gc);
+        if (ok) load_bc(after(), cf);
+      }
       ltot += decl;
       {
         const float dec = ex2(decl);
@@ -614,10 +653,15 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       if (!last) share_state();
       tc::fence_smem_to_async();
       tc::fence_before_sync();
-      __syncthreads();            // y and S are in shared memory, TMEM and the next decays are read and written
+      const bool mine = ok;
+      ok = __syncthreads_and(ok);  // y and S are in shared memory, TMEM and the next decays are read and written
       tc::fence_after_sync();
+      if (!ok) {
+        drain(gc, more && mine);
+        break;
+      }
       if (!STATE && TMA && nt == Q) {
-        if (tid == 32 && ok) {
+        if (tid == 32) {
           tma_store(&ta.my, w.p0, w.h, w.begin + t0, a.y.sn ? w.row : 0, sb + Sm::X);
           bulk_commit();
           bulk_wait_read();
@@ -626,20 +670,20 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         // a ragged chunk's rows (or unaligned ones), value by value
         uint16_t* yr = static_cast<uint16_t*>(const_cast<void*>(a.y.p)) + tok(w, a.y, t0) + (int64_t)w.h * a.P + w.p0;
         const int pw = min(PC, a.P - w.p0);
-        if (ok)
 #pragma unroll 1
-          for (int e = tid; e < nt * PC; e += TCT) {
-            const int t = e / PC, p = e % PC;
-            if (p < pw)
-              yr[(int64_t)t * a.y.st + p] =
-                  *reinterpret_cast<const uint16_t*>(sm + Sm::X + piece_off(t, p >> 3) + 2 * (p & 7));
-          }
+        for (int e = tid; e < nt * PC; e += TCT) {
+          const int t = e / PC, p = e % PC;
+          if (p < pw)
+            yr[(int64_t)t * a.y.st + p] =
+                *reinterpret_cast<const uint16_t*>(sm + Sm::X + piece_off(t, p >> 3) + 2 * (p & 7));
+        }
         __syncthreads();          // read before the place is filled again
       }
       if (more) {
         if (TMA) {
-          if (tid == 32) load_x(wf, cf);
+          if (tid == 32) load_x(after(), cf);
         } else {
+          const Unit wf = after();
           load_x(wf, cf);
           load_bc(wf, cf);
           tc::fence_smem_to_async();
@@ -647,19 +691,13 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         }
       }
     }
+    if (!ok) break;               // every thread's since the vote: the only way out of the loops
     leave_state(w, ltot);
-    u = un;
-    w = wn;
-    any = another;
+    w = Unit{wn->tile, wn->row, wn->begin, wn->h, wn->p0, wn->s0, wn->s1, wn->chunks, wn->u};
+    place ^= Sm::NEXT ^ (Sm::NEXT + 48);
   }
   if (TMA && !STATE && tid == 32) bulk_wait();
-  if (!__syncthreads_and(ok)) {    // let what was issued land before the memory is given back
-    if (tid == 0 && gc > 0) {
-      mbar_drain(barS, (gc - 1) & 1u);
-      if (!STATE) mbar_drain(barY, (gc - 1) & 1u);
-    }
-    __syncthreads();
-  }
+  __syncthreads();
   if (warp == 0) tc::tmem_dealloc(tm, COLS);
 }
 
@@ -759,6 +797,13 @@ cudaError_t launch_ssm_tc(bool vec, int64_t tokens, const SsmArgs& a, const SsmP
   t.ptiles = p.ptiles;
   t.total = tiles * p.units;
   t.empty_rows = 0;
+  t.wait_ns = WAIT_LIMIT_NS;
+  if (const char* e = getenv("DL_TEST_WAIT_MS")) {
+    const long ms = atol(e);
+    if (ms > 0) t.wait_ns = (unsigned long long)ms * 1000000ull;
+  }
+  const char* stall = getenv("DL_TEST_STALL");
+  t.test_stall = stall && atoi(stall) == 1;
   for (int i = 0; i < a.rows; ++i) t.empty_rows |= row_len(a.items[i]) == 0;
   const bool tma = vec && encode(&t.mx, a.x, a.P, a.H, tokens, a.rows) && encode(&t.mb, a.B, a.N, a.G, tokens, a.rows) &&
                    encode(&t.mc, a.C, a.N, a.G, tokens, a.rows) && encode(&t.my, a.y, a.P, a.H, tokens, a.rows);

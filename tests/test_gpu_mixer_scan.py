@@ -110,3 +110,62 @@ def test_decays_that_overflow(mx, dtype):
     rows = [(rnd(g, t, H, P, dtype=dt), step, rnd(g, t, 1, N, dtype=dt), rnd(g, t, 1, N, dtype=dt))]
     assert torch.isinf(step[5] * -1e28).all()
     check_packed(mx, rows, torch.tensor([-1e28]), mma=dtype == "bf16", S0=rnd(g, 1, H, P, N))
+
+
+# ------------------------------------------------------ a wait that runs out --
+def scan_inputs(g, T, n, H, P, N):
+    x, B, C = (rnd(g, T, n, *s, dtype=torch.bfloat16).cuda() for s in ((H, P), (1, N), (1, N)))
+    return x, rnd(g, T, n, H, dtype=torch.bfloat16).cuda(), -torch.rand(H, generator=g).cuda() - 0.1, B, C
+
+
+@pytest.mark.parametrize("P,N", [(64, 64), (128, 128), (36, 20)])      # tensor copies, and values one by one
+def test_a_wait_that_runs_out_is_reported_and_leaves_no_results(mx, monkeypatch, P, N):
+    """DL_TEST_STALL makes one thread of the first CTA wait, for 25 ms, on a barrier that nothing arrives on.  No fault
+    is involved: the CTA lets its copies and products land and leaves, and the calls after the report run as ever."""
+    from linear_attention_recurrent_gdn_gb300 import deltalog as dl
+    g = torch.Generator().manual_seed(P)
+    T, n, H = 250, 3, 2
+    args = scan_inputs(g, T, n, H, P, N)
+    start = rnd(g, n, H, P, N).cuda()
+    good = start.clone()
+    want = mx.ssm(*args, slots=[0, 1, 2], state=good)
+    mx.sync()
+    pool, out = start.clone(), torch.full_like(want, 7.0)
+    monkeypatch.setenv("DL_TEST_WAIT_MS", "50")
+    monkeypatch.setenv("DL_TEST_STALL", "1")
+    mx.ssm(*args, slots=[0, 1, 2], state=pool, out=out)
+    monkeypatch.delenv("DL_TEST_STALL")
+    monkeypatch.delenv("DL_TEST_WAIT_MS")
+    with pytest.raises(dl.DeltaLogError) as e:
+        mx.sync()
+    assert e.value.status == dl.EDEVICE and "device status %d" % dl.DEV_TEST_STALL in str(e.value)
+    # the first CTA had 64 state rows of row 0's first head: none of its results; everything else
+    p = min(P, 64)
+    assert (out[:, 0, 0, :p] == 7).all() and torch.equal(pool[0, 0, :p], start[0, 0, :p])
+    out[:, 0, 0, :p], pool[0, 0, :p] = want[:, 0, 0, :p], good[0, 0, :p]
+    assert torch.equal(out, want) and torch.equal(pool, good)
+    mx.sync()                                                          # reported once
+    pool = start.clone()
+    assert torch.equal(mx.ssm(*args, slots=[0, 1, 2], state=pool), want) and torch.equal(pool, good)
+    mx.sync()
+
+
+def test_launches_after_a_wait_that_ran_out(mx, monkeypatch):
+    """Segments: the launches after the first find the error and may leave early, and every one of them ends."""
+    from linear_attention_recurrent_gdn_gb300 import deltalog as dl
+    g = torch.Generator().manual_seed(0)
+    args = scan_inputs(g, 1200, 2, 4, 64, 128)
+    want = mx.ssm(*args)
+    mx.sync()
+    monkeypatch.setenv("DL_TEST_WAIT_MS", "50")
+    monkeypatch.setenv("DL_TEST_STALL", "1")
+    mx.ssm(*args)
+    monkeypatch.delenv("DL_TEST_STALL")
+    monkeypatch.delenv("DL_TEST_WAIT_MS")
+    for _ in range(3):
+        mx.ssm(*args)
+    with pytest.raises(dl.DeltaLogError) as e:
+        mx.sync()
+    assert e.value.status == dl.EDEVICE
+    assert torch.equal(mx.ssm(*args), want)
+    mx.sync()
