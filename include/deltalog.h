@@ -470,7 +470,10 @@ dl_status dl_conv(const dl_conv_args *args, void *stream, char *errbuf, int32_t 
  * with S [P][N] per row and head, g = h / (H / G).  state [num_slots][H][P][N]
  * fp32 (contiguous) is read and updated; without it rows start at zero and
  * the final states are dropped.  N <= 256.  dl_ssm_step is the same for one
- * token a row (T = 1), reading and writing the states of n slots once. */
+ * token a row (T = 1), reading and writing the states of n slots once.  An
+ * infinity or a NaN reaches what follows from it and nothing else: outputs that
+ * depend on it are not finite, states are what the formula gives; tokens before
+ * it, other rows, heads and channels are as without it. */
 typedef struct dl_ssm_args {
     dl_tokens tokens;
     int64_t dtype, dt_f32, softplus, H, G, P, N;

@@ -40,6 +40,13 @@
 // of 16 warps with everything doubled and the warps specialised took 138 us, 128
 // state rows a unit 127 us (spilling), two heads a unit 87 us for 59.
 //
+// A chunk with an infinity or a NaN in x, B, C or dt is run token by token
+// instead, by a function of its own: in the products such a value would meet
+// the zero weights of earlier tokens.  x shows in its terms, B, C and dt in the
+// pairs of a token with itself, a packed multiply-add for two values; the
+// check and what it branches around cost 5% (16 x 512 tokens of 32 heads of
+// 128 x 128: 106.9 us, 101.5 without).
+//
 // Rows with few heads are split into segments: a first launch (STATE) runs
 // each segment from zero and leaves its end state and decay in the workspace, a
 // second joins them to the states at the segments' starts, and the full launch
@@ -75,7 +82,8 @@ struct Sm {
   static constexpr uint32_t BAR = F + FB;            // eight mbarriers
   static constexpr uint32_t TSLOT = BAR + 64;        // TMEM address
   static constexpr uint32_t NEXT = TSLOT + 16;       // the unit after the current one, in turns
-  static constexpr uint32_t BYTES = NEXT + 2 * 48;
+  static constexpr uint32_t NOW = NEXT + 2 * 48;     // and that one, where a function wants it
+  static constexpr uint32_t BYTES = NOW + 48;
 };
 // dt, log2 of the tokens' decays, their sums from every 16th token on, the pair weights' column factors (128 of each);
 // sums over the blocks of 32 and over their first halves, e^{T} of the blocks' last tokens (4 of each); the whole sum.
@@ -180,6 +188,55 @@ __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par, int32_t code,
   return mbar_wait(bar, par, &g_mixer_status, code, ns);
 }
 __device__ __noinline__ void drain_long(uint32_t bar, uint32_t par) { mbar_drain(bar, par); }
+
+// acc + 0 x for two bf16 values: whatever is not finite leaves a NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t acc, uint32_t x) {
+  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+  return acc;
+}
+// Tokens [t0, t0 + nt) of unit w as they are defined, one after the other, with everything read from where the caller
+// left it: for a chunk whose products are not finite.  In those an infinity or a NaN of x, B, C or dt meets the zero
+// weights of earlier tokens and the terms that were split off, and 0 inf is a NaN; here it reaches what follows from
+// it.  The state is in fp32 [64][128] in C's place, y goes to x's.  About 0.2 ms a chunk.
+template <bool STATE>
+__device__ __noinline__ void chunk_by_tokens(const TcArgs& ta, unsigned char* sm, const Unit* at, int t0, int nt) {
+  const SsmArgs& a = ta.a;
+  const Unit w = *at;
+  float* S = reinterpret_cast<float*>(sm + Sm::C);
+  const int tid = threadIdx.x, n = tid & 127, pw = min(PC, a.P - w.p0), g = w.h / (a.H / a.G);
+  auto token = [&](const TokView& v, int t) {
+    return static_cast<const uint16_t*>(v.p) + (int64_t)(w.begin + t) * v.st + (int64_t)w.row * v.sn;
+  };
+  auto value = [](const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); };
+  const float A = a.A[w.h], D = a.D ? a.D[w.h] : 0.f, bias = a.dt_bias ? a.dt_bias[w.h] : 0.f;
+#pragma unroll 1
+  for (int t = t0; t < t0 + nt; ++t) {
+    const int64_t od = (int64_t)(w.begin + t) * a.dt.st + (int64_t)w.row * a.dt.sn + w.h;
+    float dt = (a.dt_f32 ? static_cast<const float*>(a.dt.p)[od] : value(static_cast<const uint16_t*>(a.dt.p) + od)) + bias;
+    if (a.softplus) dt = softplus_f(dt);
+    const float dec = expf(dt * A);
+    const uint16_t* x = token(a.x, t) + (int64_t)w.h * a.P + w.p0;
+    if (n < a.N) {
+      const float b = value(token(a.B, t) + (int64_t)g * a.N + n);
+#pragma unroll 1
+      for (int p = tid >> 7; p < pw; p += 2) S[p * 128 + n] = fmaf(S[p * 128 + n], dec, value(x + p) * dt * b);
+    }
+    __syncthreads();
+    if (!STATE) {
+      const uint16_t* c = token(a.C, t) + (int64_t)g * a.N;
+      const int p = tid >> 2;
+      float y = 0.f;
+#pragma unroll 1
+      for (int k = tid & 3; k < a.N; k += 4) y = fmaf(S[p * 128 + k], value(c + k), y);
+      y += __shfl_xor_sync(0xffffffffu, y, 1);
+      y += __shfl_xor_sync(0xffffffffu, y, 2);
+      if ((tid & 3) == 0 && p < pw)
+        *reinterpret_cast<__nv_bfloat16*>(sm + Sm::X + piece_off(t - t0, p >> 3) + 2 * (p & 7)) =
+            __float2bfloat16_rn(fmaf(D, value(x + p), y));
+      __syncthreads();
+    }
+  }
+}
 
 // TMA: tensor copies (16-byte aligned tensors, widths and strides); else
 // threads copy value by value.
@@ -467,6 +524,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         tc::fence_smem_to_async();
         __syncthreads();
       }
+      uint32_t odd2 = 0u;                           // whether something of the chunk is not finite
       if (!STATE) {
         if (tid == 0) {
           if (TMA) {
@@ -529,6 +587,11 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
               v[2 * e4] = pack2<__nv_bfloat16>(w[0], w[1]);
               v[2 * e4 + 1] = pack2<__nv_bfloat16>(w[2], w[3]);
             }
+            // B, C and dt that are not finite show in the pairs of a token with itself (C's rows past the last token
+            // are not looked at)
+            if (i < nt)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) odd2 = not_finite(odd2, v[e]);
           } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = 0u;
@@ -563,6 +626,13 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
           wait(fullX, gc);
           wait(fullB, gc);
         }
+#pragma unroll
+        for (int e = 0; e < Q * 128 / 8 / TCT; ++e) {
+          const int idx = tid + e * TCT, t = idx & (Q - 1), cv = idx / Q;
+          if (cv * 8 >= a.N) break;
+          const uint4 bv = *reinterpret_cast<const uint4*>(sm + Sm::B + piece_off(t, cv));
+          odd2 = not_finite(not_finite(not_finite(not_finite(odd2, bv.x), bv.y), bv.z), bv.w);
+        }
       }
       // ---- X's three terms, then dS
 #pragma unroll
@@ -583,13 +653,14 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
           p -= __uint_as_float(o2[k] << 16);
           q -= __uint_as_float(o2[k] & 0xffff0000u);
           o3[k] = pack2<__nv_bfloat16>(p, q);
+          odd2 = not_finite(odd2, o1[k]);
         }
         *reinterpret_cast<uint4*>(sm + Sm::X1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
         *reinterpret_cast<uint4*>(sm + Sm::X2 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
         *reinterpret_cast<uint4*>(sm + Sm::X3 + off) = make_uint4(o3[0], o3[1], o3[2], o3[3]);
       }
       tc::fence_smem_to_async();
-      __syncthreads();            // the decays are free too
+      const bool odd = __syncthreads_or((odd2 & 0x7fff7fffu) != 0u);      // the decays are free too
       if (tid == 0) {
         tc::fence_after_sync();
         constexpr uint32_t idS = tc::idesc_bf16_f32(128, PC, true, true);
@@ -606,7 +677,7 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
         wait(barY, gc);
         tc::fence_after_sync();
 #pragma unroll
-        for (int c16 = 0; c16 < HC / 16; ++c16) {
+        for (int c16 = 0; c16 < HC / 16; ++c16) {         // (not finite: overwritten below)
           uint32_t r1[16], r2[16];
           tc::tmem_ld16(tl + COL_Y1 + hf * HC + 16 * c16, r1);
           tc::tmem_ld16(tl + COL_Y2 + hf * HC + 16 * c16, r2);
@@ -633,13 +704,25 @@ ssm_tc_kernel(const __grid_constant__ TcArgs ta) {
       // ---- S' = e^{L_Q} S + dS
       wait(barS, gc);
       tc::fence_after_sync();
+      if (odd) {                  // the chunk again from what was given, with the state as it was before
+        float* Sf = reinterpret_cast<float*>(sm + Sm::C) + hf * HC * 128 + i;
+#pragma unroll
+        for (int c = 0; c < HC; ++c) Sf[c * 128] = S[c];
+        if (tid == 0) *reinterpret_cast<Unit*>(sm + Sm::NOW) = w;
+        __syncthreads();
+        chunk_by_tokens<STATE>(ta, sm, reinterpret_cast<const Unit*>(sm + Sm::NOW), t0, nt);
+#pragma unroll
+        for (int c = 0; c < HC; ++c) S[c] = Sf[c * 128];
+        tc::fence_smem_to_async();
+        __syncthreads();
+      }
       if (TMA && more && tid == 32) {
         wait(fullB, gc);          // landed long ago, unless a wait ran out
         if (!STATE) wait(fullC, gc);
         if (ok) load_bc(after(), cf);
       }
       ltot += decl;
-      {
+      if (!odd) {
         const float dec = ex2(decl);
 #pragma unroll
         for (int c16 = 0; c16 < HC / 16; ++c16) {

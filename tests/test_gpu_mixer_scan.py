@@ -169,3 +169,49 @@ def test_launches_after_a_wait_that_ran_out(mx, monkeypatch):
     assert e.value.status == dl.EDEVICE
     assert torch.equal(mx.ssm(*args), want)
     mx.sync()
+
+
+# ------------------------------------------------------- infinities and NaN --
+INF, NAN = float("inf"), float("nan")
+# which input, at which token, and its value there (one head, group, channel or state column of it)
+ODD = [("x", 3, INF), ("x", 77, NAN), ("x", 31, -INF), ("B", 64, INF), ("B", 5, NAN), ("C", 33, INF), ("C", 90, NAN),
+       ("dt", 10, INF), ("dt", 95, NAN), ("x", 127, INF), ("x", 128, INF), ("state", 0, INF)]
+
+
+@pytest.mark.parametrize("dtype,P,N", [("bf16", 64, 64), ("bf16", 72, 40), ("bf16", 40, 24), ("bf16", 20, 13),
+                                       ("fp16", 40, 24), ("fp32", 64, 64), ("fp32", 20, 13)])
+@pytest.mark.parametrize("lengths", [[140, 131], [700]])       # whole rows, and a row in segments
+@pytest.mark.parametrize("what,at,value", ODD)
+def test_infinities_and_nan_reach_what_follows_from_them(mx, dtype, P, N, lengths, what, at, value):
+    """Tokens before them, other rows, heads, channels and state columns are as without them; an output that
+    depends on one is not finite, and the state is as it is defined: an infinity of its sign, or a NaN."""
+    g = torch.Generator().manual_seed(at)
+    dt, H = DT[dtype], 2
+    rows = []
+    for t in lengths:
+        rows.append([rnd(g, t, H, P, dtype=dt), rnd(g, t, H) * 0.01 + 0.02, rnd(g, t, 1, N, dtype=dt),
+                     rnd(g, t, 1, N, dtype=dt)])
+    S0 = rnd(g, len(rows), H, P, N)
+    index = {"x": (at, 1, P // 2), "dt": (at, 1), "B": (at, 0, N // 3), "C": (at, 0, N // 3)}
+    if what == "state":
+        S0[0, 1, P // 2, N // 3] = value
+    else:
+        rows[0][("x", "dt", "B", "C").index(what)][index[what]] = value
+    A = torch.tensor([-1.0, -0.5])
+    D = rnd(g, H)
+    ys, pool = run_packed(mx, rows, A, D, S0, list(range(len(rows))))
+    for i, r in enumerate(rows):
+        want, S, ymag, Smag = ref.ssm_row(r[0], r[1], A, r[2], r[3], D, S0[i], None, False)
+        steps = 3 * r[0].shape[0] + 16
+        fine, sfine = torch.isfinite(want), torch.isfinite(S)
+        assert fine.any() and sfine.any()
+        assert torch.equal(torch.isfinite(ys[i]), fine), "y of row %d: not finite in other places" % i
+        off = (ys[i].double() - want).abs()[fine]
+        tol = half(dt) * want.abs() + 1e-30 + ((steps + N) * U + (1.01 * half(dt) if dtype == "bf16" else 0)) * ymag
+        if dtype == "fp16":
+            tol = tol + 2.0 ** -24
+        assert (off <= tol[fine]).all(), "y of row %d" % i
+        got = pool[i].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(S)), "state of row %d: NaN in other places" % i
+        assert torch.equal(got[torch.isinf(S)], S[torch.isinf(S)]), "state of row %d: infinities" % i
+        assert ((got - S).abs()[sfine] <= (steps * U * Smag + 1e-30)[sfine]).all(), "state of row %d" % i
