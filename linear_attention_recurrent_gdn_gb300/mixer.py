@@ -79,7 +79,10 @@ def _call(fn, args, dev):
     except AttributeError:
         err = ctypes.create_string_buffer(_ERR)
         err, at = _local.err = err, ctypes.addressof(err)
-    rc = _on(dev, fn, args, _raw_stream(dev), at, _ERR)
+    if dev == _device():
+        rc = fn(args, _raw_stream(dev), at, _ERR)
+    else:
+        rc = _on(dev, fn, args, _raw_stream(dev), at, _ERR)
     if rc:
         raise _dl.DeltaLogError(rc, err.value.decode())
 
@@ -117,13 +120,14 @@ def _x(t):
         raise TypeError("x must be a CUDA tensor")
     if t.dtype not in _DTYPE:
         raise ValueError("x: %s is not supported" % t.dtype)
-    if _differentiated(t):
+    if (t.requires_grad or _fwd._current_level >= 0) and _differentiated(t):
         _bad("x", t, t.dtype, t.get_device())
     return t.get_device()
 
 
 def _check(name, t, shape, dtype, dev):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or _differentiated(t):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or \
+            (t.requires_grad or _fwd._current_level >= 0) and _differentiated(t):
         _bad(name, t, dtype, dev)
     if t.shape != shape:
         raise ValueError("%s: expected %s, got %s" % (name, tuple(shape), tuple(t.shape)))
