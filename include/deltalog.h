@@ -411,12 +411,18 @@ int32_t dl_abi_version(void);
 /* nothing has been enqueued (DL_ECUDA: a launch failed), and errbuf, if not  */
 /* NULL, holds a one-line reason.  Calls may come from several host threads.  */
 /*                                                                            */
-/* Activations are fp32, bf16 or fp16 (dl_dtype); sums, states, softmax-like  */
-/* factors and norms are fp32 and rounded once on output.  Strides are in     */
-/* elements and may be any value that keeps tensors apart; tensors need only  */
-/* their element's alignment (16-byte aligned tensors whose strides and       */
-/* widths are multiples of 16 bytes move as vectors).  Outputs must not       */
-/* overlap inputs unless a call says so.                                      */
+/* Activations are fp32, bf16 or fp16 (dl_dtype); sums, states, decays and    */
+/* norms are fp32 and rounded once on output.  Two exceptions.  dl_ssm of     */
+/* bf16 rows (N <= 128, the longest of 32 tokens or more) runs on the tensor  */
+/* cores: of every term of an output, one factor (a pair weight, or the copy  */
+/* of the state that the output reads) is rounded to bf16, half a step of the */
+/* output's own type; states keep 32 bits.  And in 16-bit types silu and      */
+/* sigmoid are held from -43 down, 1e-17 off at most.                         */
+/*                                                                            */
+/* Strides are in elements and may be any value that keeps tensors apart;     */
+/* tensors need only their element's alignment (16-byte aligned tensors whose */
+/* strides and widths are multiples of 16 bytes move as vectors).  Outputs    */
+/* must not overlap inputs unless a call says so.                             */
 /* ------------------------------------------------------------------------ */
 typedef enum dl_dtype { DL_F32 = 0, DL_BF16 = 1, DL_F16 = 2 } dl_dtype;
 typedef enum dl_act { DL_ACT_NONE = 0, DL_ACT_SILU = 1, DL_ACT_SIGMOID = 2 } dl_act;

@@ -30,14 +30,17 @@
 // each other's waits.  For that a CTA keeps to half of the shared memory and of
 // TMEM: the terms take the places of C and S once Y2 has read them, W and dS
 // those of G.  With nearly all of the SM's memory used as shared memory there
-// is next to no L1 cache, so nothing may spill (300 bytes a thread cost 15%).
+// is next to no L1 cache, so nothing may spill (300 bytes a thread cost 15%, 20
+// bytes 6%), and no form does: the next unit, for one, waits in shared memory.
 //
-// Measured on a GB300: 16 x 512 tokens of 32 heads of 128 x 128 106 us (1.7
+// Measured on a GB300: 16 x 512 tokens of 32 heads of 128 x 128 107 us (1.7
 // TB/s of the 6.7 of a copy; a first kernel on the FP32 cores 1.1 ms), of 64 x
-// 128 59 us; one row of 2048 tokens of 16 heads of 64 x 128 24 us in three launches.  A chunk's
-// products are some 2500 cycles of the tensor cores and its operands 3700 of
-// shared memory, of about 5000; the schedulers issue 43% of the time.  One CTA
-// of 16 warps with everything doubled and the warps specialised took 138 us, 128
+// 128 58 us; one row of 2048 tokens of 16 heads of 64 x 128 24 us in three
+// launches.  In the first the tensor cores are busy 26% of the time, shared
+// memory 53% (the products' operands 28, the threads' accesses 25), the
+// schedulers issue 39%, and 11% of the SMs' time passes without work: 1024
+// units are four for some of the 304 CTAs and three for others.  One CTA of 16
+// warps with everything doubled and the warps specialised took 138 us, 128
 // state rows a unit 127 us (spilling), two heads a unit 87 us for 59.
 //
 // A chunk with an infinity or a NaN in x, B, C or dt is run token by token
@@ -197,7 +200,7 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t acc, uint32_t x) {
 // Tokens [t0, t0 + nt) of unit w as they are defined, one after the other, with everything read from where the caller
 // left it: for a chunk whose products are not finite.  In those an infinity or a NaN of x, B, C or dt meets the zero
 // weights of earlier tokens and the terms that were split off, and 0 inf is a NaN; here it reaches what follows from
-// it.  The state is in fp32 [64][128] in C's place, y goes to x's.  About 0.2 ms a chunk.
+// it.  The state is in fp32 [64][128] in C's place, y goes to x's.  0.6 ms a chunk of 64 x 128.
 template <bool STATE>
 __device__ __noinline__ void chunk_by_tokens(const TcArgs& ta, unsigned char* sm, const Unit* at, int t0, int nt) {
   const SsmArgs& a = ta.a;
