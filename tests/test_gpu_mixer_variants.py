@@ -190,3 +190,35 @@ def test_calls_from_several_host_threads(mx):
     for t in threads:
         t.join()
     assert not wrong
+
+
+# --------------------------------------------------------------------- outputs --
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("shift", [8, 3])            # vectors and tensor copies, and values one by one
+def test_outputs_in_wider_tensors_and_past_the_rows(mx, dtype, shift):
+    """Outputs that are ranges of wider tensors: what lies beside them and past each row's tokens is not written."""
+    g = torch.Generator().manual_seed(shift)
+    dt, lengths, T, H, P, N = DT[dtype], [300, 0, 128, 77], 300, 2, 64, 64
+    n, mark = len(lengths), 7.0
+    x, B, C = (rnd(g, T, n, *s, dtype=dt).cuda() for s in ((H, P), (1, N), (1, N)))
+    step, A = rnd(g, T, n, H, dtype=dt).cuda(), -torch.rand(H, generator=g).cuda()
+    w = rnd(g, H * P, 4, dtype=dt).cuda()
+    live = torch.arange(T)[:, None] < torch.tensor(lengths)
+    for call in (lambda out: mx.ssm(x, step, A, B, C, lengths=lengths, out=out),
+                 lambda out: mx.conv(x.flatten(2), w, lengths=lengths, out=None if out is None else out.flatten(2))):
+        want = call(None).view(T, n, H * P)
+        wide = torch.full((T, n, H * P + 16), mark, dtype=dt, device="cuda")
+        call(wide[..., shift:shift + H * P].unflatten(2, (H, P)))
+        got = wide[..., shift:shift + H * P]
+        assert torch.equal(got[live], want[live])
+        assert (got[~live] == mark).all() and (wide[..., :shift] == mark).all() and (wide[..., shift + H * P:] == mark).all()
+    y = wide[:, 0, shift:shift + H * P]
+    h = torch.full_like(wide[:, 0], mark)[:, shift:shift + H * P]
+    weight = rnd(g, H * P, dtype=dt).cuda()
+    a, b = mx.add_norm(x[:, 0].flatten(1), None, weight)
+    mx.add_norm(x[:, 0].flatten(1), None, weight, out=y, out_residual=h)
+    assert torch.equal(y, a) and torch.equal(h, b)
+    assert (wide[:, 0, :shift] == mark).all() and (wide[:, 0, shift + H * P:] == mark).all()
+    mx.gated_norm(x[:, 0], weight.view(H, P), x[:, 1], out=y.unflatten(1, (H, P)))
+    assert torch.equal(y.unflatten(1, (H, P)), mx.gated_norm(x[:, 0], weight.view(H, P), x[:, 1]))
+    assert (wide[:, 0, :shift] == mark).all() and (wide[:, 0, shift + H * P:] == mark).all()
