@@ -532,6 +532,99 @@ typedef struct dl_add_norm_args {
 } dl_add_norm_args;
 dl_status dl_add_norm(const dl_add_norm_args *args, void *stream, char *errbuf, int32_t errlen);
 
+/* ------------------------------------------------------------------------ */
+/* Attention operators: the softmax attention layers between recurrent ones.  */
+/*                                                                            */
+/* Keys and values live in pools of pages, [num_pages][G][page_size][d] each   */
+/* (any strides between pages, heads and tokens; the d values of a token's     */
+/* head are contiguous).  A slot's token p lies in page                        */
+/* table[slot][p / page_size] at place p % page_size; lengths[slot] tokens are */
+/* there.  table, lengths, slots and the numbers of tokens live on the device, */
+/* so a captured call follows them from replay to replay.  What the host       */
+/* cannot see is checked by the kernels: a slot, length or page out of range   */
+/* is never followed, and is reported by dl_attend_sync.  Otherwise the calls  */
+/* are as the mixer operators above: no context, asynchronous, nothing         */
+/* allocated or kept, all other arguments checked first.  n <= 1024; page_size */
+/* a power of two from 16 to 256; d <= 256.                                    */
+/* ------------------------------------------------------------------------ */
+typedef struct dl_pool {     /* strides in elements */
+    void *data;
+    int64_t stride_page, stride_head, stride_token;
+} dl_pool;
+
+/* dl_pages_extend: row i's slot gets tokens[i] more tokens (one if tokens is
+ * NULL).  Pages come off the stack of free ones (free[0] of them, free[1] the
+ * deepest), rows in order, and enter the table; lengths[slot] grows.  Out:
+ * starts [n + 1], the sums of the tokens before each row; where and positions
+ * (NULL: not wanted), for every token its place page * page_size + p %
+ * page_size and its position p.  T = 0: packed, row i's tokens at starts[i],
+ * `size` entries; T > 0: token t of row i at t * n + i, at most T a row, size =
+ * T * n.  Entries without a token get -1.  If a slot is out of range or named
+ * twice, a number of tokens negative or too large for the maps, a table row
+ * full or the pages too few, nothing changes, starts are 0 and places -1.
+ * work: [2 n + 2] int32 of scratch.
+ *
+ * dl_pages_truncate: row i's slot keeps its first tokens[i] tokens (none if
+ * NULL, at most its length); pages without a kept token return to the stack,
+ * in the order that undoes an extend of the same rows.  Table entries stay.
+ * starts, where, positions and work are not used. */
+typedef struct dl_pages_args {
+    const int32_t *slots, *tokens;      /* [n] */
+    int32_t *table, *lengths, *free;    /* [num_slots][max_pages], [num_slots], [1 + num_pages] */
+    int32_t *starts, *where, *positions, *work;
+    int64_t table_stride, size, n, T, num_slots, max_pages, num_pages, page_size;
+} dl_pages_args;
+dl_status dl_pages_extend(const dl_pages_args *args, void *stream, char *errbuf, int32_t errlen);
+dl_status dl_pages_truncate(const dl_pages_args *args, void *stream, char *errbuf, int32_t errlen);
+
+/* The keys and values of T tokens of n rows (packed: T = all tokens, n = 1)
+ * into their pages: token t of row i goes to place where[t * n + i], or
+ * nowhere if that is negative.  Places are distinct, and so are the pools'
+ * elements. */
+typedef struct dl_kv_append_args {
+    int64_t dtype, T, n, G, d, page_size, num_pages;
+    dl_view k, v;                       /* a token: [G][d], contiguous */
+    dl_pool k_pages, v_pages;
+    const int32_t *where;               /* [T][n] */
+} dl_kv_append_args;
+dl_status dl_kv_append(const dl_kv_append_args *args, void *stream, char *errbuf, int32_t errlen);
+
+/* Attention of the last tokens of n slots, with their keys and values in the
+ * pages already.  Row i has tokens[i] <= T of them (T each if NULL; packed:
+ * starts[i + 1] - starts[i], T tokens in all), the last of its slot's
+ * lengths[slot] tokens.  The token at position p sees the keys j <= p, with a
+ * window (> 0) only those with j > p - window or j < sinks:
+ *   o[h] = sum_j softmax_j(scale q[h] . k[j][h / (H / G)]) v[j][h / (H / G)]
+ * Scores, weights and sums are fp32 and o is rounded once; on the tensor cores
+ * (16-bit types) the weights of v are rounded to the type, half a step each.
+ * A token that sees nothing (a position below zero, scores of -inf alone) gives
+ * zero.  What a token does not see does not reach it, infinities and NaN
+ * included.  dl_attend_step: one token a row (T = 1, not packed, tokens NULL).
+ * The workspace takes the partial results of keys that are split over the GPU;
+ * the order in which they are joined depends on the sizes alone. */
+typedef struct dl_attend_args {
+    int64_t dtype, n, T, packed, H, G, d, page_size, max_pages, num_slots, num_pages, window, sinks;
+    double scale;
+    dl_view q, o;                       /* a token: [H][d], contiguous */
+    dl_pool k_pages, v_pages;
+    const int32_t *table;
+    int64_t table_stride;
+    const int32_t *lengths, *slots, *starts, *tokens;
+    void *workspace;                    /* device memory of dl_attend_workspace bytes, 16-byte aligned */
+    int64_t workspace_bytes;
+} dl_attend_args;
+dl_status dl_attend(const dl_attend_args *args, void *stream, char *errbuf, int32_t errlen);
+dl_status dl_attend_step(const dl_attend_args *args, void *stream, char *errbuf, int32_t errlen);
+/* Bytes of workspace that dl_attend and dl_attend_step want for these sizes
+ * and layouts (0 for many); -1 if the sizes are not valid. */
+int64_t dl_attend_workspace(const dl_attend_args *args);
+
+/* Synchronise `stream`, then read and clear the attention kernels' status
+ * words of the current device: DL_EDEVICE if one of them met a value out of
+ * range or gave up a wait since the last call (*device_code, if not NULL,
+ * receives the code). */
+dl_status dl_attend_sync(void *stream, int32_t *device_code, char *errbuf, int32_t errlen);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,6 +29,12 @@ constexpr int32_t DEV_TIMEOUT_EMPTY = 3;
 constexpr int32_t DEV_BAD_ITEM = 4;
 constexpr int32_t DEV_TEST_STALL = 5;   // the test-only stall below ran out (nothing else sets it)
 constexpr int32_t DEV_TIMEOUT_MMA = 6;  // a wait for tensor-core MMAs to complete gave up
+// The attention operators (block tables, lengths and slots live on the device).
+constexpr int32_t DEV_BAD_SLOT = 7;
+constexpr int32_t DEV_BAD_LENGTH = 8;
+constexpr int32_t DEV_ROW_FULL = 9;
+constexpr int32_t DEV_NO_PAGES = 10;
+constexpr int32_t DEV_BAD_PAGE = 11;
 constexpr unsigned long long WAIT_LIMIT_NS = 2000000000ull;  // 2 s (default per-launch limit)
 
 // One-line meaning of a device status code (host side).
@@ -40,6 +46,11 @@ inline const char* device_status_str(int32_t code) {
     case DEV_BAD_ITEM: return "a plan row was out of range";
     case DEV_TEST_STALL: return "the test-only stall's bounded wait gave up";
     case DEV_TIMEOUT_MMA: return "a wait for tensor-core MMAs to complete gave up";
+    case DEV_BAD_SLOT: return "a slot was out of range, or named twice";
+    case DEV_BAD_LENGTH: return "a number of tokens was negative or larger than its bound";
+    case DEV_ROW_FULL: return "a slot's row of the block table is full";
+    case DEV_NO_PAGES: return "no pages are left";
+    case DEV_BAD_PAGE: return "a page or a number of free pages was out of range";
     default: return "unknown device status";
   }
 }

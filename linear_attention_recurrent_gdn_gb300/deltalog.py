@@ -41,6 +41,8 @@ EXPORTS = [
     "dl_step_noalloc", "dl_noalloc_sync",
     "dl_conv", "dl_ssm", "dl_ssm_step", "dl_ssm_workspace", "dl_gated_norm", "dl_add_norm",
     "dl_mixer_sync",
+    "dl_pages_extend", "dl_pages_truncate", "dl_kv_append", "dl_attend", "dl_attend_step",
+    "dl_attend_workspace", "dl_attend_sync",
 ]
 
 
