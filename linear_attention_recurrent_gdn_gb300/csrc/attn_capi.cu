@@ -91,38 +91,7 @@ dl_status attend_sizes(const ErrOut& fail, const dl_attend_args& q) {
   return DL_OK;
 }
 
-// Which kernel a call runs in, and its workspace.
-struct Choice {
-  bool vec;
-  AttnPlan plan;
-};
-Choice choose(const dl_attend_args& q) {
-  Choice c{};
-  const int64_t per = 16 / elem(q.dtype);
-  c.vec = q.d % 8 == 0 && view_vec(q.q, per) && view_vec(q.o, per) && pool_vec(q.k_pages, per) && pool_vec(q.v_pages, per);
-  c.plan = simt_plan((int)q.n, (int)q.T, q.packed != 0, (int)q.H, (int)q.G, (int)q.d, num_sms());
-  return c;
-}
-
-dl_status attend(const dl_attend_args* p, void* stream, const ErrOut& fail, bool step) {
-  if (!p) return fail(DL_EINVAL, "NULL argument");
-  const dl_attend_args& q = *p;
-  const dl_status s = attend_sizes(fail, q);
-  if (s != DL_OK) return s;
-  if (step && (q.T != 1 || q.packed || q.tokens)) return fail(DL_EINVAL, "a step takes one token a row");
-  if (q.n == 0 || q.T == 0) return DL_OK;
-  if (q.packed && !q.starts) return fail(DL_EINVAL, "packed tokens need starts");
-  const int64_t e = elem(q.dtype);
-  for (const void* t : {(const void*)q.q.data, (const void*)q.o.data, (const void*)q.k_pages.data, (const void*)q.v_pages.data}) {
-    if (!t) return fail(DL_EINVAL, "NULL tensor pointer");
-    if (!al(t, e)) return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
-  }
-  if (!q.table || !q.lengths || !q.slots) return fail(DL_EINVAL, "NULL tensor pointer");
-  if (!words({q.table, q.lengths, q.slots, q.starts, q.tokens}))
-    return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
-  const Choice c = choose(q);
-  if (c.plan.ws_bytes && (!q.workspace || q.workspace_bytes < c.plan.ws_bytes || !al(q.workspace, 16)))
-    return fail(DL_EINVAL, "the workspace needs %lld bytes, 16-byte aligned (dl_attend_workspace)", (long long)c.plan.ws_bytes);
+AttnArgs attn_args(const dl_attend_args& q) {
   AttnArgs a{};
   a.q = q.q.data;
   a.o = q.o.data;
@@ -151,7 +120,53 @@ dl_status attend(const dl_attend_args* p, void* stream, const ErrOut& fail, bool
   a.sinks = (int32_t)q.sinks;
   a.scale_log2 = (float)(q.scale * 1.4426950408889634);
   a.ws = static_cast<float*>(q.workspace);
-  return done(fail, launch_simt((int)q.dtype, c.vec, a, c.plan, static_cast<cudaStream_t>(stream)));
+  return a;
+}
+
+// Which kernel a call runs in, and its workspace.
+enum class Kernel { SIMT, STEP };
+struct Choice {
+  Kernel kernel;
+  bool vec;
+  AttnPlan plan;
+};
+Choice choose(const dl_attend_args& q, const AttnArgs& a) {
+  Choice c{};
+  const int64_t per = 16 / elem(q.dtype);
+  c.vec = q.d % 8 == 0 && view_vec(q.q, per) && view_vec(q.o, per) && pool_vec(q.k_pages, per) && pool_vec(q.v_pages, per);
+  if (q.T == 1 && !q.packed && !q.tokens && step_fits((int)q.dtype, c.vec, a)) {
+    c.kernel = Kernel::STEP;
+    c.plan = step_plan(a.n, a.H, a.G, a.d, num_sms());
+    return c;
+  }
+  c.kernel = Kernel::SIMT;
+  c.plan = simt_plan(a.n, a.T, q.packed != 0, a.H, a.G, a.d, num_sms());
+  return c;
+}
+
+dl_status attend(const dl_attend_args* p, void* stream, const ErrOut& fail, bool step) {
+  if (!p) return fail(DL_EINVAL, "NULL argument");
+  const dl_attend_args& q = *p;
+  const dl_status s = attend_sizes(fail, q);
+  if (s != DL_OK) return s;
+  if (step && (q.T != 1 || q.packed || q.tokens)) return fail(DL_EINVAL, "a step takes one token a row");
+  if (q.n == 0 || q.T == 0) return DL_OK;
+  if (q.packed && !q.starts) return fail(DL_EINVAL, "packed tokens need starts");
+  const int64_t e = elem(q.dtype);
+  for (const void* t : {(const void*)q.q.data, (const void*)q.o.data, (const void*)q.k_pages.data, (const void*)q.v_pages.data}) {
+    if (!t) return fail(DL_EINVAL, "NULL tensor pointer");
+    if (!al(t, e)) return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
+  }
+  if (!q.table || !q.lengths || !q.slots) return fail(DL_EINVAL, "NULL tensor pointer");
+  if (!words({q.table, q.lengths, q.slots, q.starts, q.tokens}))
+    return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
+  const AttnArgs a = attn_args(q);
+  const Choice c = choose(q, a);
+  if (c.plan.ws_bytes && (!q.workspace || q.workspace_bytes < c.plan.ws_bytes || !al(q.workspace, 16)))
+    return fail(DL_EINVAL, "the workspace needs %lld bytes, 16-byte aligned (dl_attend_workspace)", (long long)c.plan.ws_bytes);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (c.kernel == Kernel::STEP) return done(fail, launch_step((int)q.dtype, a, c.plan, st));
+  return done(fail, launch_simt((int)q.dtype, c.vec, a, c.plan, st));
 }
 
 }  // namespace
@@ -206,7 +221,7 @@ extern "C" int64_t dl_attend_workspace(const dl_attend_args* p) {
   const ErrOut quiet(nullptr, 0);
   if (!p || attend_sizes(quiet, *p) != DL_OK) return -1;
   if (p->n == 0 || p->T == 0) return 0;
-  return choose(*p).plan.ws_bytes;
+  return choose(*p, attn_args(*p)).plan.ws_bytes;
 }
 
 extern "C" dl_status dl_attend(const dl_attend_args* p, void* stream, char* errbuf, int32_t errlen) {
@@ -221,7 +236,7 @@ extern "C" dl_status dl_attend_sync(void* stream, int32_t* device_code, char* er
   const ErrOut fail(errbuf, errlen);
   int32_t code = 0;
   cudaError_t e = cudaSuccess;
-  for (const auto read : {read_pages_status, read_simt_status}) {
+  for (const auto read : {read_pages_status, read_simt_status, read_step_status}) {
     int32_t c = 0;
     e = read(static_cast<cudaStream_t>(stream), &c);
     if (e != cudaSuccess) break;
