@@ -21,7 +21,7 @@ CU_SOURCES = ["replay_prep.cu", "append_decode.cu", "append_fused_ne8.cu", "appe
               "append_fused_ne32.cu", "eager_step.cu", "slot_ops.cu", "prefill.cu", "prefill_tc.cu", "capi.cu",
               "noalloc.cu", "mixer_capi.cu", "conv.cu", "ssm_scan.cu", "ssm_tc.cu", "ssm_step.cu", "norms.cu",
               "attn_capi.cu", "attn_pages.cu", "attn_simt.cu",
-              "attn_step.cu"]
+              "attn_step.cu", "attn_tc.cu"]
 CPP_SOURCES = ["slot_table.cpp"]
 
 

@@ -78,10 +78,16 @@ bool step_fits(int dtype, bool vec, const AttnArgs& a);
 AttnPlan step_plan(int n, int H, int G, int d, int sms);
 cudaError_t launch_step(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
+// Prompts of 16-bit types with 16-byte aligned tensors and strides, on the tensor cores.
+bool tc_fits(int dtype, bool vec, const AttnArgs& a);
+AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms);
+cudaError_t launch_tc(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
+
 // Wait for the stream, then read and clear the kernels' status words.
 cudaError_t read_pages_status(cudaStream_t s, int32_t* code);
 cudaError_t read_simt_status(cudaStream_t s, int32_t* code);
 cudaError_t read_step_status(cudaStream_t s, int32_t* code);
+cudaError_t read_tc_status(cudaStream_t s, int32_t* code);
 
 }  // namespace at
 }  // namespace dl

@@ -124,7 +124,7 @@ AttnArgs attn_args(const dl_attend_args& q) {
 }
 
 // Which kernel a call runs in, and its workspace.
-enum class Kernel { SIMT, STEP };
+enum class Kernel { SIMT, STEP, TC };
 struct Choice {
   Kernel kernel;
   bool vec;
@@ -137,6 +137,11 @@ Choice choose(const dl_attend_args& q, const AttnArgs& a) {
   if (q.T == 1 && !q.packed && !q.tokens && step_fits((int)q.dtype, c.vec, a)) {
     c.kernel = Kernel::STEP;
     c.plan = step_plan(a.n, a.H, a.G, a.d, num_sms());
+    return c;
+  }
+  if (tc_fits((int)q.dtype, c.vec, a)) {
+    c.kernel = Kernel::TC;
+    c.plan = tc_plan(a.n, a.T, q.packed != 0, a.H, a.G, a.d, num_sms());
     return c;
   }
   c.kernel = Kernel::SIMT;
@@ -166,6 +171,7 @@ dl_status attend(const dl_attend_args* p, void* stream, const ErrOut& fail, bool
     return fail(DL_EINVAL, "the workspace needs %lld bytes, 16-byte aligned (dl_attend_workspace)", (long long)c.plan.ws_bytes);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (c.kernel == Kernel::STEP) return done(fail, launch_step((int)q.dtype, a, c.plan, st));
+  if (c.kernel == Kernel::TC) return done(fail, launch_tc((int)q.dtype, a, c.plan, st));
   return done(fail, launch_simt((int)q.dtype, c.vec, a, c.plan, st));
 }
 
@@ -236,7 +242,7 @@ extern "C" dl_status dl_attend_sync(void* stream, int32_t* device_code, char* er
   const ErrOut fail(errbuf, errlen);
   int32_t code = 0;
   cudaError_t e = cudaSuccess;
-  for (const auto read : {read_pages_status, read_simt_status, read_step_status}) {
+  for (const auto read : {read_pages_status, read_simt_status, read_step_status, read_tc_status}) {
     int32_t c = 0;
     e = read(static_cast<cudaStream_t>(stream), &c);
     if (e != cudaSuccess) break;

@@ -1,0 +1,787 @@
+// Attention of prompts over pages on the 5th-generation tensor cores, 16-bit types.
+//
+// A tile is 128 rows: consecutive tokens times the query heads that share a head of keys.  Against a block of BK keys
+//   S [128 x BK] = Q K^T           exact products of the inputs, fp32 sums in TMEM
+//   P = 2^(S scale log2(e) - r)    rounded to the type, back to TMEM in the place of S
+//   O [128 x D] += P V             A from TMEM, fp32 sums in TMEM
+// with r a reference: the maximum of the row's first block, and of all so far whenever the weights of a block get too
+// large for the type.  So most blocks take no maximum, and O stays where it is; it is read back and scaled when r moves.
+// Sums of P are formed from its 32-bit values.
+//
+// Per block the products of a tile take about as long as its softmax (128 x 128 exponentials), and they wait for one
+// another.  So a CTA has two chains of them, whose softmax and products alternate: two tiles of one item for D <= 128,
+// and for D = 256, where O of one tile takes half of TMEM, two blocks of the same tile.  Both tiles use the same keys,
+// 256 rows a block that is read from L2.
+//
+// Roles: warp 0 copies (queries and pages, tensor copies into the 128-byte swizzle), warp 1 issues products, warp 2
+// looks blocks over that not every token of the tiles sees, warp 3 finds the next items, and a warp group a chain (one
+// for D = 256) does the softmax, a row a thread.  CTAs are persistent and each role goes on to the next item by itself,
+// so an item's end overlaps the next one's beginning.
+//
+// What a token does not see has weight zero, and zero times an infinity or a NaN is a NaN: keys that no token of the
+// item sees (behind the row's last, unwritten places) are zeroed in the copy of V, and a block some of whose tokens do
+// not see a value that is not finite is added up by the softmax threads, key by key, instead.
+//
+// Few items: their keys are split, parts (reference, sum, O) go to the workspace and a second launch joins them.
+#include <cmath>
+#include <cstdlib>
+
+#include <cuda.h>
+
+#include "attn_device.cuh"
+#include "mixer_device.cuh"
+#include "tc_device.cuh"
+
+namespace dl {
+namespace at {
+
+static __device__ int32_t g_tc_status;     // what was out of range
+static __device__ int32_t g_tc_waits;      // waits that gave up
+
+namespace {
+
+using mx::add2;
+using mx::ex2_f;
+using mx::f2;
+using mx::fma2;
+using mx::from_f;
+using mx::mk2;
+using mx::pack2;
+using mx::un2;
+
+constexpr int R = 128;                     // rows of a tile
+constexpr int ITEMS = 4;                   // items that are found ahead
+constexpr int MIN_BLOCKS = 4;              // blocks of keys that a split is worth
+
+template <int D> struct Cfg {
+  static constexpr int QT = D == 256 ? 1 : 2, BK = D == 256 ? 64 : 128, STAGES = D == 64 ? 4 : 2;
+  static constexpr int THREADS = 128 + 128 * QT;
+  static constexpr uint32_t QBLK = R * 128, KBLK = BK * 128;            // 64 columns of a tile, of a block
+  static constexpr uint32_t QTILE = QBLK * (D / 64), KTILE = KBLK * (D / 64);
+  static constexpr uint32_t Q = 0, K = QT * QTILE, V = K + STAGES * KTILE, MISC = V + STAGES * KTILE;
+  static constexpr uint32_t S_COL = 0, O_COL = 256;                     // chain c's S at c * BK, tile t's O at 256 + t * D
+  // barriers, eight bytes each
+  enum { QFULL = 0, QEMPTY = 2, KFULL = 4, KEMPTY = 8, VFULL = 12, VEMPTY = 16, VOK = 20, SFULL = 24, PREADY = 26, PVDONE = 28,
+         IFULL = 30, IEMPTY = 34, DRAIN = 38, NEVER = 39, BARS = 40 };
+  static constexpr uint32_t BAR = MISC, FLAGS = BAR + 8 * BARS, TSLOT = FLAGS + 16, ITEM = TSLOT + 16;
+  static constexpr uint32_t BYTES = ITEM + ITEMS * 64;
+};
+
+struct Item {
+  int32_t x, row, slot, begin, t0, nt, pos0, gh, h0;   // x < 0: no more
+  int32_t split, b0, b1, sink_blocks, first, whole;    // blocks [b0, b1); whole: all that the item has
+  int32_t pad;
+};
+static_assert(sizeof(Item) == 64, "its place in shared memory");
+
+struct TcArgs {
+  CUtensorMap mq, mk, mv;
+  AttnArgs a;
+  int32_t tpt, hpt, hgroups, tiles, splits, total, per_row;   // per_row: tiles of a row (token-major), else 0
+  int32_t test_stall;                  // test only: see below
+  unsigned long long wait_ns;
+};
+
+__device__ __forceinline__ void tma4(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap* m, int c0, int c1, int c2, int c3, int c4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+      ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar) : "memory");
+}
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par, unsigned long long ns) {
+  return mbar_wait(bar, par, &g_tc_waits, DEV_TIMEOUT_MMA, ns);
+}
+
+// acc + 0 x for two values: whatever is not finite leaves a NaN.
+template <class T> __device__ __forceinline__ uint32_t not_finite(uint32_t acc, uint32_t x) {
+  if constexpr (std::is_same<T, __half>::value) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+  else asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
+  return acc;
+}
+template <class T> __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
+  return tc::idesc_bf16_f32(R, N, false, b_mn) & ~(std::is_same<T, __half>::value ? (1u << 7) | (1u << 10) : 0u);
+}
+// The reference is the row's maximum when it is set, and stays while the weights of a block add up to at most LIMIT:
+// bf16 weights keep their precision and sums of 2^20 their range; fp16 ones must stay below 2^16, and are kept 2^7 up,
+// so that those of 2^-21 are still normal numbers (a block of them at the maximum adds up to 2^14).
+template <class T> constexpr float LIFT = 0.f;
+template <> constexpr float LIFT<__half> = 7.f;
+template <class T> constexpr float LIMIT = 0x1p20f;
+template <> constexpr float LIMIT<__half> = 0x1p15f;
+
+// O += P V for a block with values that are not finite, key by key; a row takes the keys that it sees.  P is in TMEM at
+// p_col, O at o_col (first: not yet anything).
+template <class T, int D>
+__device__ __noinline__ void by_keys(const AttnArgs& a, const unsigned char* v, uint32_t p_col, uint32_t o_col, int pos,
+                                     int j0, bool first) {
+  using C = Cfg<D>;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t o[32];
+    tc::tmem_ld32(o_col + 32 * c, o);
+    tc::tmem_wait_ld(o);
+    if (first)
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] = 0u;
+#pragma unroll 1
+    for (int j = 0; j < C::BK; ++j) {
+      uint32_t w;
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(p_col + (uint32_t)(j >> 1)));
+      asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(w)::"memory");
+      float lo, hi;
+      mx::unpack2<T>(w, lo, hi);
+      const float p = j & 1 ? hi : lo;
+      const bool see = sees(a, pos, j0 + j);
+      const unsigned char* row = v + (c >> 1) * C::KBLK + j * 128;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 x = *reinterpret_cast<const uint4*>(row + ((((c & 1) * 4 + k) ^ (j & 7)) << 4));
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          mx::unpack2<T>(xs[e], lo, hi);
+          if (see) {
+            o[8 * k + 2 * e] = __float_as_uint(fmaf(p, lo, __uint_as_float(o[8 * k + 2 * e])));
+            o[8 * k + 2 * e + 1] = __float_as_uint(fmaf(p, hi, __uint_as_float(o[8 * k + 2 * e + 1])));
+          }
+        }
+      }
+    }
+    tc::tmem_st32(o_col + 32 * c, o);
+  }
+  tc::tmem_wait_st();
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_constant__ TcArgs g) {
+  extern __shared__ __align__(1024) unsigned char sm[];
+  using C = Cfg<D>;
+  constexpr int QT = C::QT, BK = C::BK, ST = C::STAGES;
+  const AttnArgs& a = g.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t sb = smem_u32(sm);
+  auto bar = [&](int k) { return sb + C::BAR + 8u * (uint32_t)k; };
+  volatile int32_t* flags = reinterpret_cast<int32_t*>(sm + C::FLAGS);   // [stage] the block is added up key by key
+  Item* const items = reinterpret_cast<Item*>(sm + C::ITEM);
+
+  pdl_launch_dependents();
+  if (warp == 0) tc::tmem_alloc(sb + C::TSLOT, 512);
+  if (tid == 32) {
+    for (int k = 0; k < C::BARS; ++k) {
+      const int n = k >= C::PREADY && k < C::PREADY + 2 ? 4 : k >= C::IEMPTY && k < C::IEMPTY + ITEMS ? 3 + 4 * QT : 1;
+      mbar_init(bar(k), n);
+    }
+    fence_mbar_init();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + C::TSLOT);
+
+  // A wait (of a whole warp) that ran out: the warp waits no more and leaves, and so does every warp that waits for it.
+  bool ok = true;
+  auto wait = [&](int k, uint32_t phase) {
+    if (!ok) return false;
+    bool in = mbar_try_wait(bar(k), phase & 1u);
+    if (!__all_sync(0xffffffffu, in)) {
+      if (!in) in = wait_long(bar(k), phase & 1u, g.wait_ns);
+      ok = __all_sync(0xffffffffu, in);
+    }
+    return ok;
+  };
+  // The next item (number `no` of this CTA's), for whole warps.
+  auto peek = [&](uint32_t no, Item& it) {
+    if (!wait(C::IFULL + no % ITEMS, no / ITEMS)) return false;
+    it = items[no % ITEMS];
+    return it.x >= 0;
+  };
+  auto release = [&](uint32_t no) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(C::IEMPTY + no % ITEMS));
+  };
+  auto block_at = [&](const Item& it, int b) { return b < it.sink_blocks ? b : it.first + b - it.sink_blocks; };
+  auto masked = [&](const Item& it, int j0) { return !all_see(a, it.pos0, it.pos0 + it.nt - 1, j0, j0 + BK); };
+
+  if (warp < 4) {
+    if (warp == 0) {
+      // ---- copies
+      uint32_t no = 0, blocks = 0, filled = 0;
+      Item it;
+      const int box = min(1 << a.page_shift, BK), pages = BK / box;
+      const uint32_t qbytes = 128u * (uint32_t)(g.hpt * g.tpt) * (D / 64), pbytes = 128u * (uint32_t)box * (D / 64);
+      for (; peek(no, it); ++no) {
+        release(no);
+        if (it.b0 == it.b1) continue;
+        for (int t = 0; t < QT && ok; ++t) {
+          if (!wait(C::QEMPTY + t, filled + 1)) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(C::QFULL + t), qbytes);
+            for (int e = 0; e < D / 64; ++e)
+              tma5(sb + C::Q + t * C::QTILE + e * C::QBLK, &g.mq, 64 * e, it.h0, it.gh, it.begin + it.t0 + t * g.tpt,
+                   a.starts ? 0 : it.row, bar(C::QFULL + t));
+          }
+          __syncwarp();
+        }
+        ++filled;
+        const int p1 = it.pos0 + it.nt - 1;
+        for (int b = it.b0; b < it.b1 && ok; ++b, ++blocks) {
+          const int j0 = block_at(it, b) * BK, jp = j0 + lane * box;
+          // the pages of which some token sees a key
+          bool got = lane < pages && jp <= p1;
+          if (got && a.window) {
+            const int lo = it.pos0 - a.window + 1;              // keys from here on, and below sinks
+            got = jp + box > lo || jp < a.sinks;
+          }
+          const int id = got ? page_of(a, it.slot, jp, &g_tc_status) : 0;
+          const uint32_t bytes = pbytes * __popc(__ballot_sync(0xffffffffu, got));
+          const uint32_t s = blocks % ST, ph = blocks / ST;
+          const int off = jp & ((1 << a.page_shift) - 1);
+          if (!wait(C::KEMPTY + s, ph + 1)) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::KFULL + s), bytes);
+          __syncwarp();
+          if (got)
+            for (int e = 0; e < D / 64; ++e)
+              tma4(sb + C::K + s * C::KTILE + e * C::KBLK + lane * box * 128, &g.mk, 64 * e, off, it.gh, id, bar(C::KFULL + s));
+          __syncwarp();
+          if (!wait(C::VEMPTY + s, ph + 1)) {
+            ++blocks;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar(C::VFULL + s), bytes);
+          __syncwarp();
+          if (got)
+            for (int e = 0; e < D / 64; ++e)
+              tma4(sb + C::V + s * C::KTILE + e * C::KBLK + lane * box * 128, &g.mv, 64 * e, off, it.gh, id, bar(C::VFULL + s));
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+      if (!ok && lane == 0) {
+        // what is on its way lands before the memory is given back: the last copy into each place
+        for (int t = 0; t < QT; ++t)
+          if (filled) mbar_drain(bar(C::QFULL + t), (filled - 1) & 1u);
+        for (uint32_t k = 0; k < ST && k < blocks; ++k) {
+          const uint32_t b = blocks - 1 - k;
+          mbar_drain(bar(C::KFULL + b % ST), (b / ST) & 1u);
+          mbar_drain(bar(C::VFULL + b % ST), (b / ST) & 1u);
+        }
+      }
+    } else if (warp == 1) {
+      // ---- products, in the order: S of the first two steps, then O of a step and S of the one two steps on
+      struct Step {
+        uint32_t no, blocks, n, done;      // item; blocks and steps before; items with blocks before
+        int t, b, nb;
+        bool live;
+      };
+      Item it;
+      Step qk{0, 0, 0, 0, 0, 0, 0, true}, pv{0, 0, 0, 0, 0, 0, 0, true};
+      auto open = [&](Step& s, bool frees) {            // the first item from s.no on that has blocks
+        for (;; ++s.no) {
+          s.live = peek(s.no, it);
+          if (!s.live) return;
+          s.nb = it.b1 - it.b0;
+          if (frees) release(s.no);
+          if (s.nb > 0) return;
+        }
+      };
+      auto next = [&](Step& s, bool frees) {
+        ++s.n;
+        if (++s.t < QT) return;
+        s.t = 0;
+        ++s.blocks;
+        if (++s.b < s.nb) return;
+        s.b = 0;
+        ++s.no;
+        ++s.done;
+        open(s, frees);
+      };
+      const int nk = (a.d + 15) / 16;
+      auto scores = [&]() {
+        const uint32_t s = qk.blocks % ST, chain = qk.n & 1u;
+        if (qk.b == 0) wait(C::QFULL + qk.t, qk.done);
+        if (qk.t == 0) wait(C::KFULL + s, qk.blocks / ST);
+        if (!ok) return;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          const uint64_t qd = tc::sdesc128(sb + C::Q + qk.t * C::QTILE, 16u, 1024u);
+          const uint64_t kd = tc::sdesc128(sb + C::K + s * C::KTILE, 16u, 1024u);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            if (k < nk)
+              tc::mma_bf16(tm + C::S_COL + chain * BK, qd + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2u),
+                           kd + ((k >> 2) * (C::KBLK >> 4) + (k & 3) * 2u), idesc<T>(BK, false), k > 0);
+          tc::mma_commit(bar(C::SFULL + chain));
+          if (qk.t == QT - 1) tc::mma_commit(bar(C::KEMPTY + s));
+          if (qk.b == qk.nb - 1) tc::mma_commit(bar(C::QEMPTY + qk.t));
+        }
+        __syncwarp();
+      };
+      auto values = [&]() {
+        const uint32_t s = pv.blocks % ST, chain = pv.n & 1u;
+        wait(C::PREADY + chain, pv.n >> 1);
+        if (pv.t == 0) {
+          wait(C::VFULL + s, pv.blocks / ST);
+          wait(C::VOK + s, pv.blocks / ST);
+        }
+        if (!ok) return;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          if (!flags[s]) {
+            const uint64_t vd = tc::sdesc128(sb + C::V + s * C::KTILE, C::KBLK, 1024u);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)
+              tc::mma_bf16_ta(tm + C::O_COL + pv.t * D, tm + C::S_COL + chain * BK + 8 * k, vd + k * (2048u >> 4),
+                              idesc<T>(D, true), pv.b > 0 || k > 0);
+          }
+          tc::mma_commit(bar(C::PVDONE + pv.t));
+          if (pv.t == QT - 1) tc::mma_commit(bar(C::VEMPTY + s));
+        }
+        __syncwarp();
+      };
+      open(qk, false);
+      open(pv, true);
+      for (int k = 0; k < 2 && ok && qk.live; ++k) {
+        scores();
+        if (ok) next(qk, false);
+      }
+      while (ok && pv.live) {
+        values();
+        if (!ok) break;
+        next(pv, true);
+        if (ok && qk.live) {
+          scores();
+          if (ok) next(qk, false);
+        }
+      }
+      if (!ok && lane == 0) {              // products on their way end before the memory is given back
+        tc::mma_commit(bar(C::DRAIN));
+        mbar_drain(bar(C::DRAIN), 0);
+      }
+    } else if (warp == 2) {
+      // ---- blocks that not every token sees: unseen keys' values become zero, values that are not finite are found
+      uint32_t no = 0, blocks = 0;
+      Item it;
+      if (g.test_stall && blockIdx.x == 0) {
+        // Test only: a barrier that nothing arrives on, at half the limit, so that this warp's wait is the first to run out.
+        mbar_wait(bar(C::NEVER), 0, &g_tc_waits, DEV_TEST_STALL, g.wait_ns / 2);
+        ok = false;
+      }
+      for (; ok && peek(no, it); ++no) {
+        release(no);
+        const int p1 = it.pos0 + it.nt - 1;
+        for (int b = it.b0; b < it.b1 && ok; ++b, ++blocks) {
+          const uint32_t s = blocks % ST;
+          if (!wait(C::VFULL + s, blocks / ST)) break;
+          const int j0 = block_at(it, b) * BK;
+          bool odd = false;
+          if (masked(it, j0)) {
+            unsigned char* v = sm + C::V + s * C::KTILE;
+            uint32_t acc = 0;
+#pragma unroll 8
+            for (int e = lane; e < BK * D / 8; e += 32) {
+              uint4* p = reinterpret_cast<uint4*>(v + e * 16);
+              if (none_sees(a, it.pos0, p1, j0 + (e >> 3) % BK)) {
+                *p = make_uint4(0u, 0u, 0u, 0u);
+              } else {
+                const uint4 x = *p;
+                acc = not_finite<T>(not_finite<T>(not_finite<T>(not_finite<T>(acc, x.x), x.y), x.z), x.w);
+              }
+            }
+            tc::fence_smem_to_async();
+            odd = __any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0);
+          }
+          if (lane == 0) flags[s] = odd;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::VOK + s));
+        }
+      }
+    } else {
+      // ---- items: every CTA takes each grid'th of the list, longest first as far as that is known
+      uint32_t no = 0;
+      const int heads = a.G * g.hgroups;
+      auto publish = [&](const Item& it) {
+        if (!wait(C::IEMPTY + no % ITEMS, no / ITEMS + 1)) return;
+        if (lane == 0) {
+          items[no % ITEMS] = it;
+          mbar_arrive(bar(C::IFULL + no % ITEMS));
+        }
+        __syncwarp();
+        ++no;
+      };
+      Item it{};
+      for (int k = blockIdx.x; k < g.total && ok; k += gridDim.x) {
+        const int kx = k / (heads * g.splits), rest = k - kx * (heads * g.splits), h = rest / g.splits;
+        // token-major: the last tiles of all rows first
+        const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
+        Tile w;
+        if (!find_tile(a, x, QT * g.tpt, w, &g_tc_status)) continue;
+        it.split = rest - h * g.splits;
+        const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
+        const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
+        it.b0 = min(bl.count, it.split * each);
+        it.b1 = min(bl.count, it.b0 + each);
+        it.whole = each >= bl.count;
+        if (it.split > 0 && it.b0 == it.b1) continue;
+        it.sink_blocks = bl.sink_blocks;
+        it.first = bl.first;
+        it.x = x;
+        it.row = w.row;
+        it.slot = w.slot;
+        it.begin = w.begin;
+        it.t0 = w.t0;
+        it.nt = w.nt;
+        it.pos0 = w.pos0;
+        it.gh = h / g.hgroups;
+        it.h0 = (h - it.gh * g.hgroups) * R;
+        publish(it);
+      }
+      it.x = -1;
+      publish(it);
+    }
+  } else {
+    // ---- softmax: thread = row of tile t; QT = 1: of the only tile
+    const int t = (warp >> 2) - 1, q4 = warp & 3, r = 32 * q4 + lane, per = a.H / a.G;
+    const uint32_t tl = tm + ((uint32_t)(32 * q4) << 16), o_col = tl + C::O_COL + t * D;
+    const int tok = r / g.hpt, hd = r - tok * g.hpt;
+    const f2 scale2 = mk2(a.scale_log2, a.scale_log2), lift2 = mk2(LIFT<T>, LIFT<T>);
+    uint32_t no = 0, steps = 0, blocks = 0;
+    Item it;
+    for (; ok && peek(no, it); ++no) {
+      release(no);
+      const int pos = it.pos0 + t * g.tpt + tok;
+      float m = -INFINITY, l = 0.f;       // the reference is m scale log2(e) - LIFT
+      for (int b = it.b0; b < it.b1 && ok; ++b, ++steps, ++blocks) {
+        const uint32_t chain = QT == 2 ? (uint32_t)t : steps & 1u, ph = QT == 2 ? steps : steps >> 1;
+        const uint32_t s_col = tl + C::S_COL + chain * BK;
+        const int j0 = block_at(it, b) * BK;
+        const bool part = masked(it, j0);
+        if (!wait(C::SFULL + chain, ph)) break;
+        tc::fence_after_sync();
+        const int hi = pos - j0, lo = a.window ? hi - a.window : -1, sk = a.window ? a.sinks - j0 : BK;
+        auto hide = [&](uint32_t (&s)[32], int c) {      // keys of this chunk that the row does not see
+          if (!part) return;
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int j = 32 * c + k;
+            if (!(j <= hi && (j > lo || j < sk))) s[k] = 0xff800000u;
+          }
+        };
+        uint32_t p[BK / 2];
+        bool lift = b == it.b0;
+        for (bool again = false;; again = true) {
+          if (lift) {                    // a new reference: the row's maximum so far
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+            for (int c = 0; c < BK / 32; ++c) {
+              uint32_t s[32];
+              tc::tmem_ld32(s_col + 32 * c, s);
+              tc::tmem_wait_ld(s);
+              if (part) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                  const int j = 32 * c + k;
+                  if (!(j <= hi && (j > lo || j < sk))) s[k] = 0xff800000u;
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[k]));
+            }
+            const float was = m;
+            m = fmaxf(was, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+            const float f = ex2_f((was - held(m)) * a.scale_log2);
+            l *= f;
+            if (b > it.b0) {
+              if (!wait(C::PVDONE + t, steps - 1)) break;
+              tc::fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tc::tmem_ld32(o_col + 32 * c, o);
+                tc::tmem_wait_ld(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tc::tmem_st32(o_col + 32 * c, o);
+              }
+            }
+          }
+          const float base = -held(m);
+          const f2 base2 = mk2(base, base);
+          f2 sum[2] = {mk2(0.f, 0.f), mk2(0.f, 0.f)};
+          uint32_t s[2][32];
+          tc::tmem_ld32(s_col, s[0]);
+          tc::tmem_wait_ld(s[0]);
+#pragma unroll
+          for (int c = 0; c < BK / 32; ++c) {
+            if (c + 1 < BK / 32) tc::tmem_ld32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
+            hide(s[c & 1], c);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float x, y;
+              // differences first: scores as large as the type goes keep theirs
+              un2(fma2(add2(mk2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), base2), scale2, lift2), x, y);
+              x = ex2_f(x);
+              y = ex2_f(y);
+              sum[k & 1] = add2(sum[k & 1], mk2(x, y));
+              p[16 * c + k] = pack2<T>(x, y);
+            }
+            if (c + 1 < BK / 32) tc::tmem_wait_ld(s[(c + 1) & 1]);
+          }
+          float x, y, z, w;
+          un2(sum[0], x, y);
+          un2(sum[1], z, w);
+          x = (x + y) + (z + w);
+          lift = !again && __any_sync(0xffffffffu, !(x <= LIMIT<T>));
+          if (lift) continue;
+          l += x;
+          break;
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < BK / 64; ++c) tc::tmem_st32(s_col + 32 * c, *reinterpret_cast<uint32_t (*)[32]>(p + 32 * c));
+        tc::tmem_wait_st();
+        if (part) {
+          const uint32_t st = blocks % ST;
+          if (!wait(C::VOK + st, blocks / ST)) break;
+          if (flags[st]) {
+            if (!wait(C::VFULL + st, blocks / ST)) break;
+            if (b > it.b0 && !wait(C::PVDONE + t, steps - 1)) break;
+            tc::fence_after_sync();
+            by_keys<T, D>(a, sm + C::V + st * C::KTILE, s_col, o_col, pos, j0, b == it.b0);
+          }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::PREADY + chain));
+      }
+      if (!ok) break;
+      const bool any = it.b1 > it.b0;
+      if (any) {
+        if (!wait(C::PVDONE + t, steps - 1)) break;
+        tc::fence_after_sync();
+      }
+      // ---- the row's result
+      const int tk = t * g.tpt + tok;
+      const bool mine = tok < g.tpt && tk < it.nt && it.h0 + hd < per;
+      const float inv = 1.f / l;
+      T* out = static_cast<T*>(a.o) + (int64_t)(it.begin + it.t0 + tk) * a.o_st + (int64_t)it.row * a.o_sn +
+               ((int64_t)it.gh * per + it.h0 + hd) * a.d;
+      float* to = nullptr;
+      if (!it.whole) {
+        const int64_t unit = ((int64_t)it.x * (a.G * g.hgroups) + it.gh * g.hgroups + it.h0 / R) * g.splits + it.split;
+        to = a.ws + (unit * (QT * R) + t * R + r) * (D + 4);
+        if (mine) *reinterpret_cast<float2*>(to) = make_float2(m * a.scale_log2, l);   // (the same LIFT in every part)
+      }
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (any) {
+          tc::tmem_ld32(o_col + 32 * c, o);
+          tc::tmem_wait_ld(o);
+        }
+        if (mine && it.whole) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = 8 * k + 2 * e;
+              w[e] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+            }
+            if (32 * c + 8 * k < a.d) *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (mine) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(to + 4 + 32 * c + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        __syncwarp();
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tm, 512);
+  }
+}
+
+// The parts of split items, in order: a warp a row, block (tile, head).
+template <class T, int D>
+__global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcArgs g) {
+  using C = Cfg<D>;
+  constexpr int QT = C::QT, V = D / 32 < 4 ? D / 32 : 4, P = D / 32 / V;     // columns of a lane: P pieces of V
+  const AttnArgs& a = g.a;
+  const int lane = threadIdx.x & 31, per = a.H / a.G, gh = blockIdx.y / g.hgroups, h0 = (blockIdx.y % g.hgroups) * R;
+  pdl_wait_primary();
+  Tile w;
+  if (!find_tile(a, blockIdx.x, QT * g.tpt, w, &g_tc_status)) return;
+  const Blocks bl = blocks_of<C::BK>(a, w.pos0, w.pos0 + w.nt - 1);
+  const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
+  if (each >= bl.count) return;
+  const int parts = (bl.count + each - 1) / each, heads = min(g.hpt, per - h0);
+  const int64_t unit = ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * g.splits;
+  for (int e = threadIdx.x >> 5; e < w.nt * heads; e += 8) {
+    const int t = e / heads, h = e - t * heads, tile = t / g.tpt;
+    const float* part = a.ws + (unit * (QT * R) + tile * R + (t - tile * g.tpt) * g.hpt + h) * (D + 4);
+    const int64_t next = (int64_t)QT * R * (D + 4);
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, part[k * next]);
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float base = held(top);
+    float l = 0.f, o[P][V];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[p][v] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float* q = part + k * next;
+      const float f = q[1] == 0.f ? 0.f : ex2_f(q[0] - base);
+      l = fmaf(q[1], f, l);
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[p][v] = fmaf(q[4 + (32 * p + lane) * V + v], f, o[p][v]);
+    }
+    T* out = static_cast<T*>(a.o) + (int64_t)(w.begin + w.t0 + t) * a.o_st + (int64_t)w.row * a.o_sn + ((int64_t)gh * per + h0 + h) * a.d;
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if ((32 * p + lane) * V + v < a.d) out[(32 * p + lane) * V + v] = from_f<T>(l == 0.f ? 0.f : o[p][v] / l);
+  }
+}
+
+thread_local TcArgs t_tc;
+
+template <class T, int D>
+cudaError_t go(const TcArgs& g, int grid, cudaStream_t s) {
+  static thread_local int ready = -1;  // the device whose limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (ready != dev) {
+    e = cudaFuncSetAttribute(tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    ready = dev;
+  }
+  tc_kernel<T, D><<<grid, Cfg<D>::THREADS, Cfg<D>::BYTES, s>>>(g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || g.splits == 1) return e;
+  cudaLaunchConfig_t c{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.gridDim = dim3((unsigned)g.tiles, (unsigned)(g.a.G * g.hgroups));
+  c.blockDim = dim3(256);
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, tc_join<T, D>, g);
+}
+
+using EncodeFn = decltype(&cuTensorMapEncodeTiled);
+EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess) {
+      (void)cudaGetLastError();
+      return (EncodeFn) nullptr;
+    }
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+bool encode(CUtensorMap* m, int dtype, int rank, void* p, const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  return fn(m, dtype == mx::T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank, p, dims,
+            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+int tiles_a_cta(int d) { return d > 128 ? 1 : 2; }
+int keys_a_block(int d) { return d > 128 ? 64 : 128; }
+
+}  // namespace
+
+bool tc_fits(int dtype, bool vec, const AttnArgs& a) {
+  const int64_t tiles = tiles_of(a.n, a.T, a.starts != nullptr, 1);   // units are counted in 32 bits
+  return dtype != mx::T_F32 && vec && a.d <= 128 && tiles * a.H < 0x7fffffff / 32;
+}
+
+AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms) {
+  AttnPlan p{};
+  const int per = H / G, hpt = per < R ? per : R, qt = tiles_a_cta(d);
+  p.rows = qt * R;
+  p.tpt = R / hpt;
+  p.hgroups = (per + R - 1) / R;
+  const int64_t tiles = tiles_of(n, T, packed, qt * p.tpt);
+  p.tiles = (int32_t)tiles;
+  const int64_t units = tiles * G * p.hgroups;
+  // Splits for two items an SM, where there are fewer.
+  int64_t s = units > 0 ? (2 * (int64_t)sms + units - 1) / units : 1;
+  p.splits = (int32_t)(s > 32 ? 32 : s);
+  const int64_t total = units * p.splits;
+  p.grid = (int32_t)(total < sms ? total : sms);
+  p.ws_bytes = p.splits > 1 ? total * p.rows * (int64_t)(width_of(d) + 4) * 4 : 0;
+  return p;
+}
+
+cudaError_t launch_tc(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
+  TcArgs& g = t_tc;
+  const int per = a.H / a.G, page = 1 << a.page_shift, bk = keys_a_block(a.d);
+  g.a = a;
+  g.hpt = per < R ? per : R;
+  g.tpt = p.tpt;
+  g.hgroups = p.hgroups;
+  g.tiles = p.tiles;
+  g.splits = p.splits;
+  g.total = p.tiles * a.G * p.hgroups * p.splits;
+  g.per_row = a.starts ? 0 : p.tiles / a.n;
+  g.wait_ns = WAIT_LIMIT_NS;
+  if (const char* e = getenv("DL_TEST_WAIT_MS")) {
+    const long ms = atol(e);
+    if (ms > 0 && ms < 2000) g.wait_ns = (unsigned long long)ms * 1000000ull;
+  }
+  const char* stall = getenv("DL_TEST_STALL");
+  g.test_stall = stall && atoi(stall) == 1;
+  const cuuint64_t d = (cuuint64_t)a.d;
+  const cuuint64_t qdims[5] = {d, (cuuint64_t)per, (cuuint64_t)a.G, (cuuint64_t)a.T, (cuuint64_t)(a.starts ? 1 : a.n)};
+  const cuuint64_t qst[4] = {2 * d, 2 * d * per, (cuuint64_t)a.q_st * 2, (cuuint64_t)(a.starts || a.n == 1 ? a.q_st : a.q_sn) * 2};
+  const cuuint32_t qbox[5] = {64, (cuuint32_t)g.hpt, 1, (cuuint32_t)g.tpt, 1};
+  const cuuint32_t pbox[4] = {64, (cuuint32_t)(page < bk ? page : bk), 1, 1};
+  bool ok = encode(&g.mq, dtype, 5, const_cast<void*>(a.q), qdims, qst, qbox);
+  for (int k = 0; k < 2; ++k) {
+    const PoolView& v = k ? a.vp : a.kp;
+    const cuuint64_t dims[4] = {d, (cuuint64_t)page, (cuuint64_t)a.G, (cuuint64_t)a.num_pages};
+    const cuuint64_t st[3] = {(cuuint64_t)v.st * 2, (cuuint64_t)v.sg * 2, (cuuint64_t)v.sp * 2};
+    ok = ok && encode(k ? &g.mv : &g.mk, dtype, 4, v.p, dims, st, pbox);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  const int D = width_of(a.d);
+  if (dtype == mx::T_BF16)
+    return D == 64 ? go<__nv_bfloat16, 64>(g, p.grid, s) : D == 128 ? go<__nv_bfloat16, 128>(g, p.grid, s)
+                                                                    : go<__nv_bfloat16, 256>(g, p.grid, s);
+  return D == 64 ? go<__half, 64>(g, p.grid, s) : D == 128 ? go<__half, 128>(g, p.grid, s) : go<__half, 256>(g, p.grid, s);
+}
+
+cudaError_t read_tc_status(cudaStream_t s, int32_t* code) {
+  int32_t waits = 0;
+  cudaError_t e = take_status(g_tc_status, s, code);
+  if (e == cudaSuccess) e = take_status(g_tc_waits, s, &waits);
+  if (waits) *code = waits;
+  return e;
+}
+
+}  // namespace at
+}  // namespace dl
