@@ -8,15 +8,16 @@
 // large for the type.  So most blocks take no maximum, and O stays where it is; it is read back and scaled when r moves.
 // Sums of P are formed from its 32-bit values.
 //
-// Per block the products of a tile take about as long as its softmax (128 x 128 exponentials), and they wait for one
-// another.  So a CTA has two chains of them, whose softmax and products alternate: two tiles of one item for D <= 128,
-// and for D = 256, where O of one tile takes half of TMEM, two blocks of the same tile.  Both tiles use the same keys,
-// 256 rows a block that is read from L2.
+// Per block the products of a tile take about as long as its softmax, and they wait for one another: S of a block for
+// its products, P for the softmax.  So a tile has two places for S, and S of the next block is there when the softmax
+// of this one ends; the products always have another chain's to do.  A CTA has two tiles of one item for D <= 128 (for
+// D = 256 one, whose O takes half of TMEM): they use the same keys, 256 rows a block that is read from L2.
 //
-// Roles: warp 0 copies (queries and pages, tensor copies into the 128-byte swizzle), warp 1 issues products, warp 2
-// looks blocks over that not every token of the tiles sees, warp 3 finds the next items, and a warp group a chain (one
-// for D = 256) does the softmax, a row a thread.  CTAs are persistent and each role goes on to the next item by itself,
-// so an item's end overlaps the next one's beginning.
+// Roles: warp 0 finds items and copies (queries and pages, tensor copies into the 128-byte swizzle), warp 1 issues
+// Q K^T, warp 3 P V, warp 2 looks blocks over that not every token of the tiles sees, and a warp group a tile does the
+// softmax, a row a thread.  CTAs are persistent and each role goes on to the next item by itself, so an item's end
+// overlaps the next one's beginning.  An issuing thread wants its operands in uniform registers: 80 cycles a product
+// without, more than the product takes.
 //
 // What a token does not see has weight zero, and zero times an infinity or a NaN is a NaN: keys that no token of the
 // item sees (behind the row's last, unwritten places) are zeroed in the copy of V, and a block some of whose tokens do
@@ -51,19 +52,20 @@ using mx::un2;
 
 constexpr int R = 128;                     // rows of a tile
 constexpr int ITEMS = 4;                   // items that are found ahead
-constexpr int MIN_BLOCKS = 4;              // blocks of keys that a split is worth
+constexpr int BK = 64;                     // keys of a block
+constexpr int MIN_BLOCKS = 8;              // blocks that a split is worth
 
 template <int D> struct Cfg {
-  static constexpr int QT = D == 256 ? 1 : 2, BK = D == 256 ? 64 : 128, STAGES = D == 64 ? 4 : 2;
+  static constexpr int QT = D == 256 ? 1 : 2, CH = 2 * QT, STAGES = D == 256 ? 2 : 4;   // tiles, chains
   static constexpr int THREADS = 128 + 128 * QT;
   static constexpr uint32_t QBLK = R * 128, KBLK = BK * 128;            // 64 columns of a tile, of a block
   static constexpr uint32_t QTILE = QBLK * (D / 64), KTILE = KBLK * (D / 64);
   static constexpr uint32_t Q = 0, K = QT * QTILE, V = K + STAGES * KTILE, MISC = V + STAGES * KTILE;
   static constexpr uint32_t S_COL = 0, O_COL = 256;                     // chain c's S at c * BK, tile t's O at 256 + t * D
   // barriers, eight bytes each
-  enum { QFULL = 0, QEMPTY = 2, KFULL = 4, KEMPTY = 8, VFULL = 12, VEMPTY = 16, VOK = 20, SFULL = 24, PREADY = 26, PVDONE = 28,
-         IFULL = 30, IEMPTY = 34, DRAIN = 38, NEVER = 39, BARS = 40 };
-  static constexpr uint32_t BAR = MISC, FLAGS = BAR + 8 * BARS, TSLOT = FLAGS + 16, ITEM = TSLOT + 16;
+  enum { QFULL = 0, QEMPTY = 2, KFULL = 4, KEMPTY = 8, VFULL = 12, VEMPTY = 16, VOK = 20, SFULL = 24, PREADY = 28, PVDONE = 32,
+         IFULL = 36, IEMPTY = 40, DRAIN = 44, NEVER = 46, BARS = 47 };
+  static constexpr uint32_t BAR = MISC, FLAGS = BAR + 8 * (BARS + 1), TSLOT = FLAGS + 16, ITEM = TSLOT + 16;
   static constexpr uint32_t BYTES = ITEM + ITEMS * 64;
 };
 
@@ -92,6 +94,13 @@ __device__ __forceinline__ void tma5(uint32_t dst, const CUtensorMap* m, int c0,
       "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
       ::"r"(dst), "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar) : "memory");
 }
+// One thread of the warp, the same one every time.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par, unsigned long long ns) {
   return mbar_wait(bar, par, &g_tc_waits, DEV_TIMEOUT_MMA, ns);
 }
@@ -128,7 +137,7 @@ __device__ __noinline__ void by_keys(const AttnArgs& a, const unsigned char* v, 
 #pragma unroll
       for (int k = 0; k < 32; ++k) o[k] = 0u;
 #pragma unroll 1
-    for (int j = 0; j < C::BK; ++j) {
+    for (int j = 0; j < BK; ++j) {
       uint32_t w;
       asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(w) : "r"(p_col + (uint32_t)(j >> 1)));
       asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(w)::"memory");
@@ -160,9 +169,9 @@ template <class T, int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_constant__ TcArgs g) {
   extern __shared__ __align__(1024) unsigned char sm[];
   using C = Cfg<D>;
-  constexpr int QT = C::QT, BK = C::BK, ST = C::STAGES;
+  constexpr int QT = C::QT, CH = C::CH, ST = C::STAGES;
   const AttnArgs& a = g.a;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = (int)uniform(tid >> 5);
   const uint32_t sb = smem_u32(sm);
   auto bar = [&](int k) { return sb + C::BAR + 8u * (uint32_t)k; };
   volatile int32_t* flags = reinterpret_cast<int32_t*>(sm + C::FLAGS);   // [stage] the block is added up key by key
@@ -172,7 +181,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   if (warp == 0) tc::tmem_alloc(sb + C::TSLOT, 512);
   if (tid == 32) {
     for (int k = 0; k < C::BARS; ++k) {
-      const int n = k >= C::PREADY && k < C::PREADY + 2 ? 4 : k >= C::IEMPTY && k < C::IEMPTY + ITEMS ? 3 + 4 * QT : 1;
+      const int n = k >= C::PREADY && k < C::PREADY + 4 ? 4 : k >= C::IEMPTY && k < C::IEMPTY + ITEMS ? 3 + 4 * QT : 1;
       mbar_init(bar(k), n);
     }
     fence_mbar_init();
@@ -180,7 +189,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tm = *reinterpret_cast<volatile uint32_t*>(sm + C::TSLOT);
+  const uint32_t tm = uniform(*reinterpret_cast<volatile uint32_t*>(sm + C::TSLOT));
 
   // A wait (of a whole warp) that ran out: the warp waits no more and leaves, and so does every warp that waits for it.
   bool ok = true;
@@ -208,13 +217,48 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
 
   if (warp < 4) {
     if (warp == 0) {
-      // ---- copies
+      // ---- items and copies.  Every CTA takes each grid'th item of the list, longest first as far as that is known.
       uint32_t no = 0, blocks = 0, filled = 0;
-      Item it;
-      const int box = min(1 << a.page_shift, BK), pages = BK / box;
+      const int heads = a.G * g.hgroups, box = min(1 << a.page_shift, BK), pages = BK / box;
       const uint32_t qbytes = 128u * (uint32_t)(g.hpt * g.tpt) * (D / 64), pbytes = 128u * (uint32_t)box * (D / 64);
-      for (; peek(no, it); ++no) {
-        release(no);
+      auto publish = [&](const Item& it) {
+        if (!wait(C::IEMPTY + no % ITEMS, no / ITEMS + 1)) return;
+        if (lane == 0) {
+          items[no % ITEMS] = it;
+          mbar_arrive(bar(C::IFULL + no % ITEMS));
+        }
+        __syncwarp();
+        ++no;
+      };
+      auto find = [&](int k, Item& it) {   // item k of the list, if it has anything
+        const int kx = k / (heads * g.splits), rest = k - kx * (heads * g.splits), h = rest / g.splits;
+        // token-major: the last tiles of all rows first
+        const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
+        Tile w;
+        if (!find_tile(a, x, QT * g.tpt, w, &g_tc_status)) return false;
+        it.split = rest - h * g.splits;
+        const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
+        const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
+        it.b0 = min(bl.count, it.split * each);
+        it.b1 = min(bl.count, it.b0 + each);
+        it.whole = each >= bl.count;
+        it.sink_blocks = bl.sink_blocks;
+        it.first = bl.first;
+        it.x = x;
+        it.row = w.row;
+        it.slot = w.slot;
+        it.begin = w.begin;
+        it.t0 = w.t0;
+        it.nt = w.nt;
+        it.pos0 = w.pos0;
+        it.gh = h / g.hgroups;
+        it.h0 = (h - it.gh * g.hgroups) * R;
+        return it.split == 0 || it.b0 < it.b1;
+      };
+      Item it{};
+      for (int k = blockIdx.x; k < g.total && ok; k += gridDim.x) {
+        if (!find(k, it)) continue;
+        publish(it);
         if (it.b0 == it.b1) continue;
         for (int t = 0; t < QT && ok; ++t) {
           if (!wait(C::QEMPTY + t, filled + 1)) break;
@@ -258,7 +302,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
               tma4(sb + C::V + s * C::KTILE + e * C::KBLK + lane * box * 128, &g.mv, 64 * e, off, it.gh, id, bar(C::VFULL + s));
           __syncwarp();
         }
-        if (!ok) break;
+      }
+      if (ok) {
+        it.x = -1;
+        publish(it);
       }
       if (!ok && lane == 0) {
         // what is on its way lands before the memory is given back: the last copy into each place
@@ -271,95 +318,86 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         }
       }
     } else if (warp == 1) {
-      // ---- products, in the order: S of the first two steps, then O of a step and S of the one two steps on
-      struct Step {
-        uint32_t no, blocks, n, done;      // item; blocks and steps before; items with blocks before
-        int t, b, nb;
-        bool live;
-      };
+      // ---- S = Q K^T of every block and tile, as soon as its place in TMEM is free: P of the step before on the chain
+      // has been used
+      const uint32_t nk = ((uint32_t)a.d + 15) / 16;
+      const uint64_t qd = tc::sdesc128(sb + C::Q, 16u, 1024u), kd = tc::sdesc128(sb + C::K, 16u, 1024u);
+      uint32_t no = 0, s = 0, sp = 0, step = 0, done = 0;      // stage and its phase; steps of a tile; items with blocks
       Item it;
-      Step qk{0, 0, 0, 0, 0, 0, 0, true}, pv{0, 0, 0, 0, 0, 0, 0, true};
-      auto open = [&](Step& s, bool frees) {            // the first item from s.no on that has blocks
-        for (;; ++s.no) {
-          s.live = peek(s.no, it);
-          if (!s.live) return;
-          s.nb = it.b1 - it.b0;
-          if (frees) release(s.no);
-          if (s.nb > 0) return;
-        }
-      };
-      auto next = [&](Step& s, bool frees) {
-        ++s.n;
-        if (++s.t < QT) return;
-        s.t = 0;
-        ++s.blocks;
-        if (++s.b < s.nb) return;
-        s.b = 0;
-        ++s.no;
-        ++s.done;
-        open(s, frees);
-      };
-      const int nk = (a.d + 15) / 16;
-      auto scores = [&]() {
-        const uint32_t s = qk.blocks % ST, chain = qk.n & 1u;
-        if (qk.b == 0) wait(C::QFULL + qk.t, qk.done);
-        if (qk.t == 0) wait(C::KFULL + s, qk.blocks / ST);
-        if (!ok) return;
-        tc::fence_after_sync();
-        if (lane == 0) {
-          const uint64_t qd = tc::sdesc128(sb + C::Q + qk.t * C::QTILE, 16u, 1024u);
-          const uint64_t kd = tc::sdesc128(sb + C::K + s * C::KTILE, 16u, 1024u);
+      for (; ok && peek(no, it); ++no) {
+        const uint32_t nb = uniform((uint32_t)(it.b1 - it.b0));
+        release(no);
+        for (uint32_t b = 0; b < nb && ok; ++b, ++step) {
+          if (!wait(C::KFULL + s, sp)) break;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            if (k < nk)
-              tc::mma_bf16(tm + C::S_COL + chain * BK, qd + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2u),
-                           kd + ((k >> 2) * (C::KBLK >> 4) + (k & 3) * 2u), idesc<T>(BK, false), k > 0);
-          tc::mma_commit(bar(C::SFULL + chain));
-          if (qk.t == QT - 1) tc::mma_commit(bar(C::KEMPTY + s));
-          if (qk.b == qk.nb - 1) tc::mma_commit(bar(C::QEMPTY + qk.t));
-        }
-        __syncwarp();
-      };
-      auto values = [&]() {
-        const uint32_t s = pv.blocks % ST, chain = pv.n & 1u;
-        wait(C::PREADY + chain, pv.n >> 1);
-        if (pv.t == 0) {
-          wait(C::VFULL + s, pv.blocks / ST);
-          wait(C::VOK + s, pv.blocks / ST);
-        }
-        if (!ok) return;
-        tc::fence_after_sync();
-        if (lane == 0) {
-          if (!flags[s]) {
-            const uint64_t vd = tc::sdesc128(sb + C::V + s * C::KTILE, C::KBLK, 1024u);
+          for (uint32_t t = 0; t < QT; ++t) {
+            const uint32_t chain = (step & 1u) * QT + t;
+            if (b == 0) wait(C::QFULL + t, done);
+            if (!wait(C::PVDONE + chain, (step >> 1) + 1)) break;
+            tc::fence_after_sync();
+            if (elect()) {
+              const uint64_t q0 = qd + t * (C::QTILE >> 4), k0 = kd + s * (C::KTILE >> 4);
 #pragma unroll
-            for (int k = 0; k < BK / 16; ++k)
-              tc::mma_bf16_ta(tm + C::O_COL + pv.t * D, tm + C::S_COL + chain * BK + 8 * k, vd + k * (2048u >> 4),
-                              idesc<T>(D, true), pv.b > 0 || k > 0);
+              for (uint32_t k = 0; k < D / 16; ++k)
+                if (k < nk)
+                  tc::mma_bf16(tm + C::S_COL + chain * BK, q0 + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2u),
+                               k0 + ((k >> 2) * (C::KBLK >> 4) + (k & 3) * 2u), idesc<T>(BK, false), k > 0);
+              tc::mma_commit(bar(C::SFULL + chain));
+              if (t == QT - 1) tc::mma_commit(bar(C::KEMPTY + s));
+              if (b == nb - 1) tc::mma_commit(bar(C::QEMPTY + t));
+            }
+            __syncwarp();
           }
-          tc::mma_commit(bar(C::PVDONE + pv.t));
-          if (pv.t == QT - 1) tc::mma_commit(bar(C::VEMPTY + s));
+          if (++s == ST) {
+            s = 0;
+            ++sp;
+          }
         }
-        __syncwarp();
-      };
-      open(qk, false);
-      open(pv, true);
-      for (int k = 0; k < 2 && ok && qk.live; ++k) {
-        scores();
-        if (ok) next(qk, false);
+        done += nb > 0;
       }
-      while (ok && pv.live) {
-        values();
-        if (!ok) break;
-        next(pv, true);
-        if (ok && qk.live) {
-          scores();
-          if (ok) next(qk, false);
-        }
-      }
-      if (!ok && lane == 0) {              // products on their way end before the memory is given back
+      if (!ok && elect()) {                // products on their way end before the memory is given back
         tc::mma_commit(bar(C::DRAIN));
         mbar_drain(bar(C::DRAIN), 0);
+      }
+    } else if (warp == 3) {
+      // ---- O += P V
+      const uint64_t vd = tc::sdesc128(sb + C::V, C::KBLK, 1024u);
+      uint32_t no = 0, s = 0, sp = 0, step = 0;
+      Item it;
+      for (; ok && peek(no, it); ++no) {
+        const uint32_t nb = uniform((uint32_t)(it.b1 - it.b0));
+        release(no);
+        for (uint32_t b = 0; b < nb && ok; ++b, ++step) {
+          wait(C::VFULL + s, sp);
+          if (!wait(C::VOK + s, sp)) break;
+          const uint32_t skip = uniform((uint32_t)flags[s]);
+#pragma unroll
+          for (uint32_t t = 0; t < QT; ++t) {
+            const uint32_t chain = (step & 1u) * QT + t;
+            if (!wait(C::PREADY + chain, step >> 1)) break;
+            tc::fence_after_sync();
+            if (elect()) {
+              const uint64_t v0 = vd + s * (C::KTILE >> 4);
+              if (!skip) {
+#pragma unroll
+                for (uint32_t k = 0; k < BK / 16; ++k)
+                  tc::mma_bf16_ta(tm + C::O_COL + t * D, tm + C::S_COL + chain * BK + 8 * k, v0 + k * (2048u >> 4),
+                                  idesc<T>(D, true), b > 0 || k > 0);
+              }
+              tc::mma_commit(bar(C::PVDONE + chain));
+              if (t == QT - 1) tc::mma_commit(bar(C::VEMPTY + s));
+            }
+            __syncwarp();
+          }
+          if (++s == ST) {
+            s = 0;
+            ++sp;
+          }
+        }
+      }
+      if (!ok && elect()) {
+        tc::mma_commit(bar(C::DRAIN + 1));
+        mbar_drain(bar(C::DRAIN + 1), 0);
       }
     } else if (warp == 2) {
       // ---- blocks that not every token sees: unseen keys' values become zero, values that are not finite are found
@@ -399,48 +437,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           if (lane == 0) mbar_arrive(bar(C::VOK + s));
         }
       }
-    } else {
-      // ---- items: every CTA takes each grid'th of the list, longest first as far as that is known
-      uint32_t no = 0;
-      const int heads = a.G * g.hgroups;
-      auto publish = [&](const Item& it) {
-        if (!wait(C::IEMPTY + no % ITEMS, no / ITEMS + 1)) return;
-        if (lane == 0) {
-          items[no % ITEMS] = it;
-          mbar_arrive(bar(C::IFULL + no % ITEMS));
-        }
-        __syncwarp();
-        ++no;
-      };
-      Item it{};
-      for (int k = blockIdx.x; k < g.total && ok; k += gridDim.x) {
-        const int kx = k / (heads * g.splits), rest = k - kx * (heads * g.splits), h = rest / g.splits;
-        // token-major: the last tiles of all rows first
-        const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
-        Tile w;
-        if (!find_tile(a, x, QT * g.tpt, w, &g_tc_status)) continue;
-        it.split = rest - h * g.splits;
-        const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
-        const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
-        it.b0 = min(bl.count, it.split * each);
-        it.b1 = min(bl.count, it.b0 + each);
-        it.whole = each >= bl.count;
-        if (it.split > 0 && it.b0 == it.b1) continue;
-        it.sink_blocks = bl.sink_blocks;
-        it.first = bl.first;
-        it.x = x;
-        it.row = w.row;
-        it.slot = w.slot;
-        it.begin = w.begin;
-        it.t0 = w.t0;
-        it.nt = w.nt;
-        it.pos0 = w.pos0;
-        it.gh = h / g.hgroups;
-        it.h0 = (h - it.gh * g.hgroups) * R;
-        publish(it);
-      }
-      it.x = -1;
-      publish(it);
     }
   } else {
     // ---- softmax: thread = row of tile t; QT = 1: of the only tile
@@ -452,10 +448,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
     Item it;
     for (; ok && peek(no, it); ++no) {
       release(no);
-      const int pos = it.pos0 + t * g.tpt + tok;
+      const int tk = t * g.tpt + tok, pos = it.pos0 + tk;
+      const bool mine = tok < g.tpt && tk < it.nt && it.h0 + hd < per;   // other rows hold anything
       float m = -INFINITY, l = 0.f;       // the reference is m scale log2(e) - LIFT
       for (int b = it.b0; b < it.b1 && ok; ++b, ++steps, ++blocks) {
-        const uint32_t chain = QT == 2 ? (uint32_t)t : steps & 1u, ph = QT == 2 ? steps : steps >> 1;
+        const uint32_t chain = (steps & 1u) * QT + t, before = ((steps & 1u) ^ 1u) * QT + t, ph = steps >> 1;
         const uint32_t s_col = tl + C::S_COL + chain * BK;
         const int j0 = block_at(it, b) * BK;
         const bool part = masked(it, j0);
@@ -471,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           }
         };
         uint32_t p[BK / 2];
-        bool lift = b == it.b0;
+        bool lift = __any_sync(0xffffffffu, mine && m == -INFINITY);     // nothing seen so far
         for (bool again = false;; again = true) {
           if (lift) {                    // a new reference: the row's maximum so far
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -495,7 +492,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
             const float f = ex2_f((was - held(m)) * a.scale_log2);
             l *= f;
             if (b > it.b0) {
-              if (!wait(C::PVDONE + t, steps - 1)) break;
+              if (!wait(C::PVDONE + before, (steps - 1) >> 1)) break;
               tc::fence_after_sync();
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
@@ -534,7 +531,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           un2(sum[0], x, y);
           un2(sum[1], z, w);
           x = (x + y) + (z + w);
-          lift = !again && __any_sync(0xffffffffu, !(x <= LIMIT<T>));
+          lift = !again && __any_sync(0xffffffffu, mine && !(x <= LIMIT<T>));
           if (lift) continue;
           l += x;
           break;
@@ -548,7 +545,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           if (!wait(C::VOK + st, blocks / ST)) break;
           if (flags[st]) {
             if (!wait(C::VFULL + st, blocks / ST)) break;
-            if (b > it.b0 && !wait(C::PVDONE + t, steps - 1)) break;
+            if (b > it.b0 && !wait(C::PVDONE + before, (steps - 1) >> 1)) break;
             tc::fence_after_sync();
             by_keys<T, D>(a, sm + C::V + st * C::KTILE, s_col, o_col, pos, j0, b == it.b0);
           }
@@ -560,12 +557,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
       if (!ok) break;
       const bool any = it.b1 > it.b0;
       if (any) {
-        if (!wait(C::PVDONE + t, steps - 1)) break;
+        if (!wait(C::PVDONE + ((steps - 1) & 1u) * QT + t, (steps - 1) >> 1)) break;
         tc::fence_after_sync();
       }
       // ---- the row's result
-      const int tk = t * g.tpt + tok;
-      const bool mine = tok < g.tpt && tk < it.nt && it.h0 + hd < per;
       const float inv = 1.f / l;
       T* out = static_cast<T*>(a.o) + (int64_t)(it.begin + it.t0 + tk) * a.o_st + (int64_t)it.row * a.o_sn +
                ((int64_t)it.gh * per + it.h0 + hd) * a.d;
@@ -620,7 +615,7 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcArgs g)
   pdl_wait_primary();
   Tile w;
   if (!find_tile(a, blockIdx.x, QT * g.tpt, w, &g_tc_status)) return;
-  const Blocks bl = blocks_of<C::BK>(a, w.pos0, w.pos0 + w.nt - 1);
+  const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
   const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
   if (each >= bl.count) return;
   const int parts = (bl.count + each - 1) / each, heads = min(g.hpt, per - h0);
@@ -710,7 +705,6 @@ bool encode(CUtensorMap* m, int dtype, int rank, void* p, const cuuint64_t* dims
 }
 int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 int tiles_a_cta(int d) { return d > 128 ? 1 : 2; }
-int keys_a_block(int d) { return d > 128 ? 64 : 128; }
 
 }  // namespace
 
@@ -739,7 +733,7 @@ AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms) {
 
 cudaError_t launch_tc(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
   TcArgs& g = t_tc;
-  const int per = a.H / a.G, page = 1 << a.page_shift, bk = keys_a_block(a.d);
+  const int per = a.H / a.G, page = 1 << a.page_shift;
   g.a = a;
   g.hpt = per < R ? per : R;
   g.tpt = p.tpt;
@@ -759,7 +753,7 @@ cudaError_t launch_tc(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStrea
   const cuuint64_t qdims[5] = {d, (cuuint64_t)per, (cuuint64_t)a.G, (cuuint64_t)a.T, (cuuint64_t)(a.starts ? 1 : a.n)};
   const cuuint64_t qst[4] = {2 * d, 2 * d * per, (cuuint64_t)a.q_st * 2, (cuuint64_t)(a.starts || a.n == 1 ? a.q_st : a.q_sn) * 2};
   const cuuint32_t qbox[5] = {64, (cuuint32_t)g.hpt, 1, (cuuint32_t)g.tpt, 1};
-  const cuuint32_t pbox[4] = {64, (cuuint32_t)(page < bk ? page : bk), 1, 1};
+  const cuuint32_t pbox[4] = {64, (cuuint32_t)(page < BK ? page : BK), 1, 1};
   bool ok = encode(&g.mq, dtype, 5, const_cast<void*>(a.q), qdims, qst, qbox);
   for (int k = 0; k < 2; ++k) {
     const PoolView& v = k ? a.vp : a.kp;
