@@ -13,8 +13,8 @@
 // of this one ends; the products always have another chain's to do.  A CTA has two tiles of one item for D <= 128 (for
 // D = 256 one, whose O takes half of TMEM): they use the same keys, 256 rows a block that is read from L2.
 //
-// Roles: warp 0 finds items and copies (queries and pages, tensor copies into the 128-byte swizzle), warp 1 issues
-// Q K^T, warp 3 P V, warp 2 looks blocks over that not every token of the tiles sees, and a warp group a tile does the
+// Roles: warp 0 copies (queries and pages, tensor copies into the 128-byte swizzle), warp 1 issues Q K^T, warp 3 P V,
+// warp 2 looks blocks over that not every token of the tiles sees, the last warp finds the next items, and a warp group a tile does the
 // softmax, a row a thread.  CTAs are persistent and each role goes on to the next item by itself, so an item's end
 // overlaps the next one's beginning.  An issuing thread wants its operands in uniform registers: 80 cycles a product
 // without, more than the product takes.
@@ -57,16 +57,17 @@ constexpr int MIN_BLOCKS = 8;              // blocks that a split is worth
 
 template <int D> struct Cfg {
   static constexpr int QT = D == 256 ? 1 : 2, CH = 2 * QT, STAGES = D == 256 ? 2 : 4;   // tiles, chains
-  static constexpr int THREADS = 128 + 128 * QT;
+  static constexpr int THREADS = 512;
   static constexpr uint32_t QBLK = R * 128, KBLK = BK * 128;            // 64 columns of a tile, of a block
   static constexpr uint32_t QTILE = QBLK * (D / 64), KTILE = KBLK * (D / 64);
   static constexpr uint32_t Q = 0, K = QT * QTILE, V = K + STAGES * KTILE, MISC = V + STAGES * KTILE;
   static constexpr uint32_t S_COL = 0, O_COL = 256;                     // chain c's S at c * BK, tile t's O at 256 + t * D
   // barriers, eight bytes each
   enum { QFULL = 0, QEMPTY = 2, KFULL = 4, KEMPTY = 8, VFULL = 12, VEMPTY = 16, VOK = 20, SFULL = 24, PREADY = 28, PVDONE = 32,
-         IFULL = 36, IEMPTY = 40, DRAIN = 44, NEVER = 46, BARS = 47 };
-  static constexpr uint32_t BAR = MISC, FLAGS = BAR + 8 * (BARS + 1), TSLOT = FLAGS + 16, ITEM = TSLOT + 16;
-  static constexpr uint32_t BYTES = ITEM + ITEMS * 64;
+         IFULL = 36, IEMPTY = 40, DRAIN = 44, NEVER = 48, BARS = 49 };
+  static constexpr uint32_t BAR = MISC, FLAGS = BAR + 8 * (BARS + 1), TSLOT = FLAGS + 32, ITEM = TSLOT + 16;
+  static constexpr uint32_t OUT = (ITEM + ITEMS * 64 + 127) & ~127u;    // 32 rows of 128 bytes of every softmax warp
+  static constexpr uint32_t BYTES = OUT + 4 * QT * 4096;
 };
 
 struct Item {
@@ -111,6 +112,8 @@ template <class T> __device__ __forceinline__ uint32_t not_finite(uint32_t acc, 
   else asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x), "r"(0u));
   return acc;
 }
+// Bits 0 .. n of a word.
+__device__ __forceinline__ uint32_t bits_to(int n) { return n < 0 ? 0u : n >= 31 ? 0xffffffffu : (2u << n) - 1u; }
 template <class T> __host__ __device__ constexpr uint32_t idesc(int N, bool b_mn) {
   return tc::idesc_bf16_f32(R, N, false, b_mn) & ~(std::is_same<T, __half>::value ? (1u << 7) | (1u << 10) : 0u);
 }
@@ -174,14 +177,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, warp = (int)uniform(tid >> 5);
   const uint32_t sb = smem_u32(sm);
   auto bar = [&](int k) { return sb + C::BAR + 8u * (uint32_t)k; };
-  volatile int32_t* flags = reinterpret_cast<int32_t*>(sm + C::FLAGS);   // [stage] the block is added up key by key
+  volatile int32_t* flags = reinterpret_cast<int32_t*>(sm + C::FLAGS);   // [stage][checker] the block is added up key by key
   Item* const items = reinterpret_cast<Item*>(sm + C::ITEM);
 
   pdl_launch_dependents();
   if (warp == 0) tc::tmem_alloc(sb + C::TSLOT, 512);
   if (tid == 32) {
     for (int k = 0; k < C::BARS; ++k) {
-      const int n = k >= C::PREADY && k < C::PREADY + 4 ? 4 : k >= C::IEMPTY && k < C::IEMPTY + ITEMS ? 3 + 4 * QT : 1;
+      const int n = k >= C::PREADY && k < C::PREADY + 4 ? 4 : k >= C::IEMPTY && k < C::IEMPTY + ITEMS ? 1 + 7 * QT : (k >= C::KEMPTY && k < C::KEMPTY + 4) || (k >= C::VEMPTY && k < C::VEMPTY + 4) || (k >= C::VOK && k < C::VOK + 4) ? QT : 1;
       mbar_init(bar(k), n);
     }
     fence_mbar_init();
@@ -215,51 +218,29 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   auto block_at = [&](const Item& it, int b) { return b < it.sink_blocks ? b : it.first + b - it.sink_blocks; };
   auto masked = [&](const Item& it, int j0) { return !all_see(a, it.pos0, it.pos0 + it.nt - 1, j0, j0 + BK); };
 
-  if (warp < 4) {
+  constexpr int SW = 4 + 4 * QT;           // the first warp behind those of the softmax
+  if (warp < 4 || warp >= SW) {
     if (warp == 0) {
-      // ---- items and copies.  Every CTA takes each grid'th item of the list, longest first as far as that is known.
+      // ---- copies.  Pages are looked up for 32 pages at a time, a batch ahead.
       uint32_t no = 0, blocks = 0, filled = 0;
-      const int heads = a.G * g.hgroups, box = min(1 << a.page_shift, BK), pages = BK / box;
+      const int box = min(1 << a.page_shift, BK), pages = BK / box, ahead = 32 / pages;
       const uint32_t qbytes = 128u * (uint32_t)(g.hpt * g.tpt) * (D / 64), pbytes = 128u * (uint32_t)box * (D / 64);
-      auto publish = [&](const Item& it) {
-        if (!wait(C::IEMPTY + no % ITEMS, no / ITEMS + 1)) return;
-        if (lane == 0) {
-          items[no % ITEMS] = it;
-          mbar_arrive(bar(C::IFULL + no % ITEMS));
-        }
-        __syncwarp();
-        ++no;
-      };
-      auto find = [&](int k, Item& it) {   // item k of the list, if it has anything
-        const int kx = k / (heads * g.splits), rest = k - kx * (heads * g.splits), h = rest / g.splits;
-        // token-major: the last tiles of all rows first
-        const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
-        Tile w;
-        if (!find_tile(a, x, QT * g.tpt, w, &g_tc_status)) return false;
-        it.split = rest - h * g.splits;
-        const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
-        const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
-        it.b0 = min(bl.count, it.split * each);
-        it.b1 = min(bl.count, it.b0 + each);
-        it.whole = each >= bl.count;
-        it.sink_blocks = bl.sink_blocks;
-        it.first = bl.first;
-        it.x = x;
-        it.row = w.row;
-        it.slot = w.slot;
-        it.begin = w.begin;
-        it.t0 = w.t0;
-        it.nt = w.nt;
-        it.pos0 = w.pos0;
-        it.gh = h / g.hgroups;
-        it.h0 = (h - it.gh * g.hgroups) * R;
-        return it.split == 0 || it.b0 < it.b1;
-      };
-      Item it{};
-      for (int k = blockIdx.x; k < g.total && ok; k += gridDim.x) {
-        if (!find(k, it)) continue;
-        publish(it);
+      Item it;
+      for (; ok && peek(no, it); ++no) {
+        release(no);
         if (it.b0 == it.b1) continue;
+        const int p1 = it.pos0 + it.nt - 1;
+        const int32_t* const row = a.table + (int64_t)it.slot * a.table_stride;
+        // this lane's page of the batch from block b on: its id, and whether some token sees a key of it
+        auto look_up = [&](int b, uint32_t& mask) {
+          b += lane / pages;
+          const int jp = block_at(it, b) * BK + (lane % pages) * box, lo = it.pos0 - a.window + 1;
+          const bool got = b < it.b1 && jp <= p1 && (a.window == 0 || jp + box > lo || jp < a.sinks);
+          mask = __ballot_sync(0xffffffffu, got);
+          return got ? row[jp >> a.page_shift] : 0;
+        };
+        uint32_t mask, mask_next = 0;
+        int ids = look_up(it.b0, mask), ids_next = 0, used = 0;
         for (int t = 0; t < QT && ok; ++t) {
           if (!wait(C::QEMPTY + t, filled + 1)) break;
           if (lane == 0) {
@@ -271,23 +252,22 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           __syncwarp();
         }
         ++filled;
-        const int p1 = it.pos0 + it.nt - 1;
         for (int b = it.b0; b < it.b1 && ok; ++b, ++blocks) {
-          const int j0 = block_at(it, b) * BK, jp = j0 + lane * box;
-          // the pages of which some token sees a key
-          bool got = lane < pages && jp <= p1;
-          if (got && a.window) {
-            const int lo = it.pos0 - a.window + 1;              // keys from here on, and below sinks
-            got = jp + box > lo || jp < a.sinks;
+          if (used == 0 && b + ahead < it.b1) ids_next = look_up(b + ahead, mask_next);
+          const bool got = lane < pages && (mask >> (used * pages + lane) & 1u);
+          int id = __shfl_sync(0xffffffffu, ids, used * pages + lane);
+          if (got && (unsigned)id >= (unsigned)a.num_pages) {
+            atomicCAS(&g_tc_status, 0, DEV_BAD_PAGE);
+            id = 0;
           }
-          const int id = got ? page_of(a, it.slot, jp, &g_tc_status) : 0;
           const uint32_t bytes = pbytes * __popc(__ballot_sync(0xffffffffu, got));
           const uint32_t s = blocks % ST, ph = blocks / ST;
-          const int off = jp & ((1 << a.page_shift) - 1);
+          const int off = (block_at(it, b) * BK + lane * box) & ((1 << a.page_shift) - 1);
           if (!wait(C::KEMPTY + s, ph + 1)) break;
           if (lane == 0) mbar_arrive_expect_tx(bar(C::KFULL + s), bytes);
           __syncwarp();
           if (got)
+#pragma unroll
             for (int e = 0; e < D / 64; ++e)
               tma4(sb + C::K + s * C::KTILE + e * C::KBLK + lane * box * 128, &g.mk, 64 * e, off, it.gh, id, bar(C::KFULL + s));
           __syncwarp();
@@ -298,14 +278,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           if (lane == 0) mbar_arrive_expect_tx(bar(C::VFULL + s), bytes);
           __syncwarp();
           if (got)
+#pragma unroll
             for (int e = 0; e < D / 64; ++e)
               tma4(sb + C::V + s * C::KTILE + e * C::KBLK + lane * box * 128, &g.mv, 64 * e, off, it.gh, id, bar(C::VFULL + s));
           __syncwarp();
+          if (++used == ahead) {
+            used = 0;
+            ids = ids_next;
+            mask = mask_next;
+          }
         }
-      }
-      if (ok) {
-        it.x = -1;
-        publish(it);
       }
       if (!ok && lane == 0) {
         // what is on its way lands before the memory is given back: the last copy into each place
@@ -317,50 +299,46 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           mbar_drain(bar(C::VFULL + b % ST), (b / ST) & 1u);
         }
       }
-    } else if (warp == 1) {
-      // ---- S = Q K^T of every block and tile, as soon as its place in TMEM is free: P of the step before on the chain
+    } else if (warp == 1 || (QT == 2 && warp == SW + 1)) {
+      // ---- S = Q K^T of a tile, block by block, as soon as its place in TMEM is free: P of the step before on the chain
       // has been used
-      const uint32_t nk = ((uint32_t)a.d + 15) / 16;
-      const uint64_t qd = tc::sdesc128(sb + C::Q, 16u, 1024u), kd = tc::sdesc128(sb + C::K, 16u, 1024u);
-      uint32_t no = 0, s = 0, sp = 0, step = 0, done = 0;      // stage and its phase; steps of a tile; items with blocks
+      const uint32_t t = warp == 1 ? 0 : 1;
+      const uint64_t qd = tc::sdesc128(sb + C::Q + t * C::QTILE, 16u, 1024u), kd = tc::sdesc128(sb + C::K, 16u, 1024u);
+      uint32_t no = 0, s = 0, sp = 0, step = 0, done = 0;      // stage and its phase; steps; items with blocks
       Item it;
       for (; ok && peek(no, it); ++no) {
         const uint32_t nb = uniform((uint32_t)(it.b1 - it.b0));
         release(no);
+        if (nb > 0) wait(C::QFULL + t, done++);
         for (uint32_t b = 0; b < nb && ok; ++b, ++step) {
+          const uint32_t chain = (step & 1u) * QT + t;
+          const uint64_t k0 = kd + s * (C::KTILE >> 4);
+          wait(C::PVDONE + chain, (step >> 1) + 1);
           if (!wait(C::KFULL + s, sp)) break;
+          tc::fence_after_sync();
+          if (elect()) {
 #pragma unroll
-          for (uint32_t t = 0; t < QT; ++t) {
-            const uint32_t chain = (step & 1u) * QT + t;
-            if (b == 0) wait(C::QFULL + t, done);
-            if (!wait(C::PVDONE + chain, (step >> 1) + 1)) break;
-            tc::fence_after_sync();
-            if (elect()) {
-              const uint64_t q0 = qd + t * (C::QTILE >> 4), k0 = kd + s * (C::KTILE >> 4);
-#pragma unroll
-              for (uint32_t k = 0; k < D / 16; ++k)
-                if (k < nk)
-                  tc::mma_bf16(tm + C::S_COL + chain * BK, q0 + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2u),
-                               k0 + ((k >> 2) * (C::KBLK >> 4) + (k & 3) * 2u), idesc<T>(BK, false), k > 0);
-              tc::mma_commit(bar(C::SFULL + chain));
-              if (t == QT - 1) tc::mma_commit(bar(C::KEMPTY + s));
-              if (b == nb - 1) tc::mma_commit(bar(C::QEMPTY + t));
-            }
-            __syncwarp();
+            for (uint32_t k = 0; k < D / 16; ++k)
+              tc::mma_bf16(tm + C::S_COL + chain * BK, qd + ((k >> 2) * (C::QBLK >> 4) + (k & 3) * 2u),
+                           k0 + ((k >> 2) * (C::KBLK >> 4) + (k & 3) * 2u), idesc<T>(BK, false), k > 0);
+            tc::mma_commit(bar(C::SFULL + chain));
+            tc::mma_commit(bar(C::KEMPTY + s));
+            if (b == nb - 1) tc::mma_commit(bar(C::QEMPTY + t));
           }
+          __syncwarp();
           if (++s == ST) {
             s = 0;
             ++sp;
           }
         }
-        done += nb > 0;
       }
       if (!ok && elect()) {                // products on their way end before the memory is given back
-        tc::mma_commit(bar(C::DRAIN));
-        mbar_drain(bar(C::DRAIN), 0);
+        tc::mma_commit(bar(C::DRAIN + t));
+        mbar_drain(bar(C::DRAIN + t), 0);
       }
-    } else if (warp == 3) {
-      // ---- O += P V
+    } else if (warp == 3 || (QT == 2 && warp == SW + 3)) {
+      // ---- O += P V of a tile
+      const uint32_t t = warp == 3 ? 0 : 1;
       const uint64_t vd = tc::sdesc128(sb + C::V, C::KBLK, 1024u);
       uint32_t no = 0, s = 0, sp = 0, step = 0;
       Item it;
@@ -368,27 +346,24 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         const uint32_t nb = uniform((uint32_t)(it.b1 - it.b0));
         release(no);
         for (uint32_t b = 0; b < nb && ok; ++b, ++step) {
+          const uint32_t chain = (step & 1u) * QT + t;
+          const uint64_t v0 = vd + s * (C::KTILE >> 4);
           wait(C::VFULL + s, sp);
-          if (!wait(C::VOK + s, sp)) break;
-          const uint32_t skip = uniform((uint32_t)flags[s]);
+          wait(C::VOK + s, sp);
+          const uint32_t skip = uniform((uint32_t)(flags[QT * s] | flags[QT * s + QT - 1]));
+          if (!wait(C::PREADY + chain, step >> 1)) break;
+          tc::fence_after_sync();
+          if (elect()) {
+            if (!skip) {
 #pragma unroll
-          for (uint32_t t = 0; t < QT; ++t) {
-            const uint32_t chain = (step & 1u) * QT + t;
-            if (!wait(C::PREADY + chain, step >> 1)) break;
-            tc::fence_after_sync();
-            if (elect()) {
-              const uint64_t v0 = vd + s * (C::KTILE >> 4);
-              if (!skip) {
-#pragma unroll
-                for (uint32_t k = 0; k < BK / 16; ++k)
-                  tc::mma_bf16_ta(tm + C::O_COL + t * D, tm + C::S_COL + chain * BK + 8 * k, v0 + k * (2048u >> 4),
-                                  idesc<T>(D, true), b > 0 || k > 0);
-              }
-              tc::mma_commit(bar(C::PVDONE + chain));
-              if (t == QT - 1) tc::mma_commit(bar(C::VEMPTY + s));
+              for (uint32_t k = 0; k < BK / 16; ++k)
+                tc::mma_bf16_ta(tm + C::O_COL + t * D, tm + C::S_COL + chain * BK + 8 * k, v0 + k * (2048u >> 4),
+                                idesc<T>(D, true), b > 0 || k > 0);
             }
-            __syncwarp();
+            tc::mma_commit(bar(C::PVDONE + chain));
+            tc::mma_commit(bar(C::VEMPTY + s));
           }
+          __syncwarp();
           if (++s == ST) {
             s = 0;
             ++sp;
@@ -396,14 +371,58 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         }
       }
       if (!ok && elect()) {
-        tc::mma_commit(bar(C::DRAIN + 1));
-        mbar_drain(bar(C::DRAIN + 1), 0);
+        tc::mma_commit(bar(C::DRAIN + 2 + t));
+        mbar_drain(bar(C::DRAIN + 2 + t), 0);
       }
-    } else if (warp == 2) {
-      // ---- blocks that not every token sees: unseen keys' values become zero, values that are not finite are found
+    } else if (warp == SW) {
+      // ---- items: every CTA takes each grid'th of the list, longest first as far as that is known
+      uint32_t no = 0;
+      const int heads = a.G * g.hgroups;
+      auto publish = [&](const Item& it) {
+        if (!wait(C::IEMPTY + no % ITEMS, no / ITEMS + 1)) return;
+        if (lane == 0) {
+          items[no % ITEMS] = it;
+          mbar_arrive(bar(C::IFULL + no % ITEMS));
+        }
+        __syncwarp();
+        ++no;
+      };
+      Item it{};
+      for (int k = blockIdx.x; k < g.total && ok; k += gridDim.x) {
+        const int kx = k / (heads * g.splits), rest = k - kx * (heads * g.splits), h = rest / g.splits;
+        // token-major: the last tiles of all rows first
+        const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
+        Tile w;
+        if (!find_tile(a, x, QT * g.tpt, w, &g_tc_status)) continue;
+        it.split = rest - h * g.splits;
+        const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
+        const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
+        it.b0 = min(bl.count, it.split * each);
+        it.b1 = min(bl.count, it.b0 + each);
+        it.whole = each >= bl.count;
+        if (it.split > 0 && it.b0 == it.b1) continue;
+        it.sink_blocks = bl.sink_blocks;
+        it.first = bl.first;
+        it.x = x;
+        it.row = w.row;
+        it.slot = w.slot;
+        it.begin = w.begin;
+        it.t0 = w.t0;
+        it.nt = w.nt;
+        it.pos0 = w.pos0;
+        it.gh = h / g.hgroups;
+        it.h0 = (h - it.gh * g.hgroups) * R;
+        publish(it);
+      }
+      it.x = -1;
+      publish(it);
+    } else if (warp == 2 || (QT == 2 && warp == SW + 2)) {
+      // ---- blocks that not every token sees, half of the columns a warp: unseen keys' values become zero, values that
+      // are not finite are found
+      const int half = warp == 2 ? 0 : 1;
       uint32_t no = 0, blocks = 0;
       Item it;
-      if (g.test_stall && blockIdx.x == 0) {
+      if (g.test_stall && blockIdx.x == 0 && half == 0) {
         // Test only: a barrier that nothing arrives on, at half the limit, so that this warp's wait is the first to run out.
         mbar_wait(bar(C::NEVER), 0, &g_tc_waits, DEV_TEST_STALL, g.wait_ns / 2);
         ok = false;
@@ -417,22 +436,25 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           const int j0 = block_at(it, b) * BK;
           bool odd = false;
           if (masked(it, j0)) {
-            unsigned char* v = sm + C::V + s * C::KTILE;
+            const uint32_t dead[2] = {__ballot_sync(0xffffffffu, none_sees(a, it.pos0, p1, j0 + lane)),
+                                      __ballot_sync(0xffffffffu, none_sees(a, it.pos0, p1, j0 + 32 + lane))};
+            constexpr int PIECES = BK * D / 8 / QT;
+            uint4* const v = reinterpret_cast<uint4*>(sm + C::V + s * C::KTILE) + half * PIECES;
             uint32_t acc = 0;
 #pragma unroll 8
-            for (int e = lane; e < BK * D / 8; e += 32) {
-              uint4* p = reinterpret_cast<uint4*>(v + e * 16);
-              if (none_sees(a, it.pos0, p1, j0 + (e >> 3) % BK)) {
-                *p = make_uint4(0u, 0u, 0u, 0u);
+            for (int e = lane; e < PIECES; e += 32) {
+              const int row = ((e + half * PIECES) >> 3) & (BK - 1);
+              if ((row < 32 ? dead[0] : dead[1]) >> (row & 31) & 1u) {
+                v[e] = make_uint4(0u, 0u, 0u, 0u);
               } else {
-                const uint4 x = *p;
+                const uint4 x = v[e];
                 acc = not_finite<T>(not_finite<T>(not_finite<T>(not_finite<T>(acc, x.x), x.y), x.z), x.w);
               }
             }
             tc::fence_smem_to_async();
             odd = __any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0);
           }
-          if (lane == 0) flags[s] = odd;
+          if (lane == 0) flags[QT * s + half] = odd;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::VOK + s));
         }
@@ -451,39 +473,41 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
       const int tk = t * g.tpt + tok, pos = it.pos0 + tk;
       const bool mine = tok < g.tpt && tk < it.nt && it.h0 + hd < per;   // other rows hold anything
       float m = -INFINITY, l = 0.f;       // the reference is m scale log2(e) - LIFT
+      // blocks that every token of the item sees whole: [full0, full1) of the window's, those before full2 of the sinks'
+      const int shift = it.sink_blocks - it.first, p1 = it.pos0 + it.nt - 1;
+      const int full0 = a.window ? max(it.sink_blocks, shift + (max(0, p1 - a.window + 1) + BK - 1) / BK) : 0;
+      const int full1 = shift + (it.pos0 + 1) / BK, full2 = a.window ? min(min(it.sink_blocks, a.sinks / BK), (it.pos0 + 1) / BK) : 0;
       for (int b = it.b0; b < it.b1 && ok; ++b, ++steps, ++blocks) {
         const uint32_t chain = (steps & 1u) * QT + t, before = ((steps & 1u) ^ 1u) * QT + t, ph = steps >> 1;
         const uint32_t s_col = tl + C::S_COL + chain * BK;
         const int j0 = block_at(it, b) * BK;
-        const bool part = masked(it, j0);
+        const bool part = !((b >= full0 && b < full1) || b < full2);
         if (!wait(C::SFULL + chain, ph)) break;
         tc::fence_after_sync();
-        const int hi = pos - j0, lo = a.window ? hi - a.window : -1, sk = a.window ? a.sinks - j0 : BK;
-        auto hide = [&](uint32_t (&s)[32], int c) {      // keys of this chunk that the row does not see
+        uint32_t seen[BK / 32];           // keys of the block that the row sees
+        if (part) {
+          const int hi = pos - j0, lo = a.window ? hi - a.window : -1, sk = a.window ? a.sinks - j0 : 0;
+#pragma unroll
+          for (int c = 0; c < BK / 32; ++c)
+            seen[c] = bits_to(hi - 32 * c) & (~bits_to(lo - 32 * c) | bits_to(sk - 1 - 32 * c));
+        }
+        auto hide = [&](uint32_t (&s)[32], int c) {
           if (!part) return;
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int j = 32 * c + k;
-            if (!(j <= hi && (j > lo || j < sk))) s[k] = 0xff800000u;
-          }
+          for (int k = 0; k < 32; ++k)
+            if (!(seen[c] >> k & 1u)) s[k] = 0xff800000u;
         };
         uint32_t p[BK / 2];
         bool lift = __any_sync(0xffffffffu, mine && m == -INFINITY);     // nothing seen so far
         for (bool again = false;; again = true) {
           if (lift) {                    // a new reference: the row's maximum so far
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
+#pragma unroll
             for (int c = 0; c < BK / 32; ++c) {
               uint32_t s[32];
               tc::tmem_ld32(s_col + 32 * c, s);
               tc::tmem_wait_ld(s);
-              if (part) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                  const int j = 32 * c + k;
-                  if (!(j <= hi && (j > lo || j < sk))) s[k] = 0xff800000u;
-                }
-              }
+              hide(s, c);
 #pragma unroll
               for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[k]));
             }
@@ -508,24 +532,22 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           const float base = -held(m);
           const f2 base2 = mk2(base, base);
           f2 sum[2] = {mk2(0.f, 0.f), mk2(0.f, 0.f)};
-          uint32_t s[2][32];
-          tc::tmem_ld32(s_col, s[0]);
-          tc::tmem_wait_ld(s[0]);
 #pragma unroll
           for (int c = 0; c < BK / 32; ++c) {
-            if (c + 1 < BK / 32) tc::tmem_ld32(s_col + 32 * (c + 1), s[(c + 1) & 1]);
-            hide(s[c & 1], c);
+            uint32_t s[32];
+            tc::tmem_ld32(s_col + 32 * c, s);
+            tc::tmem_wait_ld(s);
+            hide(s, c);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float x, y;
               // differences first: scores as large as the type goes keep theirs
-              un2(fma2(add2(mk2(__uint_as_float(s[c & 1][2 * k]), __uint_as_float(s[c & 1][2 * k + 1])), base2), scale2, lift2), x, y);
+              un2(fma2(add2(mk2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), base2), scale2, lift2), x, y);
               x = ex2_f(x);
               y = ex2_f(y);
               sum[k & 1] = add2(sum[k & 1], mk2(x, y));
               p[16 * c + k] = pack2<T>(x, y);
             }
-            if (c + 1 < BK / 32) tc::tmem_wait_ld(s[(c + 1) & 1]);
           }
           float x, y, z, w;
           un2(sum[0], x, y);
@@ -543,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         if (part) {
           const uint32_t st = blocks % ST;
           if (!wait(C::VOK + st, blocks / ST)) break;
-          if (flags[st]) {
+          if (flags[QT * st] | flags[QT * st + QT - 1]) {
             if (!wait(C::VFULL + st, blocks / ST)) break;
             if (b > it.b0 && !wait(C::PVDONE + before, (steps - 1) >> 1)) break;
             tc::fence_after_sync();
@@ -561,37 +583,57 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         tc::fence_after_sync();
       }
       // ---- the row's result
-      const float inv = 1.f / l;
-      T* out = static_cast<T*>(a.o) + (int64_t)(it.begin + it.t0 + tk) * a.o_st + (int64_t)it.row * a.o_sn +
-               ((int64_t)it.gh * per + it.h0 + hd) * a.d;
-      float* to = nullptr;
-      if (!it.whole) {
+      // Through shared memory, 128 bytes of every row at a time, so that eight lanes write a row's together: a row a lane
+      // took 5100 cycles a tile of 128 x 128.
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      unsigned char* const stage = sm + C::OUT + (warp - 4) * 4096;
+      unsigned char* to = nullptr;         // this lane's row
+      if (mine && it.whole) {
+        to = reinterpret_cast<unsigned char*>(static_cast<T*>(a.o) + (int64_t)(it.begin + it.t0 + tk) * a.o_st +
+                                              (int64_t)it.row * a.o_sn + ((int64_t)it.gh * per + it.h0 + hd) * a.d);
+      } else if (mine) {
         const int64_t unit = ((int64_t)it.x * (a.G * g.hgroups) + it.gh * g.hgroups + it.h0 / R) * g.splits + it.split;
-        to = a.ws + (unit * (QT * R) + t * R + r) * (D + 4);
-        if (mine) *reinterpret_cast<float2*>(to) = make_float2(m * a.scale_log2, l);   // (the same LIFT in every part)
+        float* part = a.ws + (unit * (QT * R) + t * R + r) * (D + 4);
+        *reinterpret_cast<float2*>(part) = make_float2(m * a.scale_log2, l);   // (the same LIFT in every part)
+        to = reinterpret_cast<unsigned char*>(part + 4);
       }
+      const int bytes = it.whole ? 2 * a.d : 4 * D, chunks = it.whole ? D / 64 : D / 32;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (any) {
-          tc::tmem_ld32(o_col + 32 * c, o);
-          tc::tmem_wait_ld(o);
-        }
-        if (mine && it.whole) {
+      for (int c = 0; c < chunks; ++c) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 8 * k + 2 * e;
-              w[e] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[32];
+          if (it.whole || half == 0) {
+            if (any) {
+              tc::tmem_ld32(o_col + (it.whole ? 64 * c + 32 * half : 32 * c), o);
+              tc::tmem_wait_ld(o);
             }
-            if (32 * c + 8 * k < a.d) *reinterpret_cast<uint4*>(out + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (mine) {
+            if (it.whole) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            *reinterpret_cast<uint4*>(to + 4 + 32 * c + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int i = 8 * k + 2 * e;
+                  w[e] = l == 0.f ? 0u : pack2<T>(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+                }
+                *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * half + k) ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                    make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            }
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int row = 4 * i + (lane >> 3), piece = lane & 7;
+          unsigned char* const dst = reinterpret_cast<unsigned char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
+          if (dst && 128 * c + 16 * piece < bytes)
+            *reinterpret_cast<uint4*>(dst + 128 * c + 16 * piece) = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
         }
         __syncwarp();
       }
@@ -605,7 +647,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   }
 }
 
-// The parts of split items, in order: a warp a row, block (tile, head).
+// The parts of split items, in order: a warp a row, block (tile, head, part of the rows).
 template <class T, int D>
 __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcArgs g) {
   using C = Cfg<D>;
@@ -620,7 +662,7 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcArgs g)
   if (each >= bl.count) return;
   const int parts = (bl.count + each - 1) / each, heads = min(g.hpt, per - h0);
   const int64_t unit = ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * g.splits;
-  for (int e = threadIdx.x >> 5; e < w.nt * heads; e += 8) {
+  for (int e = 8 * blockIdx.z + (threadIdx.x >> 5); e < w.nt * heads; e += 8 * gridDim.z) {
     const int t = e / heads, h = e - t * heads, tile = t / g.tpt;
     const float* part = a.ws + (unit * (QT * R) + tile * R + (t - tile * g.tpt) * g.hpt + h) * (D + 4);
     const int64_t next = (int64_t)QT * R * (D + 4);
@@ -673,7 +715,7 @@ cudaError_t go(const TcArgs& g, int grid, cudaStream_t s) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  c.gridDim = dim3((unsigned)g.tiles, (unsigned)(g.a.G * g.hgroups));
+  c.gridDim = dim3((unsigned)g.tiles, (unsigned)(g.a.G * g.hgroups), 8);
   c.blockDim = dim3(256);
   c.stream = s;
   c.attrs = &at;

@@ -240,6 +240,27 @@ def test_rising_and_falling_scores(at, dtype):
     check_rows(s, host[L - 1:], last, [1], [0], None, 0)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("level", [-400.0, 400.0])
+@pytest.mark.parametrize("window,sinks", [(40, 0), (70, 3), (200, 0), (None, 0)])
+def test_scores_far_from_zero_behind_keys_that_are_not_seen(at, dtype, level, window, sinks):
+    """Rows that see nothing of their first blocks of keys, and then scores whose exponentials alone would be zero or
+    infinite."""
+    L, d = 500, 64
+    s = Setup([L], 1, d, 16, dtype, seed=6)
+    s.k[0][..., 0] = level / 20
+    for p in range(L):
+        s.k_pages[s.table[s.slots[0]][p // 16], 0, p % 16, 0] = level / 20
+    q, host = s.queries((L,), 2, scale=0.5)
+    q[..., 0] = 160
+    host[..., 0] = 160
+    o = at.attend(q, *s.args(), starts=s.dev([0, L]), window=window, sinks=sinks).cpu()
+    last = at.attend_step(q[L - 1:], *s.args(), window=window, sinks=sinks).cpu()
+    at.sync()
+    check_rows(s, host, o, [L], [0], window, sinks)
+    check_rows(s, host[L - 1:], last, [1], [0], window, sinks)
+
+
 # ---------------------------------------------------------------- wrong tables --
 def test_wrong_slots_lengths_and_pages_are_reported(at):
     from linear_attention_recurrent_gdn_gb300.deltalog import DeltaLogError
