@@ -355,10 +355,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           tc::fence_after_sync();
           if (elect()) {
             if (!skip) {
+              // 128 columns a product: one of 256 with A in TMEM ended in an illegal access
+              constexpr uint32_t N = D < 128 ? D : 128;
 #pragma unroll
-              for (uint32_t k = 0; k < BK / 16; ++k)
-                tc::mma_bf16_ta(tm + C::O_COL + t * D, tm + C::S_COL + chain * BK + 8 * k, v0 + k * (2048u >> 4),
-                                idesc<T>(D, true), b > 0 || k > 0);
+              for (uint32_t c = 0; c < D / N; ++c)
+#pragma unroll
+                for (uint32_t k = 0; k < BK / 16; ++k)
+                  tc::mma_bf16_ta(tm + C::O_COL + t * D + c * N, tm + C::S_COL + chain * BK + 8 * k,
+                                  v0 + c * (2 * C::KBLK >> 4) + k * (2048u >> 4), idesc<T>(N, true), b > 0 || k > 0);
             }
             tc::mma_commit(bar(C::PVDONE + chain));
             tc::mma_commit(bar(C::VEMPTY + s));
@@ -752,7 +756,7 @@ int tiles_a_cta(int d) { return d > 128 ? 1 : 2; }
 
 bool tc_fits(int dtype, bool vec, const AttnArgs& a) {
   const int64_t tiles = tiles_of(a.n, a.T, a.starts != nullptr, 1);   // units are counted in 32 bits
-  return dtype != mx::T_F32 && vec && a.d <= 128 && tiles * a.H < 0x7fffffff / 32;
+  return dtype != mx::T_F32 && vec && tiles * a.H < 0x7fffffff / 32;
 }
 
 AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms) {
