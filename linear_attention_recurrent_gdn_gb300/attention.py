@@ -35,12 +35,14 @@ import struct
 import torch
 
 from . import deltalog as _dl
-from .mixer import _ERR, _DTYPE, _bad, _call, _check, _differentiated, _lib, _on, _tokens
+from .mixer import _ERR, _DTYPE, _bad, _call, _check, _device, _differentiated, _lib, _on, _tokens
 
 # The C structs, every member eight bytes (see the header for their order).
 _PAGES = struct.Struct("=9q8q")
 _APPEND = struct.Struct("=7q6q8qq")
-_ATTEND = struct.Struct("=13qd6q8q2q4q2q")
+_ATTEND = struct.Struct("=13qd6q8q2q4q")          # and the workspace
+_WORKSPACE = struct.Struct("=2q")
+_NO_WORKSPACE = _WORKSPACE.pack(0, 0)
 _I32 = torch.int32
 
 
@@ -136,13 +138,14 @@ def extend(slots, tokens, size, table, lengths, free, *, page_size):
             raise ValueError("size: expected (T, %d), got %s" % (n, shape))
     if n == 0:
         raise ValueError("slots: no rows")
-    maps = torch.empty((2,) + shape, dtype=_I32, device=slots.device)
-    work = torch.empty(3 * n + 3, dtype=_I32, device=slots.device)
     entries = shape[0] if T == 0 else T * n
-    a = work.data_ptr()
-    _call(_lib.dl_pages_extend, _PAGES.pack(*head, a, maps.data_ptr(), maps.data_ptr() + 4 * entries, a + 4 * (n + 1),
-                                            stride, entries, n, T, num_slots, max_pages, num_pages, page_size), dev)
-    return work[:n + 1], maps[0], maps[1]
+    starts, where, positions, work = torch.empty(2 * entries + 3 * n + 3, dtype=_I32, device=slots.device) \
+        .split_with_sizes((n + 1, entries, entries, 2 * n + 2))
+    a = starts.data_ptr()
+    w = a + 4 * (n + 1)
+    _call(_lib.dl_pages_extend, _PAGES.pack(*head, a, w, w + 4 * entries, w + 8 * entries, stride, entries, n, T,
+                                            num_slots, max_pages, num_pages, page_size), dev)
+    return (starts, where, positions) if len(shape) == 1 else (starts, where.view(shape), positions.view(shape))
 
 
 def truncate(slots, keep, table, lengths, free, *, page_size):
@@ -153,23 +156,32 @@ def truncate(slots, keep, table, lengths, free, *, page_size):
                                               num_pages, page_size), dev)
 
 
-def _pool(name, t, dtype, dev, shape=None):
-    """A pool of pages; returns its address and strides."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 4:
-        raise TypeError("%s must be a CUDA tensor [num_pages, G, page_size, d]" % name)
-    _check(name, t, t.shape if shape is None else shape, dtype, dev)
-    stride = t.stride()
-    if stride[3] != 1 and t.shape[3] != 1:
-        raise ValueError("%s: the last dimension must be contiguous" % name)
-    return t.data_ptr(), stride[0], stride[1], stride[2]
+def _pools(k_pages, v_pages, dtype, dev):
+    """Two pools of pages alike; returns their addresses and strides."""
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
+        raise TypeError("k_pages must be a CUDA tensor [num_pages, G, page_size, d]")
+    shape = k_pages.shape
+    _check("k_pages", k_pages, shape, dtype, dev)
+    _check("v_pages", v_pages, shape, dtype, dev)
+    k, v = k_pages.stride(), v_pages.stride()
+    if (k[3] != 1 or v[3] != 1) and shape[3] != 1:
+        raise ValueError("k_pages, v_pages: the last dimension must be contiguous")
+    return k_pages.data_ptr(), k[0], k[1], k[2], v_pages.data_ptr(), v[0], v[1], v[2]
 
 
-def _type(name, t):
-    if t.dtype not in _DTYPE:
-        raise ValueError("%s: %s is not supported" % (name, t.dtype))
+def _lead(name, t, least, most):
+    """The first per-token tensor of a call, of `least` to `most` dimensions; returns its device's number and type."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if not least <= t.dim() <= most:
+        raise ValueError("%s: expected %s dimensions, got %s"
+                         % (name, least if least == most else "%d or %d" % (least, most), tuple(t.shape)))
+    dtype = t.dtype
+    if dtype not in _DTYPE:
+        raise ValueError("%s: %s is not supported" % (name, dtype))
     if _differentiated(t):
-        _bad(name, t, t.dtype, t.get_device())
-    return t.dtype
+        _bad(name, t, dtype, t.get_device())
+    return t.get_device(), dtype
 
 
 def append(k, v, k_pages, v_pages, where):
@@ -177,70 +189,69 @@ def append(k, v, k_pages, v_pages, where):
 
     Leading dimensions are [T, n], [total] or [n], as the call of ``extend``
     laid its maps out; negative places are left out, the others are distinct."""
-    if not isinstance(k, torch.Tensor) or k.dim() not in (3, 4):
-        raise TypeError("k must be a CUDA tensor [..., G, d]")
-    dev = _first("k", k, k.dim())
-    dt, shape = _type("k", k), k.shape
-    lead = shape[:-2]
-    kp = _pool("k_pages", k_pages, dt, dev)
-    vp = _pool("v_pages", v_pages, dt, dev, k_pages.shape)
+    dev, dt = _lead("k", k, 3, 4)
+    pools = _pools(k_pages, v_pages, dt, dev)
     num_pages, G, page_size, d = k_pages.shape
-    for name, pool in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if any(s == 0 and c > 1 for s, c in zip(pool.stride(), pool.shape)):
-            raise ValueError("%s: an expanded tensor cannot be written" % name)
-    kv = _tokens("k", k, lead + (G, d), dt, dev, 2, len(lead))
-    vv = _tokens("v", v, lead + (G, d), dt, dev, 2, len(lead))
+    if 0 in pools and any(s == 0 and c > 1 for p in (k_pages, v_pages) for s, c in zip(p.stride(), p.shape)):
+        raise ValueError("k_pages, v_pages: an expanded tensor cannot be written")
+    lead = k.shape[:-2]
     T, n = lead if len(lead) == 2 else (lead[0], 1)
-    _call(_lib.dl_kv_append, _APPEND.pack(_DTYPE[dt], T, n, G, d, page_size, num_pages, *kv, *vv, *kp, *vp,
+    shape = lead + (G, d)
+    _call(_lib.dl_kv_append, _APPEND.pack(_DTYPE[dt], T, n, G, d, page_size, num_pages,
+                                          *_tokens("k", k, shape, dt, dev, 2, len(lead)),
+                                          *_tokens("v", v, shape, dt, dev, 2, len(lead)), *pools,
                                           _ints("where", where, lead, dev)), dev)
 
 
 def _attend(fn, q, k_pages, v_pages, table, lengths, slots, starts, tokens, window, sinks, scale, out, step):
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 3 if step else 4):
-        raise TypeError("q must be a CUDA tensor %s" % ("[n, H, d]" if step else "[T, n, H, d] or [total, H, d]"))
-    dev = _first("q", q, q.dim())
-    dt, shape = _type("q", q), q.shape
-    lead, H, d = shape[:-2], shape[-2], shape[-1]
+    dev, dt = _lead("q", q, 3, 3 if step else 4)
     if not isinstance(slots, torch.Tensor) or slots.dim() != 1:
         raise TypeError("slots must be a CUDA tensor [n]")
-    n = slots.shape[0]
-    kp = _pool("k_pages", k_pages, dt, dev)
-    vp = _pool("v_pages", v_pages, dt, dev, k_pages.shape)
+    shape, n = q.shape, slots.shape[0]
+    H, d = shape[-2:]
+    pools = _pools(k_pages, v_pages, dt, dev)
     num_pages, G, page_size, dk = k_pages.shape
     if dk != d:
         raise ValueError("k_pages: heads of %d, q has heads of %d" % (dk, d))
     at, stride, num_slots, max_pages, lens = _table(table, lengths, dev)
-    packed, pstarts, ptokens = 0, 0, 0
+    packed = pstarts = ptokens = 0
+    T = shape[0]
     if step:
-        T, kind = 1, 0
-        if lead[0] != n:
-            raise ValueError("q: expected %d rows, got %d" % (n, lead[0]))
-    elif len(lead) == 1:
+        if T != n:
+            raise ValueError("q: expected %d rows, got %d" % (n, T))
+        T, kind, o_st, o_sn = 1, 0, 0, H * d
+    elif len(shape) == 3:
         if starts is None or tokens is not None:
             raise ValueError("packed tokens need starts, and no tokens")
-        packed, T, kind = 1, lead[0], 1
+        packed, kind, o_st, o_sn = 1, 1, H * d, 0
         pstarts = _ints("starts", starts, (n + 1,), dev)
     else:
-        T, kind = lead[0], 2
-        if lead[1] != n:
-            raise ValueError("q: expected %d rows, got %d" % (n, lead[1]))
+        kind, o_st, o_sn = 2, n * H * d, H * d
+        if shape[1] != n:
+            raise ValueError("q: expected %d rows, got %d" % (n, shape[1]))
         if starts is not None:
             raise ValueError("starts are for packed tokens")
         if tokens is not None:
             ptokens = _ints("tokens", tokens, (n,), dev)
-    if window is not None and window < 1:
+    if window is None:
+        window = 0
+    elif window < 1:
         raise ValueError("window: at least 1, or None")
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    head = (_DTYPE[dt], n, T, packed, H, G, d, page_size, max_pages, num_slots, num_pages, window or 0, sinks,
-            d ** -0.5 if scale is None else scale) + _tokens("q", q, shape, dt, dev, 2, kind) \
-        + _tokens("out", out, shape, dt, dev, 2, kind) + kp + vp \
-        + (at, stride, lens, _ints("slots", slots, (n,), dev), pstarts, ptokens)
-    args = _ATTEND.pack(*head, 0, 0)
-    size = _on(dev, _lib.dl_attend_workspace, args)
+        out = torch.empty(shape, dtype=dt, device=q.device)
+        view = out.data_ptr(), o_st, o_sn
+    else:
+        view = _tokens("out", out, shape, dt, dev, 2, kind)
+    args = _ATTEND.pack(_DTYPE[dt], n, T, packed, H, G, d, page_size, max_pages, num_slots, num_pages, window, sinks,
+                        d ** -0.5 if scale is None else scale, *_tokens("q", q, shape, dt, dev, 2, kind), *view,
+                        *pools, at, stride, lens, _ints("slots", slots, (n,), dev), pstarts, ptokens)
+    size = _lib.dl_attend_workspace(args + _NO_WORKSPACE) if dev == _device() else \
+        _on(dev, _lib.dl_attend_workspace, args + _NO_WORKSPACE)
     if size > 0:
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-        args = _ATTEND.pack(*head, workspace.data_ptr(), size)
+        args += _WORKSPACE.pack(workspace.data_ptr(), size)
+    else:
+        args += _NO_WORKSPACE
     _call(fn, args, dev)
     return out
 

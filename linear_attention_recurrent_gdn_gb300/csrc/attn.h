@@ -44,7 +44,7 @@ struct AppendArgs {
   int64_t T;
   int32_t n, G, d, page_shift, num_pages;
 };
-cudaError_t launch_append(int elem, bool vec, const AppendArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_append(int elem, bool vec, const AppendArgs& a, cudaStream_t s);
 
 struct AttnArgs {
   const void* q;             // token t of row i: packed (starts[i] + t) * st, else t * st + i * sn; [H][d] contiguous

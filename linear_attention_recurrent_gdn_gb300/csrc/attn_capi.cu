@@ -220,7 +220,7 @@ extern "C" dl_status dl_kv_append(const dl_kv_append_args* p, void* stream, char
   const AppendArgs a{q.k.data, q.v.data, q.k.stride_t, q.k.stride_n, q.v.stride_t, q.v.stride_n, pool(q.k_pages),
                      pool(q.v_pages), q.where, q.T, (int32_t)q.n, (int32_t)q.G, (int32_t)q.d, shift_of(q.page_size),
                      (int32_t)q.num_pages};
-  return done(fail, launch_append((int)e, vec, a, num_sms(), static_cast<cudaStream_t>(stream)));
+  return done(fail, launch_append((int)e, vec, a, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int64_t dl_attend_workspace(const dl_attend_args* p) {

@@ -272,42 +272,40 @@ template <> struct Piece<16> { using T = uint4; };
 template <> struct Piece<4> { using T = uint32_t; };
 template <> struct Piece<2> { using T = uint16_t; };
 
-constexpr int AT_U = 4;                // pieces of k and of v that a thread has on their way
+// A block moves AT_U * AT_T consecutive pieces of k and of v, every load of a thread before its first store.
+constexpr int AT_U = 4, AT_T = 256;
 template <int V, int EL>
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(AT_T) append_kernel(const AppendArgs a) {
   using P = typename Piece<V>::T;
   constexpr int PE = V / EL;           // elements of a piece
-  const int per_head = a.d / PE, per = a.G * per_head, page = 1 << a.page_shift;
-  const int64_t total = a.T * a.n * per, step = (int64_t)gridDim.x * 256;
-  for (int64_t e0 = (int64_t)blockIdx.x * 256 + threadIdx.x; e0 < total; e0 += AT_U * step) {
-    P kv[AT_U], vv[AT_U];
-    int64_t ko[AT_U], vo[AT_U];
+  const uint32_t per_head = (uint32_t)a.d / PE, per = (uint32_t)a.G * per_head;
+  const int64_t total = a.T * a.n * per, e0 = (int64_t)blockIdx.x * (AT_U * AT_T) + threadIdx.x;
+  P kv[AT_U], vv[AT_U];
+  int at[AT_U];
+  uint32_t c[AT_U];
 #pragma unroll
-    for (int u = 0; u < AT_U; ++u) {
-      const int64_t e = e0 + u * step;
-      ko[u] = -1;
-      if (e >= total) continue;
-      const int64_t tok = total <= 0x7fffffff ? (int64_t)((uint32_t)e / (uint32_t)per) : e / per;
-      const int c = (int)(e - tok * per), g = c / per_head, x = c - g * per_head;
-      const int at = a.where[tok];
-      const int id = at >> a.page_shift, off = at & (page - 1);
-      if (at < 0) continue;
-      if (id >= a.num_pages) {
-        atomicCAS(&g_pages_status, 0, DEV_BAD_PAGE);
-        continue;
-      }
-      const int64_t t = a.n == 1 ? tok : tok / a.n, r = tok - t * a.n;
-      kv[u] = *reinterpret_cast<const P*>(static_cast<const char*>(a.k) + EL * (t * a.k_st + r * a.k_sn + (int64_t)c * PE));
-      vv[u] = *reinterpret_cast<const P*>(static_cast<const char*>(a.v) + EL * (t * a.v_st + r * a.v_sn + (int64_t)c * PE));
-      ko[u] = id * a.kp.sp + g * a.kp.sg + off * a.kp.st + (int64_t)x * PE;
-      vo[u] = id * a.vp.sp + g * a.vp.sg + off * a.vp.st + (int64_t)x * PE;
+  for (int u = 0; u < AT_U; ++u) {
+    const int64_t e = e0 + u * AT_T;
+    at[u] = -1;
+    if (e >= total) continue;
+    const int64_t tok = total <= 0xffffffffll ? (int64_t)((uint32_t)e / per) : e / per;
+    c[u] = (uint32_t)(e - tok * per);
+    const int64_t t = a.n == 1 ? tok : (int64_t)((uint32_t)tok / (uint32_t)a.n), r = tok - t * a.n;
+    at[u] = a.where[tok];
+    kv[u] = *reinterpret_cast<const P*>(static_cast<const char*>(a.k) + EL * (t * a.k_st + r * a.k_sn + (int64_t)c[u] * PE));
+    vv[u] = *reinterpret_cast<const P*>(static_cast<const char*>(a.v) + EL * (t * a.v_st + r * a.v_sn + (int64_t)c[u] * PE));
+  }
+#pragma unroll
+  for (int u = 0; u < AT_U; ++u) {
+    if (at[u] < 0) continue;
+    const int id = at[u] >> a.page_shift, off = at[u] & ((1 << a.page_shift) - 1);
+    if (id >= a.num_pages) {
+      atomicCAS(&g_pages_status, 0, DEV_BAD_PAGE);
+      continue;
     }
-#pragma unroll
-    for (int u = 0; u < AT_U; ++u)
-      if (ko[u] >= 0) {
-        *reinterpret_cast<P*>(static_cast<char*>(a.kp.p) + EL * ko[u]) = kv[u];
-        *reinterpret_cast<P*>(static_cast<char*>(a.vp.p) + EL * vo[u]) = vv[u];
-      }
+    const uint32_t g = c[u] / per_head, x = (c[u] - g * per_head) * PE;
+    *reinterpret_cast<P*>(static_cast<char*>(a.kp.p) + EL * (id * a.kp.sp + g * a.kp.sg + off * a.kp.st + x)) = kv[u];
+    *reinterpret_cast<P*>(static_cast<char*>(a.vp.p) + EL * (id * a.vp.sp + g * a.vp.sg + off * a.vp.st + x)) = vv[u];
   }
 }
 
@@ -342,14 +340,15 @@ cudaError_t launch_truncate(const PagesArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_append(int elem, bool vec, const AppendArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_append(int elem, bool vec, const AppendArgs& a, cudaStream_t s) {
   const int64_t pieces = a.T * a.n * (int64_t)a.G * a.d / (vec ? 16 / elem : 1);
-  const int64_t want = (pieces + 255) / 256, most = 16 * (int64_t)sms;
-  const unsigned grid = (unsigned)(want < most ? want : most);
-  if (vec && elem == 4) append_kernel<16, 4><<<grid, 256, 0, s>>>(a);
-  else if (vec) append_kernel<16, 2><<<grid, 256, 0, s>>>(a);
-  else if (elem == 4) append_kernel<4, 4><<<grid, 256, 0, s>>>(a);
-  else append_kernel<2, 2><<<grid, 256, 0, s>>>(a);
+  const int64_t blocks = (pieces + AT_U * AT_T - 1) / (AT_U * AT_T);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned grid = (unsigned)blocks;
+  if (vec && elem == 4) append_kernel<16, 4><<<grid, AT_T, 0, s>>>(a);
+  else if (vec) append_kernel<16, 2><<<grid, AT_T, 0, s>>>(a);
+  else if (elem == 4) append_kernel<4, 4><<<grid, AT_T, 0, s>>>(a);
+  else append_kernel<2, 2><<<grid, AT_T, 0, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -181,6 +181,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   Item* const items = reinterpret_cast<Item*>(sm + C::ITEM);
 
   pdl_launch_dependents();
+  if (tid >= 64 && tid < 67) {            // the tensor maps, into their cache
+    const CUtensorMap* m = tid == 64 ? &g.mq : tid == 65 ? &g.mk : &g.mv;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
+  }
   if (warp == 0) tc::tmem_alloc(sb + C::TSLOT, 512);
   if (tid == 32) {
     for (int k = 0; k < C::BARS; ++k) {
@@ -632,12 +636,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           }
         }
         __syncwarp();
+        const int piece = lane & 7, at = 128 * c + 16 * piece;
+        uint4 v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int row = 4 * i + (lane >> 3), piece = lane & 7;
-          unsigned char* const dst = reinterpret_cast<unsigned char*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), row));
-          if (dst && 128 * c + 16 * piece < bytes)
-            *reinterpret_cast<uint4*>(dst + 128 * c + 16 * piece) = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+          const int row = 4 * i + (lane >> 3);
+          v[i] = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          unsigned char* const dst = reinterpret_cast<unsigned char*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), 4 * i + (lane >> 3)));
+          if (dst && at < bytes) *reinterpret_cast<uint4*>(dst + at) = v[i];
         }
         __syncwarp();
       }
