@@ -1,16 +1,18 @@
-"""Two token-mixing layers built from the library's calls, from prompts to single tokens.
+"""Three token-mixing layers built from the library's calls, from prompts to single tokens.
 
   GdnLayer   residual sum and norm -> projection -> short convolution with the
              L2 norm of q and k -> Gated DeltaNet (DeltaLog) -> gated norm ->
              projection
   SsmLayer   the same around the selective state space scan
+  AttnLayer  residual sum and norm -> projection -> keys and values into pages
+             -> softmax attention over them -> projection
 
 A layer holds random weights and the state of its slots.  ``prompt`` feeds T
 tokens to the listed slots, ``step`` one token; both return the layer's output
 and the residual stream.  The command runs a prompt and some single tokens
 after it, and the same tokens as one prompt, and compares the two:
 
-  python examples/mixer_layer.py --layer gdn --slots 4 --tokens 96 --steps 8
+  python examples/mixer_layer.py --layer gdn|ssm|attn --slots 4 --tokens 96 --steps 8
 """
 import argparse
 import os
@@ -19,6 +21,7 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from linear_attention_recurrent_gdn_gb300 import attention  # noqa: E402
 from linear_attention_recurrent_gdn_gb300 import deltalog as dl  # noqa: E402
 from linear_attention_recurrent_gdn_gb300 import mixer  # noqa: E402
 
@@ -30,8 +33,9 @@ class _Layer:
         self.gen = torch.Generator(device="cuda").manual_seed(seed)
         self.norm = self.weight(hidden, scale=0.1) + 1
         self.w_in = self.weight(hidden, width, scale=hidden ** -0.5)
-        self.conv_w = self.weight(conv_channels, 4, scale=0.5)
-        self.conv_pool = torch.zeros(slots, 3, conv_channels, dtype=BF16, device="cuda")
+        if conv_channels:
+            self.conv_w = self.weight(conv_channels, 4, scale=0.5)
+            self.conv_pool = torch.zeros(slots, 3, conv_channels, dtype=BF16, device="cuda")
 
     def weight(self, *shape, scale=1.0):
         return (scale * torch.randn(*shape, generator=self.gen, device="cuda")).to(BF16)
@@ -130,6 +134,44 @@ class SsmLayer(_Layer):
         return self.pool[slots]
 
 
+class AttnLayer(_Layer):
+    """H heads of d over G heads of keys and values in pages; hidden = heads * d.  A window and first tokens that stay
+    visible, if they are given."""
+
+    def __init__(self, heads, d, slots, max_tokens, kv_heads=1, page=16, window=None, sinks=0, seed=0):
+        hd, gd = heads * d, kv_heads * d
+        super().__init__(hd, hd + 2 * gd, 0, slots, seed)
+        self.d, self.widths, self.page, self.more = d, (hd, gd, gd), page, dict(window=window, sinks=sinks)
+        self.w_out = self.weight(hd, hd, scale=hd ** -0.5)
+        pages = -(-max_tokens // page)
+        self.tables = attention.new_tables(slots, pages, slots * pages)
+        self.pools = [torch.empty(slots * pages, kv_heads, page, d, dtype=BF16, device="cuda") for _ in range(2)]
+
+    def _mix(self, x, residual, slots, size, attend):
+        z, h = self.enter(x, residual)
+        q, k, v = (t.unflatten(-1, (-1, self.d)) for t in z.split(self.widths, -1))
+        ids = torch.tensor(slots, dtype=torch.int32, device="cuda")
+        tokens = None if size is None else torch.full_like(ids, size[0])
+        _, where, _ = attention.extend(ids, tokens, size, *self.tables, page_size=self.page)
+        attention.append(k, v, *self.pools, where)
+        o = attend(q, *self.pools, *self.tables[:2], ids, **self.more)
+        return o.flatten(-2) @ self.w_out, h
+
+    def prompt(self, x, residual, slots):
+        """x [T, n, hidden]: T more tokens of every listed slot."""
+        return self._mix(x, residual, slots, tuple(x.shape[:2]), attention.attend)
+
+    def step(self, x, residual, slots):
+        return self._mix(x, residual, slots, None, attention.attend_step)
+
+    def state(self, slots):
+        """The slots' keys and values (slots of one length)."""
+        table, lengths, _ = self.tables
+        at = torch.arange(int(lengths[slots[0]]), device="cuda")
+        rows = table[torch.tensor(slots, device="cuda")][:, at // self.page].long()
+        return torch.stack([pool[rows, :, at % self.page] for pool in self.pools])
+
+
 def compare(make, slots, tokens, steps, seed=1):
     """Largest difference, relative to the largest value, of outputs and states between a prompt with single
     tokens after it and one prompt."""
@@ -144,18 +186,20 @@ def compare(make, slots, tokens, steps, seed=1):
     parts = torch.cat([first] + [r[None] for r in rest])
     rel = lambda a, b: float((a.float() - b.float()).abs().max() / b.float().abs().max())  # noqa: E731
     mixer.sync()
+    attention.sync()
     return rel(parts, whole), rel(two.state(ids), one.state(ids))
 
 
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--layer", choices=("gdn", "ssm"), default="gdn")
+    ap.add_argument("--layer", choices=("gdn", "ssm", "attn"), default="gdn")
     ap.add_argument("--slots", type=int, default=4)
     ap.add_argument("--heads", type=int, default=4)
     ap.add_argument("--tokens", type=int, default=96)
     ap.add_argument("--steps", type=int, default=8)
     a = ap.parse_args(argv)
-    make = {"gdn": lambda: GdnLayer(a.heads, 128, a.slots), "ssm": lambda: SsmLayer(a.heads, 64, 128, a.slots)}[a.layer]
+    make = {"gdn": lambda: GdnLayer(a.heads, 128, a.slots), "ssm": lambda: SsmLayer(a.heads, 64, 128, a.slots),
+            "attn": lambda: AttnLayer(a.heads, 128, a.slots, a.tokens + a.steps)}[a.layer]
     out, state = compare(make, a.slots, a.tokens, a.steps)
     print("%s layer, %d slots: %d prompt tokens and %d single ones against one prompt: outputs %.2e, states %.2e apart"
           % (a.layer, a.slots, a.tokens, a.steps, out, state))
