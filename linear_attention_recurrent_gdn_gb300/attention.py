@@ -139,13 +139,13 @@ def extend(slots, tokens, size, table, lengths, free, *, page_size):
     if n == 0:
         raise ValueError("slots: no rows")
     entries = shape[0] if T == 0 else T * n
-    starts, where, positions, work = torch.empty(2 * entries + 3 * n + 3, dtype=_I32, device=slots.device) \
-        .split_with_sizes((n + 1, entries, entries, 2 * n + 2))
-    a = starts.data_ptr()
-    w = a + 4 * (n + 1)
-    _call(_lib.dl_pages_extend, _PAGES.pack(*head, a, w, w + 4 * entries, w + 8 * entries, stride, entries, n, T,
-                                            num_slots, max_pages, num_pages, page_size), dev)
-    return (starts, where, positions) if len(shape) == 1 else (starts, where.view(shape), positions.view(shape))
+    place, empty = slots.device, torch.empty
+    starts, work = empty(n + 1, dtype=_I32, device=place), empty(2 * n + 2, dtype=_I32, device=place)
+    where, positions = empty(shape, dtype=_I32, device=place), empty(shape, dtype=_I32, device=place)
+    _call(_lib.dl_pages_extend, _PAGES.pack(*head, starts.data_ptr(), where.data_ptr(), positions.data_ptr(),
+                                            work.data_ptr(), stride, entries, n, T, num_slots, max_pages, num_pages,
+                                            page_size), dev)
+    return starts, where, positions
 
 
 def truncate(slots, keep, table, lengths, free, *, page_size):
