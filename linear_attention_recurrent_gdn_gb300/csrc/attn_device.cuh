@@ -29,46 +29,56 @@ struct Tile {
 // least ceil(its tokens / tpt) of them before the next row's, since floor((s + t) / p) - floor(s / p) + 1 >= ceil(t / p);
 // so a tile's row is found without sums over the rows.  One warp calls; false: the tile has no tokens.
 __device__ __forceinline__ int packed_tile0(const AttnArgs& a, int i, int tpt) { return a.starts[i] / tpt + i; }
+// The tokens of a row, and where they begin in a packed tensor.
+__device__ __forceinline__ int row_tokens(const AttnArgs& a, int row, int& begin) {
+  begin = 0;
+  if (!a.starts) return a.tokens ? min(max(a.tokens[row], 0), a.T) : a.T;
+  begin = min(max(a.starts[row], 0), a.T);
+  return min(max(a.starts[row + 1], begin), a.T) - begin;
+}
+// The length of a row's slot, at most what its table holds; negative: there is no such slot.  What is out of range is
+// reported to *status, if that is given.
+__device__ __forceinline__ int row_length(const AttnArgs& a, int row, int& slot, int32_t* status) {
+  slot = a.slots[row];
+  if (slot < 0 || slot >= a.num_slots) {
+    if (status) atomicCAS(status, 0, DEV_BAD_SLOT);
+    return -1;
+  }
+  const int len = a.lengths[slot], cap = a.max_pages << a.page_shift;
+  if ((len < 0 || len > cap) && status) atomicCAS(status, 0, DEV_BAD_LENGTH);
+  return min(max(len, 0), cap);
+}
+// Tile `tile` of a row; false: it has no tokens.  (One lane reports.)
+__device__ __forceinline__ bool make_tile(const AttnArgs& a, int row, int tile, int tpt, Tile& w, int32_t* status) {
+  w.row = row;
+  const int t = row_tokens(a, row, w.begin);
+  if (tile < 0 || (int64_t)tile * tpt >= t) return false;
+  w.t0 = tile * tpt;
+  w.nt = min(tpt, t - w.t0);
+  const int len = row_length(a, row, w.slot, (threadIdx.x & 31) == 0 ? status : nullptr);
+  if (len < 0) return false;
+  w.pos0 = len - t + w.t0;             // the new tokens are the slot's last; negative positions see nothing
+  return true;
+}
 __device__ __forceinline__ bool find_tile(const AttnArgs& a, int x, int tpt, Tile& w, int32_t* status) {
-  const int lane = threadIdx.x & 31;
-  int t, tile;
+  int row, tile;
   if (a.starts) {
     // the last row that starts at or before x: every 32nd row, then the 32 from there on
-    const int i = 32 * lane;
+    const int lane = threadIdx.x & 31, i = 32 * lane;
     const unsigned m = __ballot_sync(0xffffffffu, i < a.n && packed_tile0(a, i, tpt) <= x);
     if (m == 0) return false;
     const int i0 = 32 * (31 - __clz(m)) + lane;
     const unsigned r = __ballot_sync(0xffffffffu, i0 < a.n && packed_tile0(a, i0, tpt) <= x);
     if (r == 0) return false;
-    w.row = i0 - lane + 31 - __clz(r);
-    const int s0 = min(max(a.starts[w.row], 0), a.T), s1 = min(max(a.starts[w.row + 1], s0), a.T);
-    w.begin = s0;
-    t = s1 - s0;
-    tile = x - packed_tile0(a, w.row, tpt);
+    row = i0 - lane + 31 - __clz(r);
+    tile = x - packed_tile0(a, row, tpt);
   } else {
     const int per = (a.T + tpt - 1) / tpt;
-    w.row = x / per;
-    if (w.row >= a.n) return false;
-    tile = x - w.row * per;
-    w.begin = 0;
-    t = a.tokens ? min(max(a.tokens[w.row], 0), a.T) : a.T;
+    row = x / per;
+    if (row >= a.n) return false;
+    tile = x - row * per;
   }
-  if (tile < 0 || (int64_t)tile * tpt >= t) return false;
-  w.t0 = tile * tpt;
-  w.nt = min(tpt, t - w.t0);
-  w.slot = a.slots[w.row];
-  if (w.slot < 0 || w.slot >= a.num_slots) {
-    if (lane == 0) atomicCAS(status, 0, DEV_BAD_SLOT);
-    return false;
-  }
-  int len = a.lengths[w.slot];
-  const int cap = a.max_pages << a.page_shift;
-  if (len < 0 || len > cap) {
-    if (lane == 0) atomicCAS(status, 0, DEV_BAD_LENGTH);
-    len = min(max(len, 0), cap);
-  }
-  w.pos0 = len - t + w.t0;             // the new tokens are the slot's last; negative positions see nothing
-  return true;
+  return make_tile(a, row, tile, tpt, w, status);
 }
 // Tiles that a call may have.
 inline int64_t tiles_of(int n, int T, bool packed, int tpt) {

@@ -23,7 +23,9 @@
 // item sees (behind the row's last, unwritten places) are zeroed in the copy of V, and a block some of whose tokens do
 // not see a value that is not finite is added up by the softmax threads, key by key, instead.
 //
-// Few items: their keys are split, parts (reference, sum, O) go to the workspace and a second launch joins them.
+// Few tiles (and at most 32 rows): their keys are split into items of about the same number of blocks, of the size that
+// lets the busiest CTA finish first; the lengths are on the device, so every CTA forms that plan itself.  Parts (reference, sum, O) go to the
+// workspace and a second launch joins them in order.
 #include <cmath>
 #include <cstdlib>
 
@@ -53,7 +55,10 @@ using mx::un2;
 constexpr int R = 128;                     // rows of a tile
 constexpr int ITEMS = 4;                   // items that are found ahead
 constexpr int BK = 64;                     // keys of a block
-constexpr int MIN_BLOCKS = 8;              // blocks that a split is worth
+constexpr int MIN_BLOCKS = 8;              // blocks that an item is worth
+// A split call has at most ITEMS_A_CTA items a CTA and one a tile more, and at most SPLIT_ROWS rows (a lane each).  An
+// item's start, its end and its part in the join cost about as much as ITEM_COST blocks.
+constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 32, ITEM_COST = 10;
 
 template <int D> struct Cfg {
   static constexpr int QT = D == 256 ? 1 : 2, CH = 2 * QT, STAGES = D == 256 ? 2 : 4;   // tiles, chains
@@ -71,8 +76,8 @@ template <int D> struct Cfg {
 };
 
 struct Item {
-  int32_t x, row, slot, begin, t0, nt, pos0, gh, h0;   // x < 0: no more
-  int32_t split, b0, b1, sink_blocks, first, whole;    // blocks [b0, b1); whole: all that the item has
+  int32_t x, row, slot, begin, t0, nt, pos0, gh, h0;   // x < 0: no more items
+  int32_t part, b0, b1, sink_blocks, first, whole;     // blocks [b0, b1); whole: all of the tile's; part: else its number
   int32_t pad;
 };
 static_assert(sizeof(Item) == 64, "its place in shared memory");
@@ -80,7 +85,7 @@ static_assert(sizeof(Item) == 64, "its place in shared memory");
 struct TcArgs {
   CUtensorMap mq, mk, mv;
   AttnArgs a;
-  int32_t tpt, hpt, hgroups, tiles, splits, total, per_row;   // per_row: tiles of a row (token-major), else 0
+  int32_t tpt, hpt, hgroups, tiles, split, total, per_row, ctas;   // per_row: tiles of a row (token-major), else 0
   int32_t test_stall;                  // test only: see below
   unsigned long long wait_ns;
 };
@@ -166,6 +171,53 @@ __device__ __noinline__ void by_keys(const AttnArgs& a, const unsigned char* v, 
     tc::tmem_st32(o_col + 32 * c, o);
   }
   tc::tmem_wait_st();
+}
+
+// The plan of a split call, lane = row: its tiles, the items that a tile's keys make, and the items of the rows before.
+// Returns the items of a head in all.
+struct Split {
+  int tiles, items, first;
+};
+__device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, Split& s, int32_t* status) {
+  const AttnArgs& a = g.a;
+  const int lane = threadIdx.x & 31;
+  int count = 0;
+  s.tiles = 0;
+  if (lane < a.n) {
+    int begin, slot;
+    const int t = row_tokens(a, lane, begin), len = row_length(a, lane, slot, status);
+    if (len >= 0 && t > 0) {
+      s.tiles = (t + tpt - 1) / tpt;
+      count = blocks_of<BK>(a, len - t + (s.tiles - 1) * tpt, len - 1).count;
+    }
+  }
+  long long work = (long long)count * s.tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  // Lane k tries the size that would give (k + 1) ITEMS_A_CTA / 32 items a CTA; the CTA that gets the most sets the time.
+  const long long heads = a.G * g.hgroups, want = (long long)ITEMS_A_CTA * g.ctas * (lane + 1);
+  const int mine = (int)max((long long)MIN_BLOCKS, (32 * work * heads + want - 1) / want);
+  long long items = 0;
+  int most = 0;
+  for (int i = 0; i < a.n; ++i) {
+    const int c = __shfl_sync(0xffffffffu, count, i), t = __shfl_sync(0xffffffffu, s.tiles, i);
+    const int p = c > mine ? (c + mine - 1) / mine : 1;
+    items += (long long)t * p;
+    if (t > 0) most = max(most, (c + p - 1) / p);
+  }
+  long long best = (((items * heads + g.ctas - 1) / g.ctas * (most + ITEM_COST)) << 5) | lane;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) best = min(best, (long long)__shfl_xor_sync(0xffffffffu, best, o));
+  const int each = __shfl_sync(0xffffffffu, mine, (int)(best & 31));
+  s.items = count > each ? (count + each - 1) / each : 1;
+  int run = s.tiles * s.items;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += v;
+  }
+  s.first = run - s.tiles * s.items;
+  return __shfl_sync(0xffffffffu, run, 31);
 }
 
 template <class T, int D>
@@ -396,22 +448,33 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         ++no;
       };
       Item it{};
-      for (int k = blockIdx.x; k < g.total && ok; k += gridDim.x) {
-        const int kx = k / (heads * g.splits), rest = k - kx * (heads * g.splits), h = rest / g.splits;
-        // token-major: the last tiles of all rows first
-        const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
+      Split sp{};
+      const int total = g.split ? plan_split(g, QT * g.tpt, sp, &g_tc_status) * heads : g.total;
+      for (int k = blockIdx.x; k < total && ok; k += gridDim.x) {
+        const int kx = k / heads, h = k - kx * heads;
         Tile w;
-        if (!find_tile(a, x, QT * g.tpt, w, &g_tc_status)) continue;
-        it.split = rest - h * g.splits;
+        int pieces = 1, piece = 0;
+        if (g.split) {
+          const int row = 31 - __clz(__ballot_sync(0xffffffffu, lane < a.n && sp.first <= kx));
+          const int off = kx - __shfl_sync(0xffffffffu, sp.first, row);
+          pieces = __shfl_sync(0xffffffffu, sp.items, row);
+          piece = off % pieces;
+          if (!make_tile(a, row, __shfl_sync(0xffffffffu, sp.tiles, row) - 1 - off / pieces, QT * g.tpt, w, &g_tc_status)) continue;
+        } else {
+          // token-major: the last tiles of all rows first
+          const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
+          if (!find_tile(a, x, QT * g.tpt, w, &g_tc_status)) continue;
+        }
         const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
-        const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
-        it.b0 = min(bl.count, it.split * each);
+        const int each = (bl.count + pieces - 1) / pieces;
+        it.b0 = min(bl.count, piece * each);
         it.b1 = min(bl.count, it.b0 + each);
-        it.whole = each >= bl.count;
-        if (it.split > 0 && it.b0 == it.b1) continue;
+        it.whole = pieces == 1;
+        if (piece > 0 && it.b0 == it.b1) continue;
+        it.part = k;
         it.sink_blocks = bl.sink_blocks;
         it.first = bl.first;
-        it.x = x;
+        it.x = 0;
         it.row = w.row;
         it.slot = w.slot;
         it.begin = w.begin;
@@ -600,8 +663,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         to = reinterpret_cast<unsigned char*>(static_cast<T*>(a.o) + (int64_t)(it.begin + it.t0 + tk) * a.o_st +
                                               (int64_t)it.row * a.o_sn + ((int64_t)it.gh * per + it.h0 + hd) * a.d);
       } else if (mine) {
-        const int64_t unit = ((int64_t)it.x * (a.G * g.hgroups) + it.gh * g.hgroups + it.h0 / R) * g.splits + it.split;
-        float* part = a.ws + (unit * (QT * R) + t * R + r) * (D + 4);
+        float* part = a.ws + ((int64_t)it.part * (QT * R) + t * R + r) * (D + 4);
         *reinterpret_cast<float2*>(part) = make_float2(m * a.scale_log2, l);   // (the same LIFT in every part)
         to = reinterpret_cast<unsigned char*>(part + 4);
       }
@@ -671,15 +733,18 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcArgs g)
   pdl_wait_primary();
   Tile w;
   if (!find_tile(a, blockIdx.x, QT * g.tpt, w, &g_tc_status)) return;
+  Split sp;
+  plan_split(g, QT * g.tpt, sp, nullptr);
+  const int row_items = __shfl_sync(0xffffffffu, sp.items, w.row), heads = min(g.hpt, per - h0);
+  if (row_items == 1) return;
   const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
-  const int each = max(MIN_BLOCKS, (bl.count + g.splits - 1) / g.splits);
-  if (each >= bl.count) return;
-  const int parts = (bl.count + each - 1) / each, heads = min(g.hpt, per - h0);
-  const int64_t unit = ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * g.splits;
+  const int each = (bl.count + row_items - 1) / row_items, parts = bl.count > 0 ? (bl.count + each - 1) / each : 1;
+  const int first = __shfl_sync(0xffffffffu, sp.first, w.row) +
+                    (__shfl_sync(0xffffffffu, sp.tiles, w.row) - 1 - w.t0 / (QT * g.tpt)) * row_items;
+  const int64_t item = (int64_t)first * gridDim.y + blockIdx.y, next = (int64_t)gridDim.y * QT * R * (D + 4);
   for (int e = 8 * blockIdx.z + (threadIdx.x >> 5); e < w.nt * heads; e += 8 * gridDim.z) {
     const int t = e / heads, h = e - t * heads, tile = t / g.tpt;
-    const float* part = a.ws + (unit * (QT * R) + tile * R + (t - tile * g.tpt) * g.hpt + h) * (D + 4);
-    const int64_t next = (int64_t)QT * R * (D + 4);
+    const float* part = a.ws + (item * (QT * R) + tile * R + (t - tile * g.tpt) * g.hpt + h) * (D + 4);
     float top = -INFINITY;
     for (int k = lane; k < parts; k += 32) top = fmaxf(top, part[k * next]);
 #pragma unroll
@@ -724,7 +789,7 @@ cudaError_t go(const TcArgs& g, int grid, cudaStream_t s) {
   }
   tc_kernel<T, D><<<grid, Cfg<D>::THREADS, Cfg<D>::BYTES, s>>>(g);
   e = cudaGetLastError();
-  if (e != cudaSuccess || g.splits == 1) return e;
+  if (e != cudaSuccess || !g.split) return e;
   cudaLaunchConfig_t c{};
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -778,12 +843,11 @@ AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms) {
   const int64_t tiles = tiles_of(n, T, packed, qt * p.tpt);
   p.tiles = (int32_t)tiles;
   const int64_t units = tiles * G * p.hgroups;
-  // Splits for two items an SM, where there are fewer.
-  int64_t s = units > 0 ? (2 * (int64_t)sms + units - 1) / units : 1;
-  p.splits = (int32_t)(s > 32 ? 32 : s);
-  const int64_t total = units * p.splits;
-  p.grid = (int32_t)(total < sms ? total : sms);
-  p.ws_bytes = p.splits > 1 ? total * p.rows * (int64_t)(width_of(d) + 4) * 4 : 0;
+  // Split where there are fewer than two tiles and heads for an SM.
+  const bool split = units < 2 * (int64_t)sms && n <= SPLIT_ROWS;
+  p.splits = split ? 2 : 1;
+  p.grid = (int32_t)(split || units > sms ? sms : units);
+  p.ws_bytes = split ? (ITEMS_A_CTA * (int64_t)sms + units) * p.rows * (int64_t)(width_of(d) + 4) * 4 : 0;
   return p;
 }
 
@@ -795,8 +859,9 @@ cudaError_t launch_tc(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStrea
   g.tpt = p.tpt;
   g.hgroups = p.hgroups;
   g.tiles = p.tiles;
-  g.splits = p.splits;
-  g.total = p.tiles * a.G * p.hgroups * p.splits;
+  g.split = p.splits > 1;
+  g.ctas = p.grid;
+  g.total = p.tiles * a.G * p.hgroups;
   g.per_row = a.starts ? 0 : p.tiles / a.n;
   g.wait_ns = WAIT_LIMIT_NS;
   if (const char* e = getenv("DL_TEST_WAIT_MS")) {

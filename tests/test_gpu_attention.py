@@ -288,4 +288,17 @@ def test_wrong_slots_lengths_and_pages_are_reported(at):
         at.attend(q, k, v, bad, lengths, slots, starts=s.dev([0, 1, 2]))
         with pytest.raises(DeltaLogError, match="page"):
             at.sync()
+    for what, value, word in (("slots", 99, "slot"), ("slots", -1, "slot"), ("lengths", -5, "tokens"),
+                              ("lengths", s.max_pages * 16 + 1, "tokens")):
+        more = dict(lengths=lengths, slots=slots)
+        bad = more[what].clone()
+        bad[0 if what == "slots" else s.slots[1]] = value
+        for x in (q, q.float()):                            # on the tensor cores, and not
+            at.attend(x, k.to(x.dtype), v.to(x.dtype), table, **{**more, what: bad}, starts=s.dev([0, 1, 2]))
+            with pytest.raises(DeltaLogError, match=word):
+                at.sync()
+    # starts that go backwards or past the tokens are held to them
+    for starts in ([0, 5, 2], [-7, 1, 1 << 30], [2, 0, 1]):
+        at.attend(q, k, v, table, lengths, slots, starts=s.dev(starts))
+        torch.cuda.synchronize()
     at.sync()
