@@ -20,7 +20,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["replay_prep.cu", "append_decode.cu", "append_fused_ne8.cu", "append_fused_ne16.cu",
               "append_fused_ne32.cu", "eager_step.cu", "slot_ops.cu", "prefill.cu", "prefill_tc.cu", "capi.cu",
               "noalloc.cu", "mixer_capi.cu", "conv.cu", "ssm_scan.cu", "ssm_tc.cu", "ssm_step.cu", "norms.cu",
-              "attn_capi.cu", "attn_pages.cu", "attn_simt.cu",
+              "attn_capi.cu", "attn_pages.cu", "attn_simt.cu", "attn_simt_step.cu",
               "attn_step.cu", "attn_tc.cu"]
 CPP_SOURCES = ["slot_table.cpp"]
 

@@ -69,11 +69,18 @@ struct AttnPlan {
   int32_t rows, tpt, hgroups, tiles, splits, grid;
   int64_t ws_bytes;
 };
-// The general kernel: every type, head dimension, stride and alignment.
+// Prompts of every type, head dimension, stride and alignment.
 AttnPlan simt_plan(int n, int T, bool packed, int H, int G, int d, int sms);
 cudaError_t launch_simt(int dtype, bool vec, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
-// One token a row (T = 1, not packed).
+cudaError_t launch_simt_join(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
+
+// One token a row (T = 1, not packed), any type and layout.
+AttnPlan simt_step_plan(int n, int H, int G, int d, int sms);
+cudaError_t launch_simt_step(int dtype, bool vec, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
+cudaError_t read_simt_step_status(cudaStream_t s, int32_t* code);
+
+// The same for 16-bit types and aligned tensors, on the tensor cores.
 bool step_fits(int dtype, bool vec, const AttnArgs& a);
 AttnPlan step_plan(int n, int H, int G, int d, int sms);
 cudaError_t launch_step(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);

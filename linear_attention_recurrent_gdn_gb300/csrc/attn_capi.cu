@@ -124,7 +124,7 @@ AttnArgs attn_args(const dl_attend_args& q) {
 }
 
 // Which kernel a call runs in, and its workspace.
-enum class Kernel { SIMT, STEP, TC };
+enum class Kernel { SIMT, SIMT_STEP, STEP, TC };
 struct Choice {
   Kernel kernel;
   bool vec;
@@ -134,9 +134,14 @@ Choice choose(const dl_attend_args& q, const AttnArgs& a) {
   Choice c{};
   const int64_t per = 16 / elem(q.dtype);
   c.vec = q.d % 8 == 0 && view_vec(q.q, per) && view_vec(q.o, per) && pool_vec(q.k_pages, per) && pool_vec(q.v_pages, per);
-  if (q.T == 1 && !q.packed && !q.tokens && step_fits((int)q.dtype, c.vec, a)) {
-    c.kernel = Kernel::STEP;
-    c.plan = step_plan(a.n, a.H, a.G, a.d, num_sms());
+  if (q.T == 1 && !q.packed && !q.tokens) {
+    if (step_fits((int)q.dtype, c.vec, a)) {
+      c.kernel = Kernel::STEP;
+      c.plan = step_plan(a.n, a.H, a.G, a.d, num_sms());
+    } else {
+      c.kernel = Kernel::SIMT_STEP;
+      c.plan = simt_step_plan(a.n, a.H, a.G, a.d, num_sms());
+    }
     return c;
   }
   if (tc_fits((int)q.dtype, c.vec, a)) {
@@ -171,6 +176,7 @@ dl_status attend(const dl_attend_args* p, void* stream, const ErrOut& fail, bool
     return fail(DL_EINVAL, "the workspace needs %lld bytes, 16-byte aligned (dl_attend_workspace)", (long long)c.plan.ws_bytes);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (c.kernel == Kernel::STEP) return done(fail, launch_step((int)q.dtype, a, c.plan, st));
+  if (c.kernel == Kernel::SIMT_STEP) return done(fail, launch_simt_step((int)q.dtype, c.vec, a, c.plan, st));
   if (c.kernel == Kernel::TC) return done(fail, launch_tc((int)q.dtype, a, c.plan, st));
   return done(fail, launch_simt((int)q.dtype, c.vec, a, c.plan, st));
 }
@@ -242,7 +248,7 @@ extern "C" dl_status dl_attend_sync(void* stream, int32_t* device_code, char* er
   const ErrOut fail(errbuf, errlen);
   int32_t code = 0;
   cudaError_t e = cudaSuccess;
-  for (const auto read : {read_pages_status, read_simt_status, read_step_status, read_tc_status}) {
+  for (const auto read : {read_pages_status, read_simt_status, read_simt_step_status, read_step_status, read_tc_status}) {
     int32_t c = 0;
     e = read(static_cast<cudaStream_t>(stream), &c);
     if (e != cudaSuccess) break;

@@ -311,8 +311,9 @@ __global__ void __launch_bounds__(AT_T) append_kernel(const AppendArgs a) {
 
 }  // namespace
 
-// Up to this many entries the block that sums over the rows writes the maps itself.
-constexpr int64_t FILL_ONE = 4096;
+// Up to this many entries the block that sums over the rows writes the maps itself.  256 rows, with the truncate that
+// follows: 2048 entries 7.5 us, 8.0 in two launches; 4096 entries 8.8 and 7.9.
+constexpr int64_t FILL_ONE = 2048;
 
 cudaError_t launch_extend(const PagesArgs& a, int sms, cudaStream_t s) {
   if (a.size <= FILL_ONE) {

@@ -829,9 +829,14 @@ int tiles_a_cta(int d) { return d > 128 ? 1 : 2; }
 
 }  // namespace
 
+// 16-bit types, tensors that tensor maps can describe (16-byte aligned, strides above zero and below 2^40 bytes), and
+// items that are counted in 32 bits.
 bool tc_fits(int dtype, bool vec, const AttnArgs& a) {
-  const int64_t tiles = tiles_of(a.n, a.T, a.starts != nullptr, 1);   // units are counted in 32 bits
-  return dtype != mx::T_F32 && vec && tiles * a.H < 0x7fffffff / 32;
+  auto ok = [](int64_t stride, int64_t extent) { return extent == 1 || (stride > 0 && stride < (int64_t)1 << 39); };
+  for (const PoolView& v : {a.kp, a.vp})
+    if (!ok(v.st, 2) || !ok(v.sg, a.G) || !ok(v.sp, a.num_pages)) return false;
+  const int64_t tiles = tiles_of(a.n, a.T, a.starts != nullptr, 1);
+  return dtype != mx::T_F32 && vec && ok(a.q_st, a.T) && ok(a.q_sn, a.starts ? 1 : a.n) && tiles * a.H < 0x7fffffff / 32;
 }
 
 AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms) {
@@ -872,14 +877,15 @@ cudaError_t launch_tc(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStrea
   g.test_stall = stall && atoi(stall) == 1;
   const cuuint64_t d = (cuuint64_t)a.d;
   const cuuint64_t qdims[5] = {d, (cuuint64_t)per, (cuuint64_t)a.G, (cuuint64_t)a.T, (cuuint64_t)(a.starts ? 1 : a.n)};
-  const cuuint64_t qst[4] = {2 * d, 2 * d * per, (cuuint64_t)a.q_st * 2, (cuuint64_t)(a.starts || a.n == 1 ? a.q_st : a.q_sn) * 2};
+  const auto bytes = [](int64_t stride, int64_t extent) { return (cuuint64_t)(extent == 1 ? 16 : 2 * stride); };   // (any, of one)
+  const cuuint64_t qst[4] = {2 * d, 2 * d * per, bytes(a.q_st, a.T), bytes(a.q_sn, a.starts ? 1 : a.n)};
   const cuuint32_t qbox[5] = {64, (cuuint32_t)g.hpt, 1, (cuuint32_t)g.tpt, 1};
   const cuuint32_t pbox[4] = {64, (cuuint32_t)(page < BK ? page : BK), 1, 1};
   bool ok = encode(&g.mq, dtype, 5, const_cast<void*>(a.q), qdims, qst, qbox);
   for (int k = 0; k < 2; ++k) {
     const PoolView& v = k ? a.vp : a.kp;
     const cuuint64_t dims[4] = {d, (cuuint64_t)page, (cuuint64_t)a.G, (cuuint64_t)a.num_pages};
-    const cuuint64_t st[3] = {(cuuint64_t)v.st * 2, (cuuint64_t)v.sg * 2, (cuuint64_t)v.sp * 2};
+    const cuuint64_t st[3] = {bytes(v.st, 2), bytes(v.sg, a.G), bytes(v.sp, a.num_pages)};
     ok = ok && encode(k ? &g.mv : &g.mk, dtype, 4, v.p, dims, st, pbox);
   }
   if (!ok) return cudaErrorInvalidValue;

@@ -180,6 +180,33 @@ def test_a_wait_that_runs_out_is_reported(at, monkeypatch):
     at.sync()
 
 
+@pytest.mark.parametrize("what", ["queries", "rows", "heads", "pages"])
+def test_expanded_inputs(at, what):
+    """Inputs whose entries share their memory are read like any others."""
+    s = Setup([16, 16], 2, 64, 16, "bf16", seed=2, spare=0)
+    k, v, table, lengths, slots = s.args()
+    q, host = s.queries((3, 2), 4)
+    if what == "queries":
+        q, host = q[:1].expand(3, -1, -1, -1), host[:1].expand(3, -1, -1, -1)
+    elif what == "rows":
+        q, host = q[:, :1].expand(-1, 2, -1, -1), host[:, :1].expand(-1, 2, -1, -1)
+    elif what == "heads":
+        k, v = k[:, :1].expand(-1, 2, -1, -1), v[:, :1].expand(-1, 2, -1, -1)
+        s.k, s.v = ([x[:, :1].expand(-1, 2, -1) for x in t] for t in (s.k, s.v))
+    else:
+        page = s.table[s.slots[0]][0]
+        k, v = (t[page:page + 1].expand(2, -1, -1, -1) for t in (k, v))
+        s.k, s.v = ([t[0], t[0]] for t in (s.k, s.v))
+    o = at.attend(q, k, v, table, lengths, slots)
+    last = at.attend_step(q[2], k, v, table, lengths, slots)
+    at.sync()
+    for i in range(2):
+        ref, mag, big = model.attend_row(host[:, i], s.k[i], s.v[i], torch.arange(13, 16))
+        tol = bound(ref, mag, big, s.dt, 64, 16)
+        check(o[:, i], ref, tol)
+        check(last[i:i + 1], ref[2:], tol[2:])
+
+
 @pytest.mark.parametrize("kind", ["step", "attend", "simt"])
 def test_offsets_past_32_bits(at, kind):
     """A slot's pages at both ends of pools of more than 2^31 elements."""
