@@ -10,22 +10,34 @@
 //
 // Per block the products of a tile take about as long as its softmax, and they wait for one another: S of a block for
 // its products, P for the softmax.  So a tile has two places for S, and S of the next block is there when the softmax
-// of this one ends; the products always have another chain's to do.  A CTA has two tiles of one item for D <= 128 (for
-// D = 256 one, whose O takes half of TMEM): they use the same keys, 256 rows a block that is read from L2.
+// of this one ends (blocks of 128 keys in one place each took 1.4 times as long).  A CTA has two tiles of one item for D
+// <= 128 (for D = 256 one, whose O takes half of TMEM): they use the same keys, 256 rows a block that is read from L2.
 //
-// Roles: warp 0 copies (queries and pages, tensor copies into the 128-byte swizzle), warp 1 issues Q K^T, warp 3 P V,
-// warp 2 looks blocks over that not every token of the tiles sees, the last warp finds the next items, and a warp group a tile does the
-// softmax, a row a thread.  CTAs are persistent and each role goes on to the next item by itself, so an item's end
-// overlaps the next one's beginning.  An issuing thread wants its operands in uniform registers: 80 cycles a product
-// without, more than the product takes.
+// A product that writes over P has to wait for the products that read it: products of different shapes need not run in
+// the order of their issue.
+//
+// Roles: warp 0 copies (queries and pages, tensor copies into the 128-byte swizzle), a warp a tile issues Q K^T and one
+// P V, a warp a tile looks blocks over that not every token of the tiles sees, one finds the next items, and a warp
+// group a tile does the softmax, a row a thread.  CTAs are persistent and each role goes on to the next item by itself,
+// so an item's end overlaps the next one's beginning.  The issuing warps are split because what surrounds a product
+// costs more than the product: one warp for both tiles' scores took 1850 cycles a block, now 1450 are the softmax's.
+// They are elected threads with operands in uniform registers; from a branch on the lane a product took 80 cycles.
 //
 // What a token does not see has weight zero, and zero times an infinity or a NaN is a NaN: keys that no token of the
 // item sees (behind the row's last, unwritten places) are zeroed in the copy of V, and a block some of whose tokens do
 // not see a value that is not finite is added up by the softmax threads, key by key, instead.
 //
 // Few tiles (and at most 32 rows): their keys are split into items of about the same number of blocks, of the size that
-// lets the busiest CTA finish first; the lengths are on the device, so every CTA forms that plan itself.  Parts (reference, sum, O) go to the
-// workspace and a second launch joins them in order.
+// lets the busiest CTA finish first; the lengths are on the device, so every CTA forms that plan itself.  Parts
+// (reference, sum, O) go to the workspace and a second launch joins them in order.
+//
+// Measured on a GB300, bf16, 32 heads of 128 over 8: one prompt of 8192 tokens 355 us (1.55 PFLOP/s, 0.80 of a library
+// product of the same type), of 2048 55 us, 16 of 512 52 us; pieces of 371 tokens in all behind 30000 153 us; 16 heads
+// of 256 over 2, 8192 tokens 441 us; 40 heads of 64 under a window of 1000 435 us (0.53 PFLOP/s).  Bound by the softmax
+// warps' latency: with two of them a scheduler it issues half of the time, the tensor cores are busy 59% and the
+// exponentials' units 30% of it.  Measured and left: four softmax groups with half a row a thread (the two have to
+// agree on every reference; 1.1 to 1.5 times as long), S kept in registers for the maximum (spills), the reference
+// folded into one multiply-add (2%, but a score of 2^24 or more loses its differences), tiles half a period apart.
 #include <cmath>
 #include <cstdlib>
 
