@@ -73,7 +73,7 @@ constexpr int MIN_BLOCKS = 8;              // blocks that an item is worth
 constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 32, ITEM_COST = 10;
 
 template <int D> struct Cfg {
-  static constexpr int QT = D == 256 ? 1 : 2, CH = 2 * QT, STAGES = D == 256 ? 2 : 4;   // tiles, chains
+  static constexpr int QT = D == 256 ? 1 : 2, STAGES = D == 256 ? 2 : 4;   // tiles; a tile has two chains of blocks
   static constexpr int THREADS = 512;
   static constexpr uint32_t QBLK = R * 128, KBLK = BK * 128;            // 64 columns of a tile, of a block
   static constexpr uint32_t QTILE = QBLK * (D / 64), KTILE = KBLK * (D / 64);
@@ -236,7 +236,7 @@ template <class T, int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_constant__ TcArgs g) {
   extern __shared__ __align__(1024) unsigned char sm[];
   using C = Cfg<D>;
-  constexpr int QT = C::QT, CH = C::CH, ST = C::STAGES;
+  constexpr int QT = C::QT, ST = C::STAGES;
   const AttnArgs& a = g.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = (int)uniform(tid >> 5);
   const uint32_t sb = smem_u32(sm);
@@ -252,8 +252,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   if (warp == 0) tc::tmem_alloc(sb + C::TSLOT, 512);
   if (tid == 32) {
     for (int k = 0; k < C::BARS; ++k) {
-      const int n = k >= C::PREADY && k < C::PREADY + 4 ? 4 : k >= C::IEMPTY && k < C::IEMPTY + ITEMS ? 1 + 7 * QT : (k >= C::KEMPTY && k < C::KEMPTY + 4) || (k >= C::VEMPTY && k < C::VEMPTY + 4) || (k >= C::VOK && k < C::VOK + 4) ? QT : 1;
-      mbar_init(bar(k), n);
+      auto of = [&](int first) { return k >= first && k < first + 4; };
+      // a tile's four softmax warps; everyone who reads an item; a warp a tile
+      mbar_init(bar(k), of(C::PREADY) ? 4 : of(C::IEMPTY) ? 1 + 7 * QT : of(C::KEMPTY) || of(C::VEMPTY) || of(C::VOK) ? QT : 1);
     }
     fence_mbar_init();
   }
@@ -357,8 +358,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           }
         }
       }
-      if (!ok && lane == 0) {
-        // what is on its way lands before the memory is given back: the last copy into each place
+      if (lane == 0) {
+        // what is on its way lands before the memory is given back (other roles may have given up waiting for it): the
+        // last copy into each place
         for (int t = 0; t < QT; ++t)
           if (filled) mbar_drain(bar(C::QFULL + t), (filled - 1) & 1u);
         for (uint32_t k = 0; k < ST && k < blocks; ++k) {
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           }
         }
       }
-      if (!ok && elect()) {                // products on their way end before the memory is given back
+      if (elect()) {                       // products on their way end before the memory is given back
         tc::mma_commit(bar(C::DRAIN + t));
         mbar_drain(bar(C::DRAIN + t), 0);
       }
@@ -442,7 +444,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           }
         }
       }
-      if (!ok && elect()) {
+      if (elect()) {
         tc::mma_commit(bar(C::DRAIN + 2 + t));
         mbar_drain(bar(C::DRAIN + 2 + t), 0);
       }

@@ -180,6 +180,27 @@ def test_a_wait_that_runs_out_is_reported(at, monkeypatch):
     at.sync()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_calls_behind_an_unread_report_end(at, monkeypatch, d):
+    """Waits end early once one has run out; every role still ends its copies and products before its CTA leaves."""
+    s = Setup([700, 90, 1], 2, d, 32, "bf16", seed=d)
+    q, host = s.queries((120,), 8)
+    run = lambda: at.attend(q, *s.args(), starts=s.dev([0, 70, 119, 120]))  # noqa: E731
+    run()
+    at.sync()
+    monkeypatch.setenv("DL_TEST_STALL", "1")
+    monkeypatch.setenv("DL_TEST_WAIT_MS", "20")
+    run()
+    monkeypatch.delenv("DL_TEST_STALL")
+    monkeypatch.delenv("DL_TEST_WAIT_MS")
+    for _ in range(20):
+        run()
+    with pytest.raises(Exception, match="status 5"):
+        at.sync()
+    check_rows(s, host, run().cpu(), [70, 49, 1], [0, 70, 119], None, 0)
+    at.sync()
+
+
 @pytest.mark.parametrize("what", ["queries", "rows", "heads", "pages"])
 def test_expanded_inputs(at, what):
     """Inputs whose entries share their memory are read like any others."""
