@@ -186,7 +186,8 @@ __device__ __noinline__ void by_keys(const AttnArgs& a, const unsigned char* v, 
 }
 
 // The plan of a split call, lane = row: its tiles, the items that a tile's keys make, and the items of the rows before.
-// Returns the items of a head in all.
+// Returns the items of a head in all.  Rows that have more tiles than the call may (starts that go back and forth) have
+// none here: the workspace holds the parts of g.tiles.
 struct Split {
   int tiles, items, first;
 };
@@ -203,9 +204,18 @@ __device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, Split& s, in
       count = blocks_of<BK>(a, len - t + (s.tiles - 1) * tpt, len - 1).count;
     }
   }
-  long long work = (long long)count * s.tiles;
+  long long work = (long long)count * s.tiles, tiles = s.tiles;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    work += __shfl_xor_sync(0xffffffffu, work, o);
+    tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
+  }
+  if (tiles > g.tiles) {
+    if (status && lane == 0) atomicCAS(status, 0, DEV_BAD_LENGTH);
+    s.tiles = s.first = 0;
+    s.items = 1;
+    return 0;
+  }
   // Lane k tries the size that would give (k + 1) ITEMS_A_CTA / 32 items a CTA; the CTA that gets the most sets the time.
   const long long heads = a.G * g.hgroups, want = (long long)ITEMS_A_CTA * g.ctas * (lane + 1);
   const int mine = (int)max((long long)MIN_BLOCKS, (32 * work * heads + want - 1) / want);

@@ -201,6 +201,27 @@ def test_calls_behind_an_unread_report_end(at, monkeypatch, d):
     at.sync()
 
 
+@pytest.mark.parametrize("total,reported", [(128, False), (1024, True)])
+@pytest.mark.parametrize("d", [64, 256])
+def test_starts_that_go_back_and_forth(at, d, total, reported):
+    """16 rows that claim the same tokens: 16 ceil(total / tile) tiles, where total / tile + 32 are the most of a call
+    (tiles of 128 tokens, and of 64 for heads of 256).  More are reported: the workspace has no room for their parts."""
+    rows, tile = 32, 64 if d == 256 else 128
+    assert (16 * (total // tile) > total // tile + rows) == reported
+    s = Setup([4000] * rows, 1, d, 64, "bf16", seed=d)
+    q, host = s.queries((total,), 2)
+    out = at.attend(q, *s.args(), starts=s.dev([0, total] * 16 + [0]))
+    if reported:
+        with pytest.raises(Exception, match="tokens"):
+            at.sync()
+    else:
+        at.sync()
+    starts = list(range(0, total + 1, total // rows))
+    at.attend(q, *s.args(), starts=s.dev(starts), out=out)
+    at.sync()
+    check_rows(s, host, out.cpu(), [total // rows] * rows, starts[:-1], None, 0)
+
+
 @pytest.mark.parametrize("what", ["queries", "rows", "heads", "pages"])
 def test_expanded_inputs(at, what):
     """Inputs whose entries share their memory are read like any others."""
