@@ -36,7 +36,7 @@
 // of 256 over 2, 8192 tokens 441 us; 40 heads of 64 under a window of 1000 435 us (0.53 PFLOP/s).  Bound by the softmax
 // warps' latency: with two of them a scheduler it issues half of the time, the tensor cores are busy 59% and the
 // exponentials' units 30% of it.  Measured and left: four softmax groups with half a row a thread (the two have to
-// agree on every reference; 1.1 to 1.5 times as long), S kept in registers for the maximum (spills), the reference
+// agree on every reference; 1.1 to 1.5 times as long), the reference
 // folded into one multiply-add (2%, but a score of 2^24 or more loses its differences), tiles half a period apart.
 #include <cmath>
 #include <cstdlib>
@@ -75,6 +75,10 @@ constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 32, ITEM_COST = 10;
 template <int D> struct Cfg {
   static constexpr int QT = D == 256 ? 1 : 2, STAGES = D == 256 ? 2 : 4;   // tiles; a tile has two chains of blocks
   static constexpr int THREADS = 512;
+  // Registers of a thread that is not, and that is, of the softmax; a block is launched with LAUNCH_REGS each.  A block's
+  // 64 scores and its weights stay in registers that way: 16 x 512 tokens 49.5 us, 53.5 read in halves with 128 for all.
+  static constexpr int AUX_REGS = QT == 2 ? 72 : 96, ROW_REGS = QT == 2 ? 184 : 224, LAUNCH_REGS = 128;
+  static_assert((THREADS - 128 * QT) * AUX_REGS + 128 * QT * ROW_REGS <= THREADS * LAUNCH_REGS, "what the block has");
   static constexpr uint32_t QBLK = R * 128, KBLK = BK * 128;            // 64 columns of a tile, of a block
   static constexpr uint32_t QTILE = QBLK * (D / 64), KTILE = KBLK * (D / 64);
   static constexpr uint32_t Q = 0, K = QT * QTILE, V = K + STAGES * KTILE, MISC = V + STAGES * KTILE;
@@ -119,7 +123,7 @@ __device__ __forceinline__ bool elect() {
   return p != 0;
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t par, unsigned long long ns) {
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t par, unsigned long long ns) {
   return mbar_wait(bar, par, &g_tc_waits, DEV_TIMEOUT_MMA, ns);
 }
 
@@ -145,7 +149,7 @@ template <> constexpr float LIMIT<__half> = 0x1p15f;
 // O += P V for a block with values that are not finite, key by key; a row takes the keys that it sees.  P is in TMEM at
 // p_col, O at o_col (first: not yet anything).
 template <class T, int D>
-__device__ __noinline__ void by_keys(const AttnArgs& a, const unsigned char* v, uint32_t p_col, uint32_t o_col, int pos,
+__device__ __forceinline__ void by_keys(const AttnArgs& a, const unsigned char* v, uint32_t p_col, uint32_t o_col, int pos,
                                      int j0, bool first) {
   using C = Cfg<D>;
 #pragma unroll 1
@@ -299,6 +303,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
 
   constexpr int SW = 4 + 4 * QT;           // the first warp behind those of the softmax
   if (warp < 4 || warp >= SW) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::AUX_REGS));
     if (warp == 0) {
       // ---- copies.  Pages are looked up for 32 pages at a time, a batch ahead.
       uint32_t no = 0, blocks = 0, filled = 0;
@@ -557,6 +562,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
     }
   } else {
     // ---- softmax: thread = row of tile t; QT = 1: of the only tile
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::ROW_REGS));
     const int t = (warp >> 2) - 1, q4 = warp & 3, r = 32 * q4 + lane, per = a.H / a.G;
     const uint32_t tl = tm + ((uint32_t)(32 * q4) << 16), o_col = tl + C::O_COL + t * D;
     const int tok = r / g.hpt, hd = r - tok * g.hpt;
@@ -586,25 +592,25 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           for (int c = 0; c < BK / 32; ++c)
             seen[c] = bits_to(hi - 32 * c) & (~bits_to(lo - 32 * c) | bits_to(sk - 1 - 32 * c));
         }
-        auto hide = [&](uint32_t (&s)[32], int c) {
-          if (!part) return;
+        uint32_t s[BK / 32][32], p[BK / 2];
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (!(seen[c] >> k & 1u)) s[k] = 0xff800000u;
-        };
-        uint32_t p[BK / 2];
+        for (int c = 0; c < BK / 32; ++c) tc::tmem_ld32(s_col + 32 * c, s[c]);
+#pragma unroll
+        for (int c = 0; c < BK / 32; ++c) tc::tmem_wait_ld(s[c]);
+        if (part)
+#pragma unroll
+          for (int c = 0; c < BK / 32; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!(seen[c] >> k & 1u)) s[c][k] = 0xff800000u;
         bool lift = __any_sync(0xffffffffu, mine && m == -INFINITY);     // nothing seen so far
         for (bool again = false;; again = true) {
           if (lift) {                    // a new reference: the row's maximum so far
             float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < BK / 32; ++c) {
-              uint32_t s[32];
-              tc::tmem_ld32(s_col + 32 * c, s);
-              tc::tmem_wait_ld(s);
-              hide(s, c);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[k]));
+              for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], __uint_as_float(s[c][k]));
             }
             const float was = m;
             m = fmaxf(was, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
@@ -629,15 +635,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
           f2 sum[2] = {mk2(0.f, 0.f), mk2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < BK / 32; ++c) {
-            uint32_t s[32];
-            tc::tmem_ld32(s_col + 32 * c, s);
-            tc::tmem_wait_ld(s);
-            hide(s, c);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               float x, y;
               // differences first: scores as large as the type goes keep theirs
-              un2(fma2(add2(mk2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1])), base2), scale2, lift2), x, y);
+              un2(fma2(add2(mk2(__uint_as_float(s[c][2 * k]), __uint_as_float(s[c][2 * k + 1])), base2), scale2, lift2), x, y);
               x = ex2_f(x);
               y = ex2_f(y);
               sum[k & 1] = add2(sum[k & 1], mk2(x, y));
@@ -809,6 +811,10 @@ cudaError_t go(const TcArgs& g, int grid, cudaStream_t s) {
   if (ready != dev) {
     e = cudaFuncSetAttribute(tc_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D>::BYTES);
     if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, tc_kernel<T, D>);
+    if (e != cudaSuccess) return e;
+    if ((fa.numRegs + 7) / 8 * 8 < Cfg<D>::LAUNCH_REGS) return cudaErrorInvalidConfiguration;   // the softmax would wait for its share
     ready = dev;
   }
   tc_kernel<T, D><<<grid, Cfg<D>::THREADS, Cfg<D>::BYTES, s>>>(g);
