@@ -28,8 +28,9 @@
 // not see a value that is not finite is added up by the softmax threads, key by key, instead.
 //
 // Few tiles (and at most 32 rows): their keys are split into items of about the same number of blocks, of the size that
-// lets the busiest CTA finish first; the lengths are on the device, so every CTA forms that plan itself.  Parts
-// (reference, sum, O) go to the workspace and a second launch joins them in order.
+// lets the busiest CTA finish first; the lengths are on the device, so every CTA forms that plan itself and the first
+// leaves it for the second launch, which joins the parts (reference, sum, O in the workspace) in order.  A plan formed
+// again by each of the join's blocks cost 5 to 20 us a call (32 rows of 4 tokens behind 8192: 63 us, now 45).
 //
 // Measured on a GB300, bf16, 32 heads of 128 over 8: one prompt of 8192 tokens 355 us (1.55 PFLOP/s, 0.80 of a library
 // product of the same type), of 2048 55 us, 16 of 512 52 us; pieces of 371 tokens in all behind 30000 153 us; 16 heads
@@ -71,6 +72,7 @@ constexpr int MIN_BLOCKS = 8;              // blocks that an item is worth
 // A split call has at most ITEMS_A_CTA items a CTA and one a tile more, and at most SPLIT_ROWS rows (a lane each).  An
 // item's start, its end and its part in the join cost about as much as ITEM_COST blocks.
 constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 32, ITEM_COST = 10;
+constexpr int PLAN = 4 * SPLIT_ROWS;       // words of the plan, before the parts in the workspace
 
 template <int D> struct Cfg {
   static constexpr int QT = D == 256 ? 1 : 2, STAGES = D == 256 ? 2 : 4;   // tiles; a tile has two chains of blocks
@@ -189,7 +191,7 @@ __device__ __forceinline__ void by_keys(const AttnArgs& a, const unsigned char* 
   tc::tmem_wait_st();
 }
 
-// The plan of a split call, lane = row: its tiles, the items that a tile's keys make, and the items of the rows before.
+// The plan of a split call, lane = row (SPLIT_ROWS): its tiles, the items of each, and the items of the rows before.
 // Returns the items of a head in all.  Rows that have more tiles than the call may (starts that go back and forth) have
 // none here: the workspace holds the parts of g.tiles.
 struct Split {
@@ -221,20 +223,21 @@ __device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, Split& s, in
     return 0;
   }
   // Lane k tries the size that would give (k + 1) ITEMS_A_CTA / 32 items a CTA; the CTA that gets the most sets the time.
-  const long long heads = a.G * g.hgroups, want = (long long)ITEMS_A_CTA * g.ctas * (lane + 1);
+  const long long heads = (long long)a.G * g.hgroups, want = (long long)ITEMS_A_CTA * g.ctas * (lane + 1);
   const int mine = (int)max((long long)MIN_BLOCKS, (32 * work * heads + want - 1) / want);
-  long long items = 0;
-  int most = 0;
+  // (an estimate: what is chosen is counted in integers below, and other CTAs choose the same)
+  const float inv = 1.f / (float)mine;
+  float items = 0.f, most = 0.f;
   for (int i = 0; i < a.n; ++i) {
-    const int c = __shfl_sync(0xffffffffu, count, i), t = __shfl_sync(0xffffffffu, s.tiles, i);
-    const int p = c > mine ? (c + mine - 1) / mine : 1;
-    items += (long long)t * p;
-    if (t > 0) most = max(most, (c + p - 1) / p);
+    const float c = (float)__shfl_sync(0xffffffffu, count, i), t = (float)__shfl_sync(0xffffffffu, s.tiles, i);
+    const float p = fmaxf(1.f, ceilf(fmaf(c, inv, -1e-3f)));
+    items = fmaf(t, p, items);
+    if (t > 0.f) most = fmaxf(most, ceilf(__fdividef(c, p) - 1e-3f));
   }
-  long long best = (((items * heads + g.ctas - 1) / g.ctas * (most + ITEM_COST)) << 5) | lane;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) best = min(best, (long long)__shfl_xor_sync(0xffffffffu, best, o));
-  const int each = __shfl_sync(0xffffffffu, mine, (int)(best & 31));
+  const uint32_t cost = __float_as_uint(ceilf(items * (float)heads / (float)g.ctas - 1e-3f) * (most + (float)ITEM_COST));
+  const uint32_t least = __reduce_min_sync(0xffffffffu, cost);          // (positive: ordered like its bits)
+  const int best = __ffs(__ballot_sync(0xffffffffu, cost == least)) - 1;
+  const int each = __shfl_sync(0xffffffffu, mine, best);
   s.items = count > each ? (count + each - 1) / each : 1;
   int run = s.tiles * s.items;
 #pragma unroll
@@ -479,6 +482,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
       Item it{};
       Split sp{};
       const int total = g.split ? plan_split(g, QT * g.tpt, sp, &g_tc_status) * heads : g.total;
+      if (g.split && blockIdx.x == 0)      // for the join
+        reinterpret_cast<int4*>(a.ws)[lane] = make_int4(sp.tiles, sp.items, sp.first, 0);
       for (int k = blockIdx.x; k < total && ok; k += gridDim.x) {
         const int kx = k / heads, h = k - kx * heads;
         Tile w;
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         to = reinterpret_cast<unsigned char*>(static_cast<T*>(a.o) + (int64_t)(it.begin + it.t0 + tk) * a.o_st +
                                               (int64_t)it.row * a.o_sn + ((int64_t)it.gh * per + it.h0 + hd) * a.d);
       } else if (mine) {
-        float* part = a.ws + ((int64_t)it.part * (QT * R) + t * R + r) * (D + 4);
+        float* part = a.ws + PLAN + ((int64_t)it.part * (QT * R) + t * R + r) * (D + 4);
         *reinterpret_cast<float2*>(part) = make_float2(m * a.scale_log2, l);   // (the same LIFT in every part)
         to = reinterpret_cast<unsigned char*>(part + 4);
       }
@@ -749,28 +754,33 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
   }
 }
 
-// The parts of split items, in order: a warp a row, block (tile, head, part of the rows).
+// The parts of split items.  Block (tile, head, part of the rows): a warp a row, its parts in order; or, where that is
+// less to do one after the other (few rows, many parts), all warps a row, parts in turns and their sums in order: 4
+// tokens of 8 heads over one behind 131072 take 41 us, 106 with a warp a row.
+constexpr int JOIN_WARPS = 8;
 template <class T, int D>
-__global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcArgs g) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) tc_join(const __grid_constant__ TcArgs g) {
   using C = Cfg<D>;
   constexpr int QT = C::QT, V = D / 32 < 4 ? D / 32 : 4, P = D / 32 / V;     // columns of a lane: P pieces of V
+  __shared__ float o_of[JOIN_WARPS][D], l_of[JOIN_WARPS];
   const AttnArgs& a = g.a;
-  const int lane = threadIdx.x & 31, per = a.H / a.G, gh = blockIdx.y / g.hgroups, h0 = (blockIdx.y % g.hgroups) * R;
-  pdl_wait_primary();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = a.H / a.G, gh = blockIdx.y / g.hgroups;
+  const int h0 = (blockIdx.y % g.hgroups) * R;
   Tile w;
-  if (!find_tile(a, blockIdx.x, QT * g.tpt, w, &g_tc_status)) return;
-  Split sp;
-  plan_split(g, QT * g.tpt, sp, nullptr);
-  const int row_items = __shfl_sync(0xffffffffu, sp.items, w.row), heads = min(g.hpt, per - h0);
-  if (row_items == 1) return;
+  const bool tile = find_tile(a, blockIdx.x, QT * g.tpt, w, &g_tc_status);   // (what it reads was there before the first launch)
+  pdl_wait_primary();                   // (also by blocks without work: this launch must not end before the first)
+  if (!tile) return;
+  const int4 plan = reinterpret_cast<const int4*>(a.ws)[w.row];              // tiles, items of each, items before
+  if (plan.y == 1) return;
   const Blocks bl = blocks_of<BK>(a, w.pos0, w.pos0 + w.nt - 1);
-  const int each = (bl.count + row_items - 1) / row_items, parts = bl.count > 0 ? (bl.count + each - 1) / each : 1;
-  const int first = __shfl_sync(0xffffffffu, sp.first, w.row) +
-                    (__shfl_sync(0xffffffffu, sp.tiles, w.row) - 1 - w.t0 / (QT * g.tpt)) * row_items;
+  const int each = (bl.count + plan.y - 1) / plan.y, parts = bl.count > 0 ? (bl.count + each - 1) / each : 1;
+  const int first = plan.z + (plan.x - 1 - w.t0 / (QT * g.tpt)) * plan.y;
   const int64_t item = (int64_t)first * gridDim.y + blockIdx.y, next = (int64_t)gridDim.y * QT * R * (D + 4);
-  for (int e = 8 * blockIdx.z + (threadIdx.x >> 5); e < w.nt * heads; e += 8 * gridDim.z) {
-    const int t = e / heads, h = e - t * heads, tile = t / g.tpt;
-    const float* part = a.ws + (item * (QT * R) + tile * R + (t - tile * g.tpt) * g.hpt + h) * (D + 4);
+  const int heads = min(g.hpt, per - h0), rows = w.nt * heads, z = gridDim.z;
+  const bool share = (rows + z - 1) / z * (parts / JOIN_WARPS + 4) < (rows + JOIN_WARPS * z - 1) / (JOIN_WARPS * z) * parts;
+  for (int e = share ? blockIdx.z : JOIN_WARPS * blockIdx.z + warp; e < rows; e += share ? z : JOIN_WARPS * z) {
+    const int t = e / heads, h = e - t * heads, sub = t / g.tpt;
+    const float* part = a.ws + PLAN + (item * (QT * R) + sub * R + (t - sub * g.tpt) * g.hpt + h) * (D + 4);
     float top = -INFINITY;
     for (int k = lane; k < parts; k += 32) top = fmaxf(top, part[k * next]);
 #pragma unroll
@@ -781,22 +791,47 @@ __global__ void __launch_bounds__(256) tc_join(const __grid_constant__ TcArgs g)
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int v = 0; v < V; ++v) o[p][v] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float* q = part + k * next;
+    auto add = [&](const float* q) {
       const float f = q[1] == 0.f ? 0.f : ex2_f(q[0] - base);
       l = fmaf(q[1], f, l);
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int v = 0; v < V; ++v) o[p][v] = fmaf(q[4 + (32 * p + lane) * V + v], f, o[p][v]);
+    };
+    if (share) {
+#pragma unroll 4
+      for (int k = warp; k < parts; k += JOIN_WARPS) add(part + k * next);
+    } else {
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) add(part + k * next);
     }
-    T* out = static_cast<T*>(a.o) + (int64_t)(w.begin + w.t0 + t) * a.o_st + (int64_t)w.row * a.o_sn + ((int64_t)gh * per + h0 + h) * a.d;
+    if (share) {
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+      for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if ((32 * p + lane) * V + v < a.d) out[(32 * p + lane) * V + v] = from_f<T>(l == 0.f ? 0.f : o[p][v] / l);
+        for (int v = 0; v < V; ++v) o_of[warp][(32 * p + lane) * V + v] = o[p][v];
+      if (lane == 0) l_of[warp] = l;
+      __syncthreads();
+      if (warp == 0) {
+        for (int x = 1; x < JOIN_WARPS; ++x) {
+          l += l_of[x];
+#pragma unroll
+          for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[p][v] += o_of[x][(32 * p + lane) * V + v];
+        }
+      }
+    }
+    if (!share || warp == 0) {
+      T* out = static_cast<T*>(a.o) + (int64_t)(w.begin + w.t0 + t) * a.o_st + (int64_t)w.row * a.o_sn + ((int64_t)gh * per + h0 + h) * a.d;
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if ((32 * p + lane) * V + v < a.d) out[(32 * p + lane) * V + v] = from_f<T>(l == 0.f ? 0.f : o[p][v] / l);
+    }
+    if (share) __syncthreads();         // the sums are read
   }
 }
 
@@ -824,8 +859,9 @@ cudaError_t go(const TcArgs& g, int grid, cudaStream_t s) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  c.gridDim = dim3((unsigned)g.tiles, (unsigned)(g.a.G * g.hgroups), 8);
-  c.blockDim = dim3(256);
+  const int heads = g.a.G * g.hgroups, z = 8 * g.ctas / (g.tiles * heads);        // some eight blocks an SM
+  c.gridDim = dim3((unsigned)g.tiles, (unsigned)heads, (unsigned)(z < 4 ? 4 : z > 32 ? 32 : z));
+  c.blockDim = dim3(32 * JOIN_WARPS);
   c.stream = s;
   c.attrs = &at;
   c.numAttrs = 1;
@@ -882,7 +918,7 @@ AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms) {
   const bool split = units < 2 * (int64_t)sms && n <= SPLIT_ROWS;
   p.splits = split ? 2 : 1;
   p.grid = (int32_t)(split || units > sms ? sms : units);
-  p.ws_bytes = split ? (ITEMS_A_CTA * (int64_t)sms + units) * p.rows * (int64_t)(width_of(d) + 4) * 4 : 0;
+  p.ws_bytes = split ? 4 * (PLAN + (ITEMS_A_CTA * (int64_t)sms + units) * p.rows * (width_of(d) + 4)) : 0;
   return p;
 }
 

@@ -302,3 +302,17 @@ def test_wrong_slots_lengths_and_pages_are_reported(at):
         at.attend(q, k, v, table, lengths, slots, starts=s.dev(starts))
         torch.cuda.synchronize()
     at.sync()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("after,tokens,H,G", [([20000], [4], 8, 1), ([9000, 37, 1, 6000], [3, 2, 1, 5], 6, 2),
+                                              ([30000, 12000], [1, 70], 4, 2)])
+def test_few_tokens_behind_many_keys(at, d, after, tokens, H, G):
+    """Keys split over all SMs: many parts of few rows to join, beside rows with one."""
+    s = Setup(after, G, d, 64, "bf16", seed=d + len(after))
+    starts = _starts(tokens)
+    q, host = s.queries((sum(tokens),), H)
+    out = at.attend(q, *s.args(), starts=s.dev(starts))
+    check_rows(s, host, out.cpu(), tokens, starts[:-1], None, 0)
+    assert torch.equal(out, at.attend(q, *s.args(), starts=s.dev(starts)))
+    at.sync()
