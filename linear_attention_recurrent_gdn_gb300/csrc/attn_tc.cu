@@ -27,10 +27,10 @@
 // item sees (behind the row's last, unwritten places) are zeroed in the copy of V, and a block some of whose tokens do
 // not see a value that is not finite is added up by the softmax threads, key by key, instead.
 //
-// Few tiles (and at most 32 rows): their keys are split into items of about the same number of blocks, of the size that
+// Few tiles (and at most 64 rows): their keys are split into items of about the same number of blocks, of the size that
 // lets the busiest CTA finish first; the lengths are on the device, so every CTA forms that plan itself and the first
 // leaves it for the second launch, which joins the parts (reference, sum, O in the workspace) in order.  A plan formed
-// again by each of the join's blocks cost 5 to 20 us a call (32 rows of 4 tokens behind 8192: 63 us, now 45).
+// again by each of the join's blocks cost 5 to 20 us a call (32 rows of 4 tokens behind 8192: 63 us, now 42).
 //
 // Measured on a GB300, bf16, 32 heads of 128 over 8: one prompt of 8192 tokens 355 us (1.55 PFLOP/s, 0.80 of a library
 // product of the same type), of 2048 55 us, 16 of 512 52 us; pieces of 371 tokens in all behind 30000 153 us; 16 heads
@@ -69,9 +69,10 @@ constexpr int R = 128;                     // rows of a tile
 constexpr int ITEMS = 4;                   // items that are found ahead
 constexpr int BK = 64;                     // keys of a block
 constexpr int MIN_BLOCKS = 8;              // blocks that an item is worth
-// A split call has at most ITEMS_A_CTA items a CTA and one a tile more, and at most SPLIT_ROWS rows (a lane each).  An
-// item's start, its end and its part in the join cost about as much as ITEM_COST blocks.
-constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 32, ITEM_COST = 10;
+// A split call has at most ITEMS_A_CTA items a CTA and one a tile more, and at most SPLIT_ROWS rows: 64 of up to 40
+// tokens behind 2000 take 39 us split, 55 whole (and 15.5, 14.5 behind none); 100 of 2 behind 4096 44 and 53, but 100 of
+// 4 behind 200 21.7 and 17.9.  An item's start, its end and its part in the join cost about as much as ITEM_COST blocks.
+constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 64, ITEM_COST = 10;
 constexpr int PLAN = 4 * SPLIT_ROWS;       // words of the plan, before the parts in the workspace
 
 template <int D> struct Cfg {
@@ -90,7 +91,8 @@ template <int D> struct Cfg {
          IFULL = 36, IEMPTY = 40, DRAIN = 44, NEVER = 48, BARS = 49 };
   static constexpr uint32_t BAR = MISC, FLAGS = BAR + 8 * (BARS + 1), TSLOT = FLAGS + 32, ITEM = TSLOT + 16;
   static constexpr uint32_t OUT = (ITEM + ITEMS * 64 + 127) & ~127u;    // 32 rows of 128 bytes of every softmax warp
-  static constexpr uint32_t BYTES = OUT + 4 * QT * 4096;
+  static constexpr uint32_t ROWS = OUT + 4 * QT * 4096, BYTES = ROWS + 8 * SPLIT_ROWS;          // the plan of a split call
+  static_assert(BYTES <= 232448, "of a CTA");
 };
 
 struct Item {
@@ -191,62 +193,92 @@ __device__ __forceinline__ void by_keys(const AttnArgs& a, const unsigned char* 
   tc::tmem_wait_st();
 }
 
-// The plan of a split call, lane = row (SPLIT_ROWS): its tiles, the items of each, and the items of the rows before.
-// Returns the items of a head in all.  Rows that have more tiles than the call may (starts that go back and forth) have
-// none here: the workspace holds the parts of g.tiles.
-struct Split {
-  int tiles, items, first;
-};
-__device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, Split& s, int32_t* status) {
+// The plan of a split call: of every row the blocks that its last tile's keys make (x), its tiles (the low half of y) and
+// the items of a head of the rows before (the high half; less than 2^10 in all).  One warp; a tile has items_of items of
+// `each` blocks at most.  Returns the items of a head.  Rows that have more tiles than the call may (starts that go back
+// and forth) have none here: the workspace holds the parts of g.tiles.
+__device__ __forceinline__ int items_of(int count, int each) { return count > each ? (count + each - 1) / each : 1; }
+__device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, uint2* rows, int& each, int32_t* status) {
   const AttnArgs& a = g.a;
   const int lane = threadIdx.x & 31;
-  int count = 0;
-  s.tiles = 0;
-  if (lane < a.n) {
-    int begin, slot;
-    const int t = row_tokens(a, lane, begin), len = row_length(a, lane, slot, status);
-    if (len >= 0 && t > 0) {
-      s.tiles = (t + tpt - 1) / tpt;
-      count = blocks_of<BK>(a, len - t + (s.tiles - 1) * tpt, len - 1).count;
-    }
+  long long work = 0, tiles = 0;
+  // every load before what is made of it
+  int t[SPLIT_ROWS / 32], slot[SPLIT_ROWS / 32], len[SPLIT_ROWS / 32];
+#pragma unroll
+  for (int k = 0; k < SPLIT_ROWS / 32; ++k) {
+    const int i = lane + 32 * k;
+    int begin;
+    slot[k] = i < a.n ? a.slots[i] : 0;
+    t[k] = i < a.n ? row_tokens(a, i, begin) : 0;
   }
-  long long work = (long long)count * s.tiles, tiles = s.tiles;
+  auto there = [&](int k) { return (unsigned)slot[k] < (unsigned)a.num_slots; };
+#pragma unroll
+  for (int k = 0; k < SPLIT_ROWS / 32; ++k) len[k] = lane + 32 * k < a.n && there(k) ? a.lengths[slot[k]] : 0;
+#pragma unroll
+  for (int k = 0; k < SPLIT_ROWS / 32; ++k) {
+    if (lane + 32 * k >= a.n) break;
+    const int cap = a.max_pages << a.page_shift, n = min(max(len[k], 0), cap);      // (as in row_length)
+    if (!there(k)) atomicCAS(status, 0, DEV_BAD_SLOT);
+    else if (n != len[k]) atomicCAS(status, 0, DEV_BAD_LENGTH);
+    int count = 0, own = 0;
+    if (there(k) && t[k] > 0) {
+      own = (t[k] + tpt - 1) / tpt;
+      count = blocks_of<BK>(a, n - t[k] + (own - 1) * tpt, n - 1).count;
+    }
+    rows[lane + 32 * k] = make_uint2((uint32_t)count, (uint32_t)own);
+    work += (long long)count * own;
+    tiles += own;
+  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     work += __shfl_xor_sync(0xffffffffu, work, o);
     tiles += __shfl_xor_sync(0xffffffffu, tiles, o);
   }
+  each = 0x7fffffff;
   if (tiles > g.tiles) {
-    if (status && lane == 0) atomicCAS(status, 0, DEV_BAD_LENGTH);
-    s.tiles = s.first = 0;
-    s.items = 1;
+    if (lane == 0) atomicCAS(status, 0, DEV_BAD_LENGTH);
+    for (int i = lane; i < a.n; i += 32) rows[i] = make_uint2(0, 0);
+    __syncwarp();
     return 0;
   }
-  // Lane k tries the size that would give (k + 1) ITEMS_A_CTA / 32 items a CTA; the CTA that gets the most sets the time.
-  const long long heads = (long long)a.G * g.hgroups, want = (long long)ITEMS_A_CTA * g.ctas * (lane + 1);
-  const int mine = (int)max((long long)MIN_BLOCKS, (32 * work * heads + want - 1) / want);
-  // (an estimate: what is chosen is counted in integers below, and other CTAs choose the same)
+  // `sizes` lanes try the sizes that would give 1 / sizes, 2 / sizes ... ITEMS_A_CTA items a CTA, more than
+  // 32 rows with half as many and half of the rows each; the CTA that gets the most sets the time.  (An estimate: what is
+  // chosen is counted in integers below, and other CTAs choose the same.)
+  static_assert(SPLIT_ROWS <= 64, "groups of rows");
+  const int groups = a.n <= 32 ? 1 : 2, sizes = 32 / groups;
+  const long long heads = (long long)a.G * g.hgroups, want = (long long)ITEMS_A_CTA * g.ctas * (lane % sizes + 1);
+  const int mine = (int)max((long long)MIN_BLOCKS, (sizes * work * heads + want - 1) / want);
   const float inv = 1.f / (float)mine;
   float items = 0.f, most = 0.f;
-  for (int i = 0; i < a.n; ++i) {
-    const float c = (float)__shfl_sync(0xffffffffu, count, i), t = (float)__shfl_sync(0xffffffffu, s.tiles, i);
-    const float p = fmaxf(1.f, ceilf(fmaf(c, inv, -1e-3f)));
-    items = fmaf(t, p, items);
-    if (t > 0.f) most = fmaxf(most, ceilf(__fdividef(c, p) - 1e-3f));
+  __syncwarp();
+  for (int i = lane / sizes; i < a.n; i += groups) {
+    const uint2 row = rows[i];
+    const float c = (float)row.x, p = fmaxf(1.f, ceilf(fmaf(c, inv, -1e-3f)));
+    items = fmaf((float)row.y, p, items);
+    most = fmaxf(most, ceilf(__fdividef(c, p) - 1e-3f));
   }
-  const uint32_t cost = __float_as_uint(ceilf(items * (float)heads / (float)g.ctas - 1e-3f) * (most + (float)ITEM_COST));
+  for (int o = sizes; o < 32; o <<= 1) {
+    items += __shfl_xor_sync(0xffffffffu, items, o);
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  }
+  const uint32_t cost = __float_as_uint(fabsf(ceilf(items * (float)heads / (float)g.ctas - 1e-3f)) * (most + (float)ITEM_COST));
   const uint32_t least = __reduce_min_sync(0xffffffffu, cost);          // (positive: ordered like its bits)
-  const int best = __ffs(__ballot_sync(0xffffffffu, cost == least)) - 1;
-  const int each = __shfl_sync(0xffffffffu, mine, best);
-  s.items = count > each ? (count + each - 1) / each : 1;
-  int run = s.tiles * s.items;
+  each = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, cost == least)) - 1);
+  int before = 0;
+  for (int i0 = 0; i0 < a.n; i0 += 32) {
+    const uint2 row = i0 + lane < a.n ? rows[i0 + lane] : make_uint2(0, 0);
+    const int own = (int)row.y * items_of((int)row.x, each);
+    int run = own;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += v;
+    }
+    if (i0 + lane < a.n) rows[i0 + lane].y = row.y | (uint32_t)(before + run - own) << 16;
+    before += __shfl_sync(0xffffffffu, run, 31);
   }
-  s.first = run - s.tiles * s.items;
-  return __shfl_sync(0xffffffffu, run, 31);
+  __syncwarp();
+  return before;
 }
 
 template <class T, int D>
@@ -480,20 +512,32 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
         ++no;
       };
       Item it{};
-      Split sp{};
-      const int total = g.split ? plan_split(g, QT * g.tpt, sp, &g_tc_status) * heads : g.total;
-      if (g.split && blockIdx.x == 0)      // for the join
-        reinterpret_cast<int4*>(a.ws)[lane] = make_int4(sp.tiles, sp.items, sp.first, 0);
+      uint2* const rows = reinterpret_cast<uint2*>(sm + C::ROWS);
+      int total = g.total, most = 0;       // most: blocks of an item
+      if (g.split) {
+        total = plan_split(g, QT * g.tpt, rows, most, &g_tc_status) * heads;
+        if (blockIdx.x == 0)               // for the join: tiles, items of each, items before
+          for (int i = lane; i < a.n; i += 32) {
+            const uint2 v = rows[i];
+            reinterpret_cast<int4*>(a.ws)[i] = make_int4(v.y & 0xffff, items_of((int)v.x, most), v.y >> 16, 0);
+          }
+      }
       for (int k = blockIdx.x; k < total && ok; k += gridDim.x) {
         const int kx = k / heads, h = k - kx * heads;
         Tile w;
         int pieces = 1, piece = 0;
         if (g.split) {
-          const int row = 31 - __clz(__ballot_sync(0xffffffffu, lane < a.n && sp.first <= kx));
-          const int off = kx - __shfl_sync(0xffffffffu, sp.first, row);
-          pieces = __shfl_sync(0xffffffffu, sp.items, row);
+          int row = 0;                     // the last that starts at or before item kx
+          for (int i0 = 0; i0 < a.n; i0 += 32) {
+            const uint32_t m = __ballot_sync(0xffffffffu, i0 + lane < a.n && (int)(rows[min(i0 + lane, a.n - 1)].y >> 16) <= kx);
+            if (m == 0) break;
+            row = i0 + 31 - __clz(m);
+          }
+          const uint2 v = rows[row];
+          const int off = kx - (int)(v.y >> 16);
+          pieces = items_of((int)v.x, most);
           piece = off % pieces;
-          if (!make_tile(a, row, __shfl_sync(0xffffffffu, sp.tiles, row) - 1 - off / pieces, QT * g.tpt, w, &g_tc_status)) continue;
+          if (!make_tile(a, row, (int)(v.y & 0xffff) - 1 - off / pieces, QT * g.tpt, w, &g_tc_status)) continue;
         } else {
           // token-major: the last tiles of all rows first
           const int x = g.per_row ? (kx % a.n) * g.per_row + g.per_row - 1 - kx / a.n : g.tiles - 1 - kx;
@@ -756,13 +800,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) tc_kernel(const __grid_con
 
 // The parts of split items.  Block (tile, head, part of the rows): a warp a row, its parts in order; or, where that is
 // less to do one after the other (few rows, many parts), all warps a row, parts in turns and their sums in order: 4
-// tokens of 8 heads over one behind 131072 take 41 us, 106 with a warp a row.
+// tokens of 8 heads over one behind 131072 take 33 us, 106 with a warp a row.
 constexpr int JOIN_WARPS = 8;
 template <class T, int D>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) tc_join(const __grid_constant__ TcArgs g) {
   using C = Cfg<D>;
-  constexpr int QT = C::QT, V = D / 32 < 4 ? D / 32 : 4, P = D / 32 / V;     // columns of a lane: P pieces of V
-  __shared__ float o_of[JOIN_WARPS][D], l_of[JOIN_WARPS];
+  constexpr int QT = C::QT, V = D / 32 < 4 ? 2 : 4, P = D / 32 / V;     // columns of a lane: P pieces of V
+  __shared__ float o_of[JOIN_WARPS][D];
+  __shared__ float2 ml_of[JOIN_WARPS];
   const AttnArgs& a = g.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, per = a.H / a.G, gh = blockIdx.y / g.hgroups;
   const int h0 = (blockIdx.y % g.hgroups) * R;
@@ -781,45 +826,77 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) tc_join(const __grid_constant
   for (int e = share ? blockIdx.z : JOIN_WARPS * blockIdx.z + warp; e < rows; e += share ? z : JOIN_WARPS * z) {
     const int t = e / heads, h = e - t * heads, sub = t / g.tpt;
     const float* part = a.ws + PLAN + (item * (QT * R) + sub * R + (t - sub * g.tpt) * g.hpt + h) * (D + 4);
-    float top = -INFINITY;
-    for (int k = lane; k < parts; k += 32) top = fmaxf(top, part[k * next]);
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    const float base = held(top);
-    float l = 0.f, o[P][V];
+    float m = -INFINITY, l = 0.f, o[P][V];
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
       for (int v = 0; v < V; ++v) o[p][v] = 0.f;
-    auto add = [&](const float* q) {
-      const float f = q[1] == 0.f ? 0.f : ex2_f(q[0] - base);
-      l = fmaf(q[1], f, l);
+    // four parts at a time: all of their loads, then the sums against the largest reference so far
+    const int by = share ? JOIN_WARPS : 1;
+    for (int k0 = share ? warp : 0; k0 < parts; k0 += 4 * by) {
+      float2 ml[4];
+      float x[4][P][V];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = k0 + u * by < parts;
+        const float* q = part + (in ? k0 + u * by : 0) * next;
+        ml[u] = *reinterpret_cast<const float2*>(q);
+        if (!in) ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          const float* from = q + 4 + (32 * p + lane) * V;
+          if constexpr (V == 4) {
+            const float4 w4 = *reinterpret_cast<const float4*>(from);
+            x[u][p][0] = w4.x, x[u][p][1] = w4.y, x[u][p][2] = w4.z, x[u][p][3] = w4.w;
+          } else {
+            const float2 w2 = *reinterpret_cast<const float2*>(from);
+            x[u][p][0] = w2.x, x[u][p][1] = w2.y;
+          }
+        }
+      }
+      const float was = m;
+      m = fmaxf(fmaxf(m, fmaxf(ml[0].x, ml[1].x)), fmaxf(ml[2].x, ml[3].x));
+      const float base = held(m), f0 = ex2_f(was - base);
+      l *= f0;
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[p][v] = fmaf(q[4 + (32 * p + lane) * V + v], f, o[p][v]);
-    };
-    if (share) {
-#pragma unroll 4
-      for (int k = warp; k < parts; k += JOIN_WARPS) add(part + k * next);
-    } else {
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) add(part + k * next);
+        for (int v = 0; v < V; ++v) o[p][v] *= f0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (ml[u].y == 0.f) continue;   // saw nothing
+        const float f = ex2_f(ml[u].x - base);
+        l = fmaf(ml[u].y, f, l);
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[p][v] = fmaf(x[u][p][v], f, o[p][v]);
+      }
     }
     if (share) {
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int v = 0; v < V; ++v) o_of[warp][(32 * p + lane) * V + v] = o[p][v];
-      if (lane == 0) l_of[warp] = l;
+      if (lane == 0) ml_of[warp] = make_float2(m, l);
       __syncthreads();
       if (warp == 0) {
+        float top = m;
+        for (int x = 1; x < JOIN_WARPS; ++x) top = fmaxf(top, ml_of[x].x);
+        const float base = held(top), f0 = ex2_f(m - base);
+        l *= f0;
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[p][v] *= f0;
         for (int x = 1; x < JOIN_WARPS; ++x) {
-          l += l_of[x];
+          if (ml_of[x].y == 0.f) continue;
+          const float f = ex2_f(ml_of[x].x - base);
+          l = fmaf(ml_of[x].y, f, l);
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[p][v] += o_of[x][(32 * p + lane) * V + v];
+            for (int v = 0; v < V; ++v) o[p][v] = fmaf(o_of[x][(32 * p + lane) * V + v], f, o[p][v]);
         }
       }
     }
@@ -859,8 +936,8 @@ cudaError_t go(const TcArgs& g, int grid, cudaStream_t s) {
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  const int heads = g.a.G * g.hgroups, z = 8 * g.ctas / (g.tiles * heads);        // some eight blocks an SM
-  c.gridDim = dim3((unsigned)g.tiles, (unsigned)heads, (unsigned)(z < 4 ? 4 : z > 32 ? 32 : z));
+  const int heads = g.a.G * g.hgroups, z = 4 * g.ctas / (g.tiles * heads);        // some four blocks an SM
+  c.gridDim = dim3((unsigned)g.tiles, (unsigned)heads, (unsigned)(z < 2 ? 2 : z > 32 ? 32 : z));
   c.blockDim = dim3(32 * JOIN_WARPS);
   c.stream = s;
   c.attrs = &at;

@@ -316,3 +316,18 @@ def test_few_tokens_behind_many_keys(at, d, after, tokens, H, G):
     check_rows(s, host, out.cpu(), tokens, starts[:-1], None, 0)
     assert torch.equal(out, at.attend(q, *s.args(), starts=s.dev(starts)))
     at.sync()
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("n", [32, 33, 64, 65, 100, 128, 129])
+def test_many_rows_of_uneven_lengths(at, n, d):
+    """Few tokens a row: up to 64 rows' keys are split by one plan; some rows are empty, a few long."""
+    tokens = [(5 * i + 1) % 4 for i in range(n)]
+    after = [t + (3000 + 7 * i if i % 31 == 5 else (37 * i) % 150) for i, t in enumerate(tokens)]
+    s = Setup(after, 1, d, 64, "bf16", seed=n + d)
+    starts = _starts(tokens)
+    q, host = s.queries((sum(tokens),), 4)
+    out = at.attend(q, *s.args(), starts=s.dev(starts))
+    check_rows(s, host, out.cpu(), tokens, starts[:-1], None, 0)
+    assert torch.equal(out, at.attend(q, *s.args(), starts=s.dev(starts)))
+    at.sync()
