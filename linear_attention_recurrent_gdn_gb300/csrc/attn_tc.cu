@@ -72,11 +72,13 @@ using mx::un2;
 constexpr int R = 128;                     // rows of a tile
 constexpr int ITEMS = 4;                   // items that are found ahead
 constexpr int BK = 64;                     // keys of a block
-constexpr int MIN_BLOCKS = 8;              // blocks that an item is worth
+constexpr int MIN_BLOCKS = 4;              // blocks that an item is worth
 // A split call has at most ITEMS_A_CTA items a CTA and one a tile more, and at most SPLIT_ROWS rows: 64 of up to 40
 // tokens behind 2000 take 39 us split, 55 whole (and 15.5, 14.5 behind none); 100 of 2 behind 4096 44 and 53, but 100 of
-// 4 behind 200 21.7 and 17.9.  An item's start, its end and its part in the join cost about as much as ITEM_COST blocks.
-constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 64, ITEM_COST = 10;
+// 4 behind 200 21.7 and 17.9.  An item's start, its end and its part in the join cost about as much as ITEM_COST blocks,
+// a join at all as JOIN_COST: without that, one prompt of 1000 tokens of 16 heads over 2 was split and took 28.7 us, now
+// 22.7 (and 64 tokens of 32 heads behind 3000, split into items of 4 blocks, 23.3; 24.3 into 8).
+constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 64, ITEM_COST = 10, JOIN_COST = 14;
 constexpr int PLAN = 4 * SPLIT_ROWS;       // words of the plan, before the parts in the workspace
 
 template <int D> struct Cfg {
@@ -265,7 +267,8 @@ __device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, uint2* rows,
     items += __shfl_xor_sync(0xffffffffu, items, o);
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
-  const uint32_t cost = __float_as_uint(fabsf(ceilf(items * (float)heads / (float)g.ctas - 1e-3f)) * (most + (float)ITEM_COST));
+  const float rounds = fabsf(ceilf(items * (float)heads / (float)g.ctas - 1e-3f));
+  const uint32_t cost = __float_as_uint(rounds * (most + (float)ITEM_COST) + (items > (float)tiles + 0.5f ? (float)JOIN_COST : 0.f));
   const uint32_t least = __reduce_min_sync(0xffffffffu, cost);          // (positive: ordered like its bits)
   each = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, cost == least)) - 1);
   int before = 0;
