@@ -561,12 +561,17 @@ typedef struct dl_pool {     /* strides in elements */
  * `size` entries; T > 0: token t of row i at t * n + i, at most T a row, size =
  * T * n.  Entries without a token get -1.  If a slot is out of range or named
  * twice, a number of tokens negative or too large for the maps, a table row
- * full or the pages too few, nothing changes, starts are 0 and places -1.
- * work: [2 n + 2] int32 of scratch.
+ * full, the pages too few, or a page that a token would go to (a new one, or
+ * the last one of a row that goes on) out of range, nothing changes, starts are
+ * 0 and places -1.  work: [2 n + 2] int32 of scratch.
  *
  * dl_pages_truncate: row i's slot keeps its first tokens[i] tokens (none if
  * NULL, at most its length); pages without a kept token return to the stack,
  * in the order that undoes an extend of the same rows.  Table entries stay.
+ * If a slot is out of range or named twice, a number of tokens negative or
+ * above the slot's length, or a page that would return out of range, nothing
+ * changes.  A page belongs to one slot: one that two slots' tables name returns
+ * twice, and is then handed out twice, which no call can see.
  * starts, where, positions and work are not used. */
 typedef struct dl_pages_args {
     const int32_t *slots, *tokens;      /* [n] */

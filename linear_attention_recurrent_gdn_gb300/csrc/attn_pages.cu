@@ -8,15 +8,17 @@
 //   append    [G][d] values of a token to the place that extend gave it
 // Sums over the rows are exclusive prefix sums in one block (one row a thread), so the result depends on nothing but
 // the inputs.  Slots and lengths live on the device: everything is checked here before anything is changed, and a call
-// that cannot be done (a slot that is out of range or comes twice, no pages left, a table row that is full) changes
-// nothing, hands out no places (-1) and leaves its code in the status word.
+// that cannot be done (a slot that is out of range or comes twice, no pages left, a table row that is full, a page
+// number out of range among those it would hand out or give back) changes nothing, hands out no places (-1) and leaves
+// its code in the status word.  A page number is checked before it becomes a place: id * page_size would wrap in 32 bits.
 //
 // The tokens' places are independent of one another: each finds its row and takes its page from the old table or the
 // old stack, so a second launch over as many blocks as there is work writes them.
 //
-// Measured on a GB300: extend and truncate of 256 rows of one token 6.7 us (two
+// Measured on a GB300: extend and truncate of 256 rows of one token 7.0 us (two
 // launches of one block; their checks, sums and two trips to memory), of 64
-// prompts of up to 2048 tokens in pages of 16 10.5 us (three launches).  append of
+// prompts of up to 2048 tokens in pages of 16 11.5 us (three launches).  Without
+// the checks of page numbers 6.5 and 10.2 us.  append of
 // 16 x 512 tokens of 8 heads of 128 bf16 12.3 us (5.5 TB/s of the 6.8 of a copy;
 // 18.2 us with a place looked up before each load), of 256 tokens 2.6 us.
 #include "attn.h"
@@ -124,6 +126,11 @@ __global__ void __launch_bounds__(PT) extend_kernel(const PagesArgs a) {
     tok = a.tokens ? a.tokens[i] : 1;
   }
   const int height = a.free[0];
+  const bool stack = height >= 0 && height <= a.num_pages;
+  // The i-th page from the top and the row's half-filled one: asked for early, looked at behind the sums.
+  const int top = stack && i < height ? a.free[height - i] : 0;
+  int half = 0;
+  auto out_of_range = [&](int id) { return (unsigned)id >= (unsigned)a.num_pages; };
   if (row) {
     if (slot < 0 || slot >= a.num_slots) {
       err = DEV_BAD_SLOT;
@@ -133,6 +140,7 @@ __global__ void __launch_bounds__(PT) extend_kernel(const PagesArgs a) {
       const int cap = a.max_pages << a.page_shift;
       if (tok < 0 || old < 0 || old > cap || (a.T > 0 && tok > a.T)) err = DEV_BAD_LENGTH;
       else if (tok > cap - old) err = DEV_ROW_FULL;
+      else if (tok > 0 && (old & (page - 1))) half = a.table[(int64_t)slot * a.table_stride + (old >> a.page_shift)];
     }
     if (err) tok = 0;
   }
@@ -142,10 +150,26 @@ __global__ void __launch_bounds__(PT) extend_kernel(const PagesArgs a) {
   scan2(start, base, tokens, pages, sm);
   if (i == 0) {
     if (a.T == 0 && tokens > a.size) err = DEV_BAD_LENGTH;
-    if (height < 0 || height > a.num_pages) err = DEV_BAD_PAGE;
+    if (!stack) err = DEV_BAD_PAGE;
     else if (pages > height) err = DEV_NO_PAGES;
   }
+  if (stack && pages <= height) {
+    bool odd = i < pages && out_of_range(top);
+#pragma unroll 4
+    for (int k = i + PT; k < (int)pages; k += PT) odd |= out_of_range(a.free[height - k]);
+    if (odd) err = DEV_BAD_PAGE;
+  }
+  if (out_of_range(half)) err = DEV_BAD_PAGE;
   if (err) atomicCAS(&g_pages_status, 0, err);
+  int32_t *slots = seen, *olds = seen + PT, *bases = seen + 2 * PT, *starts = seen + 3 * PT;
+  __shared__ int32_t toks[PT];
+  if (FILL) {
+    slots[i] = slot;
+    olds[i] = old;
+    bases[i] = (int32_t)base;
+    starts[i] = row ? (int32_t)start : 0x7fffffff;
+    toks[i] = tok;
+  }
   const bool bad = __syncthreads_or(err != 0);
   if (row) {
     a.starts[i] = bad ? 0 : (int32_t)start;
@@ -166,14 +190,6 @@ __global__ void __launch_bounds__(PT) extend_kernel(const PagesArgs a) {
     }
     return;
   }
-  int32_t *slots = seen, *olds = seen + PT, *bases = seen + 2 * PT, *starts = seen + 3 * PT;
-  slots[i] = slot;
-  olds[i] = old;
-  bases[i] = (int32_t)base;
-  starts[i] = row && !bad ? (int32_t)start : 0x7fffffff;
-  __shared__ int32_t toks[PT];
-  toks[i] = tok;
-  __syncthreads();
   if (a.T > 0) {
     for (int e = i; e < (int)a.size; e += PT) {
       const int t = e / a.n, r = e - t * a.n;
@@ -227,6 +243,8 @@ __global__ void __launch_bounds__(FT) fill_kernel(const PagesArgs a) {
   }
 }
 
+// Pages that a thread gives back and keeps in registers between their check and the stack; further ones are read again.
+constexpr int BACK = 4;
 __global__ void __launch_bounds__(PT) truncate_kernel(const PagesArgs a) {
   __shared__ long long sm[64];
   __shared__ int32_t seen[4 * PT];
@@ -254,22 +272,37 @@ __global__ void __launch_bounds__(PT) truncate_kernel(const PagesArgs a) {
   scan2(none, base, zero, pages, sm);
   if (i == 0 && (height < 0 || height > a.num_pages || pages > a.num_pages - height)) err = DEV_BAD_PAGE;
   if (err) atomicCAS(&g_pages_status, 0, err);
-  if (__syncthreads_or(err != 0)) return;
-  if (row) a.lengths[slot] = keep;
-  if (i == 0) a.free[0] = height + (int32_t)pages;
   int32_t *slots = seen, *firsts = seen + PT, *bases = seen + 2 * PT;
   slots[i] = slot;
   firsts[i] = first;
   bases[i] = row ? (int32_t)base : 0x7fffffff;
-  __syncthreads();
-  for (int k = i; k < (int)pages; k += PT) {
+  if (__syncthreads_or(err != 0)) return;
+  const int most = (int)pages;
+  auto page_at = [&](int k) {          // the k-th page that goes back
     int lo = 0, hi = a.n - 1;
     while (lo < hi) {                  // the last row whose pages start at or before k
       const int mid = (lo + hi + 1) >> 1;
       if (bases[mid] <= k) lo = mid; else hi = mid - 1;
     }
-    a.free[1 + height + (int32_t)pages - 1 - k] = a.table[(int64_t)slots[lo] * a.table_stride + firsts[lo] + k - bases[lo]];
+    return a.table[(int64_t)slots[lo] * a.table_stride + firsts[lo] + k - bases[lo]];
+  };
+  int ids[BACK];
+  bool odd = false;
+#pragma unroll
+  for (int u = 0; u < BACK; ++u) {
+    ids[u] = i + u * PT < most ? page_at(i + u * PT) : 0;
+    odd |= (unsigned)ids[u] >= (unsigned)a.num_pages;
   }
+  for (int k = i + BACK * PT; k < most; k += PT) odd |= (unsigned)page_at(k) >= (unsigned)a.num_pages;
+  if (odd) atomicCAS(&g_pages_status, 0, DEV_BAD_PAGE);
+  if (__syncthreads_or(odd)) return;
+  if (row) a.lengths[slot] = keep;
+  if (i == 0) a.free[0] = height + most;
+  int32_t* const to = a.free + 1 + height + most - 1;
+#pragma unroll
+  for (int u = 0; u < BACK; ++u)
+    if (i + u * PT < most) to[-(i + u * PT)] = ids[u];
+  for (int k = i + BACK * PT; k < most; k += PT) to[-k] = page_at(k);
 }
 
 // Values of V bytes (16: vectors; else one element), [G][d] of a token in E of them.
