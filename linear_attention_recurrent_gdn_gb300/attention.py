@@ -260,7 +260,8 @@ def attend(q, k_pages, v_pages, table, lengths, slots, *, starts=None, tokens=No
            out=None):
     """Attention of the last tokens of every slot: q [T, n, H, d], or packed [total, H, d] with ``starts`` [n + 1].
 
-    tokens [n]: how many of the T tokens row i has (None: T each).  H / G
+    tokens [n]: how many of the T tokens row i has (None: T each); the slot
+    of a row that has none may be anything.  H / G
     consecutive query heads share a head of keys and values.  A token sees its
     own position and those before it; with ``window`` only the last ``window``
     of them and the row's first ``sinks``.  scale: 1 / sqrt(d) unless given.

@@ -224,8 +224,10 @@ __device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, uint2* rows,
   for (int k = 0; k < SPLIT_ROWS / 32; ++k) {
     if (lane + 32 * k >= a.n) break;
     const int cap = a.max_pages << a.page_shift, n = min(max(len[k], 0), cap);      // (as in row_length)
-    if (!there(k)) atomicCAS(status, 0, DEV_BAD_SLOT);
-    else if (n != len[k]) atomicCAS(status, 0, DEV_BAD_LENGTH);
+    if (t[k] > 0) {                       // (a row without tokens is not looked at, here as in make_tile)
+      if (!there(k)) atomicCAS(status, 0, DEV_BAD_SLOT);
+      else if (n != len[k]) atomicCAS(status, 0, DEV_BAD_LENGTH);
+    }
     int count = 0, own = 0;
     if (there(k) && t[k] > 0) {
       own = (t[k] + tpt - 1) / tpt;
