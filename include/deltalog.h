@@ -597,8 +597,9 @@ dl_status dl_kv_append(const dl_kv_append_args *args, void *stream, char *errbuf
 /* Attention of the last tokens of n slots, with their keys and values in the
  * pages already.  Row i has tokens[i] <= T of them (T each if NULL; packed:
  * starts[i + 1] - starts[i], T tokens in all), the last of its slot's
- * lengths[slot] tokens.  The slot of a row without tokens is not looked at and
- * may be anything.  The token at position p sees the keys j <= p, with a
+ * lengths[slot] tokens.  tokens[i] below zero or above T is reported, and held
+ * to that; starts are held to [0, T].  The slot of a row without tokens is not
+ * looked at and may be anything.  The token at position p sees the keys j <= p, with a
  * window (> 0) only those with j > p - window or j < sinks:
  *   o[h] = sum_j softmax_j(scale q[h] . k[j][h / (H / G)]) v[j][h / (H / G)]
  * Scores, weights and sums are fp32 and o is rounded once; on the tensor cores

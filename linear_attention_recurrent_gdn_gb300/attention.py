@@ -23,8 +23,8 @@ captured step follows them from replay to replay.  One table serves the pools
 of every layer.
 
 What the host cannot see there is checked on the device: a call that meets a
-slot, length or page out of range, or runs out of pages, does not follow it,
-and ``sync`` raises.
+slot, length, number of tokens or page out of range, or runs out of pages, does
+not follow it, and ``sync`` raises.
 
 Tokens of n rows are token-major [T, n, ...], packed [total, ...] one row after
 the other, or one a row [n, ...].

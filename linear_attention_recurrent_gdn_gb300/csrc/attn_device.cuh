@@ -29,10 +29,16 @@ struct Tile {
 // least ceil(its tokens / tpt) of them before the next row's, since floor((s + t) / p) - floor(s / p) + 1 >= ceil(t / p);
 // so a tile's row is found without sums over the rows.  One warp calls; false: the tile has no tokens.
 __device__ __forceinline__ int packed_tile0(const AttnArgs& a, int i, int tpt) { return a.starts[i] / tpt + i; }
-// The tokens of a row, and where they begin in a packed tensor.
-__device__ __forceinline__ int row_tokens(const AttnArgs& a, int row, int& begin) {
+// The tokens of a row, and where they begin in a packed tensor.  A number of tokens below zero or above T is held to
+// that and reported to *status, if that is given; starts are held to [0, T].
+__device__ __forceinline__ int row_tokens(const AttnArgs& a, int row, int& begin, int32_t* status) {
   begin = 0;
-  if (!a.starts) return a.tokens ? min(max(a.tokens[row], 0), a.T) : a.T;
+  if (!a.starts) {
+    if (!a.tokens) return a.T;
+    const int t = a.tokens[row];
+    if ((unsigned)t > (unsigned)a.T && status) atomicCAS(status, 0, DEV_BAD_LENGTH);
+    return min(max(t, 0), a.T);
+  }
   begin = min(max(a.starts[row], 0), a.T);
   return min(max(a.starts[row + 1], begin), a.T) - begin;
 }
@@ -51,11 +57,12 @@ __device__ __forceinline__ int row_length(const AttnArgs& a, int row, int& slot,
 // Tile `tile` of a row; false: it has no tokens.  (One lane reports.)
 __device__ __forceinline__ bool make_tile(const AttnArgs& a, int row, int tile, int tpt, Tile& w, int32_t* status) {
   w.row = row;
-  const int t = row_tokens(a, row, w.begin);
+  if ((threadIdx.x & 31) != 0) status = nullptr;
+  const int t = row_tokens(a, row, w.begin, status);
   if (tile < 0 || (int64_t)tile * tpt >= t) return false;
   w.t0 = tile * tpt;
   w.nt = min(tpt, t - w.t0);
-  const int len = row_length(a, row, w.slot, (threadIdx.x & 31) == 0 ? status : nullptr);
+  const int len = row_length(a, row, w.slot, status);
   if (len < 0) return false;
   w.pos0 = len - t + w.t0;             // the new tokens are the slot's last; negative positions see nothing
   return true;

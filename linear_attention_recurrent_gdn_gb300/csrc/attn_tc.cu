@@ -215,7 +215,7 @@ __device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, uint2* rows,
     const int i = lane + 32 * k;
     int begin;
     slot[k] = i < a.n ? a.slots[i] : 0;
-    t[k] = i < a.n ? row_tokens(a, i, begin) : 0;
+    t[k] = i < a.n ? row_tokens(a, i, begin, status) : 0;
   }
   auto there = [&](int k) { return (unsigned)slot[k] < (unsigned)a.num_slots; };
 #pragma unroll

@@ -4,7 +4,8 @@ import itertools
 import pytest
 import torch
 
-from attention_helpers import Setup, check_rows
+from attention_helpers import Setup, bound, check, check_rows
+from oracle import attention_model as model
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +46,27 @@ def test_rows_without_tokens_are_not_looked_at(at, layout, dtype, d, n):
         host = torch.cat([rows[:c, i] for i, c in enumerate(counts)])
     at.sync()
     check_rows(s, host, o.cpu(), counts, starts, None, 0)
+
+
+@pytest.mark.parametrize("dtype,d,n", KINDS)
+@pytest.mark.parametrize("number", [-1, -(1 << 31), 5, 0x7fffffff])
+def test_numbers_of_tokens_out_of_range_are_reported(at, number, dtype, d, n):
+    """A row with a negative number of tokens has none, one with more than T has T; both are reported."""
+    T = 4
+    s = Setup([50 + i for i in range(n)], 1, d, 16, dtype, seed=n + d)
+    q, host = s.queries((T, n), 2)
+    tokens = s.dev([T - i % 2 for i in range(n)])
+    tokens[n - 2] = number
+    out = torch.full_like(q, 7.0)
+    at.attend(q, *s.args(), tokens=tokens, out=out)
+    with pytest.raises(Exception, match="tokens"):
+        at.sync()
+    for i in range(n):
+        t = min(max(int(tokens[i]), 0), T)
+        ref, mag, big = model.attend_row(host[:t, i], s.k[i], s.v[i], torch.arange(s.after[i] - t, s.after[i]))
+        check(out[:t, i], ref, bound(ref, mag, big, s.dt, d, s.after[i]), "row %d" % i)
+        assert (out[t:, i] == 7).all()
+    for good in (0, T):
+        tokens[n - 2] = good
+        at.attend(q, *s.args(), tokens=tokens, out=out)
+        at.sync()
