@@ -612,7 +612,7 @@ dl_status dl_kv_append(const dl_kv_append_args *args, void *stream, char *errbuf
 typedef struct dl_attend_args {
     int64_t dtype, n, T, packed, H, G, d, page_size, max_pages, num_slots, num_pages, window, sinks;
     double scale;
-    dl_view q, o;                       /* a token: [H][d], contiguous */
+    dl_view q, o;                       /* a token: [H][d], contiguous; those of o share no elements */
     dl_pool k_pages, v_pages;
     const int32_t *table;
     int64_t table_stride;

@@ -265,6 +265,7 @@ def attend(q, k_pages, v_pages, table, lengths, slots, *, starts=None, tokens=No
     consecutive query heads share a head of keys and values.  A token sees its
     own position and those before it; with ``window`` only the last ``window``
     of them and the row's first ``sinks``.  scale: 1 / sqrt(d) unless given.
+    out: like q, with any strides whose tokens share no elements.
     The tokens' own keys and values have to be in the pages already."""
     return _attend(_lib.dl_attend, q, k_pages, v_pages, table, lengths, slots, starts, tokens, window, sinks, scale, out,
                    False)

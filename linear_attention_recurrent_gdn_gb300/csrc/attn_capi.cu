@@ -69,6 +69,22 @@ bool pool_vec(const dl_pool& p, int64_t per) {
 }
 bool view_vec(const dl_view& v, int64_t per) { return al(v.data, 16) && v.stride_t % per == 0 && v.stride_n % per == 0; }
 
+// Whether two tokens of an output share elements: `w` of them each, token t of row i at t * st + i * sn.  Where the longer
+// stride does not span the other dimension, every distance between rows is held against its nearest multiples of st (n
+// rows are at most AT_ROWS).
+bool tokens_share(int64_t w, int64_t T, int64_t st, int64_t n, int64_t sn) {
+  using wide = __int128;
+  const wide t = st < 0 ? -(wide)st : st, r = sn < 0 ? -(wide)sn : sn;
+  if ((T > 1 && t < w) || (n > 1 && r < w)) return true;
+  if (T <= 1 || n <= 1) return false;
+  if (t >= r ? t >= (n - 1) * r + w : r >= (T - 1) * t + w) return false;
+  for (int64_t i = 1; i < n; ++i) {
+    const wide x = i * r, m = x / t;
+    if ((m < T && x - m * t < w) || (m + 1 < T && (m + 1) * t - x < w)) return true;
+  }
+  return false;
+}
+
 dl_status head_sizes(const ErrOut& fail, int64_t dtype, int64_t G, int64_t d) {
   if (bad_type(dtype)) return fail(DL_EINVAL, "unknown dtype %lld", (long long)dtype);
   if (G < 1 || G > 4096) return fail(DL_EINVAL, "%lld heads of keys", (long long)G);
@@ -167,6 +183,8 @@ dl_status attend(const dl_attend_args* p, void* stream, const ErrOut& fail, bool
     if (!t) return fail(DL_EINVAL, "NULL tensor pointer");
     if (!al(t, e)) return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
   }
+  if (tokens_share(q.H * q.d, q.T, q.o.stride_t, q.packed ? 1 : q.n, q.packed ? 0 : q.o.stride_n))
+    return fail(DL_EINVAL, "out: tokens share elements (strides %lld and %lld)", (long long)q.o.stride_t, (long long)q.o.stride_n);
   if (!q.table || !q.lengths || !q.slots) return fail(DL_EINVAL, "NULL tensor pointer");
   if (!words({q.table, q.lengths, q.slots, q.starts, q.tokens}))
     return fail(DL_EINVAL, "misaligned tensor: every tensor needs its element's alignment");
