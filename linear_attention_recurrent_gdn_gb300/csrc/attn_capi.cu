@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <limits>
 
 #include <cuda_runtime.h>
 
@@ -134,7 +135,9 @@ AttnArgs attn_args(const dl_attend_args& q) {
   a.num_pages = (int32_t)q.num_pages;
   a.window = (int32_t)(q.window < MAX_DIM ? q.window : MAX_DIM);   // positions are below 2^30: as far as any
   a.sinks = (int32_t)q.sinks;
-  a.scale_log2 = (float)(q.scale * 1.4426950408889634);
+  // Not zero: the prompts' kernel scales behind the mask, and a masked score of -inf times zero would be a NaN.  The
+  // smallest number moves no finite score by more than 2^-21.
+  a.scale_log2 = std::fmax((float)(q.scale * 1.4426950408889634), std::numeric_limits<float>::denorm_min());
   a.ws = static_cast<float*>(q.workspace);
   return a;
 }
