@@ -982,13 +982,14 @@ int tiles_a_cta(int d) { return d > 128 ? 1 : 2; }
 }  // namespace
 
 // 16-bit types, tensors that tensor maps can describe (16-byte aligned, strides above zero and below 2^40 bytes), and
-// items that are counted in 32 bits.
+// items that are counted in 32 bits, a step of the grid behind the last one included.
 bool tc_fits(int dtype, bool vec, const AttnArgs& a) {
   auto ok = [](int64_t stride, int64_t extent) { return extent == 1 || (stride > 0 && stride < (int64_t)1 << 39); };
   for (const PoolView& v : {a.kp, a.vp})
     if (!ok(v.st, 2) || !ok(v.sg, a.G) || !ok(v.sp, a.num_pages)) return false;
-  const int64_t tiles = tiles_of(a.n, a.T, a.starts != nullptr, 1);
-  return dtype != mx::T_F32 && vec && ok(a.q_st, a.T) && ok(a.q_sn, a.starts ? 1 : a.n) && tiles * a.H < 0x7fffffff / 32;
+  const int per = a.H / a.G, tpt = tiles_a_cta(a.d) * (R / (per < R ? per : R));
+  const int64_t items = tiles_of(a.n, a.T, a.starts != nullptr, tpt) * a.G * ((per + R - 1) / R);
+  return dtype != mx::T_F32 && vec && ok(a.q_st, a.T) && ok(a.q_sn, a.starts ? 1 : a.n) && items < 0x7fffffff - (1 << 16);
 }
 
 AttnPlan tc_plan(int n, int T, bool packed, int H, int G, int d, int sms) {
