@@ -76,9 +76,12 @@ constexpr int MIN_BLOCKS = 4;              // blocks that an item is worth
 // A split call has at most ITEMS_A_CTA items a CTA and one a tile more, and at most SPLIT_ROWS rows: 64 of up to 40
 // tokens behind 2000 take 39 us split, 55 whole (and 15.5, 14.5 behind none); 100 of 2 behind 4096 44 and 53, but 100 of
 // 4 behind 200 21.7 and 17.9.  An item's start, its end and its part in the join cost about as much as ITEM_COST blocks,
-// a join at all as JOIN_COST: without that, one prompt of 1000 tokens of 16 heads over 2 was split and took 28.7 us, now
-// 22.7 (and 64 tokens of 32 heads behind 3000, split into items of 4 blocks, 23.3; 24.3 into 8).
-constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 64, ITEM_COST = 10, JOIN_COST = 14;
+// a join as JOIN_COST and one for every JOIN_PARTS parts of full tiles (half of that for heads of 64), JOIN_MOST at most.
+// 4 tokens of 32 heads over 8 behind 300 keys take 14.8 us whole, 17.2 split; behind 1000 21.8 and 18.3; 64 tokens behind
+// 300 16.3 and 19.9, behind 1000 23.3 and 21.1; one prompt of 1000 tokens of 16 heads over 2 22.7 and 28.7.  (And 64
+// tokens of 32 heads behind 3000, split into items of 4 blocks, 23.3; 24.3 into 8.)
+constexpr int ITEMS_A_CTA = 4, SPLIT_ROWS = 64, ITEM_COST = 10;
+constexpr float JOIN_COST = 4.f, JOIN_PARTS = 14.f, JOIN_MOST = 16.f;
 constexpr int PLAN = 4 * SPLIT_ROWS;       // words of the plan, before the parts in the workspace
 
 template <int D> struct Cfg {
@@ -112,6 +115,7 @@ struct TcArgs {
   CUtensorMap mq, mk, mv;
   AttnArgs a;
   int32_t tpt, hpt, hgroups, tiles, split, total, per_row, ctas;   // per_row: tiles of a row (token-major), else 0
+  float join;                          // what a part costs in the join, in blocks
   int32_t test_stall;                  // test only: see below
   unsigned long long wait_ns;
 };
@@ -249,13 +253,14 @@ __device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, uint2* rows,
     __syncwarp();
     return 0;
   }
-  // `sizes` lanes try the sizes that would give 1 / sizes, 2 / sizes ... ITEMS_A_CTA items a CTA, more than
-  // 32 rows with half as many and half of the rows each; the CTA that gets the most sets the time.  (An estimate: what is
-  // chosen is counted in integers below, and other CTAs choose the same.)
+  // The first lane tries whole tiles, the others of `sizes` lanes the sizes that would give 2, 3 ... sizes parts in
+  // `sizes` of ITEMS_A_CTA items a CTA, more than 32 rows with half as many sizes and half of the rows each; the CTA that
+  // gets the most sets the time.  (An estimate: what is chosen is counted in integers below, and other CTAs choose the
+  // same.)  Without whole tiles among them short calls were split whatever that cost.
   static_assert(SPLIT_ROWS <= 64, "groups of rows");
   const int groups = a.n <= 32 ? 1 : 2, sizes = 32 / groups;
   const long long heads = (long long)a.G * g.hgroups, want = (long long)ITEMS_A_CTA * g.ctas * (lane % sizes + 1);
-  const int mine = (int)max((long long)MIN_BLOCKS, (sizes * work * heads + want - 1) / want);
+  const int mine = lane % sizes == 0 ? 0x7fffffff : (int)max((long long)MIN_BLOCKS, (sizes * work * heads + want - 1) / want);
   const float inv = 1.f / (float)mine;
   float items = 0.f, most = 0.f;
   __syncwarp();
@@ -270,7 +275,8 @@ __device__ __forceinline__ int plan_split(const TcArgs& g, int tpt, uint2* rows,
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   }
   const float rounds = fabsf(ceilf(items * (float)heads / (float)g.ctas - 1e-3f));
-  const uint32_t cost = __float_as_uint(rounds * (most + (float)ITEM_COST) + (items > (float)tiles + 0.5f ? (float)JOIN_COST : 0.f));
+  const float join = items > (float)tiles + 0.5f ? JOIN_COST + fminf(items * (float)heads * g.join, JOIN_MOST) : 0.f;
+  const uint32_t cost = __float_as_uint(rounds * (most + (float)ITEM_COST) + join);
   const uint32_t least = __reduce_min_sync(0xffffffffu, cost);          // (positive: ordered like its bits)
   each = __shfl_sync(0xffffffffu, mine, __ffs(__ballot_sync(0xffffffffu, cost == least)) - 1);
   int before = 0;
@@ -1021,6 +1027,9 @@ cudaError_t launch_tc(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStrea
   g.ctas = p.grid;
   g.total = p.tiles * a.G * p.hgroups;
   g.per_row = a.starts ? 0 : p.tiles / a.n;
+  // (tiles as full as those of rows of the average length)
+  const float fill = (float)a.T / ((float)(a.starts ? a.n : 1) * (float)(tiles_a_cta(a.d) * p.tpt));
+  g.join = (a.d <= 64 ? 0.5f : 1.f) * (fill < 1.f ? fill : 1.f) / JOIN_PARTS;
   g.wait_ns = WAIT_LIMIT_NS;
   if (const char* e = getenv("DL_TEST_WAIT_MS")) {
     const long ms = atol(e);

@@ -1,8 +1,8 @@
-"""Which kernel a call of prompts takes, where only a report tells."""
+"""Which kernel a call of prompts takes, and whether its keys are split, where only the result's bits or a report tell."""
 import pytest
 import torch
 
-from attention_helpers import Setup, bound, check
+from attention_helpers import Setup, bound, check, check_rows
 from oracle import attention_model as model
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +38,31 @@ def test_many_tokens_and_heads_run_on_the_tensor_cores(at, monkeypatch):
     with pytest.raises(Exception, match="status 5"):
         at.sync()
     at.sync()
+
+
+@pytest.mark.parametrize("tokens,before,H,G,d", [(4, 300, 32, 8, 128), (16, 300, 16, 2, 128), (64, 300, 32, 8, 128), (4, 300, 8, 1, 64),
+                                                 (300, 0, 8, 1, 64)])
+def test_short_calls_stay_whole(at, tokens, before, H, G, d):
+    """Where a join costs more than it gives, a row's bits are those it has among 70 rows, whose keys are never split."""
+    s = Setup([tokens + before], G, d, 64, "bf16", seed=tokens + d)
+    k, v, table, lengths, slots = s.args()
+    q, host = s.queries((tokens,), H)
+    one = at.attend(q, k, v, table, lengths, slots, starts=s.dev([0, tokens]))
+    many = at.attend(q.repeat(70, 1, 1), k, v, table, lengths, slots.repeat(70), starts=s.dev([tokens * i for i in range(71)]))
+    at.sync()
+    check_rows(s, host, one.cpu(), [tokens], [0], None, 0)
+    assert torch.equal(one, many[:tokens]) and torch.equal(one, many[-tokens:])
+
+
+@pytest.mark.parametrize("keys", [1000, 20000])
+def test_longer_calls_are_split(at, keys):
+    """The other side: one row of few tokens behind more keys does not walk them in one item a head."""
+    s = Setup([keys], 1, 64, 64, "bf16", seed=2)
+    k, v, table, lengths, slots = s.args()
+    q, host = s.queries((4,), 8)
+    one = at.attend(q, k, v, table, lengths, slots, starts=s.dev([0, 4]))
+    many = at.attend(q.repeat(70, 1, 1), k, v, table, lengths, slots.repeat(70), starts=s.dev([4 * i for i in range(71)]))
+    at.sync()
+    check_rows(s, host, one.cpu(), [4], [0], None, 0)
+    check_rows(s, host, many[:4].cpu(), [4], [0], None, 0)
+    assert not torch.equal(one, many[:4])
