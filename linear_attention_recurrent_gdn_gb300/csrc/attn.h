@@ -62,9 +62,9 @@ struct AttnArgs {
   float* ws;                 // partial results
 };
 
-// A tile is R consecutive rows of (token, head of the group) of one row of the
-// call and one head of keys, tpt tokens; `slots_of` tiles at most.  A tile's keys are split
-// over `splits` units whose results are joined.
+// A tile is `rows` consecutive rows of (token, head of the group) of one row of the call and one head of keys: tpt tokens,
+// and hgroups tiles for the heads of a group.  `tiles`: as many as the call may have of a head.  A tile's keys are split
+// over `splits` units whose results are joined (the tensor-core kernels: more than 1 says that they may be).
 struct AttnPlan {
   int32_t rows, tpt, hgroups, tiles, splits, grid;
   int64_t ws_bytes;
@@ -72,7 +72,7 @@ struct AttnPlan {
 // Prompts of every type, head dimension, stride and alignment.
 AttnPlan simt_plan(int n, int T, bool packed, int H, int G, int d, int sms);
 cudaError_t launch_simt(int dtype, bool vec, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
-
+// The parts of a split call's tiles become one.
 cudaError_t launch_simt_join(int dtype, const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 
 // One token a row (T = 1, not packed), any type and layout.

@@ -42,17 +42,6 @@ class Tables:
             self.stack += [self.table[s][c] for c in reversed(range(first, last))]
             self.lengths[s] = k
 
-    def free(self, num_pages):
-        """(how many are free, the stack)"""
-        return len(self.stack), self.stack
-
-
-def gather(pool, table_row, length, page):
-    """A slot's [length, G, d] from a pool [num_pages, G, page, d]."""
-    p = torch.arange(length)
-    cell = torch.as_tensor(table_row)[p // page].long()
-    return pool[cell, :, p % page]
-
 
 def attend_row(q, k, v, pos, window=None, sinks=0, scale=None):
     """q [t, H, d] at positions pos [t] over k, v [L, G, d].  Returns o, the sums of absolute weighted values, the
