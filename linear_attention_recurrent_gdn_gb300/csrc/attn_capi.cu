@@ -2,8 +2,7 @@
 // a kernel.  Nothing is allocated and nothing kept; what lives on the device
 // (slots, lengths, tables) is checked by the kernels.
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
+#include <initializer_list>
 #include <limits>
 
 #include <cuda_runtime.h>

@@ -1,11 +1,10 @@
-// Host-side helpers of the attention operators' C entry points: error text,
+// Host-side helpers of the mixer and attention operators' C entry points: error text,
 // alignment, launch status, the device's multiprocessors (internal).
 #pragma once
 #include <atomic>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
-#include <initializer_list>
 
 #include <cuda_runtime.h>
 

@@ -2,34 +2,25 @@
 // launches.  Everything is checked before the first CUDA call; nothing is
 // allocated and nothing kept.  A call's rows and the launch arguments are built
 // in a thread's own storage; calls of many rows take several launches.
-#include <atomic>
-#include <cstdarg>
-#include <cstdio>
 #include <cstring>
 
 #include <cuda_runtime.h>
 
 #include "../../include/deltalog.h"
 #include "dl_device.cuh"
+#include "host_util.h"
 #include "mixer.h"
 
 namespace {
 
 using namespace dl::mx;
 
-struct ErrOut {
-  char* buf;
-  int32_t len;
-  dl_status operator()(dl_status s, const char* fmt, ...) const {
-    if (buf && len > 0) {
-      va_list ap;
-      va_start(ap, fmt);
-      vsnprintf(buf, (size_t)len, fmt, ap);
-      va_end(ap);
-    }
-    return s;
-  }
-};
+using dl::ErrOut;
+using dl::al;
+using dl::bad_type;
+using dl::done;
+using dl::elem;
+using dl::num_sms;
 
 // Every row of a call, and the arguments of a launch.
 thread_local RowItem t_items[MX_ROWS];
@@ -39,16 +30,6 @@ thread_local SsmArgs t_ssm;
 thread_local SsmStep t_ssm_step;
 
 constexpr int64_t MAX_DIM = (int64_t)1 << 30;   // sizes that the kernels hold in 32 bits
-
-int64_t elem(int64_t dtype) { return dtype == DL_F32 ? 4 : 2; }
-bool al(const void* p, int64_t b) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(b - 1)) == 0; }
-
-// Every launch: CUDA's sticky state is left clean for the caller's next call.
-dl_status done(const ErrOut& fail, cudaError_t e) {
-  if (e == cudaSuccess) return DL_OK;
-  (void)cudaGetLastError();
-  return fail(DL_ECUDA, "launch failed: %s", cudaGetErrorString(e));
-}
 
 // Distinct ids in [0, num_slots): an open-addressing table on the stack.
 dl_status check_slots(const ErrOut& fail, const int32_t* slots, int64_t n, int64_t num_slots) {
@@ -128,26 +109,6 @@ bool view_vec(const dl_view& v, int64_t dtype, bool packed) {
   const int64_t per = 16 / elem(dtype);
   return al(v.data, 16) && v.stride_t % per == 0 && (packed || v.stride_n % per == 0);
 }
-
-// Multiprocessors of the current device (a GB300's where there is none to ask).
-int num_sms() {
-  static std::atomic<int> known[64];
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
-    (void)cudaGetLastError();
-    return 152;
-  }
-  n = known[dev].load(std::memory_order_relaxed);
-  if (n) return n;
-  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) {
-    (void)cudaGetLastError();
-    return 152;
-  }
-  known[dev].store(n, std::memory_order_relaxed);
-  return n;
-}
-
-bool bad_type(int64_t t) { return t < DL_F32 || t > DL_F16; }
 
 }  // namespace
 
