@@ -607,8 +607,13 @@ dl_status dl_kv_append(const dl_kv_append_args *args, void *stream, char *errbuf
  * A token that sees nothing (a position below zero, scores of -inf alone) gives
  * zero.  What a token does not see does not reach it, infinities and NaN
  * included.  dl_attend_step: one token a row (T = 1, not packed, tokens NULL).
- * The workspace takes the partial results of keys that are split over the GPU;
- * the order in which they are joined depends on the sizes alone. */
+ * o is summed before it is divided by the weights' sum, which can pass 2^20 for
+ * every 64 keys: values of bf16 or fp32 near the end of their range may
+ * overflow where their mean would not.
+ * The workspace takes the partial results of keys that are split over the GPU.
+ * They are joined in order, so a call repeats to the bit; where keys are split
+ * depends on the sizes, on all rows' lengths and on the number of
+ * multiprocessors, so a row's rounding changes with the rows beside it. */
 typedef struct dl_attend_args {
     int64_t dtype, n, T, packed, H, G, d, page_size, max_pages, num_slots, num_pages, window, sinks;
     double scale;

@@ -12,10 +12,11 @@
 // passes it by more than 2^8.
 //
 // HBM-bound for few heads a group, bound by instructions from eight on: fp32, 64
-// x 2048 tokens of 128, 214 us for 4 heads over each of 8 (5.0 TB/s; 979 us with
-// the tiles of attn_simt.cu), 356 us for 16 over each of 4.  A block's four warps
-// take the keys of a row (or of a part of it: few rows are split, and joined by
-// attn_simt.cu's second launch) in turns.
+// x 2048 tokens of 128, 166 us for one head over each of 8 (6.5 TB/s), 216 us for
+// 4 (5.0 TB/s; 979 us with the tiles of attn_simt.cu), 363 us for 16 over each of
+// 4.  bf16 heads of 100, which no vector divides, 790 us for 4 over each of 8.  A
+// block's four warps take the keys of a row (or of a part of it: few rows are
+// split, and joined by attn_simt.cu's second launch) in turns.
 #include <cmath>
 
 #include "attn_device.cuh"

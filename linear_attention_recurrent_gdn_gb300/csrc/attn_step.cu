@@ -92,7 +92,11 @@ struct StepKernelArgs {
 // Floats of a part: its vectors stay aligned.
 __host__ __device__ inline int part_size(int orows, int D) { return orows * D + ((2 * orows + 3) & ~3); }
 
-// Ring of stages: 16 rows of K, 16 of V, of D values.  As many as keep some 128 KB on their way on an SM.
+// Ring of stages: 16 rows of K, 16 of V, of D values.  As many as keep some 128 KB on their way on an SM, with CTAS of them
+// there.  Fewer fit where the rest of a CTA's memory grows: 12 bytes a row of the call and 4 (D + 8) a query head.  With
+// 4 query heads a head of keys that begins behind 306 rows (heads of 64: three CTAs instead of four) and 818 rows (heads of
+// 128: one instead of two), with 16 behind 18 and 274.  The parts then run in two waves: 512 rows of 2048 tokens over 2
+// heads of 128 take 166 us with 4 query heads each, 251 with 16; over 4 of 64 235 and 252; 1024 rows over 2 of 128 459.
 template <int D> struct Cfg {
   static constexpr int STAGES = 3, CTAS = D == 64 ? 4 : D == 128 ? 2 : 1;
   static constexpr uint32_t HALF = KT * D * 2, STAGE = 2 * HALF;
