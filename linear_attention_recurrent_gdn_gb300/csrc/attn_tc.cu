@@ -32,7 +32,7 @@
 // leaves it for the second launch, which joins the parts (reference, sum, O in the workspace) in order.  A plan formed
 // again by each of the join's blocks cost 5 to 20 us a call (32 rows of 4 tokens behind 8192: 63 us, now 42).
 //
-// Measured on a GB300, bf16, 32 heads of 128 over 8: one prompt of 8192 tokens 356 to 366 us on different boxes (1.5
+// Measured on a GB300, bf16, 32 heads of 128 over 8: one prompt of 8192 tokens 356 to 366 us on different machines (1.5
 // PFLOP/s, 0.78 of a library product of the same type; 391 after some 0.3 s, when the power limit holds the SMs at 1890
 // MHz instead of 2070), of 2048 44.5 us, 16 of 512 50.5 us; pieces of 371 tokens in all behind 30000 150 us; 16 heads of
 // 256 over 2, 8192 tokens 422 us; 40 heads of 64 under a window of 1000 399 us (0.58 PFLOP/s).  Heads of 128 are bound by
